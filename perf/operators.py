@@ -7,7 +7,7 @@ Two operators over rows of logits (one row per token position, `vocab` columns):
   gradient of all of them with respect to the logits;
 * distillation from a teacher's top log probabilities: the divergence of every
   row from k listed (token, log probability) pairs, and its gradient, either in
-  the same call or from the saved normalisers.
+  the same call or from the saved normalisers (maximum and sum of each row).
 
 `own` selects the side: elementary torch operations in 32 bits, or the
 library's calls.
@@ -51,7 +51,7 @@ def listed():
         # distillation step of a Llama-3-vocabulary student: loss and gradient in one call, rest of the mass in a bucket
         dict(name="distill-4096x128256-bf16-top64", op="distill", rows=4096, vocab=128256, pad=0, dtype="bf16",
              ids="i32", k=64, scale=1.0, tail="bucket"),
-        # the same for a GPT-2-vocabulary student whose head is padded to 50304 columns; every eighth position is padding
+        # the same for a GPT-2-vocabulary student, its head padded to 50304 columns; every eighth position is padding
         dict(name="distill-999x50257-bf16-top32", op="distill", rows=999, vocab=50257, pad=47, dtype="bf16",
              ids="i64", k=32, scale=0.5, tail="renorm", skip=8),
         # a micro-batch with fp32 logits and the longest list
@@ -74,8 +74,8 @@ def draw(rng):
     dtype = rng.choice(["bf16", "bf16", "fp16", "fp32"])
     vocab = rng.choice([50257, 128256, log_between(1000, 200000), log_between(1000, 200000)])
     most = max(1, min(8192, _MOST // (vocab * (4 if dtype == "fp32" else 2))))
-    case = dict(op=op, rows=log_between(1, most), vocab=vocab, pad=rng.choice([0, 0, -vocab % 64, rng.randrange(1, 100)]),
-                dtype=dtype, ids=rng.choice(["i32", "i64"]), scale=rng.choice([1.0, 1.0, 0.5, 1.0 / 0.7]))
+    case = dict(op=op, rows=log_between(1, most), vocab=vocab,
+                pad=rng.choice([0, 0, -vocab % 64, rng.randrange(1, 100)]), dtype=dtype, ids=rng.choice(["i32", "i64"]), scale=rng.choice([1.0, 1.0, 0.5, 1.0 / 0.7]))
     if op.startswith("logprobs"):
         case["k"] = rng.choice([0, 1, log_between(1, 128), log_between(1, 128)])
     else:
@@ -147,23 +147,26 @@ def prepare(case, seed):
                 s["out"]["top_logprob"] = torch.empty((rows, k), **f32)
                 s["out"]["top_id"] = torch.empty((rows, k), dtype=idt, device=dev)
         else:
-            # what a forward saved, and the upstream gradients: advantages, the bonus, the penalty
-            lse = torch.empty(rows, **f32)
+            # what a forward saved (the normaliser as the pair of maximum and sum, the entropy, the alternatives), and
+            # the upstream gradients: advantages, the bonus, the penalty
+            norm = torch.empty((rows, 2), **f32)
             ent = torch.empty(rows, **f32)
             ids = torch.empty((rows, k), dtype=idt, device=dev)
             step = max(1, (1 << 26) // vocab)
             for i in range(0, rows, step):
                 z = x[i:i + step].double() * case["scale"]
+                m = z.max(dim=1).values
                 l = torch.logsumexp(z, dim=1)
                 p = torch.exp(z - l[:, None])
-                lse[i:i + step] = l
+                norm[i:i + step, 0] = x[i:i + step].max(dim=1).values
+                norm[i:i + step, 1] = torch.exp(l - m)
                 ent[i:i + step] = l - (p * z).sum(dim=1)
                 if k:
                     ids[i:i + step] = _top(x[i:i + step], k)[1].to(idt)
-            s["lse"], s["entropy"], s["top_id"] = lse, ent, ids if k else None
+            s["norm"], s["entropy"], s["top_id"] = norm, ent, ids if k else None
             s["d_logprob"] = torch.randn(rows, generator=gen, **f32) / rows
             s["d_entropy"] = torch.full((rows,), -0.01 / rows, **f32)
-            s["d_lse"] = lse * (2e-4 / rows)
+            s["d_lse"] = (norm[:, 0] * case["scale"] + torch.log(norm[:, 1])) * (2e-4 / rows)
             s["d_top"] = torch.randn((rows, k), generator=gen, **f32) / rows if k else None
             s["d_logits"] = torch.empty((rows, vocab + case["pad"]), dtype=x.dtype, device=dev)[:, :vocab]
         return s
@@ -174,7 +177,7 @@ def prepare(case, seed):
         w[case["skip"] - 1::case["skip"]] = 0.0  # padding positions
     s["weight"] = w
     s["loss"] = torch.empty(rows, **f32)
-    s["lse"] = torch.empty(rows, **f32)
+    s["norm"] = torch.empty((rows, 2), **f32)
     s["tail_logprob"] = torch.empty(rows, **f32)
     if op != "distill_loss":
         s["d_logits"] = torch.empty((rows, vocab + case["pad"]), dtype=x.dtype, device=dev)[:, :vocab]
@@ -184,7 +187,8 @@ def prepare(case, seed):
         for i in range(0, rows, step):
             z = x[i:i + step].double() * case["scale"]
             l = torch.logsumexp(z, dim=1)
-            s["lse"][i:i + step] = l
+            s["norm"][i:i + step, 0] = x[i:i + step].max(dim=1).values
+            s["norm"][i:i + step, 1] = torch.exp(l - z.max(dim=1).values)
             z.scatter_(1, s["ids"][i:i + step].long(), -math.inf)
             s["tail_logprob"][i:i + step] = torch.logsumexp(z, dim=1) - l
     return s
@@ -249,7 +253,8 @@ def _plain_distill(s, want_grad, d_loss=None):
         loss = loss + torch.where(qt > 0, qt * (torch.log(qt) - tail_logp), 0.0)
     live = w != 0
     if not want_grad:
-        out = {"loss": torch.where(live, loss * w, 0.0), "lse": torch.where(live, (m + torch.log(t))[:, 0], 0.0)}
+        norm = torch.cat([x.max(dim=1, keepdim=True).values.float(), t], dim=1)
+        out = {"loss": torch.where(live, loss * w, 0.0), "norm": torch.where(live[:, None], norm, 0.0)}
         if mode == "bucket":
             out["tail_logprob"] = torch.where(live, tail_logp, 0.0)
         return out
@@ -286,13 +291,13 @@ def run(s):
         ss.ss_token_logprobs(s["x"], s["tokens"], scale=s["scale"], **s["out"])
         return s["out"]
     if op == "logprobs_grad":
-        ss.ss_token_logprobs_grad(s["x"], s["lse"], s["d_logits"], tokens=s["tokens"], d_logprob=s["d_logprob"],
+        ss.ss_token_logprobs_grad(s["x"], s["norm"], s["d_logits"], tokens=s["tokens"], d_logprob=s["d_logprob"],
                                   entropy=s["entropy"], d_entropy=s["d_entropy"], d_lse=s["d_lse"],
                                   top_id=s["top_id"], d_top_logprob=s["d_top"], scale=s["scale"])
         return {"d_logits": s["d_logits"]}
     tail = {"drop": ss.SS_TAIL_DROP, "renorm": ss.SS_TAIL_RENORM, "bucket": ss.SS_TAIL_BUCKET}[s["tail"]]
     if op == "distill_grad":
-        ss.ss_distill_topk_grad(s["x"], s["ids"], s["teacher"], s["lse"], s["d_logits"],
+        ss.ss_distill_topk_grad(s["x"], s["ids"], s["teacher"], s["norm"], s["d_logits"],
                                 tail_logprob=s["tail_logprob"], d_loss=s["d_loss"], row_weight=s["weight"], tail=tail,
                                 scale=s["scale"])
         return {"d_logits": s["d_logits"]}
@@ -300,7 +305,7 @@ def run(s):
         ss.ss_distill_topk(s["x"], s["ids"], s["teacher"], s["loss"], d_logits=s["d_logits"], row_weight=s["weight"],
                            tail=tail, scale=s["scale"])
         return {"loss": s["loss"], "d_logits": s["d_logits"]}
-    out = {"loss": s["loss"], "lse": s["lse"]}
+    out = {"loss": s["loss"], "norm": s["norm"]}
     if s["tail"] == "bucket":
         out["tail_logprob"] = s["tail_logprob"]
     ss.ss_distill_topk(s["x"], s["ids"], s["teacher"], row_weight=s["weight"], tail=tail, scale=s["scale"], **out)
@@ -317,13 +322,13 @@ def work(case):
     if op == "logprobs":
         return {"bytes": n * es + rows * (ib + 12 + k * (4 + ib)), "flops": 7 * n}
     if op == "logprobs_grad":
-        return {"bytes": 2 * n * es + rows * (ib + 20 + k * (4 + ib)), "flops": 6 * n}
+        return {"bytes": 2 * n * es + rows * (ib + 24 + k * (4 + ib)), "flops": 6 * n}
     lists = live * k * (4 + ib) + rows * 4
     if op == "distill_loss":
-        return {"bytes": read * es + lists, "flops": 4 * read}
+        return {"bytes": read * es + lists + rows * (16 if case["tail"] == "bucket" else 12), "flops": 4 * read}
     if op == "distill":
         return {"bytes": (read + n) * es + lists + rows * 4, "flops": 8 * read}
-    return {"bytes": (read + n) * es + lists + rows * 12, "flops": 4 * read}
+    return {"bytes": (read + n) * es + lists + rows * 16, "flops": 4 * read}
 
 
 # ------------------------------------------------------------------ the definition in 64 bits
@@ -381,7 +386,9 @@ def exact(case, seed):
         o = {"loss": loss * w}
         if op == "distill_loss":
             live = w != 0
-            o["lse"] = torch.where(live, torch.logsumexp(x[sl].double() * c, dim=1), 0.0)
+            big = x[sl].double().max(dim=1).values
+            o["norm"] = torch.where(live[:, None], torch.stack(
+                [big, ((x[sl].double() - big[:, None]) * c).exp().sum(dim=1)], dim=1), 0.0)
             if case["tail"] == "bucket":
                 o["tail_logprob"] = torch.where(live, pt.log(), 0.0)
         else:
