@@ -27,6 +27,10 @@ LIB_PATH = os.environ.get("SS_LIBRARY") or os.path.join(_HERE, "libss.so")
 
 SS_BF16, SS_FP16, SS_FP32 = 0, 1, 2
 SS_MAX_RANKS = 1024
+SS_I32, SS_I64 = 0, 1
+SS_TAIL_DROP, SS_TAIL_RENORM, SS_TAIL_BUCKET = 0, 1, 2
+SS_MAX_TOP = 128
+SS_MAX_DISTILL_VOCAB = 393216
 
 STATUS = {0: "SS_OK", 1: "SS_ERR_INVALID_ARG", 2: "SS_ERR_ALIGN", 3: "SS_ERR_OVERLAP", 4: "SS_ERR_DTYPE",
           5: "SS_ERR_OVERFLOW", 6: "SS_ERR_CUDA"}
@@ -68,6 +72,25 @@ class _Options(ctypes.Structure):
                 ("dev_grad_scale", ctypes.c_void_p), ("dev_skip_flag", ctypes.c_void_p)]
 
 
+class _Logits(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _LogprobOut(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("logprob", "entropy", "lse", "norm", "top_logprob", "top_id")]
+
+
+class _LogprobGrad(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("d_logprob", "d_entropy", "d_lse", "d_top_logprob")]
+
+
+class _Teacher(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("logprob", ctypes.c_void_p), ("row_weight", ctypes.c_void_p),
+                ("k", ctypes.c_int32), ("idtype", ctypes.c_int32), ("dtype", ctypes.c_int32), ("tail", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("pad_", ctypes.c_int32)]
+
+
 _NO_OPTIONS = _Options(None, None, None, None)
 
 
@@ -95,6 +118,11 @@ def _load():
     lib.ss_grad_sumsq_workspace.restype = i64
     lib.ss_grad_sumsq.argtypes = [i64, vp, vp, i32, i32, f32, vp, vp, i64, vp, vp, vp]
     lib.ss_clip_coef.argtypes = [vp, i32, f32, vp, vp, vp]
+    lib.ss_token_logprobs.argtypes = [ctypes.POINTER(_Logits), vp, i32, i32, ctypes.POINTER(_LogprobOut), vp]
+    lib.ss_token_logprobs_grad.argtypes = [ctypes.POINTER(_Logits), vp, i32, i32, vp, vp, vp,
+                                           ctypes.POINTER(_LogprobGrad), vp, i64, vp]
+    lib.ss_distill_topk.argtypes = [ctypes.POINTER(_Logits), ctypes.POINTER(_Teacher), vp, vp, vp, vp, i64, vp]
+    lib.ss_distill_topk_grad.argtypes = [ctypes.POINTER(_Logits), ctypes.POINTER(_Teacher), vp, vp, vp, vp, i64, vp]
     lib.ss_grad_sumsq_noalloc.argtypes = [i64, vp, vp, i32, i32, f32, vp, vp, vp, vp]
     return lib
 
@@ -349,3 +377,162 @@ def ss_reshard(flat, shard_bounds: np.ndarray, shards, *, dtype: int | None = No
     with _DeviceGuard(flat):
         _check(_lib.ss_reshard(_ptr(flat), b.ctypes.data, len(ptrs), -1 if dtype is None else dtype,
                                _addr(ptrs), _stream(stream, flat)), "ss_reshard")
+
+
+# ----------------------------------------------------------------------------- rows of logits
+
+_ID_DTYPES = None
+
+
+def _rows_of(x, shape, ld, dtype, scale):
+    """The _Logits of a 2-D tensor (unit stride along the vocabulary), or of an address with shape = (rows,
+    vocab), ld (default: vocab) and dtype."""
+    if isinstance(x, int):
+        rows, vocab = shape
+        return _Logits(x, rows, vocab, vocab if ld is None else ld, -1 if dtype is None else dtype, scale)
+    _t()
+    rows, vocab = x.shape
+    s0, s1 = x.stride()
+    if s1 != 1 and vocab > 1:
+        raise SSError(1, "logits: the vocabulary must have stride 1")
+    # torch gives a single row any stride
+    return _Logits(x.data_ptr(), rows, vocab, s0 if rows > 1 else max(s0, vocab), _DTYPES.get(x.dtype, -1), scale)
+
+
+def _grad_rows(d, x, d_ld):
+    """(address, ld) of a gradient of x's shape and dtype (x: the _Logits)."""
+    if d is None:
+        return None, 0
+    if isinstance(d, int):
+        return d, (x.vocab if d_ld is None else d_ld)
+    if tuple(d.shape) != (x.rows, x.vocab) or (d.stride(1) != 1 and x.vocab > 1):
+        raise SSError(1, "d_logits: the logits' shape, with stride 1 along the vocabulary")
+    if _DTYPES.get(d.dtype, -1) != x.dtype:
+        raise SSError(4, "d_logits")
+    return d.data_ptr(), (d.stride(0) if x.rows > 1 else max(d.stride(0), x.vocab))
+
+
+def _arg(t, n, where, dtypes=None):
+    """The address of an optional dense array of n elements: fp32, or one of `dtypes`."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.numel() != n or not t.is_contiguous():
+        raise SSError(1, f"{where}: a dense array of {n} elements")
+    if t.dtype not in dtypes if dtypes is not None else t.dtype is not _torch.float32:
+        raise SSError(4, where)
+    return t.data_ptr()
+
+
+def _idtype(ids, idtype):
+    """The ss_idtype of the call: the tensor's, or `idtype` for an address."""
+    global _ID_DTYPES
+    if _ID_DTYPES is None:
+        torch = _t()
+        _ID_DTYPES = {torch.int32: SS_I32, torch.int64: SS_I64}
+    if ids is None or isinstance(ids, int):
+        return SS_I64 if idtype is None else idtype
+    return _ID_DTYPES.get(ids.dtype, -1)
+
+
+def ss_token_logprobs(logits, tokens=None, *, scale: float = 1.0, logprob=None, entropy=None, lse=None, norm=None,
+                      top_logprob=None, top_id=None, top_k: int | None = None, shape=None, ld: int | None = None,
+                      dtype: int | None = None, idtype: int | None = None, stream=None) -> None:
+    """Log probabilities of given tokens, with entropy, normaliser and top alternatives, one pass over the logits.
+
+    logits: (rows, vocab), bf16, fp16 or fp32, any row stride. tokens: (rows,) int32 or int64, negative where a row
+    has none. Each output is optional and written into the given tensor: logprob, entropy, lse (rows,), norm
+    (rows, 2) = (max, sum of exp(scale (x - max))), top_logprob and top_id (rows, k), k <= SS_MAX_TOP, in descending
+    order, equal logits by ascending id; top_id has the tokens' type. Every figure is of scale * logits. include/ss.h
+    says what masked rows and NaN give.
+    """
+    x = _rows_of(logits, shape, ld, dtype, scale)
+    it = _idtype(tokens if tokens is not None else top_id, idtype)
+    r = x.rows
+    top = top_logprob if top_logprob is not None else top_id
+    k = top_k if top_k is not None else (0 if top is None or isinstance(top, int) else top.shape[-1])
+    out = _LogprobOut(_arg(logprob, r, "logprob"), _arg(entropy, r, "entropy"), _arg(lse, r, "lse"),
+                      _arg(norm, 2 * r, "norm"), _arg(top_logprob, r * k, "top_logprob"),
+                      _arg(top_id, r * k, "top_id", _ids_like(it)))
+    with _DeviceGuard(logits):
+        _check(_lib.ss_token_logprobs(x, _arg(tokens, r, "tokens", _ids_like(it)), it, k, out,
+                                      _stream(stream, logits)), "ss_token_logprobs")
+
+
+def _ids_like(it):
+    return (_torch.int32,) if it == SS_I32 else ((_torch.int64,) if it == SS_I64 else ())
+
+
+def ss_token_logprobs_grad(logits, norm, d_logits, *, tokens=None, d_logprob=None, entropy=None, d_entropy=None,
+                           d_lse=None, top_id=None, d_top_logprob=None, scale: float = 1.0, top_k: int | None = None,
+                           shape=None, ld: int | None = None, d_ld: int | None = None, dtype: int | None = None,
+                           idtype: int | None = None, stream=None) -> None:
+    """d_logits = the gradient of ss_token_logprobs' outputs with respect to the logits, for the upstream gradients
+    d_logprob, d_entropy, d_lse (rows,) and d_top_logprob (rows, k), each optional, one at least given.
+
+    norm, entropy and top_id are what the forward call wrote. d_logits has the logits' shape and dtype and may be the
+    logits themselves. A row whose upstream gradients are all zero is not read and gets zeros.
+    """
+    x = _rows_of(logits, shape, ld, dtype, scale)
+    it = _idtype(tokens if tokens is not None else top_id, idtype)
+    r = x.rows
+    d, dl = _grad_rows(d_logits, x, d_ld)
+    k = 0
+    if d_top_logprob is not None:
+        k = top_k if top_k is not None else (0 if isinstance(d_top_logprob, int) else d_top_logprob.shape[-1])
+    ids = _ids_like(it)
+    up = _LogprobGrad(_arg(d_logprob, r, "d_logprob"), _arg(d_entropy, r, "d_entropy"), _arg(d_lse, r, "d_lse"),
+                      _arg(d_top_logprob, r * k, "d_top_logprob"))
+    with _DeviceGuard(logits):
+        _check(_lib.ss_token_logprobs_grad(x, _arg(tokens, r, "tokens", ids), it, k,
+                                           _arg(top_id, r * k, "top_id", ids) if k else None,
+                                           _arg(norm, 2 * r, "norm"), _arg(entropy, r, "entropy"), up, d, dl,
+                                           _stream(stream, logits)), "ss_token_logprobs_grad")
+
+
+def _teacher_of(x, ids, logprob, row_weight, tail, teacher_scale, k, idtype, tdtype):
+    it = _idtype(ids, idtype)
+    if k is None:
+        k = ids.shape[-1]
+    td = _dtype_of(logprob) if not isinstance(logprob, int) else tdtype
+    n = x.rows * k
+    return _Teacher(_arg(ids, n, "ids", _ids_like(it)), _arg(logprob, n, "teacher", _DTYPES),
+                    _arg(row_weight, x.rows, "row_weight"), k, it, -1 if td is None else td, tail, teacher_scale, 0)
+
+
+def ss_distill_topk(logits, ids, teacher, loss=None, *, norm=None, tail_logprob=None, d_logits=None, row_weight=None,
+                    tail: int = SS_TAIL_BUCKET, scale: float = 1.0, teacher_scale: float = 1.0, k: int | None = None,
+                    shape=None, ld: int | None = None, d_ld: int | None = None, dtype: int | None = None,
+                    idtype: int | None = None, tdtype: int | None = None, stream=None) -> None:
+    """loss[r] = row_weight[r] * KL(teacher's list || student's row r), and, when d_logits is given, the gradient of
+    loss.sum() in the same call (d_logits may be the logits themselves).
+
+    ids (rows, k) int32 or int64 (negative: unused slot), teacher (rows, k) their log probabilities (bf16, fp16 or
+    fp32; times teacher_scale), k <= SS_MAX_TOP. tail: what the list leaves out is dropped, the list is renormalised,
+    or the rest of the mass is one more outcome (SS_TAIL_*). loss, norm (rows, 2) and tail_logprob are optional
+    outputs; the last two are what ss_distill_topk_grad takes. Rows of weight 0 are not read.
+    """
+    x = _rows_of(logits, shape, ld, dtype, scale)
+    t = _teacher_of(x, ids, teacher, row_weight, tail, teacher_scale, k, idtype, tdtype)
+    r = x.rows
+    d, dl = _grad_rows(d_logits, x, d_ld)
+    with _DeviceGuard(logits):
+        _check(_lib.ss_distill_topk(x, t, _arg(loss, r, "loss"), _arg(norm, 2 * r, "norm"),
+                                    _arg(tail_logprob, r, "tail_logprob"), d, dl, _stream(stream, logits)),
+               "ss_distill_topk")
+
+
+def ss_distill_topk_grad(logits, ids, teacher, norm, d_logits, *, tail_logprob=None, d_loss=None, row_weight=None,
+                         tail: int = SS_TAIL_BUCKET, scale: float = 1.0, teacher_scale: float = 1.0,
+                         k: int | None = None, shape=None, ld: int | None = None, d_ld: int | None = None,
+                         dtype: int | None = None, idtype: int | None = None, tdtype: int | None = None,
+                         stream=None) -> None:
+    """d_logits = d_loss[r] (default 1) times the gradient of ss_distill_topk's loss[r], from the norm and (with
+    SS_TAIL_BUCKET) the tail_logprob that it wrote."""
+    x = _rows_of(logits, shape, ld, dtype, scale)
+    t = _teacher_of(x, ids, teacher, row_weight, tail, teacher_scale, k, idtype, tdtype)
+    r = x.rows
+    d, dl = _grad_rows(d_logits, x, d_ld)
+    with _DeviceGuard(logits):
+        _check(_lib.ss_distill_topk_grad(x, t, _arg(norm, 2 * r, "norm"), _arg(tail_logprob, r, "tail_logprob"),
+                                         _arg(d_loss, r, "d_loss"), d, dl, _stream(stream, logits)),
+               "ss_distill_topk_grad")

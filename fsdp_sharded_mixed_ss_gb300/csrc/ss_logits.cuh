@@ -1,0 +1,220 @@
+// ss_logits.cuh -- pieces shared by the operators on rows of logits: element
+// access, the running maximum and sum of a softmax in base 2, and the host-side
+// checks of their arguments.
+//
+// Arithmetic. With c = scale * log2(e) and m the running maximum of x, a row's
+// exponentials are 2^((x - m) c), one hardware ex2 each (relative error below
+// 2^-21 with its argument's rounding). x - m is formed first, in x's own units:
+// it is exact near the maximum, where the mass is, and stays meaningful for rows
+// that hold the type's lowest value, where x c would overflow.
+#pragma once
+
+#include "ss_common.cuh"
+
+namespace ss {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kFloor = -1e4f;  // 2^kFloor is 0, and 0 * kFloor is 0 where 0 * -inf would be NaN
+
+template <int DT>
+struct ElemOf {
+  using T = uint16_t;
+  static constexpr int kVec = 8;  // elements in 16 bytes
+};
+template <>
+struct ElemOf<SS_FP32> {
+  using T = float;
+  static constexpr int kVec = 4;
+};
+template <int DT>
+using Elem = typename ElemOf<DT>::T;
+template <int DT>
+constexpr int kVecOf = ElemOf<DT>::kVec;
+
+template <int DT>
+__device__ __forceinline__ float to_float(Elem<DT> e) {
+  if constexpr (DT == SS_FP32) return e;
+  else return widen1<DT>(e);
+}
+
+template <int DT>
+__device__ __forceinline__ Elem<DT> from_float(float f) {
+  if constexpr (DT == SS_FP32) return f;
+  else return narrow1<DT>(f);
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack(const uint4& w, float (&f)[kVecOf<DT>]) {
+  if constexpr (DT == SS_FP32) {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  } else {
+    widen8<DT>(w, f);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float (&f)[kVecOf<DT>]) {
+  if constexpr (DT == SS_FP32)
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  else return narrow8<DT>(f);
+}
+
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7FFFFFFF); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A row's slice [0, n) of elements at p: `head` elements up to the first 16-byte
+// boundary, `nvec` whole vectors, then the rest.
+template <int DT>
+struct Slice {
+  int64_t n, nvec;
+  int head;
+  __device__ __forceinline__ Slice(const Elem<DT>* p, int64_t len) : n(len) {
+    constexpr int V = kVecOf<DT>;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(Elem<DT>));
+    head = static_cast<int>(min(static_cast<int64_t>((V - off) % V), len));
+    nvec = (len - head) / V;
+  }
+  __device__ __forceinline__ int64_t tail() const { return head + nvec * kVecOf<DT>; }
+};
+
+// m = max x (-inf before the first unmasked element), s = sum 2^d and
+// t = sum 2^d d over d = (x - m) c.
+struct RowSum {
+  float m, s, t;
+
+  __device__ __forceinline__ static RowSum none() { return {-kInf, 0.0f, 0.0f}; }
+  // Moves the maximum up to `to` (> m).
+  __device__ __forceinline__ void move(float to, float c) {
+    if (s != 0.0f) {  // NaN sums move too
+      const float d = fmaxf((m - to) * c, kFloor), f = ex2(d);
+      t = f * fmaf(s, d, t);
+      s *= f;
+    }
+    m = to;
+  }
+  // What is subtracted: finite while every element so far is masked.
+  __device__ __forceinline__ float ref() const { return m == -kInf ? 0.0f : m; }
+  __device__ __forceinline__ void add(float x, float c, float ref_) {
+    const float d = (x - ref_) * c;
+    const float e = ex2(d);
+    s += e;
+    t = fmaf(e, fmaxf(d, kFloor), t);
+  }
+  __device__ __forceinline__ void merge(RowSum b, float c) {
+    if (b.m > m) move(b.m, c);
+    else if (m > b.m) b.move(m, c);
+    s += b.s;
+    t += b.t;
+  }
+};
+
+// Merged over the block, the same in every thread. `red`: a slot per warp.
+template <int THREADS>
+__device__ __forceinline__ RowSum block_merge(RowSum a, float c, RowSum* red) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    RowSum o;
+    o.m = __shfl_xor_sync(0xFFFFFFFFu, a.m, off);
+    o.s = __shfl_xor_sync(0xFFFFFFFFu, a.s, off);
+    o.t = __shfl_xor_sync(0xFFFFFFFFu, a.t, off);
+    a.merge(o, c);
+  }
+  __syncthreads();  // an earlier call's slots have been read
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+  __syncthreads();
+  RowSum b = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) b.merge(red[w], c);
+  return b;
+}
+
+// Order of logits as unsigned integers (-0 counts as +0; NaN rows do not come here).
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+// Larger logit first, equal logits by ascending id; 0 is below every element.
+__device__ __forceinline__ uint64_t order_pair(float x, int64_t id) {
+  return (static_cast<uint64_t>(order_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+}
+
+__device__ __forceinline__ int64_t load_id(const void* p, int64_t i, bool wide) {
+  return wide ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
+}
+__device__ __forceinline__ void store_id(void* p, int64_t i, int64_t v, bool wide) {
+  if (wide) static_cast<int64_t*>(p)[i] = v;
+  else static_cast<int32_t*>(p)[i] = static_cast<int32_t>(v);
+}
+
+// ------------------------------------------------------------------ host checks
+
+// Byte ranges of one call's arrays; no allocation, so nothing can throw.
+struct Ranges {
+  Range r[16];
+  int n = 0;
+  void add(const void* p, int64_t bytes, bool out) {
+    if (p && bytes > 0) r[n++] = rng(p, bytes, out);
+  }
+  bool overlap() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = i + 1; j < n; ++j)
+        if ((r[i].out || r[j].out) && r[i].lo < r[j].hi && r[j].lo < r[i].hi) return true;
+    return false;
+  }
+};
+
+inline int64_t dtype_bytes(int32_t dt) { return dt == SS_FP32 ? 4 : 2; }
+inline bool is_float_dtype(int32_t dt) { return dt == SS_BF16 || dt == SS_FP16 || dt == SS_FP32; }
+inline bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+// Bytes from the first to the last element of rows x width elements of row stride ld.
+inline bool span_bytes(int64_t rows, int64_t width, int64_t ld, int64_t es, int64_t* out) {
+  const __int128 v = (static_cast<__int128>(rows - 1) * ld + width) * es;
+  if (v > INT64_MAX) return false;
+  *out = static_cast<int64_t>(v);
+  return true;
+}
+
+// The rules every operator has for its logits (rows > 0 is checked by the caller first).
+inline ss_status check_logits(const ss_logits* x, int64_t* bytes) {
+  if (!x->data || x->vocab < 1 || x->vocab > INT32_MAX || x->ld < x->vocab) return SS_ERR_INVALID_ARG;
+  if (!(x->scale > 0.0f) || !std::isfinite(x->scale * kLog2e)) return SS_ERR_INVALID_ARG;
+  if (!is_float_dtype(x->dtype)) return SS_ERR_DTYPE;
+  if (misaligned(x->data, dtype_bytes(x->dtype))) return SS_ERR_ALIGN;
+  if (!span_bytes(x->rows, x->vocab, x->ld, dtype_bytes(x->dtype), bytes)) return SS_ERR_OVERFLOW;
+  return SS_OK;
+}
+
+// The gradient array: x's dtype; either x itself or apart from it (`ranges` gets it as an output, and x
+// as an input unless they are the same array).
+inline ss_status check_grad_out(const ss_logits* x, int64_t x_bytes, const void* d, int64_t d_ld, Ranges* ranges) {
+  if (d_ld < x->vocab) return SS_ERR_INVALID_ARG;
+  if (misaligned(d, dtype_bytes(x->dtype))) return SS_ERR_ALIGN;
+  int64_t bytes = 0;
+  if (!span_bytes(x->rows, x->vocab, d_ld, dtype_bytes(x->dtype), &bytes)) return SS_ERR_OVERFLOW;
+  ranges->add(d, bytes, true);
+  if (d != x->data || d_ld != x->ld) ranges->add(x->data, x_bytes, false);
+  return SS_OK;
+}
+
+// True when every row of the gradient starts at its logits row's 16-byte phase, so both take the same vectors.
+inline bool same_phase(const ss_logits* x, const void* d, int64_t d_ld) {
+  const int64_t es = dtype_bytes(x->dtype);
+  return ((reinterpret_cast<uintptr_t>(x->data) ^ reinterpret_cast<uintptr_t>(d)) & 15u) == 0 &&
+         (x->rows == 1 || ((x->ld - d_ld) * es) % 16 == 0);
+}
+
+}  // namespace ss

@@ -256,6 +256,139 @@ ss_status ss_unshard(const void* const* shards, const int64_t* shard_bounds, int
 ss_status ss_reshard(const void* flat, const int64_t* shard_bounds, int32_t n_ranks, ss_dtype dtype,
                      void* const* shards, void* stream);
 
+/* ------------------------------------------------------------ logits rows
+ * No counterpart on the pages: the operators between a model's logits and the
+ * gradients that the calls above reduce. Rows of logits are read where they
+ * lie; a call enqueues one kernel and needs no workspace.
+ *
+ * z = scale * x is a row's scaled logits (scale = 1 / temperature, finite and
+ * > 0), lse = log sum exp z, p = exp(z - lse). Sums and normalisers are fp32.
+ *   - `norm` [rows][2] is a row's normaliser as the pair (max x, sum exp(scale
+ *     (x - max x))): lse = scale * norm[0] + log norm[1]. The forward calls
+ *     write it, the gradient calls take it. Kept as a pair it has all its digits
+ *     whatever the size of the logits (a row that a mask filled with the type's
+ *     lowest value is the uniform distribution that the formulas say).
+ *   - A row all of whose logits are -inf (a mask that leaves nothing) has
+ *     p = 0 everywhere, lse = -inf and norm = (-inf, 0); the calls below say
+ *     what they write.
+ *   - A row with a NaN or +inf logit has a NaN sum and lse, and everything
+ *     computed from it is NaN.
+ *   - Logits of -inf elsewhere are masked tokens: p = 0, log p = -inf, and
+ *     nothing flows back to them.
+ * x: element i of row r is data[r * ld + i]; ld >= vocab (elements), so a view
+ *   of the first `vocab` columns of a padded head's output needs no copy.
+ *   Any element alignment; 16-byte vector accesses are used from each row's
+ *   first 16-byte boundary on. vocab >= 1 and < 2^31; rows == 0 is valid.
+ *   Overlap checks take a strided array from its first to its last element.
+ * Token ids are int32 or int64 (`ss_idtype`, one type per call). */
+typedef enum ss_idtype { SS_I32 = 0, SS_I64 = 1 } ss_idtype;
+#define SS_MAX_TOP 128 /* longest list of alternatives or of a teacher's tokens */
+
+typedef struct ss_logits {
+  const void* data; /* device */
+  int64_t rows, vocab, ld;
+  int32_t dtype;    /* ss_dtype: SS_BF16, SS_FP16 or SS_FP32 */
+  float scale;
+} ss_logits;
+
+/* Outputs of ss_token_logprobs; each is optional (NULL), one at least is given. */
+typedef struct ss_logprob_out {
+  float* logprob;     /* [rows] log p of the row's token: z_t - lse */
+  float* entropy;     /* [rows] -sum p log p, in nats */
+  float* lse;         /* [rows] log sum exp z */
+  float* norm;        /* [rows][2] the normaliser as a pair; 8-byte aligned */
+  float* top_logprob; /* [rows][top_k] log p of the top_k most likely tokens */
+  void* top_id;       /* [rows][top_k] their ids (idtype) */
+} ss_logprob_out;
+
+/* ss_token_logprobs: log probabilities of given tokens, with entropy and top
+ * alternatives, in one pass over the logits.
+ * tokens [rows] (device, idtype; NULL only with out->logprob NULL): the row's
+ *   token. Negative: the row has none, its logprob is 0. >= vocab: NaN.
+ * top_k: 0 (then top_logprob and top_id are NULL) to min(vocab, SS_MAX_TOP).
+ *   The alternatives come in descending order of their logits, equal logits by
+ *   ascending id (-0 equals +0); masked tokens come last, with -inf.
+ * A masked-out row: logprob -inf (0 without a token), entropy 0, top_logprob
+ *   -inf, top_id 0, 1, 2, ... A NaN row: top_id -1. */
+ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype idtype, int32_t top_k,
+                            const ss_logprob_out* out, void* stream);
+
+/* Upstream gradients of ss_token_logprobs' outputs; all device, each optional
+ * (NULL), one at least is given. */
+typedef struct ss_logprob_grad {
+  const float* d_logprob;     /* [rows]; needs tokens */
+  const float* d_entropy;     /* [rows]; needs entropy */
+  const float* d_lse;         /* [rows] */
+  const float* d_top_logprob; /* [rows][top_k]; needs top_id */
+} ss_logprob_grad;
+
+/* ss_token_logprobs_grad: the gradient with respect to x,
+ *   d_x = scale * (d_logprob (1[i = t] - p) + d_lse p - d_entropy p (log p + H)
+ *                  + sum_j d_top_logprob_j (1[i = top_id_j] - p)),
+ * from what the forward call wrote: norm [rows][2], entropy [rows] (H; unused
+ *   without d_entropy) and top_id [rows][top_k] (with d_top_logprob). Negative
+ *   ids carry nothing (their upstream gradient is not used); ids >= vocab make
+ *   the row's gradient NaN.
+ * d_logits: element i of row r at d_logits[r * d_ld + i], x's dtype, rounded
+ *   once. It may be x itself (same address and ld: the gradient replaces the
+ *   logits) and must not overlap anything else.
+ * A row whose upstream gradients are all zero is not read and gets zeros; so
+ * does a masked-out row. top_k is 0 without d_top_logprob. */
+ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idtype idtype, int32_t top_k,
+                                 const void* top_id, const float* norm, const float* entropy,
+                                 const ss_logprob_grad* up, void* d_logits, int64_t d_ld, void* stream);
+
+/* What a teacher's list leaves out. With log q_j = teacher_scale * t_j:
+ *   SS_TAIL_DROP    nothing more: the sum over the list alone.
+ *   SS_TAIL_RENORM  log q_j is normalised over the list (t_j may then be logits
+ *                   instead of log probabilities).
+ *   SS_TAIL_BUCKET  the teacher's remaining mass q_t = max(0, 1 - sum q_j) is
+ *                   one more outcome, against the student's mass p_t of all
+ *                   unlisted tokens. */
+typedef enum ss_tail { SS_TAIL_DROP = 0, SS_TAIL_RENORM = 1, SS_TAIL_BUCKET = 2 } ss_tail;
+#define SS_MAX_DISTILL_VOCAB 393216
+
+/* A teacher's top k tokens of every row; device arrays. */
+typedef struct ss_teacher {
+  const void* ids;     /* [rows][k] idtype; negative: unused slot; >= vocab: the row's loss and gradient are NaN.
+                          An id that occurs again in its row is an unused slot from its second occurrence on. */
+  const void* logprob; /* [rows][k] of dtype: log probabilities of the ids (-inf: zero mass) */
+  const float* row_weight; /* [rows] or NULL (all 1) */
+  int32_t k;           /* 1 .. SS_MAX_TOP */
+  int32_t idtype;      /* ss_idtype */
+  int32_t dtype;       /* ss_dtype */
+  int32_t tail;        /* ss_tail */
+  float scale;         /* teacher_scale, finite and > 0 */
+  int32_t pad_;
+} ss_teacher;
+
+/* ss_distill_topk: the Kullback-Leibler divergence of the student's rows from
+ * the teacher's lists,
+ *   loss_r = row_weight_r (sum_j q_j (log q_j - log p_j) + q_t (log q_t - log p_t)),
+ * (the last term with SS_TAIL_BUCKET; terms of zero q are zero; it is left out
+ * of a row whose unlisted tokens are all masked, by -inf or by logits so low
+ * that log2 p_t <= -1e4: tail_logprob is then -inf) and, when d_logits is
+ * given, the gradient of sum_r loss_r with respect to x in the same call:
+ *   d_x = row_weight scale (p (Q + q_t) - [listed] q - [not listed] q_t p / p_t),
+ * Q = sum q_j. vocab <= SS_MAX_DISTILL_VOCAB.
+ * loss [rows], norm [rows][2], tail_logprob [rows] fp32: each optional, but one
+ *   of them or d_logits is given. norm and tail_logprob (log p_t, in any tail
+ *   mode) are what ss_distill_topk_grad takes.
+ * d_logits, d_ld: as in ss_token_logprobs_grad; may be x itself.
+ * A row of weight 0 is not read: its loss, norm, tail_logprob and gradient are
+ * 0. A masked-out row: loss +inf when the teacher gives any mass (else as the
+ * formula), gradient 0. */
+ss_status ss_distill_topk(const ss_logits* x, const ss_teacher* teacher, float* loss, float* norm,
+                          float* tail_logprob, void* d_logits, int64_t d_ld, void* stream);
+
+/* ss_distill_topk_grad: d_logits = d_loss_r times the gradient above (d_loss
+ * [rows] or NULL: all 1), from the norm and, with SS_TAIL_BUCKET, the
+ * tail_logprob that ss_distill_topk wrote. Rows with row_weight or d_loss 0 are
+ * not read and get zeros. */
+ss_status ss_distill_topk_grad(const ss_logits* x, const ss_teacher* teacher, const float* norm,
+                               const float* tail_logprob, const float* d_loss, void* d_logits, int64_t d_ld,
+                               void* stream);
+
 /* ------------------------------------------------------------------- misc */
 const char* ss_status_string(ss_status s);      /* static string, never NULL */
 const char* ss_last_cuda_error(void);           /* last CUDA error text of this thread ("" if none) */

@@ -75,7 +75,8 @@ def draw(rng):
     vocab = rng.choice([50257, 128256, log_between(1000, 200000), log_between(1000, 200000)])
     most = max(1, min(8192, _MOST // (vocab * (4 if dtype == "fp32" else 2))))
     case = dict(op=op, rows=log_between(1, most), vocab=vocab,
-                pad=rng.choice([0, 0, -vocab % 64, rng.randrange(1, 100)]), dtype=dtype, ids=rng.choice(["i32", "i64"]), scale=rng.choice([1.0, 1.0, 0.5, 1.0 / 0.7]))
+                pad=rng.choice([0, 0, -vocab % 64, rng.randrange(1, 100)]), dtype=dtype,
+                ids=rng.choice(["i32", "i64"]), scale=rng.choice([1.0, 1.0, 0.5, 1.0 / 0.7]))
     if op.startswith("logprobs"):
         case["k"] = rng.choice([0, 1, log_between(1, 128), log_between(1, 128)])
     else:
