@@ -6,8 +6,6 @@
 namespace ss {
 namespace {
 
-constexpr int kRowThreads = 256;
-
 struct DistillArgs {
   const void* x;
   const void* ids;

@@ -9,9 +9,16 @@
 // that hold the type's lowest value, where x c would overflow.
 #pragma once
 
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
 #include "ss_common.cuh"
 
 namespace ss {
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxCluster = 8;  // blocks that share a row (the portable cluster size)
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -62,6 +69,26 @@ __device__ __forceinline__ uint4 pack(const float (&f)[kVecOf<DT>]) {
   if constexpr (DT == SS_FP32)
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   else return narrow8<DT>(f);
+}
+
+// The largest of one vector's elements; NaN elements are passed over (a vector of nothing else gives NaN).
+template <int DT>
+__device__ __forceinline__ float vec_max(const uint4& w) {
+  if constexpr (DT == SS_FP32) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  } else {
+    using P = std::conditional_t<DT == SS_BF16, __nv_bfloat162, __half2>;
+    P a, b, c, d;
+    std::memcpy(&a, &w.x, 4);
+    std::memcpy(&b, &w.y, 4);
+    std::memcpy(&c, &w.z, 4);
+    std::memcpy(&d, &w.w, 4);
+    const P m = __hmax2(__hmax2(a, b), __hmax2(c, d));
+    uint32_t o;
+    std::memcpy(&o, &m, 4);
+    const float2 f = widen2<DT>(o);
+    return fmaxf(f.x, f.y);
+  }
 }
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7FFFFFFF); }
@@ -159,6 +186,42 @@ __device__ __forceinline__ void store_id(void* p, int64_t i, int64_t v, bool wid
   else static_cast<int32_t*>(p)[i] = static_cast<int32_t>(v);
 }
 
+// ------------------------------------------------------------------ rows shared by a cluster of blocks
+//
+// With few rows a row is shared by the blocks of a cluster, which exchange their
+// parts through distributed shared memory: one launch, no workspace. The arrive
+// of start() and the wait of started() make sure that every block runs before
+// another one writes into its shared memory; the waits are the hardware's
+// cluster barrier, which every block of the cluster reaches.
+
+struct Cluster {
+  unsigned size, rank;
+  __device__ __forceinline__ static Cluster start() {
+    Cluster c;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(c.size));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(c.rank));
+    if (c.size > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    return c;
+  }
+  __device__ __forceinline__ void started() const {
+    if (size > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  }
+  // Barrier over all threads of the cluster; shared memory written before it, in any block, is seen after it.
+  __device__ __forceinline__ void sync() const {
+    if (size > 1) {
+      asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  }
+  // `p` (in this block's shared memory) at the same place in block r's.
+  template <class T>
+  __device__ __forceinline__ T* at(T* p, unsigned r) const {
+    return size > 1 ? cooperative_groups::this_cluster().map_shared_rank(p, r) : p;
+  }
+};
+
 // ------------------------------------------------------------------ host checks
 
 // Byte ranges of one call's arrays; no allocation, so nothing can throw.
@@ -208,6 +271,27 @@ inline ss_status check_grad_out(const ss_logits* x, int64_t x_bytes, const void*
   ranges->add(d, bytes, true);
   if (d != x->data || d_ld != x->ld) ranges->add(x->data, x_bytes, false);
   return SS_OK;
+}
+
+// Launches one cluster of `cluster` blocks per row (a plain launch for 1).
+template <typename Args>
+ss_status launch_rows(void (*fn)(Args), int64_t rows, int cluster, size_t smem, const Args& args, void* stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args);
+  return e == cudaSuccess ? SS_OK : cuda_fail(e);
 }
 
 // True when every row of the gradient starts at its logits row's 16-byte phase, so both take the same vectors.

@@ -5,8 +5,6 @@
 namespace ss {
 namespace {
 
-constexpr int kRowThreads = 256;
-
 struct LogprobArgs {
   const void* x;
   const void* tokens;
@@ -22,38 +20,259 @@ struct LogprobArgs {
   bool wide;  // int64 ids
 };
 
-// One block per row: one pass for the maximum, the sum and the entropy's sum,
-// then one pass per alternative for the largest pair below the last.
+// ------------------------------------------------------------------ forward
+//
+// A row belongs to a cluster of 1 to 8 blocks. Vector i of the row's whole
+// 16-byte vectors is thread (i mod T) of block (i / T) mod size, so a warp reads
+// 512 consecutive bytes and neighbouring ids are spread over threads and blocks.
+//
+// One pass gives the row's maximum, sum and entropy's sum. The alternatives come
+// from the same pass: the maximum of every unit (4 vectors of a thread, more in
+// rows longer than 16 units a thread) stays in shared memory, and every thread's
+// maximum is a key. Some threshold that k of the 256 keys reach is a bound that
+// at least k elements of the row reach, and few more: for k of 256 keys drawn at
+// random -256 ln(1 - k / 256) elements, 21 for k = 20 and 177 for k = 128. Only
+// units whose maximum reaches it are read again (from L2), their elements at or
+// above it are the candidates, and each candidate's rank is the number of
+// candidates above it. Where the candidates pass the buffer (ties), the exact
+// k-th pair is searched for by counting.
+
+constexpr int kBatch = 4;     // vectors that a thread has in flight
+constexpr int kUnits = 16;    // maxima kept per thread
+constexpr int kCand = 2048;   // candidates of a row, shared out over the cluster's blocks
+constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
+
+struct TopShared {
+  float unit[kUnits][kRowThreads];
+  uint64_t cand[kCand];          // block 0's is used
+  uint32_t keys[kRowThreads];
+  int count[kMaxCluster];        // candidates of every block
+  int sums[2][kMaxCluster];      // counts being added up over the cluster
+  int warp_sums[kRowThreads / 32];
+  int n;
+};
+struct NoTops {};
+
+// What a block keeps of the row while it works on it.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+struct RowPart {
+  const Elem<DT>* x;
+  Slice<DT> sl;
+  int first, step;  // this thread's vectors: first, first + step, ... < nvec
+  int edge;         // its element outside the vectors, or -1
+
+  __device__ __forceinline__ RowPart(const Elem<DT>* row, int64_t vocab, const Cluster& cl) : x(row), sl(row, vocab) {
+    const int t = threadIdx.x;
+    first = static_cast<int>(cl.rank) * kRowThreads + t;
+    step = static_cast<int>(cl.size) * kRowThreads;
+    edge = -1;
+    if (cl.rank == 0) {  // fewer than 8 elements before the vectors, and after them
+      const int after = t - 8;
+      if (t < sl.head) edge = t;
+      else if (after >= 0 && after < sl.n - sl.tail()) edge = static_cast<int>(sl.tail()) + after;
+    }
+  }
+  __device__ __forceinline__ const uint4* vec(int i) const { return reinterpret_cast<const uint4*>(x + sl.head) + i; }
+  // f(value, id) of every element of this thread's vectors numbered [j0, j1).
+  template <class F>
+  __device__ __forceinline__ void each(int j0, int j1, const F& f) const {
+    constexpr int V = kVecOf<DT>;
+    for (int j = j0; j < j1; j += kBatch) {
+      uint4 w[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = first + static_cast<int64_t>(j + u) * step;
+        if (j + u < j1 && i < sl.nvec) w[u] = __ldg(vec(static_cast<int>(i)));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = first + static_cast<int64_t>(j + u) * step;
+        if (j + u < j1 && i < sl.nvec) {
+          float e[V];
+          unpack<DT>(w[u], e);
+#pragma unroll
+          for (int q = 0; q < V; ++q) f(e[q], sl.head + static_cast<int>(i) * V + q);
+        }
+      }
+    }
+  }
+};
+
+// N vectors into the running sums; returns their maximum.
+template <int DT, int N>
+__device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RowSum& acc) {
   constexpr int V = kVecOf<DT>;
+  float m = vec_max<DT>(w[0]);
+#pragma unroll
+  for (int u = 1; u < N; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
+  if (m > acc.m) acc.move(m, c);
+  const float ref = acc.ref();
+  float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    float f[V];
+    unpack<DT>(w[u], f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = (f[j] - ref) * c, e = ex2(d);
+      s[j & 1] += e;
+      t[j & 1] = fmaf(e, d, t[j & 1]);
+    }
+  }
+  acc.s += s[0] + s[1];
+  float tt = t[0] + t[1];
+  if (!(tt == tt)) {  // masked elements (0 * -inf): the same sum with them at kFloor
+    tt = 0.0f;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float f[V];
+      unpack<DT>(w[u], f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float d = fmaxf((f[j] - ref) * c, kFloor);
+        tt = fmaf(ex2(d), d, tt);
+      }
+    }
+  }
+  acc.t += tt;
+  return m;
+}
+
+// Sum of v over all threads of the cluster, the same in each (all call it; `it` counts the calls).
+__device__ __forceinline__ int cluster_count(const Cluster& cl, TopShared& ts, int v, int it) {
+  v = __reduce_add_sync(0xFFFFFFFFu, v);
+  if ((threadIdx.x & 31) == 0) ts.warp_sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int* slots = ts.sums[it & 1];
+  if (threadIdx.x < cl.size) {
+    int b = 0;
+    for (int w = 0; w < kRowThreads / 32; ++w) b += ts.warp_sums[w];
+    cl.at(slots, threadIdx.x)[cl.rank] = b;
+  }
+  cl.sync();
+  int all = 0;
+  for (unsigned r = 0; r < cl.size; ++r) all += slots[r];
+  return all;
+}
+
+// The exact k-th largest pair as (key, id): elements above `key`, and those equal to it with ids up to `id`, are
+// the k. At least k elements reach the key `lo`; none is above `top`.
+template <int DT>
+__device__ __noinline__ uint2 search_pair(const Cluster& cl, TopShared& ts, const RowPart<DT>& part, int vectors,
+                                          uint32_t lo, uint32_t top, int k) {
+  const int vocab = static_cast<int>(part.sl.n);
+  int it = 0;
+  auto count = [&](auto pred) {
+    int c = 0;
+    part.each(0, vectors, [&](float f, int id) { c += pred(order_key(f), id) ? 1 : 0; });
+    if (part.edge >= 0) c += pred(order_key(to_float<DT>(part.x[part.edge])), part.edge) ? 1 : 0;
+    return cluster_count(cl, ts, c, it++);
+  };
+  uint32_t hi = top;  // count(key > hi) = above < k, count(key >= lo) >= k
+  int above = 0;
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    const int c = count([&](uint32_t key, int) { return key >= mid; });
+    if (c >= k) {
+      lo = mid;
+    } else {
+      hi = mid - 1;
+      above = c;
+    }
+  }
+  const int need = k - above;
+  int a = 0, b = vocab - 1;  // the smallest id bound that gives `need` elements equal to the key
+  while (a < b) {
+    const int mid = a + (b - a) / 2;
+    const int c = count([&](uint32_t key, int id) { return key == lo && id <= mid; });
+    if (c >= need) b = mid;
+    else a = mid + 1;
+  }
+  return make_uint2(lo, static_cast<uint32_t>(a));
+}
+
+template <int DT, bool TOPS>
+__global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ RowSum red[kRowThreads / 32];
-  __shared__ uint64_t best[kRowThreads / 32];
+  __shared__ RowSum parts[kMaxCluster];
+  __shared__ std::conditional_t<TOPS, TopShared, NoTops> tops;
+  const Cluster cl = Cluster::start();
   pdl_wait();
   pdl_trigger();
-  const int64_t row = blockIdx.x;
-  const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
-  const Slice<DT> sl(x, a.vocab);
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / cl.size;
+  const RowPart<DT> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl);
+  const int nvec = static_cast<int>(part.sl.nvec);
+  const int vectors = (nvec + part.step - 1) / part.step;            // of the thread that has most
+  const int full = nvec / (part.step * kBatch);                      // batches that every thread has whole
+  const int unit_batches = ((vectors + kBatch - 1) / kBatch + kUnits - 1) / kUnits;
   RowSum acc = RowSum::none();
-  auto add1 = [&](float f) {
-    if (f > acc.m) acc.move(f, a.c);
-    acc.add(f, a.c, acc.ref());
-  };
-  for (int64_t i = threadIdx.x; i < sl.head; i += kRowThreads) add1(to_float<DT>(x[i]));
-  for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads) add1(to_float<DT>(x[i]));
-  const uint4* v = reinterpret_cast<const uint4*>(x + sl.head);
-  for (int64_t i = threadIdx.x; i < sl.nvec; i += kRowThreads) {
-    float f[V];
-    unpack<DT>(v[i], f);
-    float m = f[0];
-#pragma unroll
-    for (int j = 1; j < V; ++j) m = fmaxf(m, f[j]);
-    if (m > acc.m) acc.move(m, a.c);
-    const float ref = acc.ref();
-#pragma unroll
-    for (int j = 0; j < V; ++j) acc.add(f[j], a.c, ref);
+  float edge = -kInf;
+  if (part.edge >= 0) {
+    edge = to_float<DT>(part.x[part.edge]);
+    if (edge > acc.m) acc.m = edge;
+    acc.add(edge, a.c, acc.ref());
   }
+  float unit = -kInf;
+  int in_unit = 0, units = 0;
+  auto end_batch = [&](float m) {
+    if constexpr (TOPS) {
+      unit = fmaxf(unit, m);
+      if (++in_unit == unit_batches) {
+        tops.unit[units++][tid] = unit;
+        in_unit = 0;
+        unit = -kInf;
+      }
+    }
+  };
+  for (int b = 0; b < full; ++b) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) w[u] = __ldg(part.vec(part.first + (b * kBatch + u) * part.step));
+    end_batch(add_vectors<DT>(w, a.c, acc));
+  }
+  if (full * kBatch < vectors) {
+    uint4 w[kBatch];
+    float m = -kInf;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = part.first + static_cast<int64_t>(full * kBatch + u) * part.step;
+      if (i < nvec) w[u] = __ldg(part.vec(static_cast<int>(i)));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = part.first + static_cast<int64_t>(full * kBatch + u) * part.step;
+      if (i < nvec) {
+        const uint4 one[1] = {w[u]};
+        m = fmaxf(m, add_vectors<DT>(one, a.c, acc));
+      }
+    }
+    end_batch(m);
+  }
+  if constexpr (TOPS) {
+    if (in_unit > 0) tops.unit[units++][tid] = unit;
+  }
+  const float thread_max = acc.m;
   acc = block_merge<kRowThreads>(acc, a.c, red);
+  cl.started();
+  if (cl.size > 1) {
+    if (tid < cl.size) cl.at(parts, tid)[cl.rank] = acc;
+  }
+  if constexpr (TOPS) {
+    // 256 keys of the whole row: the maxima of groups of `size` neighbouring threads of every block
+    uint32_t key = order_key(thread_max);
+    for (unsigned off = 1; off < cl.size; off <<= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+    if (tid % cl.size == 0) {
+      const unsigned at = cl.rank * (kRowThreads / cl.size) + tid / cl.size;
+      for (unsigned r = 0; r < cl.size; ++r) cl.at(tops.keys, r)[at] = key;
+    }
+    if (tid == 0) tops.n = 0;
+  }
+  if (TOPS || cl.size > 1) cl.sync();
+  if (cl.size > 1) {
+    acc = parts[0];
+    for (unsigned r = 1; r < cl.size; ++r) acc.merge(parts[r], a.c);
+  }
   const bool nan = !(acc.s == acc.s);
   const bool empty = acc.s == 0.0f;
   const float ln_s = logf(acc.s);
@@ -61,7 +280,7 @@ __global__ void __launch_bounds__(kRowThreads) logprob_kernel(const __grid_const
     if (nan) return nan_f();
     return empty ? -kInf : fmaf(f - acc.m, a.scale, -ln_s);
   };
-  if (threadIdx.x == 0) {
+  if (cl.rank == 0 && tid == 0) {
     if (a.norm) a.norm[row] = make_float2(acc.m, acc.s);
     if (a.lse) a.lse[row] = empty ? -kInf : fmaf(acc.m, a.scale, ln_s);
     if (a.entropy) {
@@ -70,36 +289,114 @@ __global__ void __launch_bounds__(kRowThreads) logprob_kernel(const __grid_const
     }
     if (a.logprob) {
       const int64_t t = load_id(a.tokens, row, a.wide);
-      a.logprob[row] = t < 0 ? 0.0f : (t >= a.vocab ? nan_f() : logp(to_float<DT>(x[t])));
+      a.logprob[row] = t < 0 ? 0.0f : (t >= a.vocab ? nan_f() : logp(to_float<DT>(part.x[t])));
     }
   }
-  uint64_t last = ~0ull;
-  for (int j = 0; j < a.top_k; ++j) {
-    uint64_t m = 0;
-    if (!nan) {
-      for (int64_t i = threadIdx.x; i < a.vocab; i += kRowThreads) {
-        const uint64_t p = order_pair(to_float<DT>(x[i]), i);
-        if (p < last && p > m) m = p;
+  if constexpr (TOPS) {
+    const int k = a.top_k;
+    auto put = [&](int j, int64_t id, float lp) {
+      const int64_t o = row * k + j;
+      if (a.top_id) store_id(a.top_id, o, id, a.wide);
+      if (a.top_logprob) a.top_logprob[o] = lp;
+    };
+    if (nan) {  // in every block of the cluster: all have merged the same parts
+      if (cl.rank == 0 && tid < k) put(tid, -1, nan_f());
+      return;
+    }
+    // the threshold: bit by bit, the largest that k keys reach; a little less is as good
+    constexpr int kLowBit = DT == SS_BF16 ? 16 : (DT == SS_FP16 ? 13 : 0);
+    const uint32_t my_key = tops.keys[tid];
+    uint32_t tau = 0;
+    for (int bit = 31; bit >= kLowBit; --bit) {
+      const uint32_t t = tau | (1u << bit);
+      const int c = __syncthreads_count(my_key >= t);
+      if (c >= k) {
+        tau = t;
+        if (c <= k + k / 8) break;
       }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, m, off);
-      m = o > m ? o : m;
+    const bool few = tau <= kMaskedKey;  // fewer than k threads hold unmasked tokens: all of those are candidates
+    if (few) tau = kMaskedKey + 1;
+    const float bound = few ? -kInf : key_value(tau);
+    auto wanted = [&](float f) { return few ? f > bound : f >= bound; };
+    const int room = kCand / static_cast<int>(cl.size);
+    uint64_t* out = cl.at(tops.cand, 0) + cl.rank * room;
+    auto add = [&](float f, int id) {
+      const int n = atomicAdd(&tops.n, 1);
+      if (n < room) out[n] = order_pair(f, id);
+    };
+    for (int u = 0; u < units; ++u) {
+      if (wanted(tops.unit[u][tid]))
+        part.each(u * unit_batches * kBatch, min(vectors, (u + 1) * unit_batches * kBatch), [&](float f, int id) {
+          if (wanted(f)) add(f, id);
+        });
     }
+    if (part.edge >= 0 && wanted(edge)) add(edge, part.edge);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) best[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = best[0];
-#pragma unroll
-    for (int w = 1; w < kRowThreads / 32; ++w) m = best[w] > m ? best[w] : m;
-    last = m;
-    if (threadIdx.x == 0) {
-      const int64_t o = row * a.top_k + j;
-      if (a.top_id) store_id(a.top_id, o, nan ? -1 : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(m)), a.wide);
-      if (a.top_logprob) a.top_logprob[o] = logp(key_value(static_cast<uint32_t>(m >> 32)));
+    if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = tops.n;
+    cl.sync();
+    int total = 0;
+    bool over = false;
+    for (unsigned r = 0; r < cl.size; ++r) {
+      total += tops.count[r];
+      over = over || tops.count[r] > room;
+    }
+    if (over) {
+      const uint2 kth = search_pair<DT>(cl, tops, part, vectors, tau, order_key(acc.m), k);
+      if (tid == 0) tops.n = 0;
+      __syncthreads();
+      auto kept = [&](float f, int id) {
+        const uint32_t key = order_key(f);
+        if (key > kth.x || (key == kth.x && id <= static_cast<int>(kth.y))) add(f, id);
+      };
+      part.each(0, vectors, kept);
+      if (part.edge >= 0) kept(edge, part.edge);
+      __syncthreads();
+      if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = tops.n;
+      cl.sync();
+      total = k;
+    }
+    if (cl.rank != 0) return;
+    for (int i = tid; i < total; i += kRowThreads) {
+      int r = 0, at = i;
+      while (at >= tops.count[r]) at -= tops.count[r++];
+      const uint64_t mine = tops.cand[r * room + at];
+      int rank = 0;
+      for (unsigned q = 0; q < cl.size; ++q)
+        for (int j = 0; j < tops.count[q]; ++j) rank += tops.cand[q * room + j] > mine ? 1 : 0;
+      if (rank < k)
+        put(rank, static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(mine)),
+            logp(key_value(static_cast<uint32_t>(mine >> 32))));
+    }
+    if (few && total < k) {  // the rest are masked tokens, by ascending id
+      int have = total;
+      for (int64_t base = 0; base < a.vocab && have < k; base += kRowThreads) {
+        const int64_t i = base + tid;
+        const bool masked = i < a.vocab && to_float<DT>(part.x[i]) == -kInf;
+        const unsigned votes = __ballot_sync(0xFFFFFFFFu, masked);
+        __syncthreads();  // the last round's sums have been read
+        if ((tid & 31) == 0) tops.warp_sums[tid >> 5] = __popc(votes);
+        __syncthreads();
+        int before = have;
+        for (int w = 0; w < kRowThreads / 32; ++w) {
+          if (w < tid >> 5) before += tops.warp_sums[w];
+          have += tops.warp_sums[w];
+        }
+        const int j = before + __popc(votes & ((1u << (tid & 31)) - 1u));
+        if (masked && j < k) put(j, i, -kInf);
+      }
     }
   }
+}
+
+// Blocks that share a row: rows alone fill the GPU from about 4 blocks on each SM; fewer rows are split while
+// every thread keeps a batch of vectors.
+int cluster_for(int64_t rows, int64_t vocab, int vec) {
+  const int64_t blocks = 4 * std::max(1, sm_count());
+  int c = 1;
+  while (c < kMaxCluster && rows * c * 2 <= blocks && vocab >= static_cast<int64_t>(c) * 2 * kRowThreads * kBatch * vec / 2)
+    c *= 2;
+  return c;
 }
 
 struct LogprobGradArgs {
@@ -242,9 +539,15 @@ ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype id
   const LogprobArgs a = {x->data, tokens, out->logprob, out->entropy, out->lse,
                          reinterpret_cast<float2*>(out->norm), out->top_logprob, out->top_id,
                          rows, x->vocab, x->ld, x->scale * kLog2e, x->scale, top_k, idtype == SS_I64};
-  auto* fn = x->dtype == SS_BF16 ? logprob_kernel<SS_BF16>
-                                 : (x->dtype == SS_FP16 ? logprob_kernel<SS_FP16> : logprob_kernel<SS_FP32>);
-  return launch(fn, static_cast<unsigned>(rows), a, stream, kRowThreads);
+  const auto pick = [&](auto tops) {
+    constexpr bool kTops = decltype(tops)::value;
+    return x->dtype == SS_BF16 ? logprob_kernel<SS_BF16, kTops>
+                               : (x->dtype == SS_FP16 ? logprob_kernel<SS_FP16, kTops> : logprob_kernel<SS_FP32, kTops>);
+  };
+  auto* fn = top_k > 0 ? pick(std::true_type()) : pick(std::false_type());
+  const int cluster = cluster_for(rows, x->vocab, x->dtype == SS_FP32 ? 4 : 8);
+  if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
+  return launch_rows(fn, rows, cluster, 0, a, stream);
 }
 
 ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idtype idtype, int32_t top_k,
