@@ -6,6 +6,11 @@
 namespace ss {
 namespace {
 
+#ifndef SS_PART_VECTORS
+#define SS_PART_VECTORS 16
+#endif
+constexpr int kPartVectors = SS_PART_VECTORS;
+
 struct DistillArgs {
   const void* x;
   const void* ids;
@@ -139,88 +144,230 @@ __device__ __forceinline__ void zero_row(Elem<DT>* d, int64_t n) {
   for (int64_t i = threadIdx.x; i < sl.nvec; i += kRowThreads) w[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// One block per row: the list, a pass for the unlisted tokens' maximum and sum
-// (a bit per token says which are listed), the row's loss, and a second pass
-// that writes the gradient. Unlisted and listed masses are kept apart, so the
-// student's tail p_t is a sum of its own terms and not a difference.
+// ------------------------------------------------------------------ loss and gradient in one call
+//
+// The gradient needs the row's sums and then the row again. A row is shared by
+// the blocks of a cluster, each holding its part in shared memory: the logits
+// are read from HBM once, with asynchronous copies that are all issued at the
+// start, and the gradient is computed from shared memory and written once. Two
+// to four blocks fit an SM, so one's sums and barriers pass under another's
+// copies and stores.
+//
+// The listed tokens are left out of the first pass (a bit per element of the
+// part says which they are), so the unlisted mass is a sum of its own terms and
+// not a difference: log p_t keeps its digits however little is left. Their
+// logits come with the list; their gradients are written last, over what the
+// second pass put there.
+
+// Marks the elements of packed vector w whose bits are set in `bits` as masked.
+template <int DT>
+__device__ __forceinline__ void mask_elements(uint4& w, uint32_t bits) {
+  uint32_t* p = &w.x;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    if constexpr (DT == SS_FP32) {
+      if ((bits >> h) & 1u) p[h] = 0xFF800000u;
+    } else {
+      constexpr uint32_t kNegInf = DT == SS_BF16 ? 0xFF80u : 0xFC00u;
+      if ((bits >> (2 * h)) & 1u) p[h] = (p[h] & 0xFFFF0000u) | kNegInf;
+      if ((bits >> (2 * h + 1)) & 1u) p[h] = (p[h] & 0xFFFFu) | (kNegInf << 16);
+    }
+  }
+}
+
+template <int DT>
+constexpr uint32_t kMaskedWord = DT == SS_FP32 ? 0xFF800000u : (DT == SS_BF16 ? 0xFF80FF80u : 0xFC00FC00u);
+
+template <int DT>
+__device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, RowMass& acc) {
+  constexpr int V = kVecOf<DT>;
+  float m = vec_max<DT>(w[0]);
+#pragma unroll
+  for (int u = 1; u < kBatch; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
+  if (m > acc.m) acc.move(m, c);
+  const float ref = acc.ref();
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    float f[V];
+    unpack<DT>(w[u], f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j & 1] += ex2((f[j] - ref) * c);
+  }
+  acc.s += s[0] + s[1];
+}
+
+// Zeros in this block's part of a gradient row.
+template <int DT>
+__device__ __forceinline__ void zero_part(Elem<DT>* d, int64_t n, unsigned rank, unsigned size) {
+  const Slice<DT> sl(d, n);
+  if (rank == 0) {
+    for (int64_t i = threadIdx.x; i < sl.head; i += kRowThreads) d[i] = from_float<DT>(0.0f);
+    for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads) d[i] = from_float<DT>(0.0f);
+  }
+  uint4* w = reinterpret_cast<uint4*>(d + sl.head);
+  for (int64_t i = rank * kRowThreads + threadIdx.x; i < sl.nvec; i += size * kRowThreads)
+    __stcs(w + i, make_uint4(0u, 0u, 0u, 0u));
+}
+
+// Dynamic shared memory: the part's vectors [batches * kBatch][T], then a byte of listed bits for each, by thread.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
-  extern __shared__ uint32_t listed[];
-  __shared__ RowSum red[kRowThreads / 32];
+  constexpr int V = kVecOf<DT>;
+  extern __shared__ uint4 held[];
+  __shared__ RowMass red[kRowThreads / 32];
+  __shared__ RowMass parts[kMaxCluster];
   __shared__ List l;
-  __shared__ float part[kRowThreads / 32];
+  __shared__ float part_loss[kRowThreads / 32];
+  __shared__ uint32_t edge_listed;
+  const Cluster cl = Cluster::start();
   pdl_wait();
   pdl_trigger();
-  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / cl.size;
   const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
   Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
   const float w = a.weight ? a.weight[row] : 1.0f;
-  if (w == 0.0f) {
-    if (a.d) zero_row<DT>(d, a.vocab);
-    if (threadIdx.x == 0) {
+  if (w == 0.0f) {  // every block of the cluster
+    if (a.d) zero_part<DT>(d, a.vocab, cl.rank, cl.size);
+    if (cl.rank == 0 && tid == 0) {
       if (a.loss) a.loss[row] = 0.0f;
       if (a.norm) a.norm[row] = make_float2(0.0f, 0.0f);
       if (a.tail) a.tail[row] = 0.0f;
     }
+    cl.started();
     return;
   }
-  for (int64_t i = threadIdx.x; i < (a.vocab + 31) / 32; i += kRowThreads) listed[i] = 0u;
+  const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
+  const int nvec = static_cast<int>(part.sl.nvec);
+  const int batches = (part.vectors() + kBatch - 1) / kBatch;
+  uint32_t* listed = reinterpret_cast<uint32_t*>(held + static_cast<size_t>(batches) * kBatch * kRowThreads);
+  // four groups of copies, so that the first quarter is added up while the rest is on its way
+  const int quarter = (batches + 3) / 4;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    for (int j = g * quarter * kBatch; j < min((g + 1) * quarter, batches) * kBatch; ++j) {
+      const int i = part.first + j * part.step;
+      if (i < nvec) copy_async16(held + j * kRowThreads + tid, part.vec(i));
+    }
+    copies_commit();
+  }
+  for (int q = 0; q < batches; ++q) listed[q * kRowThreads + tid] = 0u;
+  if (tid == 0) edge_listed = 0u;
+  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
   list_load<DT>(a, row, x, l);
-  const int j = threadIdx.x;
-  const int32_t my_id = j < a.k ? l.id[j] : -1;
-  if (my_id >= 0) atomicOr(&listed[my_id >> 5], 1u << (my_id & 31));
+  const int32_t my_id = tid < a.k ? l.id[tid] : -1;
+  int owner = 0, slot = 0;
+  const bool mine = my_id >= 0 && part.owns(my_id, &owner, &slot);
+  if (mine) {
+    if (slot < 0) atomicOr(&edge_listed, 1u << owner);
+    else atomicOr(&listed[(slot / kBatch) * kRowThreads + owner],
+                  1u << (slot % kBatch * 8 + (my_id - part.sl.head) % V));
+  }
   __syncthreads();
-  RowSum out = RowSum::none();  // unlisted tokens
-  for (int64_t i = threadIdx.x; i < a.vocab; i += kRowThreads) {
-    const float f = (listed[i >> 5] >> (i & 31)) & 1u ? -kInf : to_float<DT>(x[i]);
-    if (f > out.m) out.move(f, a.c);
-    out.add(f, a.c, out.ref());
+  RowMass out = RowMass::none();  // unlisted tokens
+  if (part.edge >= 0 && !((edge_listed >> tid) & 1u)) {
+    out.m = edge;
+    out.s = ex2((edge - out.ref()) * a.c);
   }
+  auto add_group = [&](int g) {
+    for (int q = g * quarter; q < min((g + 1) * quarter, batches); ++q) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        v[u] = held[(q * kBatch + u) * kRowThreads + tid];
+        if (part.first + (q * kBatch + u) * part.step >= nvec)
+          v[u] = make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+      }
+      const uint32_t bits = listed[q * kRowThreads + tid];
+      if (bits != 0u) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) mask_elements<DT>(v[u], (bits >> (8 * u)) & 0xFFu);
+      }
+      add_mass<DT>(v, a.c, out);
+    }
+  };
+  copies_wait<3>();
+  add_group(0);
+  copies_wait<2>();
+  add_group(1);
+  copies_wait<1>();
+  add_group(2);
+  copies_wait<0>();
+  add_group(3);
   out = block_merge<kRowThreads>(out, a.c, red);
-  RowSum in = RowSum::none();
-  if (my_id >= 0) {
-    in.m = l.x[j];
-    in.add(l.x[j], a.c, in.ref());
-  }
+  RowMass in = RowMass::none();
+  if (my_id >= 0) in = {l.x[tid], ex2((l.x[tid] - (l.x[tid] == -kInf ? 0.0f : l.x[tid])) * a.c)};
+  cl.started();
+  if (cl.size > 1 && tid < cl.size) cl.at(parts, tid)[cl.rank] = out;
   in = block_merge<kRowThreads>(in, a.c, red);
-  RowSum all = out;
+  if (cl.size > 1) {
+    cl.sync();
+    out = parts[0];
+    for (unsigned r = 1; r < cl.size; ++r) out.merge(parts[r], a.c);
+  }
+  RowMass all = out;
   all.merge(in, a.c);
   const bool empty = all.s == 0.0f;
-  const float ln_s = logf(all.s);
   // all unlisted tokens masked, by -inf or by values so low that no p_t is left
   const bool no_tail = out.s == 0.0f || (out.m - all.m) * a.c <= kFloor;
-  const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
-  float mine = 0.0f;
-  if (my_id >= 0 && l.q[j] != 0.0f) {
-    const float lp = empty ? -kInf : fmaf(l.x[j] - all.m, a.scale, -ln_s);
-    mine = l.q[j] * (l.lq[j] - lp);
-  }
+  if (cl.rank == 0) {
+    const float ln_s = logf(all.s);
+    const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
+    float term = 0.0f;
+    if (my_id >= 0 && l.q[tid] != 0.0f) {
+      const float lp = empty ? -kInf : fmaf(l.x[tid] - all.m, a.scale, -ln_s);
+      term = l.q[tid] * (l.lq[tid] - lp);
+    }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, off);
-  if ((j & 31) == 0) part[j >> 5] = mine;
-  __syncthreads();
-  if (j == 0) {
-    float loss = 0.0f;
-    for (int i = 0; i < kRowThreads / 32; ++i) loss += part[i];
-    if (l.q_tail > 0.0f && !no_tail) loss += l.q_tail * (logf(l.q_tail) - tail);
-    if (l.bad || !(all.s == all.s) || !(l.q_sum == l.q_sum)) loss = nan_f();
-    if (a.loss) a.loss[row] = w * loss;
-    if (a.norm) a.norm[row] = make_float2(all.m, all.s);
-    if (a.tail) a.tail[row] = tail;
+    for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, off);
+    if ((tid & 31) == 0) part_loss[tid >> 5] = term;
+    __syncthreads();
+    if (tid == 0) {
+      float loss = 0.0f;
+      for (int i = 0; i < kRowThreads / 32; ++i) loss += part_loss[i];
+      if (l.q_tail > 0.0f && !no_tail) loss += l.q_tail * (logf(l.q_tail) - tail);
+      if (l.bad || !(all.s == all.s) || !(l.q_sum == l.q_sum)) loss = nan_f();
+      if (a.loss) a.loss[row] = w * loss;
+      if (a.norm) a.norm[row] = make_float2(all.m, all.s);
+      if (a.tail) a.tail[row] = tail;
+    }
   }
   if (!a.d) return;
   if (empty) {
-    zero_row<DT>(d, a.vocab);
+    zero_part<DT>(d, a.vocab, cl.rank, cl.size);
     return;
   }
   const float ws = l.bad ? nan_f() : w * a.scale;
   const float b = l.q_sum + l.q_tail;
   // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
   const float p_t = no_tail ? 0.0f : ex2((out.m - all.m) * a.c) * (out.s / all.s);
-  const float A = no_tail ? ws * 0.0f : ws * (p_t * b - l.q_tail) / out.s;
+  const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - l.q_tail) / out.s;
   const float ref = out.ref();
-  const float g = my_id >= 0 ? ws * fmaf(ex2((l.x[j] - all.ref()) * a.c) / all.s, b, -l.q[j]) : 0.0f;
-  write_row<DT>(x, d, a.vocab, a.vec, [&](float f) { return ex2((f - ref) * a.c) * A; }, my_id, g);
+  const float c = a.c;
+  auto grad = [&](float f) { return ex2((f - ref) * c) * A; };
+  if (part.edge >= 0) d[part.edge] = from_float<DT>(grad(edge));
+  for (int q = 0; q < batches; ++q) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = q * kBatch + u, i = part.first + j * part.step;
+      if (i < nvec) {
+        float f[V];
+        unpack<DT>(held[j * kRowThreads + tid], f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = grad(f[e]);
+        Elem<DT>* o = d + part.sl.head + static_cast<int64_t>(i) * V;
+        if (a.vec) {
+          __stcs(reinterpret_cast<uint4*>(o), pack<DT>(f));
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = from_float<DT>(f[e]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (mine) d[my_id] = from_float<DT>(ws * fmaf(ex2((l.x[tid] - all.ref()) * a.c) / all.s, b, -l.q[tid]));
 }
 
 // The gradient from saved normalisers: one pass.
@@ -304,10 +451,17 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   }
   auto* fn = x->dtype == SS_BF16 ? distill_kernel<SS_BF16>
                                  : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16> : distill_kernel<SS_FP32>);
-  const size_t smem = static_cast<size_t>((x->vocab + 31) / 32) * 4;
+  // a part of at most kPartVectors vectors a thread, or what 8 blocks leave
+  const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
+  const auto vectors = [&](int c) { return (nvec + c * kRowThreads - 1) / (c * kRowThreads); };
+  int cluster = 1;
+  while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
+  const int64_t batches = (vectors(cluster) + kBatch - 1) / kBatch;
+  const size_t smem = static_cast<size_t>(batches) * kRowThreads * (kBatch * sizeof(uint4) + sizeof(uint32_t));
+  if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_fail(e);
-  return launch_dependent(fn, dim3(static_cast<unsigned>(rows)), dim3(kRowThreads), smem, stream, a);
+  return launch_rows(fn, rows, cluster, smem, a, stream);
 }
 
 }  // namespace

@@ -93,6 +93,18 @@ __device__ __forceinline__ float vec_max(const uint4& w) {
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7FFFFFFF); }
 
+// 16 bytes from global to shared memory, asynchronously; the issuing thread sees them after copies_wait.
+__device__ __forceinline__ void copy_async16(void* shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+               "l"(global)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -145,21 +157,38 @@ struct RowSum {
   }
 };
 
+// The same without t: m = max x, s = sum 2^((x - m) c).
+struct RowMass {
+  float m, s;
+
+  __device__ __forceinline__ static RowMass none() { return {-kInf, 0.0f}; }
+  __device__ __forceinline__ void move(float to, float c) {
+    if (s != 0.0f) s *= ex2((m - to) * c);
+    m = to;
+  }
+  __device__ __forceinline__ float ref() const { return m == -kInf ? 0.0f : m; }
+  __device__ __forceinline__ void merge(RowMass b, float c) {
+    if (b.m > m) move(b.m, c);
+    else if (m > b.m) b.move(m, c);
+    s += b.s;
+  }
+};
+
 // Merged over the block, the same in every thread. `red`: a slot per warp.
-template <int THREADS>
-__device__ __forceinline__ RowSum block_merge(RowSum a, float c, RowSum* red) {
+template <int THREADS, class Sum>
+__device__ __forceinline__ Sum block_merge(Sum a, float c, Sum* red) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    RowSum o;
+    Sum o;
     o.m = __shfl_xor_sync(0xFFFFFFFFu, a.m, off);
     o.s = __shfl_xor_sync(0xFFFFFFFFu, a.s, off);
-    o.t = __shfl_xor_sync(0xFFFFFFFFu, a.t, off);
+    if constexpr (std::is_same_v<Sum, RowSum>) o.t = __shfl_xor_sync(0xFFFFFFFFu, a.t, off);
     a.merge(o, c);
   }
   __syncthreads();  // an earlier call's slots have been read
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
   __syncthreads();
-  RowSum b = red[0];
+  Sum b = red[0];
 #pragma unroll
   for (int w = 1; w < THREADS / 32; ++w) b.merge(red[w], c);
   return b;
@@ -219,6 +248,77 @@ struct Cluster {
   template <class T>
   __device__ __forceinline__ T* at(T* p, unsigned r) const {
     return size > 1 ? cooperative_groups::this_cluster().map_shared_rank(p, r) : p;
+  }
+};
+
+// ------------------------------------------------------------------ a block's part of a row
+//
+// Of a row shared by `size` blocks of T threads, its whole 16-byte vector i
+// belongs to thread i mod T of block (i / T) mod size: a warp reads 512
+// consecutive bytes, and neighbouring ids are spread over threads and blocks.
+// The fewer than 8 elements before the first boundary and after the last vector
+// are one each of block 0's first 16 threads.
+
+constexpr int kBatch = 4;  // vectors that a thread has in flight
+
+template <int DT>
+struct RowPart {
+  const Elem<DT>* x;
+  Slice<DT> sl;
+  int rank, size;
+  int first, step;  // this thread's vectors: first, first + step, ... < nvec
+  int edge;         // its element outside the vectors, or -1
+
+  __device__ __forceinline__ RowPart(const Elem<DT>* row, int64_t vocab, unsigned rank_, unsigned size_)
+      : x(row), sl(row, vocab), rank(static_cast<int>(rank_)), size(static_cast<int>(size_)) {
+    const int t = threadIdx.x;
+    first = rank * kRowThreads + t;
+    step = size * kRowThreads;
+    edge = -1;
+    if (rank == 0) {
+      const int after = t - 8;
+      if (t < sl.head) edge = t;
+      else if (after >= 0 && after < sl.n - sl.tail()) edge = static_cast<int>(sl.tail()) + after;
+    }
+  }
+  // Vectors of the thread that has most.
+  __device__ __forceinline__ int vectors() const { return static_cast<int>((sl.nvec + step - 1) / step); }
+  // Whether element `id` is this block's; then `j` and `thread` say which of its vectors (j = -1: an edge).
+  __device__ __forceinline__ bool owns(int id, int* thread, int* j) const {
+    const int64_t o = id - sl.head;
+    if (o < 0 || o >= sl.nvec * kVecOf<DT>) {
+      *j = -1;
+      *thread = o < 0 ? id : static_cast<int>(id - sl.tail()) + 8;
+      return rank == 0;
+    }
+    const int i = static_cast<int>(o / kVecOf<DT>), q = i / kRowThreads;
+    *thread = i % kRowThreads;
+    *j = q / size;
+    return q % size == rank;
+  }
+  __device__ __forceinline__ const uint4* vec(int i) const { return reinterpret_cast<const uint4*>(x + sl.head) + i; }
+  // f(value, id) of every element of this thread's vectors numbered [j0, j1).
+  template <class F>
+  __device__ __forceinline__ void each(int j0, int j1, const F& f) const {
+    constexpr int V = kVecOf<DT>;
+    for (int j = j0; j < j1; j += kBatch) {
+      uint4 w[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = first + static_cast<int64_t>(j + u) * step;
+        if (j + u < j1 && i < sl.nvec) w[u] = __ldg(vec(static_cast<int>(i)));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = first + static_cast<int64_t>(j + u) * step;
+        if (j + u < j1 && i < sl.nvec) {
+          float e[V];
+          unpack<DT>(w[u], e);
+#pragma unroll
+          for (int q = 0; q < V; ++q) f(e[q], sl.head + static_cast<int>(i) * V + q);
+        }
+      }
+    }
   }
 };
 

@@ -22,11 +22,8 @@ struct LogprobArgs {
 
 // ------------------------------------------------------------------ forward
 //
-// A row belongs to a cluster of 1 to 8 blocks. Vector i of the row's whole
-// 16-byte vectors is thread (i mod T) of block (i / T) mod size, so a warp reads
-// 512 consecutive bytes and neighbouring ids are spread over threads and blocks.
-//
-// One pass gives the row's maximum, sum and entropy's sum. The alternatives come
+// A row belongs to a cluster of 1 to 8 blocks (RowPart says which elements are
+// whose). One pass gives the row's maximum, sum and entropy's sum. The alternatives come
 // from the same pass: the maximum of every unit (4 vectors of a thread, more in
 // rows longer than 16 units a thread) stays in shared memory, and every thread's
 // maximum is a key. Some threshold that k of the 256 keys reach is a bound that
@@ -37,7 +34,6 @@ struct LogprobArgs {
 // candidates above it. Where the candidates pass the buffer (ties), the exact
 // k-th pair is searched for by counting.
 
-constexpr int kBatch = 4;     // vectors that a thread has in flight
 constexpr int kUnits = 16;    // maxima kept per thread
 constexpr int kCand = 2048;   // candidates of a row, shared out over the cluster's blocks
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
@@ -52,51 +48,6 @@ struct TopShared {
   int n;
 };
 struct NoTops {};
-
-// What a block keeps of the row while it works on it.
-template <int DT>
-struct RowPart {
-  const Elem<DT>* x;
-  Slice<DT> sl;
-  int first, step;  // this thread's vectors: first, first + step, ... < nvec
-  int edge;         // its element outside the vectors, or -1
-
-  __device__ __forceinline__ RowPart(const Elem<DT>* row, int64_t vocab, const Cluster& cl) : x(row), sl(row, vocab) {
-    const int t = threadIdx.x;
-    first = static_cast<int>(cl.rank) * kRowThreads + t;
-    step = static_cast<int>(cl.size) * kRowThreads;
-    edge = -1;
-    if (cl.rank == 0) {  // fewer than 8 elements before the vectors, and after them
-      const int after = t - 8;
-      if (t < sl.head) edge = t;
-      else if (after >= 0 && after < sl.n - sl.tail()) edge = static_cast<int>(sl.tail()) + after;
-    }
-  }
-  __device__ __forceinline__ const uint4* vec(int i) const { return reinterpret_cast<const uint4*>(x + sl.head) + i; }
-  // f(value, id) of every element of this thread's vectors numbered [j0, j1).
-  template <class F>
-  __device__ __forceinline__ void each(int j0, int j1, const F& f) const {
-    constexpr int V = kVecOf<DT>;
-    for (int j = j0; j < j1; j += kBatch) {
-      uint4 w[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = first + static_cast<int64_t>(j + u) * step;
-        if (j + u < j1 && i < sl.nvec) w[u] = __ldg(vec(static_cast<int>(i)));
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = first + static_cast<int64_t>(j + u) * step;
-        if (j + u < j1 && i < sl.nvec) {
-          float e[V];
-          unpack<DT>(w[u], e);
-#pragma unroll
-          for (int q = 0; q < V; ++q) f(e[q], sl.head + static_cast<int>(i) * V + q);
-        }
-      }
-    }
-  }
-};
 
 // N vectors into the running sums; returns their maximum.
 template <int DT, int N>
@@ -201,7 +152,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   pdl_trigger();
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / cl.size;
-  const RowPart<DT> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl);
+  const RowPart<DT> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl.rank, cl.size);
   const int nvec = static_cast<int>(part.sl.nvec);
   const int vectors = (nvec + part.step - 1) / part.step;            // of the thread that has most
   const int full = nvec / (part.step * kBatch);                      // batches that every thread has whole
