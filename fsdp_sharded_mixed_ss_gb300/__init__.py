@@ -470,7 +470,7 @@ def ss_token_logprobs_grad(logits, norm, d_logits, *, tokens=None, d_logprob=Non
     d_logprob, d_entropy, d_lse (rows,) and d_top_logprob (rows, k), each optional, one at least given.
 
     norm, entropy and top_id are what the forward call wrote. d_logits has the logits' shape and dtype and may be the
-    logits themselves. A row whose upstream gradients are all zero is not read and gets zeros.
+    logits themselves. A row whose upstream gradients are all zero gets zeros, whatever its logits.
     """
     x = _rows_of(logits, shape, ld, dtype, scale)
     it = _idtype(tokens if tokens is not None else top_id, idtype)

@@ -27,6 +27,7 @@ struct DistillArgs {
   float c, scale, t_scale;
   int32_t k, mode, t_dtype;
   bool wide, vec;
+  uint32_t split;  // gradient from saved normalisers: blocks that share a row
 };
 
 __device__ __forceinline__ float load_teacher(const void* p, int64_t i, int dtype) {
@@ -35,113 +36,121 @@ __device__ __forceinline__ float load_teacher(const void* p, int64_t i, int dtyp
   return dtype == SS_BF16 ? widen1<SS_BF16>(h) : widen1<SS_FP16>(h);
 }
 
-// A row's list in shared memory, filled by list_load: slot j < k is used when
-// id[j] >= 0, with log q and q of its token.
-struct List {
-  int32_t id[SS_MAX_TOP];
-  float lq[SS_MAX_TOP];
-  float q[SS_MAX_TOP];
-  float x[SS_MAX_TOP];  // the tokens' logits
-  float q_sum, q_tail;  // Q and q_t
-  bool bad;             // an id past the vocabulary
+// ------------------------------------------------------------------ a row's list
+//
+// Thread j < k holds slot j. The list's sums come in three steps around barriers
+// that the callers place other work between: list_unique (which slots count),
+// list_partials (per warp), list_sums (after a barrier).
+
+constexpr int kListWarps = SS_MAX_TOP / 32;
+
+struct ListShared {
+  int4 id[SS_MAX_TOP / 4];      // -1: unused
+  uint8_t again[SS_MAX_TOP];    // slots whose id occurs earlier in the list
+  RowMass in[kListWarps];       // the listed tokens' mass
+  RowMass teacher[kListWarps];  // SS_TAIL_RENORM: mass of the teacher's values
+  float2 q[kListWarps];         // else: sum of q as a pair
 };
 
-// All threads of the block call it. Q is added in double: q_t = 1 - Q keeps the
-// digits that a teacher with nearly all its mass on the list leaves.
-template <int DT>
-__device__ __forceinline__ void list_load(const DistillArgs& a, int64_t row, const Elem<DT>* x, List& l) {
-  const int j = threadIdx.x;
-  if (j == 0) l.bad = false;
-  __syncthreads();
-  if (j < a.k) {
-    const int64_t id = load_id(a.ids, row * a.k + j, a.wide);
-    if (id >= a.vocab) l.bad = true;
-    const bool used = id >= 0 && id < a.vocab;
-    l.id[j] = used ? static_cast<int32_t>(id) : -1;
-    l.lq[j] = used ? load_teacher(a.teacher, row * a.k + j, a.t_dtype) * a.t_scale : -kInf;
-    l.x[j] = used ? to_float<DT>(x[id]) : 0.0f;
+struct Slot {
+  int32_t id;  // -1: unused
+  float lq;    // log q, before SS_TAIL_RENORM's normalisation
+  float x;     // the token's logit
+};
+
+struct ListSums {
+  float shift;   // what log q is short of: log q = lq - shift
+  float q_sum;   // Q
+  float q_tail;  // q_t
+};
+
+// The calling thread's slot as given (x not yet); *past: its id is past the vocabulary.
+__device__ __forceinline__ Slot list_fetch(const DistillArgs& a, int64_t row, bool* past) {
+  Slot s = {-1, -kInf, -kInf};
+  *past = false;
+  if (threadIdx.x < a.k) {
+    const int64_t at = row * a.k + threadIdx.x;
+    const int64_t id = load_id(a.ids, at, a.wide);
+    s.lq = load_teacher(a.teacher, at, a.t_dtype) * a.t_scale;
+    *past = id >= a.vocab;
+    if (id >= 0 && id < a.vocab) s.id = static_cast<int32_t>(id);
   }
-  __syncthreads();
-  bool again = false;
-  if (j < a.k && l.id[j] >= 0)
-    for (int i = 0; i < j; ++i) again = again || l.id[i] == l.id[j];
-  __syncthreads();
-  if (again) {
-    l.id[j] = -1;
-    l.lq[j] = -kInf;
-  }
-  __syncthreads();
-  if (j < 32) {
-    float shift = 0.0f;
-    if (a.mode == SS_TAIL_RENORM) {
-      float m = -kInf, s = 0.0f;
-      bool nan = false;
-      for (int i = j; i < a.k; i += 32) {
-        m = fmaxf(m, l.lq[i]);
-        nan = nan || !(l.lq[i] == l.lq[i]);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-      const float ref = m == -kInf ? 0.0f : m;
-      for (int i = j; i < a.k; i += 32) s += expf(l.lq[i] - ref);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-      nan = __any_sync(0xFFFFFFFFu, nan);
-      shift = nan ? nan_f() : (s == 0.0f ? 0.0f : m + logf(s));
-    }
-    double sum = 0.0;
-    for (int i = j; i < a.k; i += 32) {
-      const float lq = l.lq[i] - shift;
-      const float q = expf(lq);
-      l.lq[i] = lq;
-      l.q[i] = q;
-      sum += static_cast<double>(q);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-    if (j == 0) {
-      l.q_sum = static_cast<float>(sum);
-      const double rest = 1.0 - sum;
-      l.q_tail = a.mode == SS_TAIL_BUCKET && !(rest <= 0.0) ? static_cast<float>(rest) : 0.0f;
-    }
-  }
-  __syncthreads();
+  return s;
 }
 
-// Writes f(x) over the row, then each used slot's own gradient g[j] (all threads
-// call it; the slots' logits were read before).
-template <int DT, class F>
-__device__ __forceinline__ void write_row(const Elem<DT>* x, Elem<DT>* d, int64_t n, bool vec, const F& f,
-                                          int32_t my_id, float mine) {
-  constexpr int V = kVecOf<DT>;
-  if (vec) {
-    const Slice<DT> sl(x, n);
-    for (int64_t i = threadIdx.x; i < sl.head; i += kRowThreads) d[i] = from_float<DT>(f(to_float<DT>(x[i])));
-    for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads)
-      d[i] = from_float<DT>(f(to_float<DT>(x[i])));
-    const uint4* v = reinterpret_cast<const uint4*>(x + sl.head);
-    uint4* w = reinterpret_cast<uint4*>(d + sl.head);
-    for (int64_t i = threadIdx.x; i < sl.nvec; i += kRowThreads) {
-      float e[V];
-      unpack<DT>(v[i], e);
+// After the slots' ids are in l.id and a barrier: finds the repeated ones, two threads a slot (a barrier follows,
+// then list_drop).
+__device__ __forceinline__ void list_unique(const DistillArgs& a, ListShared& l) {
+  static_assert(kRowThreads == 2 * SS_MAX_TOP, "two threads a slot");
+  const int j = threadIdx.x >> 1;
+  if (j < a.k) {  // k threads pairs, so whole pairs
+    const int32_t* ids = &l.id[0].x;
+    const int32_t mine = ids[j];
+    int again = 0;
+    for (int q = threadIdx.x & 1; 4 * q < j; q += 2) {
+      const int4 v = l.id[q];
+      again |= (v.x == mine) | ((v.y == mine) & (4 * q + 1 < j)) | ((v.z == mine) & (4 * q + 2 < j)) |
+               ((v.w == mine) & (4 * q + 3 < j));
+    }
+    const unsigned pair = 3u << (threadIdx.x & 30);
+    again |= __shfl_xor_sync(pair, again, 1);
+    if ((threadIdx.x & 1) == 0) l.again[j] = static_cast<uint8_t>(again);
+  }
+}
+
+__device__ __forceinline__ void list_drop(const DistillArgs& a, const ListShared& l, Slot& s) {
+  if (threadIdx.x < a.k && (s.id < 0 || l.again[threadIdx.x])) s.id = -1;
+  if (s.id < 0) s.lq = -kInf;
+}
+
+// The warps' partial sums (a barrier follows).
+__device__ __forceinline__ void list_partials(const DistillArgs& a, ListShared& l, const Slot& s) {
+  if (threadIdx.x >= SS_MAX_TOP) return;
+  const int warp = threadIdx.x >> 5;
+  auto one = [](float v, bool used) {  // the mass of one value
+    if (!used || v == -kInf) return RowMass::none();
+    return v <= 3.402823466e38f ? RowMass{v, 1.0f} : RowMass{-kInf, nan_f()};
+  };
+  const RowMass in = merge_lanes(one(s.x, s.id >= 0), a.c);
+  if ((threadIdx.x & 31) == 0) l.in[warp] = in;
+  if (a.mode == SS_TAIL_RENORM) {
+    const RowMass t = merge_lanes(one(s.lq, s.id >= 0), kLog2e);
+    if ((threadIdx.x & 31) == 0) l.teacher[warp] = t;
+  } else {
+    // q_t = 1 - Q is small when the list has nearly all the mass: Q is added as a pair
+    dd q = {expf(s.lq), 0.0f};
 #pragma unroll
-      for (int j = 0; j < V; ++j) e[j] = f(e[j]);
-      w[i] = pack<DT>(e);
+    for (int off = 16; off > 0; off >>= 1) {
+      const float h = __shfl_xor_sync(0xFFFFFFFFu, q.hi, off), lo = __shfl_xor_sync(0xFFFFFFFFu, q.lo, off);
+      const dd t = two_sum(q.hi, h);
+      q = {t.hi, t.lo + (q.lo + lo)};
+    }
+    if ((threadIdx.x & 31) == 0) l.q[warp] = make_float2(q.hi, q.lo);
+  }
+}
+
+__device__ __forceinline__ ListSums list_sums(const DistillArgs& a, const ListShared& l) {
+  ListSums o = {0.0f, 0.0f, 0.0f};
+  if (a.mode == SS_TAIL_RENORM) {
+    const RowMass t = merge_lanes(l.teacher[threadIdx.x % kListWarps], kLog2e, kListWarps);
+    if (t.s != 0.0f) {
+      o.shift = t.m + logf(t.s);
+      o.q_sum = t.s == t.s ? 1.0f : t.s;
     }
   } else {
-    for (int64_t i = threadIdx.x; i < n; i += kRowThreads) d[i] = from_float<DT>(f(to_float<DT>(x[i])));
+    dd q = {l.q[0].x, l.q[0].y};
+#pragma unroll
+    for (int i = 1; i < kListWarps; ++i) {
+      const dd t = two_sum(q.hi, l.q[i].x);
+      q = {t.hi, t.lo + (q.lo + l.q[i].y)};
+    }
+    o.q_sum = q.hi + q.lo;
+    if (a.mode == SS_TAIL_BUCKET) {
+      const float rest = (1.0f - q.hi) - q.lo;
+      o.q_tail = rest <= 0.0f ? 0.0f : rest;
+    }
   }
-  __syncthreads();
-  if (my_id >= 0) d[my_id] = from_float<DT>(mine);
-}
-
-template <int DT>
-__device__ __forceinline__ void zero_row(Elem<DT>* d, int64_t n) {
-  const Slice<DT> sl(d, n);
-  for (int64_t i = threadIdx.x; i < sl.head; i += kRowThreads) d[i] = from_float<DT>(0.0f);
-  for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads) d[i] = from_float<DT>(0.0f);
-  uint4* w = reinterpret_cast<uint4*>(d + sl.head);
-  for (int64_t i = threadIdx.x; i < sl.nvec; i += kRowThreads) w[i] = make_uint4(0u, 0u, 0u, 0u);
+  return o;
 }
 
 // ------------------------------------------------------------------ loss and gradient in one call
@@ -197,28 +206,15 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, RowM
   acc.s += s[0] + s[1];
 }
 
-// Zeros in this block's part of a gradient row.
-template <int DT>
-__device__ __forceinline__ void zero_part(Elem<DT>* d, int64_t n, unsigned rank, unsigned size) {
-  const Slice<DT> sl(d, n);
-  if (rank == 0) {
-    for (int64_t i = threadIdx.x; i < sl.head; i += kRowThreads) d[i] = from_float<DT>(0.0f);
-    for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads) d[i] = from_float<DT>(0.0f);
-  }
-  uint4* w = reinterpret_cast<uint4*>(d + sl.head);
-  for (int64_t i = rank * kRowThreads + threadIdx.x; i < sl.nvec; i += size * kRowThreads)
-    __stcs(w + i, make_uint4(0u, 0u, 0u, 0u));
-}
-
 // Dynamic shared memory: the part's vectors [batches * kBatch][T], then a byte of listed bits for each, by thread.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int V = kVecOf<DT>;
   extern __shared__ uint4 held[];
-  __shared__ RowMass red[kRowThreads / 32];
+  __shared__ RowMass red[kRowWarps];
   __shared__ RowMass parts[kMaxCluster];
-  __shared__ List l;
-  __shared__ float part_loss[kRowThreads / 32];
+  __shared__ ListShared l;
+  __shared__ float part_loss[kListWarps];
   __shared__ uint32_t edge_listed;
   const Cluster cl = Cluster::start();
   pdl_wait();
@@ -228,6 +224,8 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const __grid_const
   const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
   Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
   const float w = a.weight ? a.weight[row] : 1.0f;
+  bool past;
+  Slot s = list_fetch(a, row, &past);
   if (w == 0.0f) {  // every block of the cluster
     if (a.d) zero_part<DT>(d, a.vocab, cl.rank, cl.size);
     if (cl.rank == 0 && tid == 0) {
@@ -252,22 +250,27 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const __grid_const
     }
     copies_commit();
   }
+  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
   for (int q = 0; q < batches; ++q) listed[q * kRowThreads + tid] = 0u;
   if (tid == 0) edge_listed = 0u;
-  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
-  list_load<DT>(a, row, x, l);
-  const int32_t my_id = tid < a.k ? l.id[tid] : -1;
+  if (tid < SS_MAX_TOP) (&l.id[0].x)[tid] = s.id;
+  const bool bad = __syncthreads_or(past);
   int owner = 0, slot = 0;
-  const bool mine = my_id >= 0 && part.owns(my_id, &owner, &slot);
+  bool mine = s.id >= 0 && part.owns(s.id, &owner, &slot);
+  if (s.id >= 0) s.x = to_float<DT>(x[s.id]);
   if (mine) {
     if (slot < 0) atomicOr(&edge_listed, 1u << owner);
     else atomicOr(&listed[(slot / kBatch) * kRowThreads + owner],
-                  1u << (slot % kBatch * 8 + (my_id - part.sl.head) % V));
+                  1u << (slot % kBatch * 8 + (s.id - part.sl.head) % V));
   }
+  list_unique(a, l);
   __syncthreads();
+  list_drop(a, l, s);
+  mine = mine && s.id >= 0;
+  list_partials(a, l, s);
   RowMass out = RowMass::none();  // unlisted tokens
   if (part.edge >= 0 && !((edge_listed >> tid) & 1u)) {
-    out.m = edge;
+    if (edge > out.m) out.m = edge;
     out.s = ex2((edge - out.ref()) * a.c);
   }
   auto add_group = [&](int g) {
@@ -295,19 +298,25 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const __grid_const
   add_group(2);
   copies_wait<0>();
   add_group(3);
-  out = block_merge<kRowThreads>(out, a.c, red);
-  RowMass in = RowMass::none();
-  if (my_id >= 0) in = {l.x[tid], ex2((l.x[tid] - (l.x[tid] == -kInf ? 0.0f : l.x[tid])) * a.c)};
+  out = block_merge(out, a.c, red);
   cl.started();
-  if (cl.size > 1 && tid < cl.size) cl.at(parts, tid)[cl.rank] = out;
-  in = block_merge<kRowThreads>(in, a.c, red);
+  if (cl.size > 1) {
+    if (tid < cl.size) cl.at(parts, tid)[cl.rank] = out;
+  }
+  RowMass all = merge_lanes(l.in[tid % kListWarps], a.c, kListWarps);
+  const ListSums sums = list_sums(a, l);
+  const float lq = s.lq - sums.shift, q = expf(lq);
   if (cl.size > 1) {
     cl.sync();
-    out = parts[0];
-    for (unsigned r = 1; r < cl.size; ++r) out.merge(parts[r], a.c);
+    out = merge_lanes(parts[tid % cl.size], a.c, static_cast<int>(cl.size));
   }
-  RowMass all = out;
-  all.merge(in, a.c);
+  {
+    const float top = fmaxf(all.m, out.m);
+    RowMass o = out;
+    if (top > all.m) all.move(top, a.c);
+    if (top > o.m) o.move(top, a.c);
+    all.s += o.s;
+  }
   const bool empty = all.s == 0.0f;
   // all unlisted tokens masked, by -inf or by values so low that no p_t is left
   const bool no_tail = out.s == 0.0f || (out.m - all.m) * a.c <= kFloor;
@@ -315,19 +324,21 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const __grid_const
     const float ln_s = logf(all.s);
     const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
     float term = 0.0f;
-    if (my_id >= 0 && l.q[tid] != 0.0f) {
-      const float lp = empty ? -kInf : fmaf(l.x[tid] - all.m, a.scale, -ln_s);
-      term = l.q[tid] * (l.lq[tid] - lp);
+    if (s.id >= 0 && q != 0.0f) {
+      const float lp = empty ? -kInf : fmaf(s.x - all.m, a.scale, -ln_s);
+      term = q * (lq - lp);
     }
+    if (tid < SS_MAX_TOP) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, off);
-    if ((tid & 31) == 0) part_loss[tid >> 5] = term;
+      for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, off);
+      if ((tid & 31) == 0) part_loss[tid >> 5] = term;
+    }
     __syncthreads();
     if (tid == 0) {
       float loss = 0.0f;
-      for (int i = 0; i < kRowThreads / 32; ++i) loss += part_loss[i];
-      if (l.q_tail > 0.0f && !no_tail) loss += l.q_tail * (logf(l.q_tail) - tail);
-      if (l.bad || !(all.s == all.s) || !(l.q_sum == l.q_sum)) loss = nan_f();
+      for (int i = 0; i < kListWarps; ++i) loss += part_loss[i];
+      if (sums.q_tail > 0.0f && !no_tail) loss += sums.q_tail * (logf(sums.q_tail) - tail);
+      if (bad || !(all.s == all.s) || !(sums.q_sum == sums.q_sum)) loss = nan_f();
       if (a.loss) a.loss[row] = w * loss;
       if (a.norm) a.norm[row] = make_float2(all.m, all.s);
       if (a.tail) a.tail[row] = tail;
@@ -338,58 +349,70 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const __grid_const
     zero_part<DT>(d, a.vocab, cl.rank, cl.size);
     return;
   }
-  const float ws = l.bad ? nan_f() : w * a.scale;
-  const float b = l.q_sum + l.q_tail;
+  const float ws = bad ? nan_f() : w * a.scale;
+  const float b = sums.q_sum + sums.q_tail;
   // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
   const float p_t = no_tail ? 0.0f : ex2((out.m - all.m) * a.c) * (out.s / all.s);
-  const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - l.q_tail) / out.s;
+  const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - sums.q_tail) / out.s;
   const float ref = out.ref();
   const float c = a.c;
   auto grad = [&](float f) { return ex2((f - ref) * c) * A; };
   if (part.edge >= 0) d[part.edge] = from_float<DT>(grad(edge));
-  for (int q = 0; q < batches; ++q) {
+  for (int r = 0; r < batches; ++r) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int j = q * kBatch + u, i = part.first + j * part.step;
+      const int j = r * kBatch + u, i = part.first + j * part.step;
       if (i < nvec) {
         float f[V];
         unpack<DT>(held[j * kRowThreads + tid], f);
 #pragma unroll
         for (int e = 0; e < V; ++e) f[e] = grad(f[e]);
-        Elem<DT>* o = d + part.sl.head + static_cast<int64_t>(i) * V;
-        if (a.vec) {
-          __stcs(reinterpret_cast<uint4*>(o), pack<DT>(f));
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = from_float<DT>(f[e]);
-        }
+        store_vector<DT>(d + part.sl.head + static_cast<int64_t>(i) * V, f, a.vec);
       }
     }
   }
   __syncthreads();
-  if (mine) d[my_id] = from_float<DT>(ws * fmaf(ex2((l.x[tid] - all.ref()) * a.c) / all.s, b, -l.q[tid]));
+  if (mine) d[s.id] = from_float<DT>(ws * fmaf(ex2((s.x - all.ref()) * a.c) / all.s, b, -q));
 }
 
-// The gradient from saved normalisers: one pass.
+// ------------------------------------------------------------------ the gradient from saved normalisers
+//
+// One pass: blocks share a row as above, but nothing is exchanged between them.
+// The list's sums are taken while the first vectors are on their way.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
-  __shared__ List l;
+  __shared__ ListShared l;
   pdl_wait();
   pdl_trigger();
-  const int64_t row = blockIdx.x;
+  const unsigned rank = blockIdx.x % a.split;
+  const int64_t row = blockIdx.x / a.split;
   const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
   Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
   const float wt = a.weight ? a.weight[row] : 1.0f, dl = a.d_loss ? a.d_loss[row] : 1.0f;
   const float2 norm = a.norm_in[row];
+  bool past;
+  Slot s = list_fetch(a, row, &past);
   if (wt == 0.0f || dl == 0.0f || norm.y == 0.0f) {
-    zero_row<DT>(d, a.vocab);
+    zero_part<DT>(d, a.vocab, rank, a.split);
     return;
   }
-  list_load<DT>(a, row, x, l);
-  const int j = threadIdx.x;
-  const int32_t my_id = j < a.k ? l.id[j] : -1;
-  const float ws = l.bad ? nan_f() : wt * dl * a.scale;
-  const float b = l.q_sum + l.q_tail;
+  const RowPart<DT> part(x, a.vocab, rank, a.split);
+  uint4 first[kBatch];
+  part.load(0, first);
+  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : 0.0f;
+  if (threadIdx.x < SS_MAX_TOP) (&l.id[0].x)[threadIdx.x] = s.id;
+  const bool bad = __syncthreads_or(past);
+  int owner, slot;
+  const bool mine = s.id >= 0 && part.owns(s.id, &owner, &slot);
+  if (mine) s.x = to_float<DT>(x[s.id]);
+  list_unique(a, l);
+  __syncthreads();
+  list_drop(a, l, s);
+  list_partials(a, l, s);
+  __syncthreads();
+  const ListSums sums = list_sums(a, l);
+  const float ws = bad ? nan_f() : wt * dl * a.scale;
+  const float b = sums.q_sum + sums.q_tail;
   const float l2 = log2f(norm.y);
   float A = ws * b, K = l2;
   if (a.mode == SS_TAIL_BUCKET) {
@@ -397,12 +420,15 @@ __global__ void __launch_bounds__(kRowThreads) distill_grad_kernel(const __grid_
     if (tail == -kInf) {
       A = ws * 0.0f;
     } else {
-      A = ws * (expf(tail) * b - l.q_tail);
+      A = ws * (expf(tail) * b - sums.q_tail);
       K = fmaf(tail, kLog2e, l2);
     }
   }
-  const float g = my_id >= 0 ? ws * fmaf(ex2(fmaf(l.x[j] - norm.x, a.c, -l2)), b, -l.q[j]) : 0.0f;
-  write_row<DT>(x, d, a.vocab, a.vec, [&](float f) { return ex2(fmaf(f - norm.x, a.c, -K)) * A; }, my_id, g);
+  const float m = norm.x, c = a.c;
+  part.map(first, d, a.vec, edge, [&](float f) { return ex2(fmaf(f - m, c, -K)) * A; });
+  __syncthreads();
+  if (mine && s.id >= 0)
+    d[s.id] = from_float<DT>(ws * fmaf(ex2(fmaf(s.x - m, c, -l2)), b, -expf(s.lq - sums.shift)));
 }
 
 ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* norm_in, const float* tail_in,
@@ -439,20 +465,23 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   ranges.add(tail_in, rows * 4, false);
   ranges.add(d_loss, rows * 4, false);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
+  const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
+  const int split = split_for(nvec);
   const DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
                          reinterpret_cast<const float2*>(norm_in), tail_in, loss, reinterpret_cast<float2*>(norm),
                          tail, d_logits, rows, x->vocab, x->ld, d_ld, x->scale * kLog2e, x->scale, t->scale, t->k,
-                         t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld)};
+                         t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld),
+                         static_cast<uint32_t>(split)};
   if (saved) {
     auto* fn = x->dtype == SS_BF16
                    ? distill_grad_kernel<SS_BF16>
                    : (x->dtype == SS_FP16 ? distill_grad_kernel<SS_FP16> : distill_grad_kernel<SS_FP32>);
-    return launch(fn, static_cast<unsigned>(rows), a, stream, kRowThreads);
+    if (rows * split > INT32_MAX) return SS_ERR_OVERFLOW;
+    return launch(fn, static_cast<unsigned>(rows * split), a, stream, kRowThreads);
   }
   auto* fn = x->dtype == SS_BF16 ? distill_kernel<SS_BF16>
                                  : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16> : distill_kernel<SS_FP32>);
   // a part of at most kPartVectors vectors a thread, or what 8 blocks leave
-  const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
   const auto vectors = [&](int c) { return (nvec + c * kRowThreads - 1) / (c * kRowThreads); };
   int cluster = 1;
   while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;

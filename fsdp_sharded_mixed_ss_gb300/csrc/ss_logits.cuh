@@ -149,12 +149,6 @@ struct RowSum {
     s += e;
     t = fmaf(e, fmaxf(d, kFloor), t);
   }
-  __device__ __forceinline__ void merge(RowSum b, float c) {
-    if (b.m > m) move(b.m, c);
-    else if (m > b.m) b.move(m, c);
-    s += b.s;
-    t += b.t;
-  }
 };
 
 // The same without t: m = max x, s = sum 2^((x - m) c).
@@ -174,26 +168,6 @@ struct RowMass {
   }
 };
 
-// Merged over the block, the same in every thread. `red`: a slot per warp.
-template <int THREADS, class Sum>
-__device__ __forceinline__ Sum block_merge(Sum a, float c, Sum* red) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    Sum o;
-    o.m = __shfl_xor_sync(0xFFFFFFFFu, a.m, off);
-    o.s = __shfl_xor_sync(0xFFFFFFFFu, a.s, off);
-    if constexpr (std::is_same_v<Sum, RowSum>) o.t = __shfl_xor_sync(0xFFFFFFFFu, a.t, off);
-    a.merge(o, c);
-  }
-  __syncthreads();  // an earlier call's slots have been read
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
-  __syncthreads();
-  Sum b = red[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 32; ++w) b.merge(red[w], c);
-  return b;
-}
-
 // Order of logits as unsigned integers (-0 counts as +0; NaN rows do not come here).
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -205,6 +179,30 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // Larger logit first, equal logits by ascending id; 0 is below every element.
 __device__ __forceinline__ uint64_t order_pair(float x, int64_t id) {
   return (static_cast<uint64_t>(order_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+}
+
+// Merged over the `width` (a power of two) lanes of each aligned group, the groups being copies of one another;
+// the same in every lane. One rescale a lane: first the maximum, then plain sums.
+template <class Sum>
+__device__ __forceinline__ Sum merge_lanes(Sum a, float c, int width = 32) {
+  const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(a.m)));
+  if (top > a.m) a.move(top, c);
+  for (int off = width >> 1; off > 0; off >>= 1) {
+    a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, off);
+    if constexpr (std::is_same_v<Sum, RowSum>) a.t += __shfl_xor_sync(0xFFFFFFFFu, a.t, off);
+  }
+  return a;
+}
+
+constexpr int kRowWarps = kRowThreads / 32;
+
+// Merged over the block, the same in every thread. `red`: a slot per warp, used by one call only.
+template <class Sum>
+__device__ __forceinline__ Sum block_merge(Sum a, float c, Sum* red) {
+  a = merge_lanes(a, c);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+  __syncthreads();
+  return merge_lanes(red[threadIdx.x % kRowWarps], c, kRowWarps);
 }
 
 __device__ __forceinline__ int64_t load_id(const void* p, int64_t i, bool wide) {
@@ -261,6 +259,30 @@ struct Cluster {
 
 constexpr int kBatch = 4;  // vectors that a thread has in flight
 
+// One vector's elements to d: as 16 bytes when d lies so, else one by one.
+template <int DT>
+__device__ __forceinline__ void store_vector(Elem<DT>* d, const float (&f)[kVecOf<DT>], bool aligned) {
+  if (aligned) {
+    __stcs(reinterpret_cast<uint4*>(d), pack<DT>(f));
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVecOf<DT>; ++e) d[e] = from_float<DT>(f[e]);
+  }
+}
+
+// Zeros in block `rank`'s part, of `size`, of a gradient row.
+template <int DT>
+__device__ __forceinline__ void zero_part(Elem<DT>* d, int64_t n, unsigned rank, unsigned size) {
+  const Slice<DT> sl(d, n);
+  if (rank == 0) {
+    for (int64_t i = threadIdx.x; i < sl.head; i += kRowThreads) d[i] = from_float<DT>(0.0f);
+    for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads) d[i] = from_float<DT>(0.0f);
+  }
+  uint4* w = reinterpret_cast<uint4*>(d + sl.head);
+  for (int64_t i = rank * kRowThreads + threadIdx.x; i < sl.nvec; i += static_cast<int64_t>(size) * kRowThreads)
+    __stcs(w + i, make_uint4(0u, 0u, 0u, 0u));
+}
+
 template <int DT>
 struct RowPart {
   const Elem<DT>* x;
@@ -297,6 +319,39 @@ struct RowPart {
     return q % size == rank;
   }
   __device__ __forceinline__ const uint4* vec(int i) const { return reinterpret_cast<const uint4*>(x + sl.head) + i; }
+  // The thread's vectors number j0 .. j0 + kBatch - 1 (those past its last one are left as they are).
+  __device__ __forceinline__ void load(int j0, uint4 (&w)[kBatch]) const {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = first + static_cast<int64_t>(j0 + u) * step;
+      if (i < sl.nvec) w[u] = __ldcs(vec(static_cast<int>(i)));
+    }
+  }
+  // d = f(x) over the part, in one pass with the next batch's loads in flight. `w` holds the first batch and
+  // `edge_x` the thread's edge element; d may be x. `aligned`: d's vectors lie as x's do.
+  template <class F>
+  __device__ __forceinline__ void map(uint4 (&w)[kBatch], Elem<DT>* d, bool aligned, float edge_x, const F& f) const {
+    constexpr int V = kVecOf<DT>;
+    if (edge >= 0) d[edge] = from_float<DT>(f(edge_x));
+    const int n = vectors();
+    for (int j = 0; j < n; j += kBatch) {
+      uint4 next[kBatch];
+      load(j + kBatch, next);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = first + static_cast<int64_t>(j + u) * step;
+        if (i < sl.nvec) {
+          float e[V];
+          unpack<DT>(w[u], e);
+#pragma unroll
+          for (int q = 0; q < V; ++q) e[q] = f(e[q]);
+          store_vector<DT>(d + sl.head + i * V, e, aligned);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) w[u] = next[u];
+    }
+  }
   // f(value, id) of every element of this thread's vectors numbered [j0, j1).
   template <class F>
   __device__ __forceinline__ void each(int j0, int j1, const F& f) const {
@@ -371,6 +426,16 @@ inline ss_status check_grad_out(const ss_logits* x, int64_t x_bytes, const void*
   ranges->add(d, bytes, true);
   if (d != x->data || d_ld != x->ld) ranges->add(x->data, x_bytes, false);
   return SS_OK;
+}
+
+// Blocks that share a row where each element is read and written once and nothing is exchanged: parts of
+// kMapVectors vectors a thread.
+#ifndef SS_MAP_VECTORS
+#define SS_MAP_VECTORS 16
+#endif
+constexpr int kMapVectors = SS_MAP_VECTORS;
+inline int split_for(int64_t nvec) {
+  return static_cast<int>(std::max<int64_t>(1, (nvec + kMapVectors * kRowThreads - 1) / (kMapVectors * kRowThreads)));
 }
 
 // Launches one cluster of `cluster` blocks per row (a plain launch for 1).

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     if (in_unit > 0) tops.unit[units++][tid] = unit;
   }
   const float thread_max = acc.m;
-  acc = block_merge<kRowThreads>(acc, a.c, red);
+  acc = block_merge(acc, a.c, red);
   cl.started();
   if (cl.size > 1) {
     if (tid < cl.size) cl.at(parts, tid)[cl.rank] = acc;
@@ -221,8 +221,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   }
   if (TOPS || cl.size > 1) cl.sync();
   if (cl.size > 1) {
-    acc = parts[0];
-    for (unsigned r = 1; r < cl.size; ++r) acc.merge(parts[r], a.c);
+    acc = merge_lanes(parts[tid % cl.size], a.c, static_cast<int>(cl.size));
   }
   const bool nan = !(acc.s == acc.s);
   const bool empty = acc.s == 0.0f;
@@ -365,91 +364,77 @@ struct LogprobGradArgs {
   float c, scale;
   int32_t top_k;
   bool wide, vec;
+  uint32_t split;  // blocks that share a row
 };
 
-// One block per row. Every element is p (A + B log2 p); the listed ids, whose
-// logits are read before anything is written (the gradient may replace the
-// logits), get their own terms on top afterwards.
+// One pass, each row shared by blocks that exchange nothing. Every element is
+// p (A + B log2 p); the listed ids, whose logits are read before anything is
+// written (the gradient may replace the logits), get their own terms on top.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) logprob_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
-  constexpr int V = kVecOf<DT>;
-  __shared__ int64_t ids[SS_MAX_TOP + 1];
+  __shared__ int32_t ids[SS_MAX_TOP + 1];
   __shared__ float up[SS_MAX_TOP + 1];
   pdl_wait();
   pdl_trigger();
-  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const unsigned rank = blockIdx.x % a.split;
+  const int64_t row = blockIdx.x / a.split;
   const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
   Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
   const int n_ids = a.top_k + 1;
-  for (int j = threadIdx.x; j < n_ids; j += kRowThreads) {
-    int64_t id = -1;
-    float u = 0.0f;
-    if (j < a.top_k) {
-      if (a.d_top) {
-        id = load_id(a.top_id, row * a.top_k + j, a.wide);
-        u = a.d_top[row * a.top_k + j];
-      }
-    } else if (a.d_logprob) {
-      id = load_id(a.tokens, row, a.wide);
-      u = a.d_logprob[row];
-    }
-    ids[j] = id;
-    up[j] = id < 0 ? 0.0f : (id >= a.vocab ? nan_f() : u);
-  }
-  __syncthreads();
-  const float dl = a.d_lse ? a.d_lse[row] : 0.0f;
-  const float dh = a.d_entropy ? a.d_entropy[row] : 0.0f;
-  float sum = 0.0f;
-  bool any = dl != 0.0f || dh != 0.0f;
-  for (int j = 0; j < n_ids; ++j) {
-    sum += up[j];
-    any = any || up[j] != 0.0f;
+  int64_t id = -1;
+  float u = 0.0f;
+  if (tid < a.top_k) {
+    id = load_id(a.top_id, row * a.top_k + tid, a.wide);
+    u = a.d_top[row * a.top_k + tid];
+  } else if (tid == a.top_k && a.d_logprob) {
+    id = load_id(a.tokens, row, a.wide);
+    u = a.d_logprob[row];
   }
   const float2 norm = a.norm[row];
-  const bool dead = !any || norm.y == 0.0f;
+  const float dl = a.d_lse ? a.d_lse[row] : 0.0f;
+  const float dh = a.d_entropy ? a.d_entropy[row] : 0.0f;
+  const float h = a.d_entropy ? a.entropy[row] : 0.0f;
+  const RowPart<DT> part(x, a.vocab, rank, a.split);
+  uint4 first[kBatch];
+  part.load(0, first);
+  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : 0.0f;
+  u = id < 0 ? 0.0f : (id >= a.vocab ? nan_f() : u);
+  if (id >= a.vocab) id = -1;
+  if (tid < n_ids) {
+    ids[tid] = static_cast<int32_t>(id);
+    up[tid] = u;
+  }
+  const bool any = __syncthreads_or(u != 0.0f) || dl != 0.0f || dh != 0.0f;
+  if (!any || norm.y == 0.0f) {
+    zero_part<DT>(d, a.vocab, rank, a.split);
+    return;
+  }
+  float sum = 0.0f;
+  for (int j = 0; j < n_ids; ++j) sum += up[j];
   const float l2 = log2f(norm.y);
-  const float A = dead ? 0.0f : a.scale * (dl - sum - (a.d_entropy ? dh * a.entropy[row] : 0.0f));
-  const float B = dead ? 0.0f : -a.scale * dh * kLn2;
-  // the listed elements' whole gradients, by the threads that hold them: several slots may name one id
-  float mine = 0.0f;
-  int64_t my_id = -1;
+  const float A = a.scale * (dl - sum - (a.d_entropy ? dh * h : 0.0f));
+  const float B = -a.scale * dh * kLn2;
+  const float m = norm.x, c = a.c;
   auto grad = [&](float f) {
-    const float l = fmaf(f - norm.x, a.c, -l2);
+    const float l = fmaf(f - m, c, -l2);
     return ex2(l) * fmaf(B, fmaxf(l, kFloor), A);
   };
-  if (threadIdx.x < n_ids && !dead && ids[threadIdx.x] >= 0 && ids[threadIdx.x] < a.vocab) {
-    my_id = ids[threadIdx.x];
-    float u = 0.0f;
+  // a listed element's whole gradient, by the thread that holds its slot: several slots may name one id, and all
+  // of them write the same
+  float whole = 0.0f;
+  int owner, slot;
+  const bool mine = id >= 0 && part.owns(static_cast<int>(id), &owner, &slot);
+  if (mine) {
+    float v = 0.0f;
     for (int j = 0; j < n_ids; ++j)
-      if (ids[j] == my_id) u += up[j];
-    mine = fmaf(a.scale, u, grad(to_float<DT>(x[my_id])));
+      if (ids[j] == static_cast<int32_t>(id)) v += up[j];
+    whole = fmaf(a.scale, v, grad(to_float<DT>(x[id])));
   }
   __syncthreads();
-  if (a.vec) {
-    const Slice<DT> sl(x, a.vocab);
-    for (int64_t i = threadIdx.x; i < sl.head; i += kRowThreads)
-      d[i] = from_float<DT>(dead ? 0.0f : grad(to_float<DT>(x[i])));
-    for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads)
-      d[i] = from_float<DT>(dead ? 0.0f : grad(to_float<DT>(x[i])));
-    const uint4* v = reinterpret_cast<const uint4*>(x + sl.head);
-    uint4* w = reinterpret_cast<uint4*>(d + sl.head);
-    for (int64_t i = threadIdx.x; i < sl.nvec; i += kRowThreads) {
-      float f[V];
-      if (dead) {
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        unpack<DT>(v[i], f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = grad(f[j]);
-        w[i] = pack<DT>(f);
-      }
-    }
-  } else {
-    for (int64_t i = threadIdx.x; i < a.vocab; i += kRowThreads)
-      d[i] = from_float<DT>(dead ? 0.0f : grad(to_float<DT>(x[i])));
-  }
+  part.map(first, d, a.vec, edge, grad);
   __syncthreads();
-  if (my_id >= 0) d[my_id] = from_float<DT>(mine);
+  if (mine) d[id] = from_float<DT>(whole);
 }
 
 }  // namespace
@@ -534,13 +519,16 @@ ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idty
   ranges.add(up->d_lse, rows * 4, false);
   ranges.add(up->d_top_logprob, rows * top_k * 4, false);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
-  const LogprobGradArgs a = {x->data, tokens, top_id, reinterpret_cast<const float2*>(norm), entropy, up->d_logprob, up->d_entropy, up->d_lse,
-                             up->d_top_logprob, d_logits, rows, x->vocab, x->ld, d_ld, x->scale * kLog2e, x->scale,
-                             top_k, idtype == SS_I64, same_phase(x, d_logits, d_ld)};
+  const int split = split_for(x->vocab / (x->dtype == SS_FP32 ? 4 : 8));
+  if (rows * split > INT32_MAX) return SS_ERR_OVERFLOW;
+  const LogprobGradArgs a = {x->data, tokens, top_id, reinterpret_cast<const float2*>(norm), entropy, up->d_logprob,
+                             up->d_entropy, up->d_lse, up->d_top_logprob, d_logits, rows, x->vocab, x->ld, d_ld,
+                             x->scale * kLog2e, x->scale, top_k, idtype == SS_I64, same_phase(x, d_logits, d_ld),
+                             static_cast<uint32_t>(split)};
   auto* fn = x->dtype == SS_BF16
                  ? logprob_grad_kernel<SS_BF16>
                  : (x->dtype == SS_FP16 ? logprob_grad_kernel<SS_FP16> : logprob_grad_kernel<SS_FP32>);
-  return launch(fn, static_cast<unsigned>(rows), a, stream, kRowThreads);
+  return launch(fn, static_cast<unsigned>(rows * split), a, stream, kRowThreads);
 }
 
 }  // extern "C"

@@ -332,8 +332,8 @@ typedef struct ss_logprob_grad {
  * d_logits: element i of row r at d_logits[r * d_ld + i], x's dtype, rounded
  *   once. It may be x itself (same address and ld: the gradient replaces the
  *   logits) and must not overlap anything else.
- * A row whose upstream gradients are all zero is not read and gets zeros; so
- * does a masked-out row. top_k is 0 without d_top_logprob. */
+ * A row whose upstream gradients are all zero gets zeros, whatever its logits;
+ * so does a masked-out row. top_k is 0 without d_top_logprob. */
 ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idtype idtype, int32_t top_k,
                                  const void* top_id, const float* norm, const float* entropy,
                                  const ss_logprob_grad* up, void* d_logits, int64_t d_ld, void* stream);
