@@ -3,10 +3,10 @@
 // checks of their arguments.
 //
 // Arithmetic. With c = scale * log2(e) and m the running maximum of x, a row's
-// exponentials are 2^((x - m) c), one hardware ex2 each (relative error below
-// 2^-21 with its argument's rounding). x - m is formed first, in x's own units:
-// it is exact near the maximum, where the mass is, and stays meaningful for rows
-// that hold the type's lowest value, where x c would overflow.
+// exponentials are 2^((x - m) c), one FMA and one hardware ex2 an element: ExpRef
+// holds the FMA's constants and puts right, once per batch of vectors, what the
+// rounding of m c shifts them by. Their relative error is 2^-22 and the
+// argument's rounding.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -64,8 +64,63 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&f)[kVecOf<DT>]) {
   }
 }
 
+// Two floats in a register pair: Blackwell's packed fp32 instructions do both at once, which halves the issue slots
+// of everything here but the conversions and ex2.
+struct Pair {
+  unsigned long long v;
+
+  __device__ __forceinline__ static Pair of(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+    return p;
+  }
+  __device__ __forceinline__ static Pair both(float f) { return of(f, f); }
+  __device__ __forceinline__ float2 split() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+  __device__ __forceinline__ float sum() const {
+    const float2 f = split();
+    return f.x + f.y;
+  }
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return p;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+
 template <int DT>
-__device__ __forceinline__ uint4 pack(const float (&f)[kVecOf<DT>]) {
+constexpr int kPairsOf = kVecOf<DT> / 2;
+
+template <int DT>
+__device__ __forceinline__ void unpack_pairs(const uint4& w, Pair (&p)[kPairsOf<DT>]) {
+  float f[kVecOf<DT>];
+  unpack<DT>(w, f);
+#pragma unroll
+  for (int i = 0; i < kPairsOf<DT>; ++i) p[i] = Pair::of(f[2 * i], f[2 * i + 1]);
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack_pairs(const Pair (&p)[kPairsOf<DT>]) {
+  float f[kVecOf<DT>];
+#pragma unroll
+  for (int i = 0; i < kPairsOf<DT>; ++i) {
+    const float2 v = p[i].split();
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
   if constexpr (DT == SS_FP32)
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   else return narrow8<DT>(f);
@@ -111,19 +166,51 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ Pair ex2_pair(Pair a) {
+  const float2 f = a.split();
+  return Pair::of(ex2(f.x), ex2(f.y));
+}
+
 // A row's slice [0, n) of elements at p: `head` elements up to the first 16-byte
 // boundary, `nvec` whole vectors, then the rest.
 template <int DT>
 struct Slice {
-  int64_t n, nvec;
-  int head;
-  __device__ __forceinline__ Slice(const Elem<DT>* p, int64_t len) : n(len) {
+  int n, nvec, head;
+  __device__ __forceinline__ Slice(const Elem<DT>* p, int64_t len) : n(static_cast<int>(len)) {
     constexpr int V = kVecOf<DT>;
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(Elem<DT>));
-    head = static_cast<int>(min(static_cast<int64_t>((V - off) % V), len));
-    nvec = (len - head) / V;
+    const int off = static_cast<int>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) /
+                    static_cast<int>(sizeof(Elem<DT>));
+    head = min((V - off) % V, n);
+    nvec = (n - head) / V;
   }
-  __device__ __forceinline__ int64_t tail() const { return head + nvec * kVecOf<DT>; }
+  __device__ __forceinline__ int tail() const { return head + nvec * kVecOf<DT>; }
+};
+
+// 2^((x - m) c) as k 2^(x c' - r).
+//   |m c| < 1e30: c' = c, r = fl(m c), and k = 2^(r - m c) makes good r's rounding (k is 1 to a few digits).
+//   else: c' = 1, r = m. Neighbouring numbers there are more than 1e22 / c apart, and c < 2e20: an element is m and
+//   its exponential 1, or it is far below and its exponential 0, which x - m gives as well, exactly and where m c
+//   would overflow (a row that a mask filled with the type's lowest value).
+// Before the first unmasked element (m = -inf) r = 0, and all exponentials are 0.
+struct ExpRef {
+  float c, r, k, shift;  // k = 2^shift
+
+  __device__ __forceinline__ ExpRef(float m, float scale2) {
+    r = m * scale2;
+    if (fabsf(r) < 1e30f) {
+      c = scale2;
+      shift = fmaf(-m, scale2, r);
+      k = ex2(shift);
+    } else {
+      c = 1.0f;
+      r = m == -kInf ? 0.0f : m;
+      shift = 0.0f;
+      k = 1.0f;
+    }
+  }
+  __device__ __forceinline__ float arg(float x) const { return fmaf(x, c, -r); }
+  __device__ __forceinline__ float exp(float x) const { return ex2(arg(x)); }  // without k
+  __device__ __forceinline__ Pair arg(Pair x) const { return fma2(x, Pair::both(c), Pair::both(-r)); }
 };
 
 // m = max x (-inf before the first unmasked element), s = sum 2^d and
@@ -141,14 +228,6 @@ struct RowSum {
     }
     m = to;
   }
-  // What is subtracted: finite while every element so far is masked.
-  __device__ __forceinline__ float ref() const { return m == -kInf ? 0.0f : m; }
-  __device__ __forceinline__ void add(float x, float c, float ref_) {
-    const float d = (x - ref_) * c;
-    const float e = ex2(d);
-    s += e;
-    t = fmaf(e, fmaxf(d, kFloor), t);
-  }
 };
 
 // The same without t: m = max x, s = sum 2^((x - m) c).
@@ -160,7 +239,6 @@ struct RowMass {
     if (s != 0.0f) s *= ex2((m - to) * c);
     m = to;
   }
-  __device__ __forceinline__ float ref() const { return m == -kInf ? 0.0f : m; }
   __device__ __forceinline__ void merge(RowMass b, float c) {
     if (b.m > m) move(b.m, c);
     else if (m > b.m) b.move(m, c);
@@ -236,12 +314,15 @@ struct Cluster {
   // Barrier over all threads of the cluster; shared memory written before it, in any block, is seen after it.
   __device__ __forceinline__ void sync() const {
     if (size > 1) {
-      asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+      arrive();
+      wait();
     } else {
       __syncthreads();
     }
   }
+  // The two halves of sync() for a cluster of more than one block.
+  __device__ __forceinline__ void arrive() const { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+  __device__ __forceinline__ void wait() const { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
   // `p` (in this block's shared memory) at the same place in block r's.
   template <class T>
   __device__ __forceinline__ T* at(T* p, unsigned r) const {
@@ -261,12 +342,22 @@ constexpr int kBatch = 4;  // vectors that a thread has in flight
 
 // One vector's elements to d: as 16 bytes when d lies so, else one by one.
 template <int DT>
-__device__ __forceinline__ void store_vector(Elem<DT>* d, const float (&f)[kVecOf<DT>], bool aligned) {
+__device__ __forceinline__ void store_vector(void* d, const Pair (&p)[kPairsOf<DT>], bool aligned) {
+  const uint4 v = pack_pairs<DT>(p);
   if (aligned) {
-    __stcs(reinterpret_cast<uint4*>(d), pack<DT>(f));
+    __stcs(static_cast<uint4*>(d), v);
   } else {
+    Elem<DT>* e = static_cast<Elem<DT>*>(d);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < kVecOf<DT>; ++e) d[e] = from_float<DT>(f[e]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == SS_FP32) {
+        e[i] = __uint_as_float(w[i]);
+      } else {
+        e[2 * i] = static_cast<uint16_t>(w[i]);
+        e[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+      }
+    }
   }
 }
 
@@ -279,75 +370,102 @@ __device__ __forceinline__ void zero_part(Elem<DT>* d, int64_t n, unsigned rank,
     for (int64_t i = sl.tail() + threadIdx.x; i < sl.n; i += kRowThreads) d[i] = from_float<DT>(0.0f);
   }
   uint4* w = reinterpret_cast<uint4*>(d + sl.head);
-  for (int64_t i = rank * kRowThreads + threadIdx.x; i < sl.nvec; i += static_cast<int64_t>(size) * kRowThreads)
+  for (int i = rank * kRowThreads + threadIdx.x; i < sl.nvec; i += size * kRowThreads)
     __stcs(w + i, make_uint4(0u, 0u, 0u, 0u));
 }
 
-template <int DT>
+// SIZE: the number of blocks, or 0 where it is known at run time only.
+template <int DT, int SIZE = 0>
 struct RowPart {
+  static constexpr int V = kVecOf<DT>;
   const Elem<DT>* x;
   Slice<DT> sl;
-  int rank, size;
-  int first, step;  // this thread's vectors: first, first + step, ... < nvec
-  int edge;         // its element outside the vectors, or -1
+  int rank, blocks;
+  int first;  // this thread's vectors: first, first + step(), ... < nvec
+  int whole;  // vectors that every thread of every block has
+  int edge;   // this thread's element outside the vectors, or -1
 
   __device__ __forceinline__ RowPart(const Elem<DT>* row, int64_t vocab, unsigned rank_, unsigned size_)
-      : x(row), sl(row, vocab), rank(static_cast<int>(rank_)), size(static_cast<int>(size_)) {
+      : x(row), sl(row, vocab), rank(static_cast<int>(rank_)), blocks(static_cast<int>(size_)) {
     const int t = threadIdx.x;
     first = rank * kRowThreads + t;
-    step = size * kRowThreads;
+    whole = sl.nvec / step();
     edge = -1;
     if (rank == 0) {
       const int after = t - 8;
       if (t < sl.head) edge = t;
-      else if (after >= 0 && after < sl.n - sl.tail()) edge = static_cast<int>(sl.tail()) + after;
+      else if (after >= 0 && after < sl.n - sl.tail()) edge = sl.tail() + after;
     }
   }
+  __device__ __forceinline__ int size() const { return SIZE ? SIZE : blocks; }
+  __device__ __forceinline__ int step() const { return size() * kRowThreads; }
+  __device__ __forceinline__ int64_t step_bytes() const { return static_cast<int64_t>(step()) * 16; }
   // Vectors of the thread that has most.
-  __device__ __forceinline__ int vectors() const { return static_cast<int>((sl.nvec + step - 1) / step); }
+  __device__ __forceinline__ int vectors() const { return whole + (whole * step() < sl.nvec ? 1 : 0); }
+  // Whether this thread has a vector number j.
+  __device__ __forceinline__ bool more(int j) const {
+    return j < whole || (j == whole && first + whole * step() < sl.nvec);
+  }
+  // The thread's first vector in x, and in an array that lies as x does or not.
+  __device__ __forceinline__ const char* at() const {
+    return reinterpret_cast<const char*>(x + sl.head) + static_cast<int64_t>(first) * 16;
+  }
+  __device__ __forceinline__ char* at(Elem<DT>* d) const {
+    return reinterpret_cast<char*>(d + sl.head) + static_cast<int64_t>(first) * 16;
+  }
   // Whether element `id` is this block's; then `j` and `thread` say which of its vectors (j = -1: an edge).
   __device__ __forceinline__ bool owns(int id, int* thread, int* j) const {
-    const int64_t o = id - sl.head;
-    if (o < 0 || o >= sl.nvec * kVecOf<DT>) {
+    const int o = id - sl.head;
+    if (o < 0 || o >= sl.nvec * V) {
       *j = -1;
-      *thread = o < 0 ? id : static_cast<int>(id - sl.tail()) + 8;
+      *thread = o < 0 ? id : id - sl.tail() + 8;
       return rank == 0;
     }
-    const int i = static_cast<int>(o / kVecOf<DT>), q = i / kRowThreads;
+    const int i = o / V, q = i / kRowThreads;
     *thread = i % kRowThreads;
-    *j = q / size;
-    return q % size == rank;
+    *j = q / size();
+    return q % size() == rank;
   }
-  __device__ __forceinline__ const uint4* vec(int i) const { return reinterpret_cast<const uint4*>(x + sl.head) + i; }
   // The thread's vectors number j0 .. j0 + kBatch - 1 (those past its last one are left as they are).
   __device__ __forceinline__ void load(int j0, uint4 (&w)[kBatch]) const {
+    const char* p = at() + j0 * step_bytes();
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = first + static_cast<int64_t>(j0 + u) * step;
-      if (i < sl.nvec) w[u] = __ldcs(vec(static_cast<int>(i)));
-    }
+    for (int u = 0; u < kBatch; ++u)
+      if (more(j0 + u)) w[u] = __ldcs(reinterpret_cast<const uint4*>(p + u * step_bytes()));
   }
   // d = f(x) over the part, in one pass with the next batch's loads in flight. `w` holds the first batch and
   // `edge_x` the thread's edge element; d may be x. `aligned`: d's vectors lie as x's do.
   template <class F>
   __device__ __forceinline__ void map(uint4 (&w)[kBatch], Elem<DT>* d, bool aligned, float edge_x, const F& f) const {
-    constexpr int V = kVecOf<DT>;
-    if (edge >= 0) d[edge] = from_float<DT>(f(edge_x));
-    const int n = vectors();
-    for (int j = 0; j < n; j += kBatch) {
+    if (edge >= 0) d[edge] = from_float<DT>(f(Pair::both(edge_x)).split().x);
+    auto put = [&](const uint4& v, char* o) {
+      Pair p[kPairsOf<DT>];
+      unpack_pairs<DT>(v, p);
+#pragma unroll
+      for (int q = 0; q < kPairsOf<DT>; ++q) p[q] = f(p[q]);
+      store_vector<DT>(o, p, aligned);
+    };
+    const int64_t sb = step_bytes();
+    const char* src = at() + kBatch * sb;
+    char* dst = at(d);
+    int j = 0;
+#pragma unroll 1
+    for (; j + 2 * kBatch <= whole; j += kBatch, src += kBatch * sb, dst += kBatch * sb) {
+      uint4 next[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) next[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * sb));
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) put(w[u], dst + u * sb);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) w[u] = next[u];
+    }
+#pragma unroll 1
+    for (; more(j); j += kBatch, dst += kBatch * sb) {
       uint4 next[kBatch];
       load(j + kBatch, next);
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = first + static_cast<int64_t>(j + u) * step;
-        if (i < sl.nvec) {
-          float e[V];
-          unpack<DT>(w[u], e);
-#pragma unroll
-          for (int q = 0; q < V; ++q) e[q] = f(e[q]);
-          store_vector<DT>(d + sl.head + i * V, e, aligned);
-        }
-      }
+      for (int u = 0; u < kBatch; ++u)
+        if (more(j + u)) put(w[u], dst + u * sb);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) w[u] = next[u];
     }
@@ -355,22 +473,19 @@ struct RowPart {
   // f(value, id) of every element of this thread's vectors numbered [j0, j1).
   template <class F>
   __device__ __forceinline__ void each(int j0, int j1, const F& f) const {
-    constexpr int V = kVecOf<DT>;
     for (int j = j0; j < j1; j += kBatch) {
       uint4 w[kBatch];
+      const char* p = at() + j * step_bytes();
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (j + u < j1 && more(j + u)) w[u] = __ldg(reinterpret_cast<const uint4*>(p + u * step_bytes()));
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = first + static_cast<int64_t>(j + u) * step;
-        if (j + u < j1 && i < sl.nvec) w[u] = __ldg(vec(static_cast<int>(i)));
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = first + static_cast<int64_t>(j + u) * step;
-        if (j + u < j1 && i < sl.nvec) {
+        if (j + u < j1 && more(j + u)) {
           float e[V];
           unpack<DT>(w[u], e);
 #pragma unroll
-          for (int q = 0; q < V; ++q) f(e[q], sl.head + static_cast<int>(i) * V + q);
+          for (int q = 0; q < V; ++q) f(e[q], sl.head + (first + (j + u) * step()) * V + q);
         }
       }
     }
@@ -409,7 +524,7 @@ inline bool span_bytes(int64_t rows, int64_t width, int64_t ld, int64_t es, int6
 // The rules every operator has for its logits (rows > 0 is checked by the caller first).
 inline ss_status check_logits(const ss_logits* x, int64_t* bytes) {
   if (!x->data || x->vocab < 1 || x->vocab > INT32_MAX || x->ld < x->vocab) return SS_ERR_INVALID_ARG;
-  if (!(x->scale > 0.0f) || !std::isfinite(x->scale * kLog2e)) return SS_ERR_INVALID_ARG;
+  if (!(x->scale > 0.0f) || !(x->scale <= 1e20f)) return SS_ERR_INVALID_ARG;
   if (!is_float_dtype(x->dtype)) return SS_ERR_DTYPE;
   if (misaligned(x->data, dtype_bytes(x->dtype))) return SS_ERR_ALIGN;
   if (!span_bytes(x->rows, x->vocab, x->ld, dtype_bytes(x->dtype), bytes)) return SS_ERR_OVERFLOW;
@@ -438,11 +553,11 @@ inline int split_for(int64_t nvec) {
   return static_cast<int>(std::max<int64_t>(1, (nvec + kMapVectors * kRowThreads - 1) / (kMapVectors * kRowThreads)));
 }
 
-// Launches one cluster of `cluster` blocks per row (a plain launch for 1).
+// Launches `clusters` clusters of `cluster` blocks (a plain launch for 1).
 template <typename Args>
-ss_status launch_rows(void (*fn)(Args), int64_t rows, int cluster, size_t smem, const Args& args, void* stream) {
+ss_status launch_rows(void (*fn)(Args), int64_t clusters, int cluster, size_t smem, const Args& args, void* stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);

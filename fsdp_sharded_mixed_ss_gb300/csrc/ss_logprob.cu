@@ -49,29 +49,31 @@ struct TopShared {
 };
 struct NoTops {};
 
-// N vectors into the running sums; returns their maximum.
+// N vectors into the running sums, `ref` being that of acc.m; returns their maximum.
 template <int DT, int N>
-__device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RowSum& acc) {
+__device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RowSum& acc, ExpRef& ref) {
   constexpr int V = kVecOf<DT>;
   float m = vec_max<DT>(w[0]);
 #pragma unroll
   for (int u = 1; u < N; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
-  if (m > acc.m) acc.move(m, c);
-  const float ref = acc.ref();
-  float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
+  if (m > acc.m) {
+    acc.move(m, c);
+    ref = ExpRef(m, c);
+  }
+  Pair s = Pair::both(0.0f), t = s;
 #pragma unroll
   for (int u = 0; u < N; ++u) {
-    float f[V];
-    unpack<DT>(w[u], f);
+    Pair f[kPairsOf<DT>];
+    unpack_pairs<DT>(w[u], f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float d = (f[j] - ref) * c, e = ex2(d);
-      s[j & 1] += e;
-      t[j & 1] = fmaf(e, d, t[j & 1]);
+    for (int j = 0; j < kPairsOf<DT>; ++j) {
+      const Pair d = ref.arg(f[j]), e = ex2_pair(d);
+      s = add2(s, e);
+      t = fma2(e, d, t);
     }
   }
-  acc.s += s[0] + s[1];
-  float tt = t[0] + t[1];
+  const float ss = s.sum();
+  float tt = t.sum();
   if (!(tt == tt)) {  // masked elements (0 * -inf): the same sum with them at kFloor
     tt = 0.0f;
 #pragma unroll
@@ -80,12 +82,13 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RowSu
       unpack<DT>(w[u], f);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float d = fmaxf((f[j] - ref) * c, kFloor);
+        const float d = fmaxf(ref.arg(f[j]), kFloor);
         tt = fmaf(ex2(d), d, tt);
       }
     }
   }
-  acc.t += tt;
+  acc.s = fmaf(ss, ref.k, acc.s);
+  acc.t = fmaf(fmaf(ref.shift, ss, tt), ref.k, acc.t);
   return m;
 }
 
@@ -153,17 +156,19 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / cl.size;
   const RowPart<DT> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl.rank, cl.size);
-  const int nvec = static_cast<int>(part.sl.nvec);
-  const int vectors = (nvec + part.step - 1) / part.step;            // of the thread that has most
-  const int full = nvec / (part.step * kBatch);                      // batches that every thread has whole
+  const int vectors = part.vectors();
+  const int full = part.whole / kBatch;  // batches that every thread has whole
+  const int64_t sb = part.step_bytes();
+  const char* src = part.at();
   const int unit_batches = ((vectors + kBatch - 1) / kBatch + kUnits - 1) / kUnits;
   RowSum acc = RowSum::none();
   float edge = -kInf;
-  if (part.edge >= 0) {
+  if (part.edge >= 0) {  // its own maximum: 2^0 (0 when masked, NaN for NaN and +inf)
     edge = to_float<DT>(part.x[part.edge]);
     if (edge > acc.m) acc.m = edge;
-    acc.add(edge, a.c, acc.ref());
+    acc.s = edge == -kInf ? 0.0f : (edge <= 3.402823466e38f ? 1.0f : nan_f());
   }
+  ExpRef ref(acc.m, a.c);
   float unit = -kInf;
   int in_unit = 0, units = 0;
   auto end_batch = [&](float m) {
@@ -176,26 +181,23 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
       }
     }
   };
-  for (int b = 0; b < full; ++b) {
+  for (int b = 0; b < full; ++b, src += kBatch * sb) {
     uint4 w[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) w[u] = __ldg(part.vec(part.first + (b * kBatch + u) * part.step));
-    end_batch(add_vectors<DT>(w, a.c, acc));
+    for (int u = 0; u < kBatch; ++u) w[u] = __ldg(reinterpret_cast<const uint4*>(src + u * sb));
+    end_batch(add_vectors<DT>(w, a.c, acc, ref));
   }
   if (full * kBatch < vectors) {
     uint4 w[kBatch];
     float m = -kInf;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = part.first + static_cast<int64_t>(full * kBatch + u) * part.step;
-      if (i < nvec) w[u] = __ldg(part.vec(static_cast<int>(i)));
-    }
+    for (int u = 0; u < kBatch; ++u)
+      if (part.more(full * kBatch + u)) w[u] = __ldg(reinterpret_cast<const uint4*>(src + u * sb));
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = part.first + static_cast<int64_t>(full * kBatch + u) * part.step;
-      if (i < nvec) {
+      if (part.more(full * kBatch + u)) {
         const uint4 one[1] = {w[u]};
-        m = fmaxf(m, add_vectors<DT>(one, a.c, acc));
+        m = fmaxf(m, add_vectors<DT>(one, a.c, acc, ref));
       }
     }
     end_batch(m);
@@ -371,7 +373,7 @@ struct LogprobGradArgs {
 // p (A + B log2 p); the listed ids, whose logits are read before anything is
 // written (the gradient may replace the logits), get their own terms on top.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads) logprob_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 4) logprob_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
   __shared__ int32_t ids[SS_MAX_TOP + 1];
   __shared__ float up[SS_MAX_TOP + 1];
   pdl_wait();
@@ -412,14 +414,18 @@ __global__ void __launch_bounds__(kRowThreads) logprob_grad_kernel(const __grid_
   }
   float sum = 0.0f;
   for (int j = 0; j < n_ids; ++j) sum += up[j];
-  const float l2 = log2f(norm.y);
-  const float A = a.scale * (dl - sum - (a.d_entropy ? dh * h : 0.0f));
-  const float B = -a.scale * dh * kLn2;
-  const float m = norm.x, c = a.c;
-  auto grad = [&](float f) {
-    const float l = fmaf(f - m, c, -l2);
-    return ex2(l) * fmaf(B, fmaxf(l, kFloor), A);
+  // p = 2^l with l = arg(x) + lift = log2 p; the gradient is p (A + B l)
+  const ExpRef ref(norm.x, a.c);
+  const float lift = ref.shift - log2f(norm.y), over = ref.k / norm.y;
+  const float B = -a.scale * dh * kLn2 * over;
+  const float A = a.scale * (dl - sum - (a.d_entropy ? dh * h : 0.0f)) * over;
+  auto grad = [&](Pair f) {
+    const Pair l = ref.arg(f);
+    const float2 g = add2(l, Pair::both(lift)).split();
+    const Pair clear = Pair::of(fmaxf(g.x, kFloor), fmaxf(g.y, kFloor));
+    return mul2(ex2_pair(l), fma2(Pair::both(B), clear, Pair::both(A)));
   };
+  auto grad_flat = [&](Pair f) { return mul2(ex2_pair(ref.arg(f)), Pair::both(A)); };  // no entropy
   // a listed element's whole gradient, by the thread that holds its slot: several slots may name one id, and all
   // of them write the same
   float whole = 0.0f;
@@ -429,10 +435,11 @@ __global__ void __launch_bounds__(kRowThreads) logprob_grad_kernel(const __grid_
     float v = 0.0f;
     for (int j = 0; j < n_ids; ++j)
       if (ids[j] == static_cast<int32_t>(id)) v += up[j];
-    whole = fmaf(a.scale, v, grad(to_float<DT>(x[id])));
+    whole = fmaf(a.scale, v, grad(Pair::both(to_float<DT>(x[id]))).split().x);
   }
   __syncthreads();
-  part.map(first, d, a.vec, edge, grad);
+  if (dh != 0.0f) part.map(first, d, a.vec, edge, grad);
+  else part.map(first, d, a.vec, edge, grad_flat);
   __syncthreads();
   if (mine) d[id] = from_float<DT>(whole);
 }

@@ -261,8 +261,8 @@ ss_status ss_reshard(const void* flat, const int64_t* shard_bounds, int32_t n_ra
  * gradients that the calls above reduce. Rows of logits are read where they
  * lie; a call enqueues one kernel and needs no workspace.
  *
- * z = scale * x is a row's scaled logits (scale = 1 / temperature, finite and
- * > 0), lse = log sum exp z, p = exp(z - lse). Sums and normalisers are fp32.
+ * z = scale * x is a row's scaled logits (scale = 1 / temperature, > 0 and
+ * <= 1e20), lse = log sum exp z, p = exp(z - lse). Sums and normalisers are fp32.
  *   - `norm` [rows][2] is a row's normaliser as the pair (max x, sum exp(scale
  *     (x - max x))): lse = scale * norm[0] + log norm[1]. The forward calls
  *     write it, the gradient calls take it. Kept as a pair it has all its digits
