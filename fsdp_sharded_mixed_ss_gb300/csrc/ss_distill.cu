@@ -26,7 +26,7 @@ struct DistillArgs {
   int64_t rows, vocab, ld, d_ld;
   float c, scale, t_scale;
   int32_t k, mode, t_dtype;
-  bool wide, vec;
+  bool wide, vec, in_place;
   uint32_t split;   // gradient from saved normalisers: blocks that share a row
   int32_t batches;  // of vectors a thread holds
 };
@@ -39,138 +39,139 @@ __device__ __forceinline__ float load_teacher(const void* p, int64_t i, int dtyp
 
 // ------------------------------------------------------------------ a row's list
 //
-// Thread j < k holds slot j. The list's sums come in three steps around barriers
-// that the callers place other work between: list_unique (which slots count),
-// list_partials (per warp), list_sums (after a barrier).
+// One warp of the block has the list, lane i its slots i, i + 32, ...: it loads
+// them and their logits, drops repeated ids, sums them up and writes their
+// gradients, while the block's other warps go through the row's elements.
 
-constexpr int kListWarps = SS_MAX_TOP / 32;
+constexpr int kListThreads = kRowThreads + 32;  // the row's warps and the list's
+constexpr int kSlots = SS_MAX_TOP / 32;
 
-struct ListShared {
-  int4 id[SS_MAX_TOP / 4];      // -1: unused
-  uint8_t again[SS_MAX_TOP];    // slots whose id occurs earlier in the list
-  RowMass in[kListWarps];       // the listed tokens' mass
-  RowMass teacher[kListWarps];  // SS_TAIL_RENORM: mass of the teacher's values
-  float2 q[kListWarps];         // else: sum of q as a pair
-};
+template <int DT>
+struct RowList {
+  int32_t id[kSlots];    // -1: unused
+  float lq[kSlots];      // log q
+  float q[kSlots];
+  float x[kSlots];       // the token's logit
+  RowMass in;            // the listed tokens' mass
+  float q_sum, q_tail;   // Q and q_t
+  bool bad;              // an id past the vocabulary
 
-struct Slot {
-  int32_t id;  // -1: unused
-  float lq;    // log q, before SS_TAIL_RENORM's normalisation
-  float x;     // the token's logit
-};
-
-struct ListSums {
-  float shift;   // what log q is short of: log q = lq - shift
-  float q_sum;   // Q
-  float q_tail;  // q_t
-};
-
-// The calling thread's slot as given (x not yet); *past: its id is past the vocabulary.
-__device__ __forceinline__ Slot list_fetch(const DistillArgs& a, int64_t row, bool* past) {
-  Slot s = {-1, -kInf, -kInf};
-  *past = false;
-  if (threadIdx.x < a.k) {
-    const int64_t at = row * a.k + threadIdx.x;
-    const int64_t id = load_id(a.ids, at, a.wide);
-    s.lq = load_teacher(a.teacher, at, a.t_dtype) * a.t_scale;
-    *past = id >= a.vocab;
-    if (id >= 0 && id < a.vocab) s.id = static_cast<int32_t>(id);
-  }
-  return s;
-}
-
-// After the slots' ids are in l.id and a barrier: finds the repeated ones, two threads a slot (a barrier follows,
-// then list_drop).
-__device__ __forceinline__ void list_unique(const DistillArgs& a, ListShared& l) {
-  static_assert(kRowThreads == 2 * SS_MAX_TOP, "two threads a slot");
-  const int j = threadIdx.x >> 1;
-  if (j < a.k) {  // k threads pairs, so whole pairs
-    const int32_t* ids = &l.id[0].x;
-    const int32_t mine = ids[j];
-    int again = 0;
-    for (int q = threadIdx.x & 1; 4 * q < j; q += 2) {
-      const int4 v = l.id[q];
-      again |= (v.x == mine) | ((v.y == mine) & (4 * q + 1 < j)) | ((v.z == mine) & (4 * q + 2 < j)) |
-               ((v.w == mine) & (4 * q + 3 < j));
-    }
-    const unsigned pair = 3u << (threadIdx.x & 30);
-    again |= __shfl_xor_sync(pair, again, 1);
-    if ((threadIdx.x & 1) == 0) l.again[j] = static_cast<uint8_t>(again);
-  }
-}
-
-__device__ __forceinline__ void list_drop(const DistillArgs& a, const ListShared& l, Slot& s) {
-  if (threadIdx.x < a.k && (s.id < 0 || l.again[threadIdx.x])) s.id = -1;
-  if (s.id < 0) s.lq = -kInf;
-}
-
-// The warps' partial sums (a barrier follows).
-__device__ __forceinline__ void list_partials(const DistillArgs& a, ListShared& l, const Slot& s) {
-  if (threadIdx.x >= SS_MAX_TOP) return;
-  const int warp = threadIdx.x >> 5;
-  auto one = [](float v, bool used) {  // the mass of one value
-    if (!used || v == -kInf) return RowMass::none();
-    return v <= 3.402823466e38f ? RowMass{v, 1.0f} : RowMass{-kInf, nan_f()};
-  };
-  const RowMass in = merge_lanes(one(s.x, s.id >= 0), a.c);
-  if ((threadIdx.x & 31) == 0) l.in[warp] = in;
-  if (a.mode == SS_TAIL_RENORM) {
-    const RowMass t = merge_lanes(one(s.lq, s.id >= 0), kLog2e);
-    if ((threadIdx.x & 31) == 0) l.teacher[warp] = t;
-  } else {
-    // q_t = 1 - Q is small when the list has nearly all the mass: Q is added as a pair
-    dd q = {expf(s.lq), 0.0f};
+  // ids_shared: SS_MAX_TOP / 4 int4 of shared memory, this warp's own.
+  __device__ __forceinline__ void load(const DistillArgs& a, int64_t row, const Elem<DT>* xr, int4* ids_shared) {
+    const int lane = threadIdx.x & 31;
+    bool past = false;
+    __syncwarp();
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float h = __shfl_xor_sync(0xFFFFFFFFu, q.hi, off), lo = __shfl_xor_sync(0xFFFFFFFFu, q.lo, off);
-      const dd t = two_sum(q.hi, h);
-      q = {t.hi, t.lo + (q.lo + lo)};
+    for (int i = 0; i < kSlots; ++i) {
+      id[i] = -1;
+      lq[i] = x[i] = -kInf;
+      const int j = lane + 32 * i;
+      if (32 * i < a.k) {
+        if (j < a.k) {
+          const int64_t wide_id = load_id(a.ids, row * a.k + j, a.wide);
+          lq[i] = load_teacher(a.teacher, row * a.k + j, a.t_dtype) * a.t_scale;
+          past = past || wide_id >= a.vocab;
+          if (wide_id >= 0 && wide_id < a.vocab) id[i] = static_cast<int32_t>(wide_id);
+        }
+        (&ids_shared[0].x)[j] = id[i];
+      }
     }
-    if ((threadIdx.x & 31) == 0) l.q[warp] = make_float2(q.hi, q.lo);
-  }
-}
-
-__device__ __forceinline__ ListSums list_sums(const DistillArgs& a, const ListShared& l) {
-  ListSums o = {0.0f, 0.0f, 0.0f};
-  if (a.mode == SS_TAIL_RENORM) {
-    const RowMass t = merge_lanes(l.teacher[threadIdx.x % kListWarps], kLog2e, kListWarps);
-    if (t.s != 0.0f) {
-      o.shift = t.m + logf(t.s);
-      o.q_sum = t.s == t.s ? 1.0f : t.s;
-    }
-  } else {
-    dd q = {l.q[0].x, l.q[0].y};
 #pragma unroll
-    for (int i = 1; i < kListWarps; ++i) {
-      const dd t = two_sum(q.hi, l.q[i].x);
-      q = {t.hi, t.lo + (q.lo + l.q[i].y)};
-    }
-    o.q_sum = q.hi + q.lo;
-    if (a.mode == SS_TAIL_BUCKET) {
-      const float rest = (1.0f - q.hi) - q.lo;
-      o.q_tail = rest <= 0.0f ? 0.0f : rest;
+    for (int i = 0; i < kSlots; ++i)
+      if (id[i] >= 0) x[i] = to_float<DT>(xr[id[i]]);
+    bad = __any_sync(0xFFFFFFFFu, past);
+    __syncwarp();
+    // an id that an earlier slot has: of its own 32, or of those before them
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      if (32 * i < a.k) {
+        int again = __match_any_sync(0xFFFFFFFFu, id[i]) & ((1u << lane) - 1u);
+        for (int q = 0; q < 8 * i; ++q) {
+          const int4 v = ids_shared[q];
+          again |= (v.x == id[i]) | (v.y == id[i]) | (v.z == id[i]) | (v.w == id[i]);
+        }
+        if (again) id[i] = -1;
+      }
+      if (id[i] < 0) {
+        lq[i] = -kInf;
+        x[i] = -kInf;
+      }
     }
   }
-  return o;
-}
+
+  __device__ __forceinline__ static RowMass mass(const float (&v)[kSlots], float c) {
+    RowMass m = one_element<RowMass>(v[0]);
+#pragma unroll
+    for (int i = 1; i < kSlots; ++i) {
+      RowMass o = one_element<RowMass>(v[i]);
+      if (o.m > m.m) m.move(o.m, c);
+      else if (m.m > o.m) o.move(m.m, c);
+      m.s += o.s;
+    }
+    return merge_lanes(m, c);
+  }
+
+  __device__ __forceinline__ void mass_in(const DistillArgs& a) { in = mass(x, a.c); }
+  // log q, q, Q and q_t.
+  __device__ __forceinline__ void sums(const DistillArgs& a) {
+    q_sum = q_tail = 0.0f;
+    if (a.mode == SS_TAIL_RENORM) {
+      const RowMass t = mass(lq, kLog2e);
+      const float shift = t.s == 0.0f ? 0.0f : t.m + logf(t.s);
+      q_sum = t.s == t.s ? (t.s == 0.0f ? 0.0f : 1.0f) : t.s;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        lq[i] -= shift;
+        q[i] = 32 * i < a.k ? expf(lq[i]) : 0.0f;
+      }
+    } else {
+      // q_t = 1 - Q is small when the list has nearly all the mass: Q is added as a pair
+      dd s = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        q[i] = 32 * i < a.k ? expf(lq[i]) : 0.0f;
+        const dd t = two_sum(s.hi, q[i]);
+        s = {t.hi, t.lo + s.lo};
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        const float h = __shfl_xor_sync(0xFFFFFFFFu, s.hi, off), lo = __shfl_xor_sync(0xFFFFFFFFu, s.lo, off);
+        const dd t = two_sum(s.hi, h);
+        s = {t.hi, t.lo + (s.lo + lo)};
+      }
+      q_sum = s.hi + s.lo;
+      if (a.mode == SS_TAIL_BUCKET) {
+        const float rest = (1.0f - s.hi) - s.lo;
+        q_tail = rest <= 0.0f ? 0.0f : rest;
+      }
+    }
+  }
+};
 
 // ------------------------------------------------------------------ loss and gradient in one call
 //
 // The gradient needs the row's sums and then the row again. A row is shared by
 // the blocks of a cluster, each holding its part in shared memory: the logits
-// are read from HBM once, with asynchronous copies that are all issued at the
-// start, and the gradient is computed from shared memory and written once. The
-// grid is one wave of clusters that go through the rows; a thread that has read
-// a batch for the last time starts the copy of the next row's batch into its
-// place, so the next row arrives while this one's gradient is written (or, for
-// the loss alone, while the row's other batches are added up). Two to four
-// blocks fit an SM, and one's sums and barriers pass under another's traffic.
+// are read from HBM once, with asynchronous copies, and the gradient is computed
+// from shared memory and written once. The grid is one wave of clusters that go
+// through the rows; a thread that has read a batch for the last time starts the
+// copy of the next row's batch into its place, so the next row arrives while
+// this one's gradient is written (or, for the loss alone, while the row's other
+// batches are added up). Two to four blocks fit an SM, and one's sums and
+// barriers pass under another's traffic.
 //
-// The listed tokens are left out of the first pass (a bit per element of the
-// part says which they are), so the unlisted mass is a sum of its own terms and
-// not a difference: log p_t keeps its digits however little is left. Their
-// logits come with the list; their gradients are written last, over what the
-// second pass put there.
+// Eight warps go through the elements and do as little else as can be; the ninth
+// has the row's list, the exchange between the blocks and the row's loss, and
+// prepares the next row's list meanwhile. Per row:
+//   ready   list -> row    the listed tokens are marked
+//   added   row -> list    the warps' sums are in `red`
+//   scales  list -> row    the gradient's factors are in `factor`
+//   written row -> list    the gradient is written; the list's own goes on top
+// The listed tokens are left out of the sums (a bit per element of the part says
+// which they are), so the unlisted mass is a sum of its own terms and not a
+// difference: log p_t keeps its digits however little is left.
+
+enum Barrier : int { kReady = 1, kAdded = 3, kScales = 5, kWritten = 6 };  // kReady, kAdded: two each, by turns
 
 // Marks the elements of packed vector w whose bits are set in `bits` as masked.
 template <int DT>
@@ -191,54 +192,54 @@ __device__ __forceinline__ void mask_elements(uint4& w, uint32_t bits) {
 template <int DT>
 constexpr uint32_t kMaskedWord = DT == SS_FP32 ? 0xFF800000u : (DT == SS_BF16 ? 0xFF80FF80u : 0xFC00FC00u);
 
-// N vectors into the running sum, `ref` being that of acc.m.
-template <int DT, int N>
-__device__ __forceinline__ void add_mass(const uint4 (&w)[N], float c, RowMass& acc, ExpRef& ref) {
+using RunningMass = Running<RowMass, 40>;
+
+// A batch of vectors into the running sum.
+template <int DT>
+__device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, RunningMass& acc) {
   float m = vec_max<DT>(w[0]);
 #pragma unroll
-  for (int u = 1; u < N; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
-  if (m > acc.m) {
-    acc.move(m, c);
-    ref = ExpRef(m, c);
-  }
+  for (int u = 1; u < kBatch; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
+  acc.see(m, c);
   Pair s = Pair::both(0.0f);
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
+  for (int u = 0; u < kBatch; ++u) {
     Pair f[kPairsOf<DT>];
     unpack_pairs<DT>(w[u], f);
 #pragma unroll
-    for (int j = 0; j < kPairsOf<DT>; ++j) s = add2(s, ex2_pair(ref.arg(f[j])));
+    for (int j = 0; j < kPairsOf<DT>; ++j) s = add2(s, ex2_pair(acc.ref.arg(f[j])));
   }
-  acc.s = fmaf(s.sum(), ref.k, acc.s);
+  acc.at.s = fmaf(s.sum(), acc.ref.k, acc.at.s);
 }
 
-// Dynamic shared memory: the part's vectors [batches * kBatch][T], then a byte of listed bits for each, by thread.
+// Dynamic shared memory: the part's vectors [batches * kBatch][T], then a word of listed bits for each batch, by
+// thread (twice for the loss alone, where a row's marks are set while the last one's are read).
 // SIZE: blocks of the cluster.
 template <int DT, bool GRAD, int SIZE>
-__global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(const __grid_constant__ DistillArgs a) {
-  constexpr int V = kVecOf<DT>;
+__global__ void __launch_bounds__(kListThreads, 3) distill_kernel(const __grid_constant__ DistillArgs a) {
   extern __shared__ uint4 held[];
-  __shared__ RowMass red[kRowWarps];
+  __shared__ RowMass red[2][kRowWarps];
   __shared__ RowMass parts[2][kMaxCluster];  // by turns: a block may be one row ahead of another's reading
-  __shared__ ListShared l;
-  __shared__ float part_loss[kListWarps];
-  __shared__ uint32_t edge_listed;
+  __shared__ int4 list_ids[SS_MAX_TOP / 4];
+  __shared__ float factor[3];
+  __shared__ uint32_t edge_listed[2];
   Cluster cl = Cluster::start();
   cl.size = SIZE;
   using Part = RowPart<DT, SIZE>;
   pdl_wait();
-  pdl_trigger();
   const int tid = threadIdx.x;
-  const int64_t clusters = gridDim.x / cl.size;
+  const int64_t clusters = gridDim.x / SIZE;
   const float c = a.c;
+  const int batches = a.batches;
+  uint32_t* marks = reinterpret_cast<uint32_t*>(held + static_cast<size_t>(batches) * kBatch * kRowThreads);
   auto row_x = [&](int64_t row) { return static_cast<const Elem<DT>*>(a.x) + row * a.ld; };
   auto row_d = [&](int64_t row) { return static_cast<Elem<DT>*>(a.d) + row * a.d_ld; };
   auto weight = [&](int64_t row) { return a.weight && row < a.rows ? a.weight[row] : 1.0f; };
   // The first row from `row` on, of this cluster's, that counts (w: its weight); those before it get their zeros.
   auto next_live = [&](int64_t row, float* w) {
     while (row < a.rows && *w == 0.0f) {
-      if (GRAD) zero_part<DT>(row_d(row), a.vocab, cl.rank, cl.size);
-      if (cl.rank == 0 && tid == 0) {
+      if (GRAD && tid < kRowThreads) zero_part<DT>(row_d(row), a.vocab, cl.rank, SIZE);
+      if (cl.rank == 0 && tid == kRowThreads) {
         if (a.loss) a.loss[row] = 0.0f;
         if (a.norm) a.norm[row] = make_float2(0.0f, 0.0f);
         if (a.tail) a.tail[row] = 0.0f;
@@ -248,255 +249,306 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(const __grid_co
     }
     return row;
   };
-  auto copy_batch = [&](const Part& part, int q) {
-    const char* src = part.at() + q * kBatch * part.step_bytes();
-    uint4* h = held + q * kBatch * kRowThreads + tid;
-    if ((q + 1) * kBatch <= part.whole) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) copy_async16(h + u * kRowThreads, src + u * part.step_bytes());
-    } else {
-#pragma unroll 1
-      for (int u = 0; u < kBatch && part.more(q * kBatch + u); ++u)
-        copy_async16(h + u * kRowThreads, src + u * part.step_bytes());
-    }
-  };
-  // Rows differ by their 16-byte phase alone, so by one vector: the buffer has room for the longer ones.
-  const int held_batches = a.batches;
-  uint32_t* listed = reinterpret_cast<uint32_t*>(held + static_cast<size_t>(held_batches) * kBatch * kRowThreads);
-  const int quarter = (held_batches + 3) / 4;
-
-  int64_t row = blockIdx.x / cl.size;
+  int64_t row = blockIdx.x / SIZE;
   float w = weight(row);
   row = next_live(row, &w);
-  bool past = false;
-  Slot s = {-1, -kInf, -kInf};
-  float edge = -kInf;
-  Part part(row_x(row < a.rows ? row : 0), a.vocab, cl.rank, cl.size);
-  if (row < a.rows) {
-    s = list_fetch(a, row, &past);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      for (int q = g * quarter; q < min((g + 1) * quarter, held_batches); ++q) copy_batch(part, q);
-      copies_commit();
-    }
-    if (part.edge >= 0) edge = to_float<DT>(part.x[part.edge]);
-  }
+  for (int i = tid; i < (GRAD ? 1 : 2) * batches * kRowThreads; i += kListThreads) marks[i] = 0u;
+  if (tid < 2) edge_listed[tid] = 0u;
+  __syncthreads();
   cl.started();
-  for (int turn = 0; row < a.rows; turn ^= 1) {
-    const Elem<DT>* x = part.x;
-    Elem<DT>* d = row_d(row);
-    float next_w = weight(row + clusters);
-    for (int q = 0; q < held_batches; ++q) listed[q * kRowThreads + tid] = 0u;
-    if (tid == 0) edge_listed = 0u;
-    if (tid < SS_MAX_TOP) (&l.id[0].x)[tid] = s.id;
-    const bool bad = __syncthreads_or(past);
-    int owner = 0, slot = 0;
-    bool mine = s.id >= 0 && part.owns(s.id, &owner, &slot);
-    if (s.id >= 0) s.x = to_float<DT>(x[s.id]);
-    if (mine) {
-      if (slot < 0) atomicOr(&edge_listed, 1u << owner);
-      else atomicOr(&listed[(slot / kBatch) * kRowThreads + owner],
-                    1u << (slot % kBatch * 8 + (s.id - part.sl.head) % V));
-    }
-    list_unique(a, l);
-    __syncthreads();
-    list_drop(a, l, s);
-    mine = mine && s.id >= 0;
 
-    // the next row, its list, and (loss alone) its copies as this row's batches are done with
-    int64_t next = row + clusters;
-    bool next_past = false;
-    Slot next_s = {-1, -kInf, -kInf};
-    float next_edge = -kInf;
-    Part next_part = part;
-    auto look_ahead = [&] {
-      next = next_live(next, &next_w);
-      if (next < a.rows) {
-        next_part = Part(row_x(next), a.vocab, cl.rank, cl.size);
-        next_s = list_fetch(a, next, &next_past);
-        if (next_part.edge >= 0) next_edge = to_float<DT>(next_part.x[next_part.edge]);
+  if (tid < kRowThreads) {  // ---------------------------------------------------- the row's warps
+    // Rows differ by their 16-byte phase alone, so by one vector: the buffer has room for the longer ones.
+    const int quarter = (batches + 3) / 4;
+    auto copy_batch = [&](const Part& part, int q) {
+      const char* src = part.at() + q * kBatch * part.step_bytes();
+      uint4* h = held + q * kBatch * kRowThreads + tid;
+      if ((q + 1) * kBatch <= part.whole) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) copy_async16(h + u * kRowThreads, src + u * part.step_bytes());
+      } else {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (part.more(q * kBatch + u)) copy_async16(h + u * kRowThreads, src + u * part.step_bytes());
       }
     };
-    if (!GRAD) look_ahead();
-
-    RowMass out = RowMass::none();  // unlisted tokens
-    if (part.edge >= 0 && !((edge_listed >> tid) & 1u)) {
-      if (edge > out.m) out.m = edge;
-      out.s = edge == -kInf ? 0.0f : (edge <= 3.402823466e38f ? 1.0f : nan_f());
+    Part part(row_x(row < a.rows ? row : 0), a.vocab, cl.rank, SIZE);
+    float edge = -kInf;
+    if (row < a.rows) {
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        for (int q = g * quarter; q < min((g + 1) * quarter, batches); ++q) copy_batch(part, q);
+        copies_commit();
+      }
+      if (part.edge >= 0) edge = to_float<DT>(part.x[part.edge]);
     }
-    ExpRef ref(out.m, c);
+    bool waits = false;  // a cluster barrier that this thread has announced itself at and not yet waited for
+    for (int turn = 0; row < a.rows; turn ^= 1) {
+      int64_t next = row + clusters;
+      float next_edge = -kInf;
+      Part next_part = part;
+      auto look_ahead = [&] {
+        float next_w = weight(next);
+        next = next_live(next, &next_w);
+        if (next < a.rows) {
+          next_part = Part(row_x(next), a.vocab, cl.rank, SIZE);
+          if (next_part.edge >= 0) next_edge = to_float<DT>(next_part.x[next_part.edge]);
+        }
+      };
+      if (!GRAD) look_ahead();
+      const uint32_t* listed = marks + (GRAD ? 0 : turn * batches * kRowThreads) + tid;
+      if (turn == 0) barrier_sync<kReady, kListThreads>();
+      else barrier_sync<kReady + 1, kListThreads>();
+      const bool edge_out = part.edge >= 0 && !((edge_listed[GRAD ? 0 : turn] >> tid) & 1u);
+      RunningMass out(one_element<RowMass>(edge_out ? edge : -kInf), c);
 #pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
-      // copies still under way: this row's later quarters, and (loss alone) the next row's earlier ones
-      if (!GRAD || g == 0) copies_wait<3>();
-      else if (g == 1) copies_wait<2>();
-      else if (g == 2) copies_wait<1>();
-      else copies_wait<0>();
+      for (int g = 0; g < 4; ++g) {
+        // copies still under way: this row's later quarters, and (loss alone) the next row's earlier ones
+        if (!GRAD || g == 0) copies_wait<3>();
+        else if (g == 1) copies_wait<2>();
+        else if (g == 2) copies_wait<1>();
+        else copies_wait<0>();
 #pragma unroll 1
-      for (int q = g * quarter; q < min((g + 1) * quarter, held_batches); ++q) {
-        const uint4* h = held + q * kBatch * kRowThreads + tid;
-        const uint32_t bits = listed[q * kRowThreads + tid];
-        if ((q + 1) * kBatch <= part.whole) {
+        for (int q = g * quarter; q < min((g + 1) * quarter, batches); ++q) {
+          const uint4* h = held + q * kBatch * kRowThreads + tid;
           uint4 v[kBatch];
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) v[u] = h[u * kRowThreads];
+          const uint32_t bits = listed[q * kRowThreads];
           if (bits != 0u) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) mask_elements<DT>(v[u], (bits >> (8 * u)) & 0xFFu);
+            for (int u = 0; u < kBatch; ++u)
+              if ((bits >> (8 * u)) & 0xFFu) mask_elements<DT>(v[u], bits >> (8 * u));
           }
-          add_mass<DT>(v, c, out, ref);
-        } else {
-#pragma unroll 1
-          for (int u = 0; u < kBatch && part.more(q * kBatch + u); ++u) {
-            uint4 v[1] = {h[u * kRowThreads]};
-            mask_elements<DT>(v[0], (bits >> (8 * u)) & 0xFFu);
-            add_mass<DT>(v, c, out, ref);
+          if ((q + 1) * kBatch > part.whole) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+              if (!part.more(q * kBatch + u))
+                v[u] = make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+          }
+          add_mass<DT>(v, c, out);
+          if (!GRAD && next < a.rows) {
+            // the sums that the held vectors went into are formed before their place is given away
+            asm volatile("" ::"f"(out.at.s) : "memory");
+            copy_batch(next_part, q);
           }
         }
-        if (!GRAD && next < a.rows) {
-          // the sums that the held vectors went into are formed before their place is given away
-          asm volatile("" ::"f"(out.s) : "memory");
-          copy_batch(next_part, q);
+        if (!GRAD) copies_commit();
+      }
+      const RowMass warp_out = merge_lanes(out.done(c), c);
+      if ((tid & 31) == 0) red[turn][tid >> 5] = warp_out;
+      if (turn == 0) barrier_arrive<kAdded, kListThreads>();
+      else barrier_arrive<kAdded + 1, kListThreads>();
+      if (SIZE > 1) {
+        if (waits) cl.wait();
+        cl.arrive();
+        waits = true;
+      }
+      if constexpr (GRAD) {
+        look_ahead();
+        Elem<DT>* d = row_d(row);
+        barrier_sync<kScales, kListThreads>();
+        const float f_c = factor[0], f_r = factor[1], f_a = factor[2];
+        if (part.edge >= 0) d[part.edge] = from_float<DT>(ex2(fmaf(edge, f_c, -f_r)) * f_a);
+        const Pair pc = Pair::both(f_c), pr = Pair::both(-f_r), pa = Pair::both(f_a);
+        char* dst = part.at(d);
+        auto put = [&](const uint4& v, char* o) {
+          Pair p[kPairsOf<DT>];
+          unpack_pairs<DT>(v, p);
+#pragma unroll
+          for (int e = 0; e < kPairsOf<DT>; ++e) p[e] = mul2(ex2_pair(fma2(p[e], pc, pr)), pa);
+          store_vector<DT>(o, p, a.vec);
+        };
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll 1
+          for (int q = g * quarter; q < min((g + 1) * quarter, batches); ++q) {
+            const uint4* h = held + q * kBatch * kRowThreads + tid;
+            if ((q + 1) * kBatch <= part.whole) {
+#pragma unroll
+              for (int u = 0; u < kBatch; ++u) put(h[u * kRowThreads], dst + u * part.step_bytes());
+            } else {
+#pragma unroll 1
+              for (int u = 0; u < kBatch && part.more(q * kBatch + u); ++u)
+                put(h[u * kRowThreads], dst + u * part.step_bytes());
+            }
+            dst += kBatch * part.step_bytes();
+            if (next < a.rows) copy_batch(next_part, q);
+          }
+          copies_commit();
         }
+        barrier_arrive<kWritten, kListThreads>();
       }
-      if (!GRAD) copies_commit();
+      row = next;
+      edge = next_edge;
+      part = next_part;
     }
-    list_partials(a, l, s);
-    out = block_merge(out, c, red);
-    if (cl.size > 1) {
-      if (tid < cl.size) cl.at(parts[turn], tid)[cl.rank] = out;
-      cl.arrive();
-    }
-    RowMass all = merge_lanes(l.in[tid % kListWarps], c, kListWarps);
-    const ListSums sums = list_sums(a, l);
-    const float lq = s.lq - sums.shift, q = expf(lq);
-    if (cl.size > 1) {
-      cl.wait();
-      out = merge_lanes(parts[turn][tid % cl.size], c, static_cast<int>(cl.size));
-    }
-    {
-      const float top = fmaxf(all.m, out.m);
-      RowMass o = out;
-      if (top > all.m) all.move(top, c);
-      if (top > o.m) o.move(top, c);
-      all.s += o.s;
-    }
-    const bool empty = all.s == 0.0f;
-    // all unlisted tokens masked, by -inf or by values so low that no p_t is left
-    const bool no_tail = out.s == 0.0f || (out.m - all.m) * c <= kFloor;
-    if (cl.rank == 0) {
-      const float ln_s = logf(all.s);
-      const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
-      float term = 0.0f;
-      if (s.id >= 0 && q != 0.0f) {
-        const float lp = empty ? -kInf : fmaf(s.x - all.m, a.scale, -ln_s);
-        term = q * (lq - lp);
-      }
-      if (tid < SS_MAX_TOP) {
+    if (SIZE > 1 && waits) cl.wait();
+  } else {  // -------------------------------------------------------------------- the list's warp
+    const int lane = tid & 31;
+    RowList<DT> l;
+    int marked[2][kSlots];  // the words of `marks` that were set (-1: none), by turn
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, off);
-        if ((tid & 31) == 0) part_loss[tid >> 5] = term;
-      }
-      __syncthreads();
-      if (tid == 0) {
-        float loss = 0.0f;
-        for (int i = 0; i < kListWarps; ++i) loss += part_loss[i];
-        if (sums.q_tail > 0.0f && !no_tail) loss += sums.q_tail * (logf(sums.q_tail) - tail);
-        if (bad || !(all.s == all.s) || !(sums.q_sum == sums.q_sum)) loss = nan_f();
-        if (a.loss) a.loss[row] = w * loss;
-        if (a.norm) a.norm[row] = make_float2(all.m, all.s);
-        if (a.tail) a.tail[row] = tail;
-      }
-    }
-    if constexpr (GRAD) {
-      look_ahead();
-      const float ws = bad ? nan_f() : w * a.scale;
-      const float b = sums.q_sum + sums.q_tail;
-      // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
-      const float p_t = no_tail ? 0.0f : ex2((out.m - all.m) * c) * (out.s / all.s);
-      const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - sums.q_tail) / out.s;
-      const ExpRef outer(out.m, c);
-      const float B = A * outer.k;
-      if (part.edge >= 0) d[part.edge] = from_float<DT>(outer.exp(edge) * B);
-      char* dst = part.at(d);
-      auto put = [&](const uint4& v, char* o) {
-        Pair p[kPairsOf<DT>];
-        unpack_pairs<DT>(v, p);
+    for (int i = 0; i < kSlots; ++i) marked[0][i] = marked[1][i] = -1;
+    unsigned mine = 0u;  // slots whose element is this block's
+    auto fetch = [&](int64_t r) {
+      l.load(a, r, row_x(r), list_ids);
+      l.sums(a);
+      l.mass_in(a);
+    };
+    // Row r's marks for `turn`, and word that they are ready.
+    auto mark = [&](int64_t r, int turn) {
+      const Part part(row_x(r), a.vocab, cl.rank, SIZE);
+      const int set = GRAD ? 0 : turn;
+      uint32_t* listed = marks + set * batches * kRowThreads;
 #pragma unroll
-        for (int e = 0; e < kPairsOf<DT>; ++e) p[e] = mul2(ex2_pair(outer.arg(p[e])), Pair::both(B));
-        store_vector<DT>(o, p, a.vec);
-      };
-#pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-#pragma unroll 1
-        for (int r = g * quarter; r < min((g + 1) * quarter, held_batches); ++r) {
-          const uint4* h = held + r * kBatch * kRowThreads + tid;
-          if ((r + 1) * kBatch <= part.whole) {
+      for (int i = 0; i < kSlots; ++i) {
+        const int old = set ? marked[1][i] : marked[0][i];
+        if (old >= 0) listed[old] = 0u;
+      }
+      if (lane == 0) edge_listed[set] = 0u;
+      __syncwarp();
+      mine = 0u;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) put(h[u * kRowThreads], dst + u * part.step_bytes());
+      for (int i = 0; i < kSlots; ++i) {
+        int owner, slot, word = -1;
+        if (l.id[i] >= 0 && part.owns(l.id[i], &owner, &slot)) {
+          mine |= 1u << i;
+          if (slot < 0) {
+            atomicOr(&edge_listed[set], 1u << owner);
           } else {
-#pragma unroll 1
-            for (int u = 0; u < kBatch && part.more(r * kBatch + u); ++u)
-              put(h[u * kRowThreads], dst + u * part.step_bytes());
+            word = (slot / kBatch) * kRowThreads + owner;
+            atomicOr(&listed[word], 1u << (slot % kBatch * 8 + (l.id[i] - part.sl.head) % kVecOf<DT>));
           }
-          dst += kBatch * part.step_bytes();
-          if (next < a.rows) copy_batch(next_part, r);
         }
-        copies_commit();
+        if (set) marked[1][i] = word;
+        else marked[0][i] = word;
       }
-      __syncthreads();
-      if (mine) {
-        const ExpRef top(all.m, c);
-        d[s.id] = from_float<DT>(empty ? 0.0f : ws * fmaf(top.exp(s.x) * (top.k / all.s), b, -q));
-      }
+      if (turn == 0) barrier_arrive<kReady, kListThreads>();
+      else barrier_arrive<kReady + 1, kListThreads>();
+    };
+    if (row < a.rows) {
+      fetch(row);
+      mark(row, 0);
     }
-    row = next;
-    w = next_w;
-    s = next_s;
-    past = next_past;
-    edge = next_edge;
-    part = next_part;
+    for (int turn = 0; row < a.rows; turn ^= 1) {
+      int64_t next = row + clusters;
+      float next_w = weight(next);
+      const RowList<DT> now = l;  // this row's; `l` is the next one's from its fetch on
+      const unsigned now_mine = mine;  // as `mark` left it
+      next = next_live(next, &next_w);
+      if (next < a.rows) {
+        fetch(next);
+        if (!GRAD) mark(next, turn ^ 1);
+      }
+      if (turn == 0) barrier_sync<kAdded, kListThreads>();
+      else barrier_sync<kAdded + 1, kListThreads>();
+      RowMass out = merge_lanes(red[turn][lane % kRowWarps], c, kRowWarps);
+      if (SIZE > 1) {
+        if (lane < SIZE) cl.at(parts[turn], lane)[cl.rank] = out;
+        cl.arrive();
+        cl.wait();
+        out = merge_lanes(parts[turn][lane % SIZE], c, SIZE);
+      }
+      RowMass all = now.in, o = out;
+      if (o.m > all.m) all.move(o.m, c);
+      else if (all.m > o.m) o.move(all.m, c);
+      all.s += o.s;
+      const bool empty = all.s == 0.0f;
+      // all unlisted tokens masked, by -inf or by values so low that no p_t is left
+      const bool no_tail = out.s == 0.0f || (out.m - all.m) * c <= kFloor;
+      const float ws = now.bad ? nan_f() : w * a.scale;
+      const float b = now.q_sum + now.q_tail;
+      if constexpr (GRAD) {
+        // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
+        const float p_t = no_tail ? 0.0f : ex2((out.m - all.m) * c) * (out.s / all.s);
+        const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - now.q_tail) / out.s;
+        const ExpRef ref(out.m, c);
+        if (lane == 0) {
+          factor[0] = ref.c;
+          factor[1] = ref.r;
+          factor[2] = A * ref.k;
+        }
+        barrier_arrive<kScales, kListThreads>();
+        if (next < a.rows) mark(next, turn ^ 1);
+      }
+      if (cl.rank == 0) {
+        const float ln_s = logf(all.s);
+        const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
+        float loss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+          if (now.id[i] >= 0 && now.q[i] != 0.0f) {
+            const float lp = empty ? -kInf : fmaf(now.x[i] - all.m, a.scale, -ln_s);
+            loss += now.q[i] * (now.lq[i] - lp);
+          }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, off);
+        if (lane == 0) {
+          if (now.q_tail > 0.0f && !no_tail) loss += now.q_tail * (logf(now.q_tail) - tail);
+          if (now.bad || !(all.s == all.s) || !(now.q_sum == now.q_sum)) loss = nan_f();
+          if (a.loss) a.loss[row] = w * loss;
+          if (a.norm) a.norm[row] = make_float2(all.m, all.s);
+          if (a.tail) a.tail[row] = tail;
+        }
+      }
+      if constexpr (GRAD) {
+        const ExpRef top(all.m, c);
+        const float over = top.k / all.s;
+        Elem<DT>* d = row_d(row);
+        barrier_sync<kWritten, kListThreads>();
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+          if ((now_mine >> i) & 1u)
+            d[now.id[i]] = from_float<DT>(empty ? 0.0f : ws * fmaf(top.exp(now.x[i]) * over, b, -now.q[i]));
+      }
+      row = next;
+      w = next_w;
+    }
   }
+  // Late: the next kernel's blocks would else take the places that this wave leaves one by one, and its clusters,
+  // of which all have to be resident for an even share of the rows, would not all find room.
+  pdl_trigger();
 }
 
 // ------------------------------------------------------------------ the gradient from saved normalisers
 //
 // One pass: blocks share a row as above, but nothing is exchanged between them.
-// The list's sums are taken while the first vectors are on their way.
+// A ninth warp has the list while the first vectors are on their way.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads, 4) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
-  __shared__ ListShared l;
+__global__ void __launch_bounds__(kListThreads, 3) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
+  __shared__ int4 list_ids[SS_MAX_TOP / 4];
+  __shared__ float factor[3];
   pdl_wait();
   pdl_trigger();
+  const int tid = threadIdx.x;
   const unsigned rank = blockIdx.x % a.split;
   const int64_t row = blockIdx.x / a.split;
   const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
   Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
   const float wt = a.weight ? a.weight[row] : 1.0f, dl = a.d_loss ? a.d_loss[row] : 1.0f;
   const float2 norm = a.norm_in[row];
-  bool past;
-  Slot s = list_fetch(a, row, &past);
   if (wt == 0.0f || dl == 0.0f || norm.y == 0.0f) {
-    zero_part<DT>(d, a.vocab, rank, a.split);
+    if (tid < kRowThreads) zero_part<DT>(d, a.vocab, rank, a.split);
     return;
   }
   const RowPart<DT> part(x, a.vocab, rank, a.split);
-  uint4 first[kBatch];
-  part.load(0, first);
-  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : 0.0f;
-  if (threadIdx.x < SS_MAX_TOP) (&l.id[0].x)[threadIdx.x] = s.id;
-  const bool bad = __syncthreads_or(past);
-  int owner, slot;
-  const bool mine = s.id >= 0 && part.owns(s.id, &owner, &slot);
-  if (mine) s.x = to_float<DT>(x[s.id]);
-  list_unique(a, l);
-  __syncthreads();
-  list_drop(a, l, s);
-  list_partials(a, l, s);
-  __syncthreads();
-  const ListSums sums = list_sums(a, l);
-  const float ws = bad ? nan_f() : wt * dl * a.scale;
-  const float b = sums.q_sum + sums.q_tail;
+  if (tid < kRowThreads) {
+    uint4 first[kBatch];
+    part.load(0, first);
+    const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : 0.0f;
+    barrier_sync<kScales, kListThreads>();
+    const Pair c = Pair::both(factor[0]), r = Pair::both(-factor[1]), A = Pair::both(factor[2]);
+    part.map(first, d, a.vec, edge, [&](Pair f) { return mul2(ex2_pair(fma2(f, c, r)), A); });
+    barrier_arrive<kWritten, kListThreads>();
+    return;
+  }
+  RowList<DT> l;
+  l.load(a, row, x, list_ids);
+  l.sums(a);
+  const float ws = l.bad ? nan_f() : wt * dl * a.scale;
+  const float b = l.q_sum + l.q_tail;
   // p = k 2^arg / s; with the bucket the unlisted take (p / p_t) (p_t b - q_t), p_t inside the exponent where it is
   // so small that the exponentials without it would vanish
   const ExpRef ref(norm.x, a.c);
@@ -507,19 +559,36 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_grad_kernel(const __gr
     if (tail == -kInf) {
       A = ws * 0.0f;
     } else if (tail > -60.0f) {
-      A = ws * (p_t * b - sums.q_tail) * (over / p_t);
+      A = ws * (p_t * b - l.q_tail) * (over / p_t);
     } else {
-      A = ws * (p_t * b - sums.q_tail) * over;
+      A = ws * (p_t * b - l.q_tail) * over;
       r = fmaf(tail, kLog2e, r);
     }
   }
-  const float rc = ref.c;
-  part.map(first, d, a.vec, edge, [&](Pair f) {
-    return mul2(ex2_pair(fma2(f, Pair::both(rc), Pair::both(-r))), Pair::both(A));
-  });
-  __syncthreads();
-  if (mine && s.id >= 0)
-    d[s.id] = from_float<DT>(ws * fmaf(ref.exp(s.x) * over, b, -expf(s.lq - sums.shift)));
+  if ((tid & 31) == 0) {
+    factor[0] = ref.c;
+    factor[1] = r;
+    factor[2] = A;
+  }
+  float g[kSlots];
+  if (a.in_place) {  // the logits have to be here before the other warps write over them
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      g[i] = ws * fmaf(ref.exp(l.x[i]) * over, b, -l.q[i]);
+      asm volatile("" ::"f"(g[i]) : "memory");
+    }
+  }
+  barrier_arrive<kScales, kListThreads>();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    int owner, slot;
+    if (l.id[i] >= 0 && !part.owns(l.id[i], &owner, &slot)) l.id[i] = -1;
+    if (!a.in_place) g[i] = ws * fmaf(ref.exp(l.x[i]) * over, b, -l.q[i]);
+  }
+  barrier_sync<kWritten, kListThreads>();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (l.id[i] >= 0) d[l.id[i]] = from_float<DT>(g[i]);
 }
 
 template <bool GRAD, int DT>
@@ -569,12 +638,12 @@ ss_status resident_clusters(const void* fn, size_t smem, int cluster, int* out) 
   }
   int n = 0;
   if (cluster == 1) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kRowThreads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kListThreads, smem);
     n *= sm_count();
   } else {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3(kListThreads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -631,14 +700,14 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
                          reinterpret_cast<const float2*>(norm_in), tail_in, loss, reinterpret_cast<float2*>(norm),
                          tail, d_logits, rows, x->vocab, x->ld, d_ld, x->scale * kLog2e, x->scale, t->scale, t->k,
-                         t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld),
+                         t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld), d_logits == x->data,
                          static_cast<uint32_t>(split), 0};
   if (saved) {
     auto* fn = x->dtype == SS_BF16
                    ? distill_grad_kernel<SS_BF16>
                    : (x->dtype == SS_FP16 ? distill_grad_kernel<SS_FP16> : distill_grad_kernel<SS_FP32>);
     if (rows * split > INT32_MAX) return SS_ERR_OVERFLOW;
-    return launch(fn, static_cast<unsigned>(rows * split), a, stream, kRowThreads);
+    return launch(fn, static_cast<unsigned>(rows * split), a, stream, kListThreads);
   }
   // a part of at most kPartVectors vectors a thread, or what 8 blocks leave
   const auto vectors = [&](int n) { return (nvec + n * kRowThreads - 1) / (n * kRowThreads); };
@@ -646,11 +715,11 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
   auto* fn = d_logits ? distill_for<true>(x->dtype, cluster) : distill_for<false>(x->dtype, cluster);
   a.batches = static_cast<int>((vectors(cluster) + kBatch - 1) / kBatch);
-  const size_t smem = static_cast<size_t>(a.batches) * kRowThreads * (kBatch * sizeof(uint4) + sizeof(uint32_t));
+  const size_t smem = static_cast<size_t>(a.batches) * kRowThreads * (kBatch * sizeof(uint4) + (d_logits ? 1 : 2) * sizeof(uint32_t));
   int clusters = 0;
   st = resident_clusters(reinterpret_cast<const void*>(fn), smem, cluster, &clusters);
   if (st != SS_OK) return st;
-  return launch_rows(fn, std::min<int64_t>(rows, clusters), cluster, smem, a, stream);
+  return launch_rows(fn, std::min<int64_t>(rows, clusters), cluster, kListThreads, smem, a, stream);
 }
 
 }  // namespace

@@ -25,6 +25,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFloor = -1e4f;  // 2^kFloor is 0, and 0 * kFloor is 0 where 0 * -inf would be NaN
 
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7FFFFFFF); }
+
 template <int DT>
 struct ElemOf {
   using T = uint16_t;
@@ -146,8 +148,6 @@ __device__ __forceinline__ float vec_max(const uint4& w) {
   }
 }
 
-__device__ __forceinline__ float nan_f() { return __int_as_float(0x7FFFFFFF); }
-
 // 16 bytes from global to shared memory, asynchronously; the issuing thread sees them after copies_wait.
 __device__ __forceinline__ void copy_async16(void* shared, const void* global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
@@ -259,6 +259,47 @@ __device__ __forceinline__ uint64_t order_pair(float x, int64_t id) {
   return (static_cast<uint64_t>(order_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
 }
 
+// A thread's running sums around a reference that stays where it is while the elements are at most 2^SLACK times its
+// exponential: the reference is the first batch's maximum for nearly all threads, and `top` the maximum.
+template <class Sum, int SLACK>
+struct Running {
+  Sum at;        // around the reference at.m
+  float top;     // max x
+  float limit;   // elements above it move the reference
+  ExpRef ref;    // of at.m
+
+  __device__ __forceinline__ Running(Sum first, float c) : at(first), top(first.m), ref(first.m, c) {
+    limit = first.m + SLACK / c;
+  }
+  __device__ __forceinline__ void see(float m, float c) {
+    top = fmaxf(top, m);
+    if (m > limit) {
+      at.move(m, c);
+      ref = ExpRef(m, c);
+      limit = m + SLACK / c;
+    }
+  }
+  // The sums around the maximum.
+  __device__ __forceinline__ Sum done(float c) {
+    if (top > at.m) at.move(top, c);
+    return at;
+  }
+};
+
+// One element as a sum: 2^0 (0 when masked, NaN for NaN and +inf, with any maximum that is a number).
+template <class Sum>
+__device__ __forceinline__ Sum one_element(float x) {
+  Sum a = Sum::none();
+  if (x == -kInf) return a;
+  if (x <= 3.402823466e38f) {
+    a.m = x;
+    a.s = 1.0f;
+  } else {
+    a.s = nan_f();
+  }
+  return a;
+}
+
 // Merged over the `width` (a power of two) lanes of each aligned group, the groups being copies of one another;
 // the same in every lane. One rescale a lane: first the maximum, then plain sums.
 template <class Sum>
@@ -289,6 +330,16 @@ __device__ __forceinline__ int64_t load_id(const void* p, int64_t i, bool wide) 
 __device__ __forceinline__ void store_id(void* p, int64_t i, int64_t v, bool wide) {
   if (wide) static_cast<int64_t*>(p)[i] = v;
   else static_cast<int32_t*>(p)[i] = static_cast<int32_t>(v);
+}
+
+// Hardware barrier ID (1 to 15) of the block, for THREADS threads of which some only announce themselves.
+template <int ID, int THREADS>
+__device__ __forceinline__ void barrier_sync() {
+  asm volatile("barrier.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+template <int ID, int THREADS>
+__device__ __forceinline__ void barrier_arrive() {
+  asm volatile("barrier.arrive %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
 
 // ------------------------------------------------------------------ rows shared by a cluster of blocks
@@ -555,10 +606,11 @@ inline int split_for(int64_t nvec) {
 
 // Launches `clusters` clusters of `cluster` blocks (a plain launch for 1).
 template <typename Args>
-ss_status launch_rows(void (*fn)(Args), int64_t clusters, int cluster, size_t smem, const Args& args, void* stream) {
+ss_status launch_rows(void (*fn)(Args), int64_t clusters, int cluster, int threads, size_t smem, const Args& args,
+                      void* stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
-  cfg.blockDim = dim3(kRowThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];

@@ -49,17 +49,17 @@ struct TopShared {
 };
 struct NoTops {};
 
-// N vectors into the running sums, `ref` being that of acc.m; returns their maximum.
+using RunningSum = Running<RowSum, 8>;
+
+// N vectors into the running sums; returns their maximum.
 template <int DT, int N>
-__device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RowSum& acc, ExpRef& ref) {
+__device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RunningSum& acc) {
   constexpr int V = kVecOf<DT>;
   float m = vec_max<DT>(w[0]);
 #pragma unroll
   for (int u = 1; u < N; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
-  if (m > acc.m) {
-    acc.move(m, c);
-    ref = ExpRef(m, c);
-  }
+  acc.see(m, c);
+  const ExpRef& ref = acc.ref;
   Pair s = Pair::both(0.0f), t = s;
 #pragma unroll
   for (int u = 0; u < N; ++u) {
@@ -87,8 +87,8 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RowSu
       }
     }
   }
-  acc.s = fmaf(ss, ref.k, acc.s);
-  acc.t = fmaf(fmaf(ref.shift, ss, tt), ref.k, acc.t);
+  acc.at.s = fmaf(ss, ref.k, acc.at.s);
+  acc.at.t = fmaf(fmaf(ref.shift, ss, tt), ref.k, acc.at.t);
   return m;
 }
 
@@ -161,14 +161,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   const int64_t sb = part.step_bytes();
   const char* src = part.at();
   const int unit_batches = ((vectors + kBatch - 1) / kBatch + kUnits - 1) / kUnits;
-  RowSum acc = RowSum::none();
-  float edge = -kInf;
-  if (part.edge >= 0) {  // its own maximum: 2^0 (0 when masked, NaN for NaN and +inf)
-    edge = to_float<DT>(part.x[part.edge]);
-    if (edge > acc.m) acc.m = edge;
-    acc.s = edge == -kInf ? 0.0f : (edge <= 3.402823466e38f ? 1.0f : nan_f());
-  }
-  ExpRef ref(acc.m, a.c);
+  const float edge = part.edge >= 0 ? to_float<DT>(part.x[part.edge]) : -kInf;
+  RunningSum run(one_element<RowSum>(edge), a.c);
   float unit = -kInf;
   int in_unit = 0, units = 0;
   auto end_batch = [&](float m) {
@@ -185,7 +179,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     uint4 w[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) w[u] = __ldg(reinterpret_cast<const uint4*>(src + u * sb));
-    end_batch(add_vectors<DT>(w, a.c, acc, ref));
+    end_batch(add_vectors<DT>(w, a.c, run));
   }
   if (full * kBatch < vectors) {
     uint4 w[kBatch];
@@ -197,7 +191,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     for (int u = 0; u < kBatch; ++u) {
       if (part.more(full * kBatch + u)) {
         const uint4 one[1] = {w[u]};
-        m = fmaxf(m, add_vectors<DT>(one, a.c, acc, ref));
+        m = fmaxf(m, add_vectors<DT>(one, a.c, run));
       }
     }
     end_batch(m);
@@ -205,8 +199,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   if constexpr (TOPS) {
     if (in_unit > 0) tops.unit[units++][tid] = unit;
   }
-  const float thread_max = acc.m;
-  acc = block_merge(acc, a.c, red);
+  const float thread_max = run.top;
+  RowSum acc = block_merge(run.done(a.c), a.c, red);
   cl.started();
   if (cl.size > 1) {
     if (tid < cl.size) cl.at(parts, tid)[cl.rank] = acc;
@@ -490,7 +484,7 @@ ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype id
   auto* fn = top_k > 0 ? pick(std::true_type()) : pick(std::false_type());
   const int cluster = cluster_for(rows, x->vocab, x->dtype == SS_FP32 ? 4 : 8);
   if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
-  return launch_rows(fn, rows, cluster, 0, a, stream);
+  return launch_rows(fn, rows, cluster, kRowThreads, 0, a, stream);
 }
 
 ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idtype idtype, int32_t top_k,
