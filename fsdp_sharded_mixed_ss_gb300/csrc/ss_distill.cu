@@ -7,7 +7,7 @@ namespace ss {
 namespace {
 
 #ifndef SS_PART_VECTORS
-#define SS_PART_VECTORS 16
+#define SS_PART_VECTORS 32
 #endif
 constexpr int kPartVectors = SS_PART_VECTORS;
 
@@ -27,8 +27,7 @@ struct DistillArgs {
   float c, scale, t_scale;
   int32_t k, mode, t_dtype;
   bool wide, vec, in_place;
-  uint32_t split;   // gradient from saved normalisers: blocks that share a row
-  int32_t batches;  // of vectors a thread holds
+  uint32_t split;  // gradient from saved normalisers: blocks that share a row
 };
 
 __device__ __forceinline__ float load_teacher(const void* p, int64_t i, int dtype) {
@@ -151,18 +150,12 @@ struct RowList {
 // ------------------------------------------------------------------ loss and gradient in one call
 //
 // The gradient needs the row's sums and then the row again. A row is shared by
-// the blocks of a cluster, each holding its part in shared memory: the logits
-// are read from HBM once, with asynchronous copies, and the gradient is computed
-// from shared memory and written once. The grid is one wave of clusters that go
-// through the rows; a thread that has read a batch for the last time starts the
-// copy of the next row's batch into its place, so the next row arrives while
-// this one's gradient is written (or, for the loss alone, while the row's other
-// batches are added up). Two to four blocks fit an SM, and one's sums and
-// barriers pass under another's traffic.
+// the blocks of a cluster: small enough parts that all the rows in flight stay
+// in L2, so the second pass reads them from there, and HBM sees each logit read
+// once and each gradient written once.
 //
 // Eight warps go through the elements and do as little else as can be; the ninth
-// has the row's list, the exchange between the blocks and the row's loss, and
-// prepares the next row's list meanwhile. Per row:
+// has the row's list, the exchange between the blocks and the row's loss:
 //   ready   list -> row    the listed tokens are marked
 //   added   row -> list    the warps' sums are in `red`
 //   scales  list -> row    the gradient's factors are in `factor`
@@ -171,7 +164,7 @@ struct RowList {
 // which they are), so the unlisted mass is a sum of its own terms and not a
 // difference: log p_t keeps its digits however little is left.
 
-enum Barrier : int { kReady = 1, kAdded = 3, kScales = 5, kWritten = 6 };  // kReady, kAdded: two each, by turns
+enum Barrier : int { kReady = 1, kAdded = 2, kScales = 3, kWritten = 4 };
 
 // Marks the elements of packed vector w whose bits are set in `bits` as masked.
 template <int DT>
@@ -212,304 +205,170 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
   acc.at.s = fmaf(s.sum(), acc.ref.k, acc.at.s);
 }
 
-// Dynamic shared memory: the part's vectors [batches * kBatch][T], then a word of listed bits for each batch, by
-// thread (twice for the loss alone, where a row's marks are set while the last one's are read).
-// SIZE: blocks of the cluster.
-template <int DT, bool GRAD, int SIZE>
+// Dynamic shared memory: a word of listed bits for each batch of vectors, by thread.
+template <int DT, bool GRAD>
 __global__ void __launch_bounds__(kListThreads, 3) distill_kernel(const __grid_constant__ DistillArgs a) {
-  extern __shared__ uint4 held[];
-  __shared__ RowMass red[2][kRowWarps];
-  __shared__ RowMass parts[2][kMaxCluster];  // by turns: a block may be one row ahead of another's reading
+  extern __shared__ uint32_t marks[];
+  __shared__ RowMass red[kRowWarps];
+  __shared__ RowMass parts[kMaxCluster];
   __shared__ int4 list_ids[SS_MAX_TOP / 4];
   __shared__ float factor[3];
-  __shared__ uint32_t edge_listed[2];
-  Cluster cl = Cluster::start();
-  cl.size = SIZE;
-  using Part = RowPart<DT, SIZE>;
+  __shared__ uint32_t edge_listed;
+  const Cluster cl = Cluster::start();
   pdl_wait();
+  pdl_trigger();
   const int tid = threadIdx.x;
-  const int64_t clusters = gridDim.x / SIZE;
+  const int64_t row = blockIdx.x / cl.size;
+  const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
+  Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
   const float c = a.c;
-  const int batches = a.batches;
-  uint32_t* marks = reinterpret_cast<uint32_t*>(held + static_cast<size_t>(batches) * kBatch * kRowThreads);
-  auto row_x = [&](int64_t row) { return static_cast<const Elem<DT>*>(a.x) + row * a.ld; };
-  auto row_d = [&](int64_t row) { return static_cast<Elem<DT>*>(a.d) + row * a.d_ld; };
-  auto weight = [&](int64_t row) { return a.weight && row < a.rows ? a.weight[row] : 1.0f; };
-  // The first row from `row` on, of this cluster's, that counts (w: its weight); those before it get their zeros.
-  auto next_live = [&](int64_t row, float* w) {
-    while (row < a.rows && *w == 0.0f) {
-      if (GRAD && tid < kRowThreads) zero_part<DT>(row_d(row), a.vocab, cl.rank, SIZE);
-      if (cl.rank == 0 && tid == kRowThreads) {
-        if (a.loss) a.loss[row] = 0.0f;
-        if (a.norm) a.norm[row] = make_float2(0.0f, 0.0f);
-        if (a.tail) a.tail[row] = 0.0f;
-      }
-      row += clusters;
-      *w = weight(row);
+  const float w = a.weight ? a.weight[row] : 1.0f;
+  if (w == 0.0f) {  // every block of the cluster
+    if (GRAD && tid < kRowThreads) zero_part<DT>(d, a.vocab, cl.rank, cl.size);
+    if (cl.rank == 0 && tid == kRowThreads) {
+      if (a.loss) a.loss[row] = 0.0f;
+      if (a.norm) a.norm[row] = make_float2(0.0f, 0.0f);
+      if (a.tail) a.tail[row] = 0.0f;
     }
-    return row;
-  };
-  int64_t row = blockIdx.x / SIZE;
-  float w = weight(row);
-  row = next_live(row, &w);
-  for (int i = tid; i < (GRAD ? 1 : 2) * batches * kRowThreads; i += kListThreads) marks[i] = 0u;
-  if (tid < 2) edge_listed[tid] = 0u;
-  __syncthreads();
-  cl.started();
-
+    cl.started();
+    return;
+  }
+  const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
   if (tid < kRowThreads) {  // ---------------------------------------------------- the row's warps
-    // Rows differ by their 16-byte phase alone, so by one vector: the buffer has room for the longer ones.
-    const int quarter = (batches + 3) / 4;
-    auto copy_batch = [&](const Part& part, int q) {
-      const char* src = part.at() + q * kBatch * part.step_bytes();
-      uint4* h = held + q * kBatch * kRowThreads + tid;
-      if ((q + 1) * kBatch <= part.whole) {
+    const int vectors = part.vectors();
+    const int64_t sb = part.step_bytes();
+    const char* src = part.at();
+    auto fetch = [&](const char* p, int j, uint4 (&v)[kBatch]) {
+      if (j + kBatch <= part.whole) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) copy_async16(h + u * kRowThreads, src + u * part.step_bytes());
+        for (int u = 0; u < kBatch; ++u) v[u] = load_row<GRAD>(p + u * sb);
       } else {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-          if (part.more(q * kBatch + u)) copy_async16(h + u * kRowThreads, src + u * part.step_bytes());
+          v[u] = part.more(j + u)
+                     ? load_row<GRAD>(p + u * sb)
+                     : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
       }
     };
-    Part part(row_x(row < a.rows ? row : 0), a.vocab, cl.rank, SIZE);
-    float edge = -kInf;
-    if (row < a.rows) {
+    uint4 v[kBatch];
+    fetch(src, 0, v);
+    const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
+    barrier_sync<kReady, kListThreads>();
+    const bool edge_out = part.edge >= 0 && !((edge_listed >> tid) & 1u);
+    RunningMass out(one_element<RowMass>(edge_out ? edge : -kInf), c);
+    const uint32_t* listed = marks + tid;
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        for (int q = g * quarter; q < min((g + 1) * quarter, batches); ++q) copy_batch(part, q);
-        copies_commit();
+    for (int j = 0; j < vectors; j += kBatch, listed += kRowThreads) {
+      uint4 next[kBatch];
+      src += kBatch * sb;
+      fetch(src, j + kBatch, next);
+      const uint32_t bits = *listed;
+      if (bits != 0u) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if ((bits >> (8 * u)) & 0xFFu) mask_elements<DT>(v[u], bits >> (8 * u));
       }
-      if (part.edge >= 0) edge = to_float<DT>(part.x[part.edge]);
+      add_mass<DT>(v, c, out);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) v[u] = next[u];
     }
-    bool waits = false;  // a cluster barrier that this thread has announced itself at and not yet waited for
-    for (int turn = 0; row < a.rows; turn ^= 1) {
-      int64_t next = row + clusters;
-      float next_edge = -kInf;
-      Part next_part = part;
-      auto look_ahead = [&] {
-        float next_w = weight(next);
-        next = next_live(next, &next_w);
-        if (next < a.rows) {
-          next_part = Part(row_x(next), a.vocab, cl.rank, SIZE);
-          if (next_part.edge >= 0) next_edge = to_float<DT>(next_part.x[next_part.edge]);
-        }
-      };
-      if (!GRAD) look_ahead();
-      const uint32_t* listed = marks + (GRAD ? 0 : turn * batches * kRowThreads) + tid;
-      if (turn == 0) barrier_sync<kReady, kListThreads>();
-      else barrier_sync<kReady + 1, kListThreads>();
-      const bool edge_out = part.edge >= 0 && !((edge_listed[GRAD ? 0 : turn] >> tid) & 1u);
-      RunningMass out(one_element<RowMass>(edge_out ? edge : -kInf), c);
-#pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        // copies still under way: this row's later quarters, and (loss alone) the next row's earlier ones
-        if (!GRAD || g == 0) copies_wait<3>();
-        else if (g == 1) copies_wait<2>();
-        else if (g == 2) copies_wait<1>();
-        else copies_wait<0>();
-#pragma unroll 1
-        for (int q = g * quarter; q < min((g + 1) * quarter, batches); ++q) {
-          const uint4* h = held + q * kBatch * kRowThreads + tid;
-          uint4 v[kBatch];
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) v[u] = h[u * kRowThreads];
-          const uint32_t bits = listed[q * kRowThreads];
-          if (bits != 0u) {
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-              if ((bits >> (8 * u)) & 0xFFu) mask_elements<DT>(v[u], bits >> (8 * u));
-          }
-          if ((q + 1) * kBatch > part.whole) {
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-              if (!part.more(q * kBatch + u))
-                v[u] = make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
-          }
-          add_mass<DT>(v, c, out);
-          if (!GRAD && next < a.rows) {
-            // the sums that the held vectors went into are formed before their place is given away
-            asm volatile("" ::"f"(out.at.s) : "memory");
-            copy_batch(next_part, q);
-          }
-        }
-        if (!GRAD) copies_commit();
-      }
-      const RowMass warp_out = merge_lanes(out.done(c), c);
-      if ((tid & 31) == 0) red[turn][tid >> 5] = warp_out;
-      if (turn == 0) barrier_arrive<kAdded, kListThreads>();
-      else barrier_arrive<kAdded + 1, kListThreads>();
-      if (SIZE > 1) {
-        if (waits) cl.wait();
-        cl.arrive();
-        waits = true;
-      }
-      if constexpr (GRAD) {
-        look_ahead();
-        Elem<DT>* d = row_d(row);
-        barrier_sync<kScales, kListThreads>();
-        const float f_c = factor[0], f_r = factor[1], f_a = factor[2];
-        if (part.edge >= 0) d[part.edge] = from_float<DT>(ex2(fmaf(edge, f_c, -f_r)) * f_a);
-        const Pair pc = Pair::both(f_c), pr = Pair::both(-f_r), pa = Pair::both(f_a);
-        char* dst = part.at(d);
-        auto put = [&](const uint4& v, char* o) {
-          Pair p[kPairsOf<DT>];
-          unpack_pairs<DT>(v, p);
-#pragma unroll
-          for (int e = 0; e < kPairsOf<DT>; ++e) p[e] = mul2(ex2_pair(fma2(p[e], pc, pr)), pa);
-          store_vector<DT>(o, p, a.vec);
-        };
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-#pragma unroll 1
-          for (int q = g * quarter; q < min((g + 1) * quarter, batches); ++q) {
-            const uint4* h = held + q * kBatch * kRowThreads + tid;
-            if ((q + 1) * kBatch <= part.whole) {
-#pragma unroll
-              for (int u = 0; u < kBatch; ++u) put(h[u * kRowThreads], dst + u * part.step_bytes());
-            } else {
-#pragma unroll 1
-              for (int u = 0; u < kBatch && part.more(q * kBatch + u); ++u)
-                put(h[u * kRowThreads], dst + u * part.step_bytes());
-            }
-            dst += kBatch * part.step_bytes();
-            if (next < a.rows) copy_batch(next_part, q);
-          }
-          copies_commit();
-        }
-        barrier_arrive<kWritten, kListThreads>();
-      }
-      row = next;
-      edge = next_edge;
-      part = next_part;
+    const RowMass warp_out = merge_lanes(out.done(c), c);
+    if ((tid & 31) == 0) red[tid >> 5] = warp_out;
+    barrier_arrive<kAdded, kListThreads>();
+    cl.started();
+    if (cl.size > 1) cl.arrive();
+    if constexpr (GRAD) {
+      part.load(0, v);
+      barrier_sync<kScales, kListThreads>();
+      const Pair f_c = Pair::both(factor[0]), f_r = Pair::both(-factor[1]), f_a = Pair::both(factor[2]);
+      part.map(v, d, a.vec, edge, [&](Pair f) { return mul2(ex2_pair(fma2(f, f_c, f_r)), f_a); });
+      barrier_arrive<kWritten, kListThreads>();
     }
-    if (SIZE > 1 && waits) cl.wait();
-  } else {  // -------------------------------------------------------------------- the list's warp
-    const int lane = tid & 31;
-    RowList<DT> l;
-    int marked[2][kSlots];  // the words of `marks` that were set (-1: none), by turn
+    if (cl.size > 1) cl.wait();
+    return;
+  }
+  // ---------------------------------------------------------------------------------- the list's warp
+  const int lane = tid & 31;
+  RowList<DT> l;
+  l.load(a, row, x, list_ids);
+  const int words = (part.vectors() + kBatch - 1) / kBatch * kRowThreads;
+  for (int i = lane; i < words; i += 32) marks[i] = 0u;
+  if (lane == 0) edge_listed = 0u;
+  __syncwarp();
+  unsigned mine = 0u;  // slots whose element is this block's
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) marked[0][i] = marked[1][i] = -1;
-    unsigned mine = 0u;  // slots whose element is this block's
-    auto fetch = [&](int64_t r) {
-      l.load(a, r, row_x(r), list_ids);
-      l.sums(a);
-      l.mass_in(a);
-    };
-    // Row r's marks for `turn`, and word that they are ready.
-    auto mark = [&](int64_t r, int turn) {
-      const Part part(row_x(r), a.vocab, cl.rank, SIZE);
-      const int set = GRAD ? 0 : turn;
-      uint32_t* listed = marks + set * batches * kRowThreads;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        const int old = set ? marked[1][i] : marked[0][i];
-        if (old >= 0) listed[old] = 0u;
-      }
-      if (lane == 0) edge_listed[set] = 0u;
-      __syncwarp();
-      mine = 0u;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        int owner, slot, word = -1;
-        if (l.id[i] >= 0 && part.owns(l.id[i], &owner, &slot)) {
-          mine |= 1u << i;
-          if (slot < 0) {
-            atomicOr(&edge_listed[set], 1u << owner);
-          } else {
-            word = (slot / kBatch) * kRowThreads + owner;
-            atomicOr(&listed[word], 1u << (slot % kBatch * 8 + (l.id[i] - part.sl.head) % kVecOf<DT>));
-          }
-        }
-        if (set) marked[1][i] = word;
-        else marked[0][i] = word;
-      }
-      if (turn == 0) barrier_arrive<kReady, kListThreads>();
-      else barrier_arrive<kReady + 1, kListThreads>();
-    };
-    if (row < a.rows) {
-      fetch(row);
-      mark(row, 0);
-    }
-    for (int turn = 0; row < a.rows; turn ^= 1) {
-      int64_t next = row + clusters;
-      float next_w = weight(next);
-      const RowList<DT> now = l;  // this row's; `l` is the next one's from its fetch on
-      const unsigned now_mine = mine;  // as `mark` left it
-      next = next_live(next, &next_w);
-      if (next < a.rows) {
-        fetch(next);
-        if (!GRAD) mark(next, turn ^ 1);
-      }
-      if (turn == 0) barrier_sync<kAdded, kListThreads>();
-      else barrier_sync<kAdded + 1, kListThreads>();
-      RowMass out = merge_lanes(red[turn][lane % kRowWarps], c, kRowWarps);
-      if (SIZE > 1) {
-        if (lane < SIZE) cl.at(parts[turn], lane)[cl.rank] = out;
-        cl.arrive();
-        cl.wait();
-        out = merge_lanes(parts[turn][lane % SIZE], c, SIZE);
-      }
-      RowMass all = now.in, o = out;
-      if (o.m > all.m) all.move(o.m, c);
-      else if (all.m > o.m) o.move(all.m, c);
-      all.s += o.s;
-      const bool empty = all.s == 0.0f;
-      // all unlisted tokens masked, by -inf or by values so low that no p_t is left
-      const bool no_tail = out.s == 0.0f || (out.m - all.m) * c <= kFloor;
-      const float ws = now.bad ? nan_f() : w * a.scale;
-      const float b = now.q_sum + now.q_tail;
-      if constexpr (GRAD) {
-        // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
-        const float p_t = no_tail ? 0.0f : ex2((out.m - all.m) * c) * (out.s / all.s);
-        const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - now.q_tail) / out.s;
-        const ExpRef ref(out.m, c);
-        if (lane == 0) {
-          factor[0] = ref.c;
-          factor[1] = ref.r;
-          factor[2] = A * ref.k;
-        }
-        barrier_arrive<kScales, kListThreads>();
-        if (next < a.rows) mark(next, turn ^ 1);
-      }
-      if (cl.rank == 0) {
-        const float ln_s = logf(all.s);
-        const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
-        float loss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-          if (now.id[i] >= 0 && now.q[i] != 0.0f) {
-            const float lp = empty ? -kInf : fmaf(now.x[i] - all.m, a.scale, -ln_s);
-            loss += now.q[i] * (now.lq[i] - lp);
-          }
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, off);
-        if (lane == 0) {
-          if (now.q_tail > 0.0f && !no_tail) loss += now.q_tail * (logf(now.q_tail) - tail);
-          if (now.bad || !(all.s == all.s) || !(now.q_sum == now.q_sum)) loss = nan_f();
-          if (a.loss) a.loss[row] = w * loss;
-          if (a.norm) a.norm[row] = make_float2(all.m, all.s);
-          if (a.tail) a.tail[row] = tail;
-        }
-      }
-      if constexpr (GRAD) {
-        const ExpRef top(all.m, c);
-        const float over = top.k / all.s;
-        Elem<DT>* d = row_d(row);
-        barrier_sync<kWritten, kListThreads>();
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-          if ((now_mine >> i) & 1u)
-            d[now.id[i]] = from_float<DT>(empty ? 0.0f : ws * fmaf(top.exp(now.x[i]) * over, b, -now.q[i]));
-      }
-      row = next;
-      w = next_w;
+  for (int i = 0; i < kSlots; ++i) {
+    int owner, slot;
+    if (l.id[i] >= 0 && part.owns(l.id[i], &owner, &slot)) {
+      mine |= 1u << i;
+      if (slot < 0) atomicOr(&edge_listed, 1u << owner);
+      else atomicOr(&marks[(slot / kBatch) * kRowThreads + owner],
+                    1u << (slot % kBatch * 8 + (l.id[i] - part.sl.head) % kVecOf<DT>));
     }
   }
-  // Late: the next kernel's blocks would else take the places that this wave leaves one by one, and its clusters,
-  // of which all have to be resident for an even share of the rows, would not all find room.
-  pdl_trigger();
+  barrier_arrive<kReady, kListThreads>();
+  l.sums(a);
+  l.mass_in(a);
+  cl.started();
+  barrier_sync<kAdded, kListThreads>();
+  RowMass out = merge_lanes(red[lane % kRowWarps], c, kRowWarps);
+  if (cl.size > 1) {
+    if (lane < cl.size) cl.at(parts, lane)[cl.rank] = out;
+    cl.arrive();
+    cl.wait();
+    out = merge_lanes(parts[lane % cl.size], c, static_cast<int>(cl.size));
+  }
+  RowMass all = l.in, o = out;
+  if (o.m > all.m) all.move(o.m, c);
+  else if (all.m > o.m) o.move(all.m, c);
+  all.s += o.s;
+  const bool empty = all.s == 0.0f;
+  // all unlisted tokens masked, by -inf or by values so low that no p_t is left
+  const bool no_tail = out.s == 0.0f || (out.m - all.m) * c <= kFloor;
+  const float ws = l.bad ? nan_f() : w * a.scale;
+  const float b = l.q_sum + l.q_tail;
+  if constexpr (GRAD) {
+    // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
+    const float p_t = no_tail ? 0.0f : ex2((out.m - all.m) * c) * (out.s / all.s);
+    const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - l.q_tail) / out.s;
+    const ExpRef ref(out.m, c);
+    if (lane == 0) {
+      factor[0] = ref.c;
+      factor[1] = ref.r;
+      factor[2] = A * ref.k;
+    }
+    barrier_arrive<kScales, kListThreads>();
+  }
+  if (cl.rank == 0) {
+    const float ln_s = logf(all.s);
+    const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
+    float loss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      if (l.id[i] >= 0 && l.q[i] != 0.0f) {
+        const float lp = empty ? -kInf : fmaf(l.x[i] - all.m, a.scale, -ln_s);
+        loss += l.q[i] * (l.lq[i] - lp);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, off);
+    if (lane == 0) {
+      if (l.q_tail > 0.0f && !no_tail) loss += l.q_tail * (logf(l.q_tail) - tail);
+      if (l.bad || !(all.s == all.s) || !(l.q_sum == l.q_sum)) loss = nan_f();
+      if (a.loss) a.loss[row] = w * loss;
+      if (a.norm) a.norm[row] = make_float2(all.m, all.s);
+      if (a.tail) a.tail[row] = tail;
+    }
+  }
+  if constexpr (GRAD) {
+    const ExpRef top(all.m, c);
+    const float over = top.k / all.s;
+    barrier_sync<kWritten, kListThreads>();
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if ((mine >> i) & 1u)
+        d[l.id[i]] = from_float<DT>(empty ? 0.0f : ws * fmaf(top.exp(l.x[i]) * over, b, -l.q[i]));
+  }
 }
 
 // ------------------------------------------------------------------ the gradient from saved normalisers
@@ -591,76 +450,6 @@ __global__ void __launch_bounds__(kListThreads, 3) distill_grad_kernel(const __g
     if (l.id[i] >= 0) d[l.id[i]] = from_float<DT>(g[i]);
 }
 
-template <bool GRAD, int DT>
-auto distill_of_size(int cluster) {
-  return cluster == 1   ? distill_kernel<DT, GRAD, 1>
-         : cluster == 2 ? distill_kernel<DT, GRAD, 2>
-         : cluster == 4 ? distill_kernel<DT, GRAD, 4>
-                        : distill_kernel<DT, GRAD, 8>;
-}
-template <bool GRAD>
-auto distill_for(int32_t dtype, int cluster) {
-  return dtype == SS_BF16   ? distill_of_size<GRAD, SS_BF16>(cluster)
-         : dtype == SS_FP16 ? distill_of_size<GRAD, SS_FP16>(cluster)
-                            : distill_of_size<GRAD, SS_FP32>(cluster);
-}
-
-// Clusters of `cluster` blocks of `fn` that the GPU holds at once with `smem` bytes of dynamic shared memory, which
-// are allowed to it here (kept per device, kernel and size, without allocation).
-ss_status resident_clusters(const void* fn, size_t smem, int cluster, int* out) {
-  struct Entry {
-    int dev, cluster;
-    const void* fn;
-    size_t smem;
-    int clusters;
-  };
-  static std::mutex mu;
-  static Entry cache[64] = {};
-  static int used = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e);
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < std::min(used, 64); ++i) {
-    const Entry& c = cache[i];
-    if (c.dev == dev && c.fn == fn && c.smem == smem && c.cluster == cluster) {
-      *out = c.clusters;
-      return SS_OK;
-    }
-  }
-  // the limit only grows: another thread may be about to launch with a larger size
-  cudaFuncAttributes now;
-  e = cudaFuncGetAttributes(&now, fn);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (static_cast<size_t>(now.maxDynamicSharedSizeBytes) < smem) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  int n = 0;
-  if (cluster == 1) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kListThreads, smem);
-    n *= sm_count();
-  } else {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(kListThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
-  }
-  if (e != cudaSuccess) return cuda_fail(e);
-  n = std::max(n, 1);
-  cache[used++ % 64] = {dev, cluster, fn, smem, n};
-  *out = n;
-  return SS_OK;
-}
-
 ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* norm_in, const float* tail_in,
                        const float* d_loss, float* loss, float* norm, float* tail, void* d_logits, int64_t d_ld,
                        void* stream) {
@@ -697,11 +486,11 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
   const int split = split_for(nvec);
-  DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
+  const DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
                          reinterpret_cast<const float2*>(norm_in), tail_in, loss, reinterpret_cast<float2*>(norm),
                          tail, d_logits, rows, x->vocab, x->ld, d_ld, x->scale * kLog2e, x->scale, t->scale, t->k,
                          t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld), d_logits == x->data,
-                         static_cast<uint32_t>(split), 0};
+                         static_cast<uint32_t>(split)};
   if (saved) {
     auto* fn = x->dtype == SS_BF16
                    ? distill_grad_kernel<SS_BF16>
@@ -709,17 +498,18 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
     if (rows * split > INT32_MAX) return SS_ERR_OVERFLOW;
     return launch(fn, static_cast<unsigned>(rows * split), a, stream, kListThreads);
   }
-  // a part of at most kPartVectors vectors a thread, or what 8 blocks leave
+  const auto pick = [&](auto grad) {
+    constexpr bool kGrad = decltype(grad)::value;
+    return x->dtype == SS_BF16 ? distill_kernel<SS_BF16, kGrad>
+                               : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16, kGrad> : distill_kernel<SS_FP32, kGrad>);
+  };
+  auto* fn = d_logits ? pick(std::true_type()) : pick(std::false_type());
   const auto vectors = [&](int n) { return (nvec + n * kRowThreads - 1) / (n * kRowThreads); };
   int cluster = 1;
   while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
-  auto* fn = d_logits ? distill_for<true>(x->dtype, cluster) : distill_for<false>(x->dtype, cluster);
-  a.batches = static_cast<int>((vectors(cluster) + kBatch - 1) / kBatch);
-  const size_t smem = static_cast<size_t>(a.batches) * kRowThreads * (kBatch * sizeof(uint4) + (d_logits ? 1 : 2) * sizeof(uint32_t));
-  int clusters = 0;
-  st = resident_clusters(reinterpret_cast<const void*>(fn), smem, cluster, &clusters);
-  if (st != SS_OK) return st;
-  return launch_rows(fn, std::min<int64_t>(rows, clusters), cluster, kListThreads, smem, a, stream);
+  const size_t smem = static_cast<size_t>((vectors(cluster) + kBatch - 1) / kBatch) * kRowThreads * sizeof(uint32_t);
+  if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
+  return launch_rows(fn, rows, cluster, kListThreads, smem, a, stream);
 }
 
 }  // namespace

@@ -148,16 +148,11 @@ __device__ __forceinline__ float vec_max(const uint4& w) {
   }
 }
 
-// 16 bytes from global to shared memory, asynchronously; the issuing thread sees them after copies_wait.
-__device__ __forceinline__ void copy_async16(void* shared, const void* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
-               "l"(global)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+// 16 bytes of a row: AGAIN when a later pass reads them again (from L2), else read once.
+template <bool AGAIN>
+__device__ __forceinline__ uint4 load_row(const void* p) {
+  if constexpr (AGAIN) return __ldcg(static_cast<const uint4*>(p));
+  else return __ldcs(static_cast<const uint4*>(p));
 }
 
 __device__ __forceinline__ float ex2(float x) {
