@@ -55,11 +55,11 @@ struct RowList {
   float q_sum, q_tail;   // Q and q_t
   bool bad;              // an id past the vocabulary
 
-  // ids_shared: SS_MAX_TOP / 4 int4 of shared memory, this warp's own.
+  // The ids and the teacher's values, and the logits on their way. ids_shared: SS_MAX_TOP / 4 int4 of shared memory,
+  // this warp's own.
   __device__ __forceinline__ void load(const DistillArgs& a, int64_t row, const Elem<DT>* xr, int4* ids_shared) {
     const int lane = threadIdx.x & 31;
     bool past = false;
-    __syncwarp();
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       id[i] = -1;
@@ -79,8 +79,12 @@ struct RowList {
     for (int i = 0; i < kSlots; ++i)
       if (id[i] >= 0) x[i] = to_float<DT>(xr[id[i]]);
     bad = __any_sync(0xFFFFFFFFu, past);
+  }
+
+  // Drops the slots whose id an earlier slot has: of its own 32, or of those before them.
+  __device__ __forceinline__ void drop_repeated(const DistillArgs& a, const int4* ids_shared) {
+    const int lane = threadIdx.x & 31;
     __syncwarp();
-    // an id that an earlier slot has: of its own 32, or of those before them
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       if (32 * i < a.k) {
@@ -156,6 +160,7 @@ struct RowList {
 //
 // Eight warps go through the elements and do as little else as can be; the ninth
 // has the row's list, the exchange between the blocks and the row's loss:
+//   clear   row -> list    the marks are zero
 //   ready   list -> row    the listed tokens are marked
 //   added   row -> list    the warps' sums are in `red`
 //   scales  list -> row    the gradient's factors are in `factor`
@@ -164,7 +169,7 @@ struct RowList {
 // which they are), so the unlisted mass is a sum of its own terms and not a
 // difference: log p_t keeps its digits however little is left.
 
-enum Barrier : int { kReady = 1, kAdded = 2, kScales = 3, kWritten = 4 };
+enum Barrier : int { kReady = 1, kAdded = 2, kScales = 3, kWritten = 4, kClear = 5 };
 
 // Marks the elements of packed vector w whose bits are set in `bits` as masked.
 template <int DT>
@@ -207,7 +212,7 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
 
 // Dynamic shared memory: a word of listed bits for each batch of vectors, by thread.
 template <int DT, bool GRAD>
-__global__ void __launch_bounds__(kListThreads, 3) distill_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(const __grid_constant__ DistillArgs a) {
   extern __shared__ uint32_t marks[];
   __shared__ RowMass red[kRowWarps];
   __shared__ RowMass parts[kMaxCluster];
@@ -236,6 +241,9 @@ __global__ void __launch_bounds__(kListThreads, 3) distill_kernel(const __grid_c
   const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
   if (tid < kRowThreads) {  // ---------------------------------------------------- the row's warps
     const int vectors = part.vectors();
+    for (int j = 0; j < vectors; j += kBatch) marks[j / kBatch * kRowThreads + tid] = 0u;
+    if (tid == 0) edge_listed = 0u;
+    barrier_arrive<kClear, kListThreads>();
     const int64_t sb = part.step_bytes();
     const char* src = part.at();
     auto fetch = [&](const char* p, int j, uint4 (&v)[kBatch]) {
@@ -291,10 +299,7 @@ __global__ void __launch_bounds__(kListThreads, 3) distill_kernel(const __grid_c
   const int lane = tid & 31;
   RowList<DT> l;
   l.load(a, row, x, list_ids);
-  const int words = (part.vectors() + kBatch - 1) / kBatch * kRowThreads;
-  for (int i = lane; i < words; i += 32) marks[i] = 0u;
-  if (lane == 0) edge_listed = 0u;
-  __syncwarp();
+  barrier_sync<kClear, kListThreads>();
   unsigned mine = 0u;  // slots whose element is this block's
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
@@ -307,6 +312,10 @@ __global__ void __launch_bounds__(kListThreads, 3) distill_kernel(const __grid_c
     }
   }
   barrier_arrive<kReady, kListThreads>();
+  l.drop_repeated(a, list_ids);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (l.id[i] < 0) mine &= ~(1u << i);
   l.sums(a);
   l.mass_in(a);
   cl.started();
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kListThreads, 3) distill_kernel(const __grid_c
 // One pass: blocks share a row as above, but nothing is exchanged between them.
 // A ninth warp has the list while the first vectors are on their way.
 template <int DT>
-__global__ void __launch_bounds__(kListThreads, 3) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ int4 list_ids[SS_MAX_TOP / 4];
   __shared__ float factor[3];
   pdl_wait();
@@ -405,6 +414,7 @@ __global__ void __launch_bounds__(kListThreads, 3) distill_grad_kernel(const __g
   }
   RowList<DT> l;
   l.load(a, row, x, list_ids);
+  l.drop_repeated(a, list_ids);
   l.sums(a);
   const float ws = l.bad ? nan_f() : wt * dl * a.scale;
   const float b = l.q_sum + l.q_tail;
@@ -485,7 +495,7 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   ranges.add(d_loss, rows * 4, false);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
-  const int split = split_for(nvec);
+  const int split = split_for(nvec, 32);
   const DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
                          reinterpret_cast<const float2*>(norm_in), tail_in, loss, reinterpret_cast<float2*>(norm),
                          tail, d_logits, rows, x->vocab, x->ld, d_ld, x->scale * kLog2e, x->scale, t->scale, t->k,

@@ -589,14 +589,10 @@ inline ss_status check_grad_out(const ss_logits* x, int64_t x_bytes, const void*
   return SS_OK;
 }
 
-// Blocks that share a row where each element is read and written once and nothing is exchanged: parts of
-// kMapVectors vectors a thread.
-#ifndef SS_MAP_VECTORS
-#define SS_MAP_VECTORS 16
-#endif
-constexpr int kMapVectors = SS_MAP_VECTORS;
-inline int split_for(int64_t nvec) {
-  return static_cast<int>(std::max<int64_t>(1, (nvec + kMapVectors * kRowThreads - 1) / (kMapVectors * kRowThreads)));
+// Blocks that share a row where nothing is exchanged between them: parts of `vectors` vectors a thread.
+inline int split_for(int64_t nvec, int vectors) {
+  const int64_t part = static_cast<int64_t>(vectors) * kRowThreads;
+  return static_cast<int>(std::max<int64_t>(1, (nvec + part - 1) / part));
 }
 
 // Launches `clusters` clusters of `cluster` blocks (a plain launch for 1).

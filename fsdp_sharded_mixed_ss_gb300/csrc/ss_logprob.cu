@@ -520,7 +520,7 @@ ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idty
   ranges.add(up->d_lse, rows * 4, false);
   ranges.add(up->d_top_logprob, rows * top_k * 4, false);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
-  const int split = split_for(x->vocab / (x->dtype == SS_FP32 ? 4 : 8));
+  const int split = split_for(x->vocab / (x->dtype == SS_FP32 ? 4 : 8), 16);
   if (rows * split > INT32_MAX) return SS_ERR_OVERFLOW;
   const LogprobGradArgs a = {x->data, tokens, top_id, reinterpret_cast<const float2*>(norm), entropy, up->d_logprob,
                              up->d_entropy, up->d_lse, up->d_top_logprob, d_logits, rows, x->vocab, x->ld, d_ld,
