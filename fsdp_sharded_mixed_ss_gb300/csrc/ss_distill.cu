@@ -187,9 +187,6 @@ __device__ __forceinline__ void mask_elements(uint4& w, uint32_t bits) {
   }
 }
 
-template <int DT>
-constexpr uint32_t kMaskedWord = DT == SS_FP32 ? 0xFF800000u : (DT == SS_BF16 ? 0xFF80FF80u : 0xFC00FC00u);
-
 using RunningMass = Running<RowMass, 40>;
 
 // A batch of vectors into the running sum.

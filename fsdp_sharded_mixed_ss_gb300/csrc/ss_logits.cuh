@@ -42,6 +42,10 @@ using Elem = typename ElemOf<DT>::T;
 template <int DT>
 constexpr int kVecOf = ElemOf<DT>::kVec;
 
+// Packed masked elements (-inf).
+template <int DT>
+constexpr uint32_t kMaskedWord = DT == SS_FP32 ? 0xFF800000u : (DT == SS_BF16 ? 0xFF80FF80u : 0xFC00FC00u);
+
 template <int DT>
 __device__ __forceinline__ float to_float(Elem<DT> e) {
   if constexpr (DT == SS_FP32) return e;

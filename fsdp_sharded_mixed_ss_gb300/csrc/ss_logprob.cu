@@ -36,6 +36,7 @@ struct LogprobArgs {
 
 constexpr int kUnits = 16;    // maxima kept per thread
 constexpr int kCand = 2048;   // candidates of a row, shared out over the cluster's blocks
+constexpr int kFlagged = 1024;  // units of a block that are read again
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
 
 struct TopShared {
@@ -45,7 +46,8 @@ struct TopShared {
   int count[kMaxCluster];        // candidates of every block
   int sums[2][kMaxCluster];      // counts being added up over the cluster
   int warp_sums[kRowThreads / 32];
-  int n;
+  uint16_t flagged[kFlagged];
+  int n, n_flagged;
 };
 struct NoTops {};
 
@@ -183,18 +185,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   }
   if (full * kBatch < vectors) {
     uint4 w[kBatch];
-    float m = -kInf;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if (part.more(full * kBatch + u)) w[u] = __ldg(reinterpret_cast<const uint4*>(src + u * sb));
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (part.more(full * kBatch + u)) {
-        const uint4 one[1] = {w[u]};
-        m = fmaxf(m, add_vectors<DT>(one, a.c, run));
-      }
-    }
-    end_batch(m);
+      w[u] = part.more(full * kBatch + u)
+                 ? __ldg(reinterpret_cast<const uint4*>(src + u * sb))
+                 : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+    end_batch(add_vectors<DT>(w, a.c, run));
   }
   if constexpr (TOPS) {
     if (in_unit > 0) tops.unit[units++][tid] = unit;
@@ -213,7 +209,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
       const unsigned at = cl.rank * (kRowThreads / cl.size) + tid / cl.size;
       for (unsigned r = 0; r < cl.size; ++r) cl.at(tops.keys, r)[at] = key;
     }
-    if (tid == 0) tops.n = 0;
+    if (tid == 0) tops.n = tops.n_flagged = 0;
   }
   if (TOPS || cl.size > 1) cl.sync();
   if (cl.size > 1) {
@@ -252,9 +248,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     // the threshold: bit by bit, the largest that k keys reach; a little less is as good
     constexpr int kLowBit = DT == SS_BF16 ? 16 : (DT == SS_FP16 ? 13 : 0);
     const uint32_t my_key = tops.keys[tid];
+    const uint32_t top_key = order_key(acc.m);
     uint32_t tau = 0;
     for (int bit = 31; bit >= kLowBit; --bit) {
       const uint32_t t = tau | (1u << bit);
+      if (t > top_key) continue;
       const int c = __syncthreads_count(my_key >= t);
       if (c >= k) {
         tau = t;
@@ -272,12 +270,51 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
       if (n < room) out[n] = order_pair(f, id);
     };
     for (int u = 0; u < units; ++u) {
-      if (wanted(tops.unit[u][tid]))
-        part.each(u * unit_batches * kBatch, min(vectors, (u + 1) * unit_batches * kBatch), [&](float f, int id) {
-          if (wanted(f)) add(f, id);
-        });
+      if (wanted(tops.unit[u][tid])) {
+        const int f = atomicAdd(&tops.n_flagged, 1);
+        if (f < kFlagged) tops.flagged[f] = static_cast<uint16_t>(u * kRowThreads + tid);
+      }
     }
     if (part.edge >= 0 && wanted(edge)) add(edge, part.edge);
+    __syncthreads();
+    // a warp reads a flagged unit's elements again, one a lane, four units at a time
+    constexpr int V = kVecOf<DT>;
+    const int flagged = min(tops.n_flagged, kFlagged), lane = tid & 31;
+    const int unit_elems = unit_batches * kBatch * V;
+#pragma unroll 1
+    for (int f0 = (tid >> 5) * 4; f0 < flagged; f0 += kRowWarps * 4) {
+#pragma unroll 1
+      for (int e = lane; e < unit_elems; e += 32) {
+        float val[4];
+        int id[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          id[q] = -1;
+          if (f0 + q < flagged) {
+            const int unit_at = tops.flagged[f0 + q];
+            const int64_t vec = static_cast<int64_t>((unit_at / kRowThreads) * unit_batches * kBatch + e / V) * part.step() +
+                                part.rank * kRowThreads + unit_at % kRowThreads;
+            if (vec < part.sl.nvec) {
+              id[q] = part.sl.head + static_cast<int>(vec) * V + e % V;
+              val[q] = to_float<DT>(part.x[id[q]]);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool hit = id[q] >= 0 && wanted(val[q]);
+          const unsigned hits = __ballot_sync(__activemask(), hit);
+          if (hit) {
+            const int leader = __ffs(hits) - 1;
+            int at = 0;
+            if (lane == leader) at = atomicAdd(&tops.n, __popc(hits));
+            at = __shfl_sync(hits, at, leader) + __popc(hits & ((1u << lane) - 1u));
+            if (at < room) out[at] = order_pair(val[q], id[q]);
+          }
+        }
+      }
+    }
+    if (tid == 0 && tops.n_flagged > kFlagged) tops.n = room + 1;
     __syncthreads();
     if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = tops.n;
     cl.sync();
