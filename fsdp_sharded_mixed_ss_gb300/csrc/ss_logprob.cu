@@ -17,39 +17,34 @@ struct LogprobArgs {
   int64_t rows, vocab, ld;
   float c, scale;
   int32_t top_k;
-  bool wide;  // int64 ids
+  bool wide;         // int64 ids
+  int32_t resident;  // rows in flight at a time
 };
 
 // ------------------------------------------------------------------ forward
 //
-// A row belongs to a cluster of 1 to 8 blocks (RowPart says which elements are
-// whose). One pass gives the row's maximum, sum and entropy's sum. The alternatives come
-// from the same pass: the maximum of every unit (4 vectors of a thread, more in
-// rows longer than 16 units a thread) stays in shared memory, and every thread's
-// maximum is a key. Some threshold that k of the 256 keys reach is a bound that
-// at least k elements of the row reach, and few more: for k of 256 keys drawn at
-// random -256 ln(1 - k / 256) elements, 21 for k = 20 and 177 for k = 128. Only
-// units whose maximum reaches it are read again (from L2), their elements at or
-// above it are the candidates, and each candidate's rank is the number of
-// candidates above it. Where the candidates pass the buffer (ties), the exact
-// k-th pair is searched for by counting.
+// One pass over the row gives its maximum, sum and entropy's sum. The
+// alternatives come from the same pass: the maximum of every unit (4 vectors of
+// a thread, more in rows longer than 16 units a thread) stays in shared memory,
+// and the 256 threads' maxima are keys. Some threshold that k of the keys reach
+// is a bound that at least k elements of the row reach, and few more: for k of
+// 256 keys drawn at random -256 ln(1 - k / 256) elements, 21 for k = 20 and 177
+// for k = 128. Only units whose maximum reaches it are read again, their elements
+// at or above it are the candidates, and a candidate's place is the number of
+// candidates above it. Where the candidates pass the buffer (ties), the part's
+// elements go through the buffer once more, which is cut to the k best whenever
+// it is full.
+//
+// The selection is a chain of small dependent reads beside a loaded memory system,
+// as long as a third of a 128256-token row's stream. A block that begins it asks
+// for the start of the row that will take its place on the SM, so that HBM does
+// not idle meanwhile.
 
-constexpr int kUnits = 16;    // maxima kept per thread
-constexpr int kCand = 2048;   // candidates of a row, shared out over the cluster's blocks
-constexpr int kFlagged = 1024;  // units of a block that are read again
+constexpr int kAheadBytes = 32768;  // of the row that comes after (0, 32, 64, 128 KB measured: 129.5, 126.4, 127.9, 132.9 us)
+constexpr int kUnits = 16;      // maxima kept per thread
+constexpr int kFlagged = 1024;  // units that are read again
+constexpr int kUnitPairs = kUnits * kRowThreads / 2;  // the units' memory as a buffer of pairs, once they are done with
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
-
-struct TopShared {
-  float unit[kUnits][kRowThreads];
-  uint64_t cand[kCand];          // block 0's is used
-  uint32_t keys[kRowThreads];
-  int count[kMaxCluster];        // candidates of every block
-  int sums[2][kMaxCluster];      // counts being added up over the cluster
-  int warp_sums[kRowThreads / 32];
-  uint16_t flagged[kFlagged];
-  int n, n_flagged;
-};
-struct NoTops {};
 
 using RunningSum = Running<RowSum, 8>;
 
@@ -94,62 +89,302 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, Runni
   return m;
 }
 
-// Sum of v over all threads of the cluster, the same in each (all call it; `it` counts the calls).
-__device__ __forceinline__ int cluster_count(const Cluster& cl, TopShared& ts, int v, int it) {
-  v = __reduce_add_sync(0xFFFFFFFFu, v);
-  if ((threadIdx.x & 31) == 0) ts.warp_sums[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int* slots = ts.sums[it & 1];
-  if (threadIdx.x < cl.size) {
-    int b = 0;
-    for (int w = 0; w < kRowThreads / 32; ++w) b += ts.warp_sums[w];
-    cl.at(slots, threadIdx.x)[cl.rank] = b;
-  }
-  cl.sync();
-  int all = 0;
-  for (unsigned r = 0; r < cl.size; ++r) all += slots[r];
-  return all;
-}
-
-// The exact k-th largest pair as (key, id): elements above `key`, and those equal to it with ids up to `id`, are
-// the k. At least k elements reach the key `lo`; none is above `top`.
-template <int DT>
-__device__ __noinline__ uint2 search_pair(const Cluster& cl, TopShared& ts, const RowPart<DT>& part, int vectors,
-                                          uint32_t lo, uint32_t top, int k) {
-  const int vocab = static_cast<int>(part.sl.n);
-  int it = 0;
-  auto count = [&](auto pred) {
-    int c = 0;
-    part.each(0, vectors, [&](float f, int id) { c += pred(order_key(f), id) ? 1 : 0; });
-    if (part.edge >= 0) c += pred(order_key(to_float<DT>(part.x[part.edge])), part.edge) ? 1 : 0;
-    return cluster_count(cl, ts, c, it++);
-  };
-  uint32_t hi = top;  // count(key > hi) = above < k, count(key >= lo) >= k
-  int above = 0;
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo + 1) / 2;
-    const int c = count([&](uint32_t key, int) { return key >= mid; });
-    if (c >= k) {
-      lo = mid;
+// The pass over a thread's vectors; `unit` (with TOPS) receives its units' maxima. `units`: how many, `unit_batches`:
+// of how many batches each (both the same for all threads).
+template <int DT, bool TOPS>
+__device__ __forceinline__ RowSum stream_row(const RowPart<DT>& part, float c, float edge, float (*unit)[kRowThreads],
+                                             float* thread_max) {
+  const int full = part.whole / kBatch;  // batches that every thread has whole
+  const int batches = (part.vectors() + kBatch - 1) / kBatch;
+  const int unit_batches = (batches + kUnits - 1) / kUnits;
+  const int64_t sb = part.step_bytes();
+  const char* src = part.at();
+  RunningSum run(one_element<RowSum>(edge), c);
+  float best = -kInf;
+  int in_unit = 0, units = 0;
+  for (int b = 0; b < batches; ++b, src += kBatch * sb) {
+    uint4 w[kBatch];
+    if (b < full) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) w[u] = __ldg(reinterpret_cast<const uint4*>(src + u * sb));
     } else {
-      hi = mid - 1;
-      above = c;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        w[u] = part.more(b * kBatch + u)
+                   ? __ldg(reinterpret_cast<const uint4*>(src + u * sb))
+                   : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+    }
+    const float m = add_vectors<DT>(w, c, run);
+    if constexpr (TOPS) {
+      best = fmaxf(best, m);
+      if (++in_unit == unit_batches || b + 1 == batches) {
+        unit[units++][threadIdx.x] = best;
+        in_unit = 0;
+        best = -kInf;
+      }
     }
   }
-  const int need = k - above;
-  int a = 0, b = vocab - 1;  // the smallest id bound that gives `need` elements equal to the key
-  while (a < b) {
-    const int mid = a + (b - a) / 2;
-    const int c = count([&](uint32_t key, int id) { return key == lo && id <= mid; });
-    if (c >= need) b = mid;
-    else a = mid + 1;
+  *thread_max = run.top;
+  return run.done(c);
+}
+
+constexpr int kCand = 2048;
+struct TopShared {
+  float unit[kUnits][kRowThreads];
+  uint64_t cand[kCand];  // block 0's is used, shared out over the cluster's blocks
+  uint64_t best[SS_MAX_TOP];
+  uint32_t keys[kRowThreads];
+  uint16_t flagged[kFlagged];
+  int count[kMaxCluster];  // candidates of every block
+  int warp_sums[kRowWarps];
+  uint32_t tau;
+  int n, n_flagged;
+};
+struct NoTops {};
+
+// The largest threshold, to the type's digits, that k of the 256 keys reach; a little less is as good. All lanes of
+// one warp call it.
+template <int DT>
+__device__ __forceinline__ uint32_t find_threshold(const uint32_t* key, uint32_t top_key, int k) {
+  constexpr int kLowBit = DT == SS_BF16 ? 16 : (DT == SS_FP16 ? 13 : 0);
+  uint32_t keys[kRowWarps];
+#pragma unroll
+  for (int i = 0; i < kRowWarps; ++i) keys[i] = key[(threadIdx.x & 31) + 32 * i];
+  uint32_t t = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= kLowBit; --bit) {
+    const uint32_t next = t | (1u << bit);
+    if (next > top_key) continue;
+    int c[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kRowWarps; ++i) c[i & 1] += keys[i] >= next ? 1 : 0;
+    const int all = __reduce_add_sync(0xFFFFFFFFu, c[0] + c[1]);
+    if (all >= k) {
+      t = next;
+      if (all <= k + k / 8) break;
+    }
   }
-  return make_uint2(lo, static_cast<uint32_t>(a));
+  return t;
+}
+
+// What a candidate is: at or above the threshold, or, where fewer than k threads hold unmasked tokens, unmasked.
+struct Wanted {
+  float bound;
+  bool few;
+
+  __device__ __forceinline__ explicit Wanted(uint32_t tau) : few(tau <= kMaskedKey) {
+    bound = few ? -kInf : key_value(tau);
+  }
+  __device__ __forceinline__ bool operator()(float f) const { return few ? f > bound : f >= bound; }
+};
+
+// The part's candidates into out[0, room); returns their number, to all threads (above `room`: they did not fit).
+// s.n and s.n_flagged are zero before; s is the caller's again when this returns.
+template <int DT>
+__device__ __forceinline__ int collect(const RowPart<DT>& part, const Wanted& wanted, TopShared& s, uint64_t* out,
+                                       int room) {
+  constexpr int V = kVecOf<DT>;
+  const int tt = threadIdx.x, lane = tt & 31;
+  const int batches = (part.vectors() + kBatch - 1) / kBatch;
+  const int unit_batches = (batches + kUnits - 1) / kUnits;
+  const int units = unit_batches > 0 ? (batches + unit_batches - 1) / unit_batches : 0;
+  unsigned mask = 0u;  // this thread's flagged units
+  for (int u = 0; u < units; ++u) mask |= wanted(s.unit[u][tt]) ? 1u << u : 0u;
+  int before = __popc(mask);
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, before, off);
+    if (lane >= off) before += o;
+  }
+  int base = 0;
+  if (lane == 31 && before > 0) base = atomicAdd(&s.n_flagged, before);
+  base = __shfl_sync(0xFFFFFFFFu, base, 31) + before - __popc(mask);
+  for (; mask != 0u; mask &= mask - 1u, ++base)
+    if (base < kFlagged) s.flagged[base] = static_cast<uint16_t>((__ffs(mask) - 1) * kRowThreads + tt);
+  if (part.rank == 0 && tt < 16) {  // the elements outside the vectors
+    const int id = tt < 8 ? (tt < part.sl.head ? tt : -1)
+                          : (tt - 8 < part.sl.n - part.sl.tail() ? part.sl.tail() + tt - 8 : -1);
+    if (id >= 0) {
+      const float f = to_float<DT>(part.x[id]);
+      if (wanted(f)) {
+        const int at = atomicAdd(&s.n, 1);
+        if (at < room) out[at] = order_pair(f, id);
+      }
+    }
+  }
+  __syncthreads();
+  // one vector of a flagged unit a thread, four in flight
+  constexpr int kAgain = 4;
+  const int per_unit = unit_batches * kBatch;
+  const int items = min(s.n_flagged, kFlagged) * per_unit;
+#pragma unroll 1
+  for (int i0 = tt; i0 < items; i0 += kAgain * kRowThreads) {
+    uint4 w[kAgain];
+    int at[kAgain];
+#pragma unroll
+    for (int q = 0; q < kAgain; ++q) {
+      const int i = i0 + q * kRowThreads;
+      at[q] = -1;
+      if (i < items) {
+        const int f = s.flagged[i / per_unit];
+        const int64_t vec = static_cast<int64_t>((f / kRowThreads) * per_unit + i % per_unit) * part.step() +
+                            part.rank * kRowThreads + f % kRowThreads;
+        if (vec < part.sl.nvec) {
+          at[q] = static_cast<int>(vec);
+          w[q] = __ldg(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kAgain; ++q) {
+      if (at[q] < 0) continue;
+      float e[V];
+      unpack<DT>(w[q], e);
+      unsigned hits = 0u;
+#pragma unroll
+      for (int j = 0; j < V; ++j) hits |= wanted(e[j]) ? 1u << j : 0u;
+      if (hits != 0u) {
+        int n = atomicAdd(&s.n, __popc(hits));
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if ((hits >> j) & 1u) {
+            if (n < room) out[n] = order_pair(e[j], part.sl.head + at[q] * V + j);
+            ++n;
+          }
+      }
+    }
+  }
+  __syncthreads();
+  const int n = s.n_flagged > kFlagged ? room + 1 : s.n;
+  __syncthreads();  // every thread has read them
+  return n;
+}
+
+// The k largest of the part's pairs that reach the threshold, into s.best[0, k) in order: the elements go through a
+// buffer of kUnitPairs (the units' memory), which is cut to its k best, and the bound raised to the last of them,
+// whenever it is full. At least k of the part's pairs reach the threshold. Ascending ids make ties cheap: a later one
+// is below the bound. How full the buffer is, each thread counts for itself (`n`, from block-wide counts), so all
+// decide alike; s.n only hands out places.
+template <int DT>
+__device__ __noinline__ void select_through_buffer(const RowPart<DT>& part, TopShared& s, uint32_t tau, int k) {
+  constexpr int V = kVecOf<DT>;
+  const int tt = threadIdx.x;
+  uint64_t* buffer = reinterpret_cast<uint64_t*>(s.unit);
+  uint64_t bound = static_cast<uint64_t>(tau) << 32;  // pairs above it are wanted
+  int n = 0;
+  if (tt == 0) s.n = 0;
+  __syncthreads();
+  auto cut = [&] {  // the buffer to its k best (n >= k), the bound to the k-th
+    for (int i = tt; i < n; i += kRowThreads) {
+      const uint64_t mine = buffer[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j) above += buffer[j] > mine ? 1 : 0;
+      if (above < k) s.best[above] = mine;
+    }
+    __syncthreads();
+    for (int i = tt; i < k; i += kRowThreads) buffer[i] = s.best[i];
+    if (tt == 0) s.n = k;
+    bound = s.best[k - 1];
+    n = k;
+    __syncthreads();
+  };
+  auto step = [&](bool there, float f, int id) {  // one element of every thread
+    if (n + kRowThreads > kUnitPairs) cut();
+    const uint64_t pair = order_pair(f, id);
+    const bool enters = there && pair > bound;
+    if (enters) buffer[atomicAdd(&s.n, 1)] = pair;
+    n += __syncthreads_count(enters);
+  };
+  if (part.rank == 0) {
+    const bool there = tt < part.sl.head;
+    step(there, there ? to_float<DT>(part.x[tt]) : 0.0f, tt);
+  }
+  const int vectors = part.vectors();
+#pragma unroll 1
+  for (int j = 0; j < vectors; ++j) {
+    const int vec = part.first + j * part.step();
+    const bool there = vec < part.sl.nvec;
+    uint4 w = make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+    if (there) w = __ldg(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec);
+    float e[V];
+    unpack<DT>(w, e);
+    unsigned hits = 0u;
+#pragma unroll
+    for (int q = 0; q < V; ++q)
+      if (there && order_pair(e[q], part.sl.head + vec * V + q) > bound) hits |= 1u << q;
+    if (!__syncthreads_or(hits != 0u)) continue;
+#pragma unroll
+    for (int q = 0; q < V; ++q) step((hits >> q) & 1u, e[q], part.sl.head + vec * V + q);
+  }
+  if (part.rank == 0) {
+    const int id = part.sl.tail() + tt;
+    const bool there = tt < part.sl.n - part.sl.tail();
+    step(there, there ? to_float<DT>(part.x[id]) : 0.0f, id);
+  }
+  cut();
+}
+
+// Where a row's alternatives go.
+struct TopOut {
+  float* logprob;
+  void* id;
+  int64_t base;
+  bool wide;
+
+  __device__ __forceinline__ void put(int j, int64_t i, float lp) const {
+    if (id) store_id(id, base + j, i, wide);
+    if (logprob) logprob[base + j] = lp;
+  }
+};
+
+// What a row's sums say.
+struct RowValues {
+  RowSum all;
+  float scale, ln_s;
+  bool nan, empty;
+
+  __device__ __forceinline__ RowValues(const RowSum& a, float scale_)
+      : all(a), scale(scale_), ln_s(logf(a.s)), nan(!(a.s == a.s)), empty(a.s == 0.0f) {}
+  __device__ __forceinline__ float logp(float x) const {
+    if (nan) return nan_f();
+    return empty ? -kInf : fmaf(x - all.m, scale, -ln_s);
+  }
+  __device__ __forceinline__ void write(const LogprobArgs& a, int64_t row, int64_t token, float token_x) const {
+    if (a.norm) a.norm[row] = make_float2(all.m, all.s);
+    if (a.lse) a.lse[row] = empty ? -kInf : fmaf(all.m, scale, ln_s);
+    if (a.entropy) {
+      const float h = empty ? 0.0f : ln_s - all.t / all.s * kLn2;
+      a.entropy[row] = h < 0.0f ? 0.0f : h;
+    }
+    if (a.logprob) a.logprob[row] = token < 0 ? 0.0f : (token >= a.vocab ? nan_f() : logp(token_x));
+  }
+};
+
+// Masked tokens by ascending id into the places from `have` on.
+template <int DT>
+__device__ __forceinline__ void put_masked(const Elem<DT>* x, int64_t vocab, int have, int k, const TopOut& out,
+                                           int* warp_sums) {
+  const int tt = threadIdx.x;
+  for (int64_t base = 0; base < vocab && have < k; base += kRowThreads) {
+    const int64_t i = base + tt;
+    const bool masked = i < vocab && to_float<DT>(x[i]) == -kInf;
+    const unsigned votes = __ballot_sync(0xFFFFFFFFu, masked);
+    __syncthreads();  // the last round's sums have been read
+    if ((tt & 31) == 0) warp_sums[tt >> 5] = __popc(votes);
+    __syncthreads();
+    int before = have;
+    for (int w = 0; w < kRowWarps; ++w) {
+      if (w < tt >> 5) before += warp_sums[w];
+      have += warp_sums[w];
+    }
+    const int j = before + __popc(votes & ((1u << (tt & 31)) - 1u));
+    if (masked && j < k) out.put(j, i, -kInf);
+  }
 }
 
 template <int DT, bool TOPS>
 __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_constant__ LogprobArgs a) {
-  __shared__ RowSum red[kRowThreads / 32];
+  __shared__ RowSum red[kRowWarps];
   __shared__ RowSum parts[kMaxCluster];
   __shared__ std::conditional_t<TOPS, TopShared, NoTops> tops;
   const Cluster cl = Cluster::start();
@@ -158,45 +393,21 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / cl.size;
   const RowPart<DT> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl.rank, cl.size);
-  const int vectors = part.vectors();
-  const int full = part.whole / kBatch;  // batches that every thread has whole
-  const int64_t sb = part.step_bytes();
-  const char* src = part.at();
-  const int unit_batches = ((vectors + kBatch - 1) / kBatch + kUnits - 1) / kUnits;
   const float edge = part.edge >= 0 ? to_float<DT>(part.x[part.edge]) : -kInf;
-  RunningSum run(one_element<RowSum>(edge), a.c);
-  float unit = -kInf;
-  int in_unit = 0, units = 0;
-  auto end_batch = [&](float m) {
-    if constexpr (TOPS) {
-      unit = fmaxf(unit, m);
-      if (++in_unit == unit_batches) {
-        tops.unit[units++][tid] = unit;
-        in_unit = 0;
-        unit = -kInf;
-      }
-    }
-  };
-  for (int b = 0; b < full; ++b, src += kBatch * sb) {
-    uint4 w[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) w[u] = __ldg(reinterpret_cast<const uint4*>(src + u * sb));
-    end_batch(add_vectors<DT>(w, a.c, run));
+  // the row's token and its logit are on their way from the start
+  const bool writes = cl.rank == 0 && tid == kRowThreads - 1;
+  int64_t token = -1;
+  float token_x = 0.0f;
+  if (writes && a.logprob) {
+    token = load_id(a.tokens, row, a.wide);
+    if (token >= 0 && token < a.vocab) token_x = to_float<DT>(part.x[token]);
   }
-  if (full * kBatch < vectors) {
-    uint4 w[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      w[u] = part.more(full * kBatch + u)
-                 ? __ldg(reinterpret_cast<const uint4*>(src + u * sb))
-                 : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
-    end_batch(add_vectors<DT>(w, a.c, run));
-  }
-  if constexpr (TOPS) {
-    if (in_unit > 0) tops.unit[units++][tid] = unit;
-  }
-  const float thread_max = run.top;
-  RowSum acc = block_merge(run.done(a.c), a.c, red);
+  float thread_max;
+  float(*unit)[kRowThreads] = nullptr;
+  if constexpr (TOPS) unit = tops.unit;
+  RowSum acc = block_merge(stream_row<DT, TOPS>(part, a.c, edge, unit, &thread_max), a.c, red);
+  if (TOPS && cl.size == 1 && tid == 0 && row + a.resident < a.rows)
+    prefetch_row<DT>(static_cast<const Elem<DT>*>(a.x) + (row + a.resident) * a.ld, a.vocab, kAheadBytes);
   cl.started();
   if (cl.size > 1) {
     if (tid < cl.size) cl.at(parts, tid)[cl.rank] = acc;
@@ -212,163 +423,47 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     if (tid == 0) tops.n = tops.n_flagged = 0;
   }
   if (TOPS || cl.size > 1) cl.sync();
-  if (cl.size > 1) {
-    acc = merge_lanes(parts[tid % cl.size], a.c, static_cast<int>(cl.size));
-  }
-  const bool nan = !(acc.s == acc.s);
-  const bool empty = acc.s == 0.0f;
-  const float ln_s = logf(acc.s);
-  auto logp = [&](float f) {
-    if (nan) return nan_f();
-    return empty ? -kInf : fmaf(f - acc.m, a.scale, -ln_s);
-  };
-  if (cl.rank == 0 && tid == 0) {
-    if (a.norm) a.norm[row] = make_float2(acc.m, acc.s);
-    if (a.lse) a.lse[row] = empty ? -kInf : fmaf(acc.m, a.scale, ln_s);
-    if (a.entropy) {
-      const float h = empty ? 0.0f : ln_s - acc.t / acc.s * kLn2;
-      a.entropy[row] = h < 0.0f ? 0.0f : h;
-    }
-    if (a.logprob) {
-      const int64_t t = load_id(a.tokens, row, a.wide);
-      a.logprob[row] = t < 0 ? 0.0f : (t >= a.vocab ? nan_f() : logp(to_float<DT>(part.x[t])));
-    }
-  }
+  if (cl.size > 1) acc = merge_lanes(parts[tid % cl.size], a.c, static_cast<int>(cl.size));
+  const RowValues v(acc, a.scale);
+  if (writes) v.write(a, row, token, token_x);
   if constexpr (TOPS) {
     const int k = a.top_k;
-    auto put = [&](int j, int64_t id, float lp) {
-      const int64_t o = row * k + j;
-      if (a.top_id) store_id(a.top_id, o, id, a.wide);
-      if (a.top_logprob) a.top_logprob[o] = lp;
-    };
-    if (nan) {  // in every block of the cluster: all have merged the same parts
-      if (cl.rank == 0 && tid < k) put(tid, -1, nan_f());
+    const TopOut out = {a.top_logprob, a.top_id, row * k, a.wide};
+    if (v.nan) {  // in every block of the cluster: all have merged the same parts
+      if (cl.rank == 0 && tid < k) out.put(tid, -1, nan_f());
       return;
     }
-    // the threshold: bit by bit, the largest that k keys reach; a little less is as good
-    constexpr int kLowBit = DT == SS_BF16 ? 16 : (DT == SS_FP16 ? 13 : 0);
-    const uint32_t my_key = tops.keys[tid];
-    const uint32_t top_key = order_key(acc.m);
-    uint32_t tau = 0;
-    for (int bit = 31; bit >= kLowBit; --bit) {
-      const uint32_t t = tau | (1u << bit);
-      if (t > top_key) continue;
-      const int c = __syncthreads_count(my_key >= t);
-      if (c >= k) {
-        tau = t;
-        if (c <= k + k / 8) break;
-      }
+    if (tid < 32) {
+      const uint32_t t = find_threshold<DT>(tops.keys, order_key(acc.m), k);
+      if (tid == 0) tops.tau = t;
     }
-    const bool few = tau <= kMaskedKey;  // fewer than k threads hold unmasked tokens: all of those are candidates
-    if (few) tau = kMaskedKey + 1;
-    const float bound = few ? -kInf : key_value(tau);
-    auto wanted = [&](float f) { return few ? f > bound : f >= bound; };
+    __syncthreads();
+    const Wanted wanted(tops.tau);
     const int room = kCand / static_cast<int>(cl.size);
-    uint64_t* out = cl.at(tops.cand, 0) + cl.rank * room;
-    auto add = [&](float f, int id) {
-      const int n = atomicAdd(&tops.n, 1);
-      if (n < room) out[n] = order_pair(f, id);
-    };
-    for (int u = 0; u < units; ++u) {
-      if (wanted(tops.unit[u][tid])) {
-        const int f = atomicAdd(&tops.n_flagged, 1);
-        if (f < kFlagged) tops.flagged[f] = static_cast<uint16_t>(u * kRowThreads + tid);
-      }
+    uint64_t* mine = cl.at(tops.cand, 0) + cl.rank * room;
+    int found = collect<DT>(part, wanted, tops, mine, room);
+    if (found > room) {  // this block's own k best instead
+      select_through_buffer<DT>(part, tops, wanted.few ? kMaskedKey + 1 : tops.tau, k);
+      if (tid < k) mine[tid] = tops.best[tid];
+      found = k;
     }
-    if (part.edge >= 0 && wanted(edge)) add(edge, part.edge);
-    __syncthreads();
-    // a warp reads a flagged unit's elements again, one a lane, four units at a time
-    constexpr int V = kVecOf<DT>;
-    const int flagged = min(tops.n_flagged, kFlagged), lane = tid & 31;
-    const int unit_elems = unit_batches * kBatch * V;
-#pragma unroll 1
-    for (int f0 = (tid >> 5) * 4; f0 < flagged; f0 += kRowWarps * 4) {
-#pragma unroll 1
-      for (int e = lane; e < unit_elems; e += 32) {
-        float val[4];
-        int id[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          id[q] = -1;
-          if (f0 + q < flagged) {
-            const int unit_at = tops.flagged[f0 + q];
-            const int64_t vec = static_cast<int64_t>((unit_at / kRowThreads) * unit_batches * kBatch + e / V) * part.step() +
-                                part.rank * kRowThreads + unit_at % kRowThreads;
-            if (vec < part.sl.nvec) {
-              id[q] = part.sl.head + static_cast<int>(vec) * V + e % V;
-              val[q] = to_float<DT>(part.x[id[q]]);
-            }
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bool hit = id[q] >= 0 && wanted(val[q]);
-          const unsigned hits = __ballot_sync(__activemask(), hit);
-          if (hit) {
-            const int leader = __ffs(hits) - 1;
-            int at = 0;
-            if (lane == leader) at = atomicAdd(&tops.n, __popc(hits));
-            at = __shfl_sync(hits, at, leader) + __popc(hits & ((1u << lane) - 1u));
-            if (at < room) out[at] = order_pair(val[q], id[q]);
-          }
-        }
-      }
-    }
-    if (tid == 0 && tops.n_flagged > kFlagged) tops.n = room + 1;
-    __syncthreads();
-    if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = tops.n;
+    if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = found;
     cl.sync();
-    int total = 0;
-    bool over = false;
-    for (unsigned r = 0; r < cl.size; ++r) {
-      total += tops.count[r];
-      over = over || tops.count[r] > room;
-    }
-    if (over) {
-      const uint2 kth = search_pair<DT>(cl, tops, part, vectors, tau, order_key(acc.m), k);
-      if (tid == 0) tops.n = 0;
-      __syncthreads();
-      auto kept = [&](float f, int id) {
-        const uint32_t key = order_key(f);
-        if (key > kth.x || (key == kth.x && id <= static_cast<int>(kth.y))) add(f, id);
-      };
-      part.each(0, vectors, kept);
-      if (part.edge >= 0) kept(edge, part.edge);
-      __syncthreads();
-      if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = tops.n;
-      cl.sync();
-      total = k;
-    }
     if (cl.rank != 0) return;
+    int total = 0;
+    for (unsigned r = 0; r < cl.size; ++r) total += tops.count[r];
     for (int i = tid; i < total; i += kRowThreads) {
       int r = 0, at = i;
       while (at >= tops.count[r]) at -= tops.count[r++];
-      const uint64_t mine = tops.cand[r * room + at];
-      int rank = 0;
+      const uint64_t pair = tops.cand[r * room + at];
+      int place = 0;
       for (unsigned q = 0; q < cl.size; ++q)
-        for (int j = 0; j < tops.count[q]; ++j) rank += tops.cand[q * room + j] > mine ? 1 : 0;
-      if (rank < k)
-        put(rank, static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(mine)),
-            logp(key_value(static_cast<uint32_t>(mine >> 32))));
+        for (int j = 0; j < tops.count[q]; ++j) place += tops.cand[q * room + j] > pair ? 1 : 0;
+      if (place < k)
+        out.put(place, static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(pair)),
+                v.logp(key_value(static_cast<uint32_t>(pair >> 32))));
     }
-    if (few && total < k) {  // the rest are masked tokens, by ascending id
-      int have = total;
-      for (int64_t base = 0; base < a.vocab && have < k; base += kRowThreads) {
-        const int64_t i = base + tid;
-        const bool masked = i < a.vocab && to_float<DT>(part.x[i]) == -kInf;
-        const unsigned votes = __ballot_sync(0xFFFFFFFFu, masked);
-        __syncthreads();  // the last round's sums have been read
-        if ((tid & 31) == 0) tops.warp_sums[tid >> 5] = __popc(votes);
-        __syncthreads();
-        int before = have;
-        for (int w = 0; w < kRowThreads / 32; ++w) {
-          if (w < tid >> 5) before += tops.warp_sums[w];
-          have += tops.warp_sums[w];
-        }
-        const int j = before + __popc(votes & ((1u << (tid & 31)) - 1u));
-        if (masked && j < k) put(j, i, -kInf);
-      }
-    }
+    if (wanted.few && total < k) put_masked<DT>(part.x, a.vocab, total, k, out, tops.warp_sums);
   }
 }
 
@@ -512,14 +607,14 @@ ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype id
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const LogprobArgs a = {x->data, tokens, out->logprob, out->entropy, out->lse,
                          reinterpret_cast<float2*>(out->norm), out->top_logprob, out->top_id,
-                         rows, x->vocab, x->ld, x->scale * kLog2e, x->scale, top_k, idtype == SS_I64};
+                         rows, x->vocab, x->ld, x->scale * kLog2e, x->scale, top_k, idtype == SS_I64, 4 * sm_count()};
   const auto pick = [&](auto tops) {
     constexpr bool kTops = decltype(tops)::value;
     return x->dtype == SS_BF16 ? logprob_kernel<SS_BF16, kTops>
                                : (x->dtype == SS_FP16 ? logprob_kernel<SS_FP16, kTops> : logprob_kernel<SS_FP32, kTops>);
   };
-  auto* fn = top_k > 0 ? pick(std::true_type()) : pick(std::false_type());
   const int cluster = cluster_for(rows, x->vocab, x->dtype == SS_FP32 ? 4 : 8);
+  auto* fn = top_k > 0 ? pick(std::true_type()) : pick(std::false_type());
   if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
   return launch_rows(fn, rows, cluster, kRowThreads, 0, a, stream);
 }
