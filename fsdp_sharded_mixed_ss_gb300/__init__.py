@@ -17,6 +17,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 from typing import Sequence
 
 import numpy as np
@@ -72,23 +73,12 @@ class _Options(ctypes.Structure):
                 ("dev_grad_scale", ctypes.c_void_p), ("dev_skip_flag", ctypes.c_void_p)]
 
 
-class _Logits(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
-                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
-
-
-class _LogprobOut(ctypes.Structure):
-    _fields_ = [(f, ctypes.c_void_p) for f in ("logprob", "entropy", "lse", "norm", "top_logprob", "top_id")]
-
-
-class _LogprobGrad(ctypes.Structure):
-    _fields_ = [(f, ctypes.c_void_p) for f in ("d_logprob", "d_entropy", "d_lse", "d_top_logprob")]
-
-
-class _Teacher(ctypes.Structure):
-    _fields_ = [("ids", ctypes.c_void_p), ("logprob", ctypes.c_void_p), ("row_weight", ctypes.c_void_p),
-                ("k", ctypes.c_int32), ("idtype", ctypes.c_int32), ("dtype", ctypes.c_int32), ("tail", ctypes.c_int32),
-                ("scale", ctypes.c_float), ("pad_", ctypes.c_int32)]
+# ss_logits, ss_logprob_out, ss_logprob_grad and ss_teacher as bytes: packing them costs a quarter of building a
+# ctypes structure, which calls on a few rows feel
+_LOGITS = struct.Struct("@Pqqqif")
+_LOGPROB_OUT = struct.Struct("@6P")
+_LOGPROB_GRAD = struct.Struct("@4P")
+_TEACHER = struct.Struct("@3P4ifi")
 
 
 _NO_OPTIONS = _Options(None, None, None, None)
@@ -118,11 +108,11 @@ def _load():
     lib.ss_grad_sumsq_workspace.restype = i64
     lib.ss_grad_sumsq.argtypes = [i64, vp, vp, i32, i32, f32, vp, vp, i64, vp, vp, vp]
     lib.ss_clip_coef.argtypes = [vp, i32, f32, vp, vp, vp]
-    lib.ss_token_logprobs.argtypes = [ctypes.POINTER(_Logits), vp, i32, i32, ctypes.POINTER(_LogprobOut), vp]
-    lib.ss_token_logprobs_grad.argtypes = [ctypes.POINTER(_Logits), vp, i32, i32, vp, vp, vp,
-                                           ctypes.POINTER(_LogprobGrad), vp, i64, vp]
-    lib.ss_distill_topk.argtypes = [ctypes.POINTER(_Logits), ctypes.POINTER(_Teacher), vp, vp, vp, vp, i64, vp]
-    lib.ss_distill_topk_grad.argtypes = [ctypes.POINTER(_Logits), ctypes.POINTER(_Teacher), vp, vp, vp, vp, i64, vp]
+    lib.ss_token_logprobs.argtypes = [vp, vp, i32, i32, vp, vp]
+    lib.ss_token_logprobs_grad.argtypes = [vp, vp, i32, i32, vp, vp, vp,
+                                           vp, vp, i64, vp]
+    lib.ss_distill_topk.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.ss_distill_topk_grad.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
     lib.ss_grad_sumsq_noalloc.argtypes = [i64, vp, vp, i32, i32, f32, vp, vp, vp, vp]
     return lib
 
@@ -382,56 +372,95 @@ def ss_reshard(flat, shard_bounds: np.ndarray, shards, *, dtype: int | None = No
 # ----------------------------------------------------------------------------- rows of logits
 
 _ID_DTYPES = None
+_F32 = None
 
 
 def _rows_of(x, shape, ld, dtype, scale):
-    """The _Logits of a 2-D tensor (unit stride along the vocabulary), or of an address with shape = (rows,
-    vocab), ld (default: vocab) and dtype."""
+    """(ss_logits, rows, vocab, dtype) of a 2-D tensor (unit stride along the vocabulary), or of an address with shape
+    = (rows, vocab), ld (default: vocab) and dtype."""
     if isinstance(x, int):
         rows, vocab = shape
-        return _Logits(x, rows, vocab, vocab if ld is None else ld, -1 if dtype is None else dtype, scale)
-    _t()
+        if dtype is None:
+            dtype = -1
+        return _LOGITS.pack(x, rows, vocab, vocab if ld is None else ld, dtype, scale), rows, vocab, dtype
+    if _ID_DTYPES is None:
+        _load_dtypes()
     rows, vocab = x.shape
-    s0, s1 = x.stride()
-    if s1 != 1 and vocab > 1:
+    ld, one = x.stride()
+    if one != 1 and vocab > 1:
         raise SSError(1, "logits: the vocabulary must have stride 1")
-    # torch gives a single row any stride
-    return _Logits(x.data_ptr(), rows, vocab, s0 if rows > 1 else max(s0, vocab), _DTYPES.get(x.dtype, -1), scale)
+    if ld < vocab and rows == 1:  # torch gives a single row any stride
+        ld = vocab
+    dtype = _DTYPES.get(x.dtype, -1)
+    return _LOGITS.pack(x.data_ptr(), rows, vocab, ld, dtype, scale), rows, vocab, dtype
 
 
-def _grad_rows(d, x, d_ld):
-    """(address, ld) of a gradient of x's shape and dtype (x: the _Logits)."""
+def _load_dtypes():
+    global _ID_DTYPES, _F32
+    torch = _t()
+    _F32 = torch.float32
+    _ID_DTYPES = {torch.int32: SS_I32, torch.int64: SS_I64}
+
+
+def _grad_rows(d, rows, vocab, dtype, d_ld):
+    """(address, ld) of a gradient of the logits' shape and dtype."""
     if d is None:
         return None, 0
     if isinstance(d, int):
-        return d, (x.vocab if d_ld is None else d_ld)
-    if tuple(d.shape) != (x.rows, x.vocab) or (d.stride(1) != 1 and x.vocab > 1):
+        return d, (vocab if d_ld is None else d_ld)
+    ld, one = d.stride()
+    if tuple(d.shape) != (rows, vocab) or (one != 1 and vocab > 1):
         raise SSError(1, "d_logits: the logits' shape, with stride 1 along the vocabulary")
-    if _DTYPES.get(d.dtype, -1) != x.dtype:
+    if _DTYPES.get(d.dtype, -1) != dtype:
         raise SSError(4, "d_logits")
-    return d.data_ptr(), (d.stride(0) if x.rows > 1 else max(d.stride(0), x.vocab))
+    return d.data_ptr(), (vocab if ld < vocab and rows == 1 else ld)
 
 
-def _arg(t, n, where, dtypes=None):
-    """The address of an optional dense array of n elements: fp32, or one of `dtypes`."""
-    if t is None or isinstance(t, int):
+def _f32(t, n, where):
+    """The address of an optional dense fp32 array of n elements (0: none)."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
         return t
+    if t.dtype is not _F32:
+        raise SSError(4, where)
     if t.numel() != n or not t.is_contiguous():
         raise SSError(1, f"{where}: a dense array of {n} elements")
-    if t.dtype not in dtypes if dtypes is not None else t.dtype is not _torch.float32:
+    return t.data_ptr()
+
+
+def _ids(t, n, idtype, where):
+    """The address of an optional dense array of n ids of the call's type (0: none)."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
+        return t
+    if _ID_DTYPES.get(t.dtype, -1) != idtype:
         raise SSError(4, where)
+    if t.numel() != n or not t.is_contiguous():
+        raise SSError(1, f"{where}: a dense array of {n} elements")
     return t.data_ptr()
 
 
 def _idtype(ids, idtype):
     """The ss_idtype of the call: the tensor's, or `idtype` for an address."""
-    global _ID_DTYPES
-    if _ID_DTYPES is None:
-        torch = _t()
-        _ID_DTYPES = {torch.int32: SS_I32, torch.int64: SS_I64}
     if ids is None or isinstance(ids, int):
         return SS_I64 if idtype is None else idtype
+    if _ID_DTYPES is None:
+        _load_dtypes()
     return _ID_DTYPES.get(ids.dtype, -1)
+
+
+def _call(fn, where, like, stream, *args) -> None:
+    """fn(*args, stream) with `like`'s device current."""
+    dev = -1 if isinstance(like, int) else like.get_device()
+    if _RAW_STREAM is not None and dev >= 0 and dev == _GET_DEVICE():
+        rc = fn(*args, _RAW_STREAM(dev) if stream is None else _stream(stream))
+    else:
+        with _DeviceGuard(like):
+            rc = fn(*args, _stream(stream, like))
+    if rc != 0:
+        raise SSError(rc, where)
 
 
 def ss_token_logprobs(logits, tokens=None, *, scale: float = 1.0, logprob=None, entropy=None, lse=None, norm=None,
@@ -445,21 +474,14 @@ def ss_token_logprobs(logits, tokens=None, *, scale: float = 1.0, logprob=None, 
     order, equal logits by ascending id; top_id has the tokens' type. Every figure is of scale * logits. include/ss.h
     says what masked rows and NaN give.
     """
-    x = _rows_of(logits, shape, ld, dtype, scale)
+    x, r, _, _ = _rows_of(logits, shape, ld, dtype, scale)
     it = _idtype(tokens if tokens is not None else top_id, idtype)
-    r = x.rows
     top = top_logprob if top_logprob is not None else top_id
     k = top_k if top_k is not None else (0 if top is None or isinstance(top, int) else top.shape[-1])
-    out = _LogprobOut(_arg(logprob, r, "logprob"), _arg(entropy, r, "entropy"), _arg(lse, r, "lse"),
-                      _arg(norm, 2 * r, "norm"), _arg(top_logprob, r * k, "top_logprob"),
-                      _arg(top_id, r * k, "top_id", _ids_like(it)))
-    with _DeviceGuard(logits):
-        _check(_lib.ss_token_logprobs(x, _arg(tokens, r, "tokens", _ids_like(it)), it, k, out,
-                                      _stream(stream, logits)), "ss_token_logprobs")
-
-
-def _ids_like(it):
-    return (_torch.int32,) if it == SS_I32 else ((_torch.int64,) if it == SS_I64 else ())
+    out = _LOGPROB_OUT.pack(_f32(logprob, r, "logprob"), _f32(entropy, r, "entropy"), _f32(lse, r, "lse"),
+                            _f32(norm, 2 * r, "norm"), _f32(top_logprob, r * k, "top_logprob"),
+                            _ids(top_id, r * k, it, "top_id"))
+    _call(_lib.ss_token_logprobs, "ss_token_logprobs", logits, stream, x, _ids(tokens, r, it, "tokens"), it, k, out)
 
 
 def ss_token_logprobs_grad(logits, norm, d_logits, *, tokens=None, d_logprob=None, entropy=None, d_entropy=None,
@@ -472,31 +494,31 @@ def ss_token_logprobs_grad(logits, norm, d_logits, *, tokens=None, d_logprob=Non
     norm, entropy and top_id are what the forward call wrote. d_logits has the logits' shape and dtype and may be the
     logits themselves. A row whose upstream gradients are all zero gets zeros, whatever its logits.
     """
-    x = _rows_of(logits, shape, ld, dtype, scale)
+    x, r, v, dt = _rows_of(logits, shape, ld, dtype, scale)
     it = _idtype(tokens if tokens is not None else top_id, idtype)
-    r = x.rows
-    d, dl = _grad_rows(d_logits, x, d_ld)
+    d, dl = _grad_rows(d_logits, r, v, dt, d_ld)
     k = 0
     if d_top_logprob is not None:
         k = top_k if top_k is not None else (0 if isinstance(d_top_logprob, int) else d_top_logprob.shape[-1])
-    ids = _ids_like(it)
-    up = _LogprobGrad(_arg(d_logprob, r, "d_logprob"), _arg(d_entropy, r, "d_entropy"), _arg(d_lse, r, "d_lse"),
-                      _arg(d_top_logprob, r * k, "d_top_logprob"))
-    with _DeviceGuard(logits):
-        _check(_lib.ss_token_logprobs_grad(x, _arg(tokens, r, "tokens", ids), it, k,
-                                           _arg(top_id, r * k, "top_id", ids) if k else None,
-                                           _arg(norm, 2 * r, "norm"), _arg(entropy, r, "entropy"), up, d, dl,
-                                           _stream(stream, logits)), "ss_token_logprobs_grad")
+    up = _LOGPROB_GRAD.pack(_f32(d_logprob, r, "d_logprob"), _f32(d_entropy, r, "d_entropy"), _f32(d_lse, r, "d_lse"),
+                            _f32(d_top_logprob, r * k, "d_top_logprob"))
+    _call(_lib.ss_token_logprobs_grad, "ss_token_logprobs_grad", logits, stream, x, _ids(tokens, r, it, "tokens"), it,
+          k, _ids(top_id, r * k, it, "top_id") if k else None, _f32(norm, 2 * r, "norm"),
+          _f32(entropy, r, "entropy"), up, d, dl)
 
 
-def _teacher_of(x, ids, logprob, row_weight, tail, teacher_scale, k, idtype, tdtype):
+def _teacher_of(r, ids, logprob, row_weight, tail, teacher_scale, k, idtype, tdtype):
     it = _idtype(ids, idtype)
     if k is None:
         k = ids.shape[-1]
-    td = _dtype_of(logprob) if not isinstance(logprob, int) else tdtype
-    n = x.rows * k
-    return _Teacher(_arg(ids, n, "ids", _ids_like(it)), _arg(logprob, n, "teacher", _DTYPES),
-                    _arg(row_weight, x.rows, "row_weight"), k, it, -1 if td is None else td, tail, teacher_scale, 0)
+    if isinstance(logprob, int):
+        at, td = logprob, -1 if tdtype is None else tdtype
+    else:
+        at, td = logprob.data_ptr(), _DTYPES.get(logprob.dtype, -1)
+        if logprob.numel() != r * k or not logprob.is_contiguous():
+            raise SSError(1, f"teacher: a dense array of {r * k} elements")
+    return _TEACHER.pack(_ids(ids, r * k, it, "ids"), at, _f32(row_weight, r, "row_weight"), k, it, td, tail,
+                         teacher_scale, 0)
 
 
 def ss_distill_topk(logits, ids, teacher, loss=None, *, norm=None, tail_logprob=None, d_logits=None, row_weight=None,
@@ -511,14 +533,11 @@ def ss_distill_topk(logits, ids, teacher, loss=None, *, norm=None, tail_logprob=
     or the rest of the mass is one more outcome (SS_TAIL_*). loss, norm (rows, 2) and tail_logprob are optional
     outputs; the last two are what ss_distill_topk_grad takes. Rows of weight 0 are not read.
     """
-    x = _rows_of(logits, shape, ld, dtype, scale)
-    t = _teacher_of(x, ids, teacher, row_weight, tail, teacher_scale, k, idtype, tdtype)
-    r = x.rows
-    d, dl = _grad_rows(d_logits, x, d_ld)
-    with _DeviceGuard(logits):
-        _check(_lib.ss_distill_topk(x, t, _arg(loss, r, "loss"), _arg(norm, 2 * r, "norm"),
-                                    _arg(tail_logprob, r, "tail_logprob"), d, dl, _stream(stream, logits)),
-               "ss_distill_topk")
+    x, r, v, dt = _rows_of(logits, shape, ld, dtype, scale)
+    t = _teacher_of(r, ids, teacher, row_weight, tail, teacher_scale, k, idtype, tdtype)
+    d, dl = _grad_rows(d_logits, r, v, dt, d_ld)
+    _call(_lib.ss_distill_topk, "ss_distill_topk", logits, stream, x, t, _f32(loss, r, "loss"),
+          _f32(norm, 2 * r, "norm"), _f32(tail_logprob, r, "tail_logprob"), d, dl)
 
 
 def ss_distill_topk_grad(logits, ids, teacher, norm, d_logits, *, tail_logprob=None, d_loss=None, row_weight=None,
@@ -528,11 +547,8 @@ def ss_distill_topk_grad(logits, ids, teacher, norm, d_logits, *, tail_logprob=N
                          stream=None) -> None:
     """d_logits = d_loss[r] (default 1) times the gradient of ss_distill_topk's loss[r], from the norm and (with
     SS_TAIL_BUCKET) the tail_logprob that it wrote."""
-    x = _rows_of(logits, shape, ld, dtype, scale)
-    t = _teacher_of(x, ids, teacher, row_weight, tail, teacher_scale, k, idtype, tdtype)
-    r = x.rows
-    d, dl = _grad_rows(d_logits, x, d_ld)
-    with _DeviceGuard(logits):
-        _check(_lib.ss_distill_topk_grad(x, t, _arg(norm, 2 * r, "norm"), _arg(tail_logprob, r, "tail_logprob"),
-                                         _arg(d_loss, r, "d_loss"), d, dl, _stream(stream, logits)),
-               "ss_distill_topk_grad")
+    x, r, v, dt = _rows_of(logits, shape, ld, dtype, scale)
+    t = _teacher_of(r, ids, teacher, row_weight, tail, teacher_scale, k, idtype, tdtype)
+    d, dl = _grad_rows(d_logits, r, v, dt, d_ld)
+    _call(_lib.ss_distill_topk_grad, "ss_distill_topk_grad", logits, stream, x, t, _f32(norm, 2 * r, "norm"),
+          _f32(tail_logprob, r, "tail_logprob"), _f32(d_loss, r, "d_loss"), d, dl)

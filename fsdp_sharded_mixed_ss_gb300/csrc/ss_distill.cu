@@ -27,7 +27,8 @@ struct DistillArgs {
   float c, scale, t_scale;
   int32_t k, mode, t_dtype;
   bool wide, vec, in_place;
-  uint32_t split;  // gradient from saved normalisers: blocks that share a row
+  uint32_t split;    // gradient from saved normalisers: blocks that share a row
+  int32_t resident;  // rows in flight at a time
 };
 
 __device__ __forceinline__ float load_teacher(const void* p, int64_t i, int dtype) {
@@ -207,95 +208,24 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
   acc.at.s = fmaf(s.sum(), acc.ref.k, acc.at.s);
 }
 
-// Dynamic shared memory: a word of listed bits for each batch of vectors, by thread.
+struct DistillShared {
+  RowMass red[kRowWarps];
+  RowMass parts[kMaxCluster];
+  int4 list_ids[SS_MAX_TOP / 4];
+  float factor[3];
+  uint32_t edge_listed;
+};
+
+constexpr int kAheadBytes = 65536;  // of the row that comes after (loss alone; 0, 16, 32, 64 KB: 24.6, 24.3, 23.6, 22.9 us)
+
+// The ninth warp's part in a row. `marks`: a word of listed bits for each batch of vectors, by thread.
 template <int DT, bool GRAD>
-__global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(const __grid_constant__ DistillArgs a) {
-  extern __shared__ uint32_t marks[];
-  __shared__ RowMass red[kRowWarps];
-  __shared__ RowMass parts[kMaxCluster];
-  __shared__ int4 list_ids[SS_MAX_TOP / 4];
-  __shared__ float factor[3];
-  __shared__ uint32_t edge_listed;
-  const Cluster cl = Cluster::start();
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x / cl.size;
-  const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
-  Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
+__device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& cl, const RowPart<DT>& part, int64_t row,
+                                          float w, const Elem<DT>* x, Elem<DT>* d, DistillShared& sh, uint32_t* marks) {
+  const int lane = threadIdx.x & 31;
   const float c = a.c;
-  const float w = a.weight ? a.weight[row] : 1.0f;
-  if (w == 0.0f) {  // every block of the cluster
-    if (GRAD && tid < kRowThreads) zero_part<DT>(d, a.vocab, cl.rank, cl.size);
-    if (cl.rank == 0 && tid == kRowThreads) {
-      if (a.loss) a.loss[row] = 0.0f;
-      if (a.norm) a.norm[row] = make_float2(0.0f, 0.0f);
-      if (a.tail) a.tail[row] = 0.0f;
-    }
-    cl.started();
-    return;
-  }
-  const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
-  if (tid < kRowThreads) {  // ---------------------------------------------------- the row's warps
-    const int vectors = part.vectors();
-    for (int j = 0; j < vectors; j += kBatch) marks[j / kBatch * kRowThreads + tid] = 0u;
-    if (tid == 0) edge_listed = 0u;
-    barrier_arrive<kClear, kListThreads>();
-    const int64_t sb = part.step_bytes();
-    const char* src = part.at();
-    auto fetch = [&](const char* p, int j, uint4 (&v)[kBatch]) {
-      if (j + kBatch <= part.whole) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) v[u] = load_row<GRAD>(p + u * sb);
-      } else {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          v[u] = part.more(j + u)
-                     ? load_row<GRAD>(p + u * sb)
-                     : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
-      }
-    };
-    uint4 v[kBatch];
-    fetch(src, 0, v);
-    const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
-    barrier_sync<kReady, kListThreads>();
-    const bool edge_out = part.edge >= 0 && !((edge_listed >> tid) & 1u);
-    RunningMass out(one_element<RowMass>(edge_out ? edge : -kInf), c);
-    const uint32_t* listed = marks + tid;
-#pragma unroll 1
-    for (int j = 0; j < vectors; j += kBatch, listed += kRowThreads) {
-      uint4 next[kBatch];
-      src += kBatch * sb;
-      fetch(src, j + kBatch, next);
-      const uint32_t bits = *listed;
-      if (bits != 0u) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if ((bits >> (8 * u)) & 0xFFu) mask_elements<DT>(v[u], bits >> (8 * u));
-      }
-      add_mass<DT>(v, c, out);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) v[u] = next[u];
-    }
-    const RowMass warp_out = merge_lanes(out.done(c), c);
-    if ((tid & 31) == 0) red[tid >> 5] = warp_out;
-    barrier_arrive<kAdded, kListThreads>();
-    cl.started();
-    if (cl.size > 1) cl.arrive();
-    if constexpr (GRAD) {
-      part.load(0, v);
-      barrier_sync<kScales, kListThreads>();
-      const Pair f_c = Pair::both(factor[0]), f_r = Pair::both(-factor[1]), f_a = Pair::both(factor[2]);
-      part.map(v, d, a.vec, edge, [&](Pair f) { return mul2(ex2_pair(fma2(f, f_c, f_r)), f_a); });
-      barrier_arrive<kWritten, kListThreads>();
-    }
-    if (cl.size > 1) cl.wait();
-    return;
-  }
-  // ---------------------------------------------------------------------------------- the list's warp
-  const int lane = tid & 31;
   RowList<DT> l;
-  l.load(a, row, x, list_ids);
+  l.load(a, row, x, sh.list_ids);
   barrier_sync<kClear, kListThreads>();
   unsigned mine = 0u;  // slots whose element is this block's
 #pragma unroll
@@ -303,13 +233,19 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
     int owner, slot;
     if (l.id[i] >= 0 && part.owns(l.id[i], &owner, &slot)) {
       mine |= 1u << i;
-      if (slot < 0) atomicOr(&edge_listed, 1u << owner);
+      if (slot < 0) atomicOr(&sh.edge_listed, 1u << owner);
       else atomicOr(&marks[(slot / kBatch) * kRowThreads + owner],
                     1u << (slot % kBatch * 8 + (l.id[i] - part.sl.head) % kVecOf<DT>));
     }
   }
   barrier_arrive<kReady, kListThreads>();
-  l.drop_repeated(a, list_ids);
+  const int64_t after = row + a.resident;
+  if (after < a.rows) {  // the list that comes after on this SM
+    const int64_t id_bytes = a.wide ? 8 : 4, t_bytes = a.t_dtype == SS_FP32 ? 4 : 2;
+    if (lane * 128 < a.k * id_bytes) prefetch_line(static_cast<const char*>(a.ids) + after * a.k * id_bytes + lane * 128);
+    if (lane * 128 < a.k * t_bytes) prefetch_line(static_cast<const char*>(a.teacher) + after * a.k * t_bytes + lane * 128);
+  }
+  l.drop_repeated(a, sh.list_ids);
 #pragma unroll
   for (int i = 0; i < kSlots; ++i)
     if (l.id[i] < 0) mine &= ~(1u << i);
@@ -317,12 +253,14 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
   l.mass_in(a);
   cl.started();
   barrier_sync<kAdded, kListThreads>();
-  RowMass out = merge_lanes(red[lane % kRowWarps], c, kRowWarps);
+  if (!GRAD && lane == 0 && after < a.rows)  // HBM has little else to do while the blocks exchange their sums
+    prefetch_row<DT>(static_cast<const Elem<DT>*>(a.x) + after * a.ld, a.vocab, kAheadBytes, cl.rank, cl.size);
+  RowMass out = merge_lanes(sh.red[lane % kRowWarps], c, kRowWarps);
   if (cl.size > 1) {
-    if (lane < cl.size) cl.at(parts, lane)[cl.rank] = out;
+    if (lane < cl.size) cl.at(sh.parts, lane)[cl.rank] = out;
     cl.arrive();
     cl.wait();
-    out = merge_lanes(parts[lane % cl.size], c, static_cast<int>(cl.size));
+    out = merge_lanes(sh.parts[lane % cl.size], c, static_cast<int>(cl.size));
   }
   RowMass all = l.in, o = out;
   if (o.m > all.m) all.move(o.m, c);
@@ -339,9 +277,9 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
     const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - l.q_tail) / out.s;
     const ExpRef ref(out.m, c);
     if (lane == 0) {
-      factor[0] = ref.c;
-      factor[1] = ref.r;
-      factor[2] = A * ref.k;
+      sh.factor[0] = ref.c;
+      sh.factor[1] = ref.r;
+      sh.factor[2] = A * ref.k;
     }
     barrier_arrive<kScales, kListThreads>();
   }
@@ -375,6 +313,98 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
       if ((mine >> i) & 1u)
         d[l.id[i]] = from_float<DT>(empty ? 0.0f : ws * fmaf(top.exp(l.x[i]) * over, b, -l.q[i]));
   }
+}
+
+// A row of weight 0: its zeros, by every block of its cluster.
+template <int DT, bool GRAD>
+__device__ __forceinline__ void skip_row(const DistillArgs& a, const Cluster& cl, int64_t row, Elem<DT>* d) {
+  if (GRAD && threadIdx.x < kRowThreads) zero_part<DT>(d, a.vocab, cl.rank, cl.size);
+  if (cl.rank == 0 && threadIdx.x == kRowThreads) {
+    if (a.loss) a.loss[row] = 0.0f;
+    if (a.norm) a.norm[row] = make_float2(0.0f, 0.0f);
+    if (a.tail) a.tail[row] = 0.0f;
+  }
+  cl.started();
+}
+
+// Marks cleared by the row's warps before the list's sets its own.
+__device__ __forceinline__ void clear_marks(uint32_t* marks, DistillShared& sh, int vectors) {
+  for (int j = 0; j < vectors; j += kBatch) marks[j / kBatch * kRowThreads + threadIdx.x] = 0u;
+  if (threadIdx.x == 0) sh.edge_listed = 0u;
+  barrier_arrive<kClear, kListThreads>();
+}
+
+// Masks a batch's listed elements.
+template <int DT>
+__device__ __forceinline__ void mask_batch(uint4* v, uint32_t bits) {
+  if (bits != 0u) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if ((bits >> (8 * u)) & 0xFFu) mask_elements<DT>(v[u], bits >> (8 * u));
+  }
+}
+
+template <int DT, bool GRAD>
+__global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(const __grid_constant__ DistillArgs a) {
+  extern __shared__ uint32_t marks[];
+  __shared__ DistillShared sh;
+  const Cluster cl = Cluster::start();
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / cl.size;
+  const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
+  Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
+  const float c = a.c;
+  const float w = a.weight ? a.weight[row] : 1.0f;
+  if (w == 0.0f) return skip_row<DT, GRAD>(a, cl, row, d);
+  const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
+  if (tid >= kRowThreads) return list_warp<DT, GRAD>(a, cl, part, row, w, x, d, sh, marks);
+  const int vectors = part.vectors();
+  clear_marks(marks, sh, vectors);
+  const int64_t sb = part.step_bytes();
+  const char* src = part.at();
+  auto fetch = [&](const char* p, int j, uint4 (&v)[kBatch]) {
+    if (j + kBatch <= part.whole) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) v[u] = load_row<GRAD>(p + u * sb);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        v[u] = part.more(j + u) ? load_row<GRAD>(p + u * sb)
+                                : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+    }
+  };
+  uint4 v[kBatch];
+  fetch(src, 0, v);
+  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
+  barrier_sync<kReady, kListThreads>();
+  const bool edge_out = part.edge >= 0 && !((sh.edge_listed >> tid) & 1u);
+  RunningMass out(one_element<RowMass>(edge_out ? edge : -kInf), c);
+  const uint32_t* listed = marks + tid;
+#pragma unroll 1
+  for (int j = 0; j < vectors; j += kBatch, listed += kRowThreads) {
+    uint4 next[kBatch];
+    src += kBatch * sb;
+    fetch(src, j + kBatch, next);
+    mask_batch<DT>(v, *listed);
+    add_mass<DT>(v, c, out);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) v[u] = next[u];
+  }
+  const RowMass warp_out = merge_lanes(out.done(c), c);
+  if ((tid & 31) == 0) sh.red[tid >> 5] = warp_out;
+  barrier_arrive<kAdded, kListThreads>();
+  cl.started();
+  if (cl.size > 1) cl.arrive();
+  if constexpr (GRAD) {
+    part.load(0, v);
+    barrier_sync<kScales, kListThreads>();
+    const Pair f_c = Pair::both(sh.factor[0]), f_r = Pair::both(-sh.factor[1]), f_a = Pair::both(sh.factor[2]);
+    part.map(v, d, a.vec, edge, [&](Pair f) { return mul2(ex2_pair(fma2(f, f_c, f_r)), f_a); });
+    barrier_arrive<kWritten, kListThreads>();
+  }
+  if (cl.size > 1) cl.wait();
 }
 
 // ------------------------------------------------------------------ the gradient from saved normalisers
@@ -493,11 +523,11 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
   const int split = split_for(nvec, 32);
-  const DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
+  DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
                          reinterpret_cast<const float2*>(norm_in), tail_in, loss, reinterpret_cast<float2*>(norm),
                          tail, d_logits, rows, x->vocab, x->ld, d_ld, x->scale * kLog2e, x->scale, t->scale, t->k,
                          t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld), d_logits == x->data,
-                         static_cast<uint32_t>(split)};
+                         static_cast<uint32_t>(split), 0};
   if (saved) {
     auto* fn = x->dtype == SS_BF16
                    ? distill_grad_kernel<SS_BF16>
@@ -510,12 +540,13 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
     return x->dtype == SS_BF16 ? distill_kernel<SS_BF16, kGrad>
                                : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16, kGrad> : distill_kernel<SS_FP32, kGrad>);
   };
-  auto* fn = d_logits ? pick(std::true_type()) : pick(std::false_type());
   const auto vectors = [&](int n) { return (nvec + n * kRowThreads - 1) / (n * kRowThreads); };
   int cluster = 1;
+  auto* fn = d_logits ? pick(std::true_type()) : pick(std::false_type());
   while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
   const size_t smem = static_cast<size_t>((vectors(cluster) + kBatch - 1) / kBatch) * kRowThreads * sizeof(uint32_t);
   if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
+  a.resident = (d_logits ? 3 : 4) * sm_count() / cluster;
   return launch_rows(fn, rows, cluster, kListThreads, smem, a, stream);
 }
 

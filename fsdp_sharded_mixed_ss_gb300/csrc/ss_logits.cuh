@@ -424,15 +424,20 @@ __device__ __forceinline__ void zero_part(Elem<DT>* d, int64_t n, unsigned rank,
     __stcs(w + i, make_uint4(0u, 0u, 0u, 0u));
 }
 
-// Asks the L2 for the first `bytes` bytes of a row (as many of its whole vectors as that is).
+// Asks the L2 for the first `bytes` bytes of block `rank`'s of `size` equal runs of a row (as many of its whole
+// vectors as that is).
 template <int DT>
-__device__ __forceinline__ void prefetch_row(const Elem<DT>* row, int64_t vocab, int bytes) {
+__device__ __forceinline__ void prefetch_row(const Elem<DT>* row, int64_t vocab, int bytes, int rank = 0, int size = 1) {
   const Slice<DT> sl(row, vocab);
-  const char* p = reinterpret_cast<const char*>(row + sl.head);
-  const int64_t n = min(static_cast<int64_t>(bytes), static_cast<int64_t>(sl.nvec) * 16);
-  constexpr int kPiece = 16384;
-  for (int64_t at = 0; at < n; at += kPiece) prefetch_l2(p + at, static_cast<uint32_t>(min(n - at, static_cast<int64_t>(kPiece))));
+  const int64_t first = static_cast<int64_t>(sl.nvec) * rank / size, last = static_cast<int64_t>(sl.nvec) * (rank + 1) / size;
+  const char* p = reinterpret_cast<const char*>(row + sl.head) + first * 16;
+  const int64_t n = min(static_cast<int64_t>(bytes), (last - first) * 16);
+  constexpr int64_t kPiece = 16384;
+  for (int64_t at = 0; at < n; at += kPiece) prefetch_l2(p + at, static_cast<uint32_t>(min(n - at, kPiece)));
 }
+
+// Asks the L2 for the line at p.
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // SIZE: the number of blocks, or 0 where it is known at run time only.
 template <int DT, int SIZE = 0>
