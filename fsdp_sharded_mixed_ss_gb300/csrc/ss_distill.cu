@@ -56,30 +56,51 @@ struct RowList {
   float q_sum, q_tail;   // Q and q_t
   bool bad;              // an id past the vocabulary
 
-  // The ids and the teacher's values, and the logits on their way. ids_shared: SS_MAX_TOP / 4 int4 of shared memory,
-  // this warp's own.
-  __device__ __forceinline__ void load(const DistillArgs& a, int64_t row, const Elem<DT>* xr, int4* ids_shared) {
+  // The ids and the teacher's values (the list's warp only): all loads first, then what is made of them.
+  __device__ __forceinline__ void start(const DistillArgs& a, int64_t row) {
     const int lane = threadIdx.x & 31;
-    bool past = false;
+    const int64_t at = row * a.k + lane;
+    int64_t given[kSlots];
+    if (a.wide) {
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-      id[i] = -1;
-      lq[i] = x[i] = -kInf;
-      const int j = lane + 32 * i;
-      if (32 * i < a.k) {
-        if (j < a.k) {
-          const int64_t wide_id = load_id(a.ids, row * a.k + j, a.wide);
-          lq[i] = load_teacher(a.teacher, row * a.k + j, a.t_dtype) * a.t_scale;
-          past = past || wide_id >= a.vocab;
-          if (wide_id >= 0 && wide_id < a.vocab) id[i] = static_cast<int32_t>(wide_id);
-        }
-        (&ids_shared[0].x)[j] = id[i];
-      }
+      for (int i = 0; i < kSlots; ++i) given[i] = lane + 32 * i < a.k ? static_cast<const int64_t*>(a.ids)[at + 32 * i] : -1;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) given[i] = lane + 32 * i < a.k ? static_cast<const int32_t*>(a.ids)[at + 32 * i] : -1;
+    }
+    if (a.t_dtype == SS_FP32) {
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        lq[i] = lane + 32 * i < a.k ? static_cast<const float*>(a.teacher)[at + 32 * i] : -kInf;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        lq[i] = lane + 32 * i < a.k ? load_teacher(a.teacher, at + 32 * i, a.t_dtype) : -kInf;
     }
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (id[i] >= 0) x[i] = to_float<DT>(xr[id[i]]);
+    for (int i = 0; i < kSlots; ++i) {
+      id[i] = given[i] < 0 ? -1 : (given[i] >= a.vocab ? INT32_MAX : static_cast<int32_t>(given[i]));
+      lq[i] *= a.t_scale;
+    }
+  }
+  // The ids checked, and their logits on their way. ids_shared: SS_MAX_TOP / 4 int4 of shared memory, this warp's own.
+  __device__ __forceinline__ void look_up(const DistillArgs& a, const Elem<DT>* xr, int4* ids_shared) {
+    const int lane = threadIdx.x & 31;
+    bool past = false;
+    Elem<DT> raw[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      past = past || id[i] == INT32_MAX;
+      if (id[i] == INT32_MAX) id[i] = -1;
+      raw[i] = xr[max(id[i], 0)];
+    }
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      if (32 * i < a.k) (&ids_shared[0].x)[lane + 32 * i] = id[i];
+    }
     bad = __any_sync(0xFFFFFFFFu, past);
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) x[i] = to_float<DT>(raw[i]);
   }
 
   // Drops the slots whose id an earlier slot has: of its own 32, or of those before them.
@@ -221,17 +242,17 @@ constexpr int kAheadBytes = 65536;  // of the row that comes after (loss alone; 
 // The ninth warp's part in a row. `marks`: a word of listed bits for each batch of vectors, by thread.
 template <int DT, bool GRAD>
 __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& cl, const RowPart<DT>& part, int64_t row,
-                                          float w, const Elem<DT>* x, Elem<DT>* d, DistillShared& sh, uint32_t* marks) {
+                                          float w, RowList<DT>& l, const Elem<DT>* x, Elem<DT>* d, DistillShared& sh,
+                                          uint32_t* marks) {
   const int lane = threadIdx.x & 31;
   const float c = a.c;
-  RowList<DT> l;
-  l.load(a, row, x, sh.list_ids);
+  l.look_up(a, x, sh.list_ids);
   barrier_sync<kClear, kListThreads>();
   unsigned mine = 0u;  // slots whose element is this block's
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     int owner, slot;
-    if (l.id[i] >= 0 && part.owns(l.id[i], &owner, &slot)) {
+    if (32 * i < a.k && l.id[i] >= 0 && part.owns(l.id[i], &owner, &slot)) {
       mine |= 1u << i;
       if (slot < 0) atomicOr(&sh.edge_listed, 1u << owner);
       else atomicOr(&marks[(slot / kBatch) * kRowThreads + owner],
@@ -356,10 +377,12 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
   const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
   Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
   const float c = a.c;
+  RowList<DT> l;
+  if (tid >= kRowThreads) l.start(a, row);
   const float w = a.weight ? a.weight[row] : 1.0f;
   if (w == 0.0f) return skip_row<DT, GRAD>(a, cl, row, d);
   const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
-  if (tid >= kRowThreads) return list_warp<DT, GRAD>(a, cl, part, row, w, x, d, sh, marks);
+  if (tid >= kRowThreads) return list_warp<DT, GRAD>(a, cl, part, row, w, l, x, d, sh, marks);
   const int vectors = part.vectors();
   clear_marks(marks, sh, vectors);
   const int64_t sb = part.step_bytes();
@@ -422,6 +445,8 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
   const int64_t row = blockIdx.x / a.split;
   const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
   Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
+  RowList<DT> l;
+  if (tid >= kRowThreads) l.start(a, row);
   const float wt = a.weight ? a.weight[row] : 1.0f, dl = a.d_loss ? a.d_loss[row] : 1.0f;
   const float2 norm = a.norm_in[row];
   if (wt == 0.0f || dl == 0.0f || norm.y == 0.0f) {
@@ -439,8 +464,7 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
     barrier_arrive<kWritten, kListThreads>();
     return;
   }
-  RowList<DT> l;
-  l.load(a, row, x, list_ids);
+  l.look_up(a, x, list_ids);
   l.drop_repeated(a, list_ids);
   l.sums(a);
   const float ws = l.bad ? nan_f() : wt * dl * a.scale;

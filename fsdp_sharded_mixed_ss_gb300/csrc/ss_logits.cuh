@@ -18,6 +18,7 @@
 namespace ss {
 
 constexpr int kRowThreads = 256;
+constexpr int kLog2RowThreads = 8;
 constexpr int kMaxCluster = 8;  // blocks that share a row (the portable cluster size)
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -382,7 +383,7 @@ struct Cluster {
 
 // ------------------------------------------------------------------ a block's part of a row
 //
-// Of a row shared by `size` blocks of T threads, its whole 16-byte vector i
+// Of a row shared by `size` blocks (a power of two) of T threads, its whole 16-byte vector i
 // belongs to thread i mod T of block (i / T) mod size: a warp reads 512
 // consecutive bytes, and neighbouring ids are spread over threads and blocks.
 // The fewer than 8 elements before the first boundary and after the last vector
@@ -439,22 +440,27 @@ __device__ __forceinline__ void prefetch_row(const Elem<DT>* row, int64_t vocab,
 // Asks the L2 for the line at p.
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// SIZE: the number of blocks, or 0 where it is known at run time only.
-template <int DT, int SIZE = 0>
+__device__ __forceinline__ int log2_of(unsigned power) { return 31 - __clz(static_cast<int>(power)); }
+
+template <int DT>
 struct RowPart {
   static constexpr int V = kVecOf<DT>;
   const Elem<DT>* x;
   Slice<DT> sl;
-  int rank, blocks;
+  int rank, blocks, log2_blocks;
   int first;  // this thread's vectors: first, first + step(), ... < nvec
   int whole;  // vectors that every thread of every block has
   int edge;   // this thread's element outside the vectors, or -1
 
   __device__ __forceinline__ RowPart(const Elem<DT>* row, int64_t vocab, unsigned rank_, unsigned size_)
-      : x(row), sl(row, vocab), rank(static_cast<int>(rank_)), blocks(static_cast<int>(size_)) {
+      : x(row),
+        sl(row, vocab),
+        rank(static_cast<int>(rank_)),
+        blocks(static_cast<int>(size_)),
+        log2_blocks(log2_of(size_)) {
     const int t = threadIdx.x;
     first = rank * kRowThreads + t;
-    whole = sl.nvec / step();
+    whole = sl.nvec >> (kLog2RowThreads + log2_blocks);
     edge = -1;
     if (rank == 0) {
       const int after = t - 8;
@@ -462,8 +468,7 @@ struct RowPart {
       else if (after >= 0 && after < sl.n - sl.tail()) edge = sl.tail() + after;
     }
   }
-  __device__ __forceinline__ int size() const { return SIZE ? SIZE : blocks; }
-  __device__ __forceinline__ int step() const { return size() * kRowThreads; }
+  __device__ __forceinline__ int step() const { return blocks * kRowThreads; }
   __device__ __forceinline__ int64_t step_bytes() const { return static_cast<int64_t>(step()) * 16; }
   // Vectors of the thread that has most.
   __device__ __forceinline__ int vectors() const { return whole + (whole * step() < sl.nvec ? 1 : 0); }
@@ -488,8 +493,8 @@ struct RowPart {
     }
     const int i = o / V, q = i / kRowThreads;
     *thread = i % kRowThreads;
-    *j = q / size();
-    return q % size() == rank;
+    *j = q >> log2_blocks;
+    return (q & (blocks - 1)) == rank;
   }
   // The thread's vectors number j0 .. j0 + kBatch - 1 (those past its last one are left as they are).
   __device__ __forceinline__ void load(int j0, uint4 (&w)[kBatch]) const {
@@ -608,10 +613,12 @@ inline ss_status check_grad_out(const ss_logits* x, int64_t x_bytes, const void*
   return SS_OK;
 }
 
-// Blocks that share a row where nothing is exchanged between them: parts of `vectors` vectors a thread.
+// Blocks that share a row where nothing is exchanged between them (a power of two): parts of at most `vectors` vectors
+// a thread.
 inline int split_for(int64_t nvec, int vectors) {
-  const int64_t part = static_cast<int64_t>(vectors) * kRowThreads;
-  return static_cast<int>(std::max<int64_t>(1, (nvec + part - 1) / part));
+  int64_t split = 1;
+  while (split * vectors * kRowThreads < nvec) split *= 2;
+  return static_cast<int>(split);
 }
 
 // Launches `clusters` clusters of `cluster` blocks (a plain launch for 1).
