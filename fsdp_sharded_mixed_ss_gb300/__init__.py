@@ -531,7 +531,8 @@ def ss_distill_topk(logits, ids, teacher, loss=None, *, norm=None, tail_logprob=
     ids (rows, k) int32 or int64 (negative: unused slot), teacher (rows, k) their log probabilities (bf16, fp16 or
     fp32; times teacher_scale), k <= SS_MAX_TOP. tail: what the list leaves out is dropped, the list is renormalised,
     or the rest of the mass is one more outcome (SS_TAIL_*). loss, norm (rows, 2) and tail_logprob are optional
-    outputs; the last two are what ss_distill_topk_grad takes. Rows of weight 0 are not read.
+    outputs; the last two are what ss_distill_topk_grad takes. Rows of weight 0 give
+    zeros, whatever their logits.
     """
     x, r, v, dt = _rows_of(logits, shape, ld, dtype, scale)
     t = _teacher_of(r, ids, teacher, row_weight, tail, teacher_scale, k, idtype, tdtype)

@@ -380,11 +380,8 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
   RowList<DT> l;
   if (tid >= kRowThreads) l.start(a, row);
   const float w = a.weight ? a.weight[row] : 1.0f;
-  if (w == 0.0f) return skip_row<DT, GRAD>(a, cl, row, d);
   const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
-  if (tid >= kRowThreads) return list_warp<DT, GRAD>(a, cl, part, row, w, l, x, d, sh, marks);
   const int vectors = part.vectors();
-  clear_marks(marks, sh, vectors);
   const int64_t sb = part.step_bytes();
   const char* src = part.at();
   auto fetch = [&](const char* p, int j, uint4 (&v)[kBatch]) {
@@ -399,7 +396,10 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
     }
   };
   uint4 v[kBatch];
-  fetch(src, 0, v);
+  if (tid < kRowThreads) fetch(src, 0, v);  // on its way while the weight is
+  if (w == 0.0f) return skip_row<DT, GRAD>(a, cl, row, d);
+  if (tid >= kRowThreads) return list_warp<DT, GRAD>(a, cl, part, row, w, l, x, d, sh, marks);
+  clear_marks(marks, sh, vectors);
   const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
   barrier_sync<kReady, kListThreads>();
   const bool edge_out = part.edge >= 0 && !((sh.edge_listed >> tid) & 1u);
@@ -449,14 +449,14 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
   if (tid >= kRowThreads) l.start(a, row);
   const float wt = a.weight ? a.weight[row] : 1.0f, dl = a.d_loss ? a.d_loss[row] : 1.0f;
   const float2 norm = a.norm_in[row];
+  const RowPart<DT> part(x, a.vocab, rank, a.split);
+  uint4 first[kBatch];
+  if (tid < kRowThreads) part.load(0, first);  // on its way while the row's scalars are
   if (wt == 0.0f || dl == 0.0f || norm.y == 0.0f) {
     if (tid < kRowThreads) zero_part<DT>(d, a.vocab, rank, a.split);
     return;
   }
-  const RowPart<DT> part(x, a.vocab, rank, a.split);
   if (tid < kRowThreads) {
-    uint4 first[kBatch];
-    part.load(0, first);
     const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : 0.0f;
     barrier_sync<kScales, kListThreads>();
     const Pair c = Pair::both(factor[0]), r = Pair::both(-factor[1]), A = Pair::both(factor[2]);

@@ -394,18 +394,16 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   const int64_t row = blockIdx.x / cl.size;
   const RowPart<DT> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl.rank, cl.size);
   const float edge = part.edge >= 0 ? to_float<DT>(part.x[part.edge]) : -kInf;
-  // the row's token and its logit are on their way from the start
+  // the row's token comes beside the pass, its logit beside the sums
   const bool writes = cl.rank == 0 && tid == kRowThreads - 1;
   int64_t token = -1;
-  float token_x = 0.0f;
-  if (writes && a.logprob) {
-    token = load_id(a.tokens, row, a.wide);
-    if (token >= 0 && token < a.vocab) token_x = to_float<DT>(part.x[token]);
-  }
+  if (writes && a.logprob) token = load_id(a.tokens, row, a.wide);
   float thread_max;
   float(*unit)[kRowThreads] = nullptr;
   if constexpr (TOPS) unit = tops.unit;
-  RowSum acc = block_merge(stream_row<DT, TOPS>(part, a.c, edge, unit, &thread_max), a.c, red);
+  const RowSum mine_sum = stream_row<DT, TOPS>(part, a.c, edge, unit, &thread_max);
+  const Elem<DT> token_x = token >= 0 && token < a.vocab ? part.x[token] : Elem<DT>(0);
+  RowSum acc = block_merge(mine_sum, a.c, red);
   if (TOPS && cl.size == 1 && tid == 0 && row + a.resident < a.rows)
     prefetch_row<DT>(static_cast<const Elem<DT>*>(a.x) + (row + a.resident) * a.ld, a.vocab, kAheadBytes);
   cl.started();
@@ -425,11 +423,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
   if (TOPS || cl.size > 1) cl.sync();
   if (cl.size > 1) acc = merge_lanes(parts[tid % cl.size], a.c, static_cast<int>(cl.size));
   const RowValues v(acc, a.scale);
-  if (writes) v.write(a, row, token, token_x);
-  if constexpr (TOPS) {
+  if constexpr (!TOPS) {
+    if (writes) v.write(a, row, token, to_float<DT>(token_x));
+  } else {
     const int k = a.top_k;
     const TopOut out = {a.top_logprob, a.top_id, row * k, a.wide};
     if (v.nan) {  // in every block of the cluster: all have merged the same parts
+      if (writes) v.write(a, row, token, to_float<DT>(token_x));
       if (cl.rank == 0 && tid < k) out.put(tid, -1, nan_f());
       return;
     }
@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     const int room = kCand / static_cast<int>(cl.size);
     uint64_t* mine = cl.at(tops.cand, 0) + cl.rank * room;
     int found = collect<DT>(part, wanted, tops, mine, room);
+    if (writes) v.write(a, row, token, to_float<DT>(token_x));
     if (found > room) {  // this block's own k best instead
       select_through_buffer<DT>(part, tops, wanted.few ? kMaskedKey + 1 : tops.tau, k);
       if (tid < k) mine[tid] = tops.best[tid];

@@ -375,7 +375,7 @@ typedef struct ss_teacher {
  *   of them or d_logits is given. norm and tail_logprob (log p_t, in any tail
  *   mode) are what ss_distill_topk_grad takes.
  * d_logits, d_ld: as in ss_token_logprobs_grad; may be x itself.
- * A row of weight 0 is not read: its loss, norm, tail_logprob and gradient are
+ * A row of weight 0, whatever its logits: loss, norm, tail_logprob and gradient
  * 0. A masked-out row: loss +inf when the teacher gives any mass (else as the
  * formula), gradient 0. */
 ss_status ss_distill_topk(const ss_logits* x, const ss_teacher* teacher, float* loss, float* norm,
@@ -383,8 +383,8 @@ ss_status ss_distill_topk(const ss_logits* x, const ss_teacher* teacher, float* 
 
 /* ss_distill_topk_grad: d_logits = d_loss_r times the gradient above (d_loss
  * [rows] or NULL: all 1), from the norm and, with SS_TAIL_BUCKET, the
- * tail_logprob that ss_distill_topk wrote. Rows with row_weight or d_loss 0 are
- * not read and get zeros. */
+ * tail_logprob that ss_distill_topk wrote. Rows with row_weight or d_loss 0
+ * get zeros, whatever their logits. */
 ss_status ss_distill_topk_grad(const ss_logits* x, const ss_teacher* teacher, const float* norm,
                                const float* tail_logprob, const float* d_loss, void* d_logits, int64_t d_ld,
                                void* stream);
