@@ -18,7 +18,6 @@
 namespace ss {
 
 constexpr int kRowThreads = 256;
-constexpr int kLog2RowThreads = 8;
 constexpr int kMaxCluster = 8;  // blocks that share a row (the portable cluster size)
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -316,12 +315,12 @@ __device__ __forceinline__ Sum merge_lanes(Sum a, float c, int width = 32) {
 constexpr int kRowWarps = kRowThreads / 32;
 
 // Merged over the block, the same in every thread. `red`: a slot per warp, used by one call only.
-template <class Sum>
+template <int WARPS = kRowWarps, class Sum>
 __device__ __forceinline__ Sum block_merge(Sum a, float c, Sum* red) {
   a = merge_lanes(a, c);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
   __syncthreads();
-  return merge_lanes(red[threadIdx.x % kRowWarps], c, kRowWarps);
+  return merge_lanes(red[threadIdx.x % WARPS], c, WARPS);
 }
 
 __device__ __forceinline__ int64_t load_id(const void* p, int64_t i, bool wide) {
@@ -442,7 +441,7 @@ __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("pre
 
 __device__ __forceinline__ int log2_of(unsigned power) { return 31 - __clz(static_cast<int>(power)); }
 
-template <int DT>
+template <int DT, int T = kRowThreads>
 struct RowPart {
   static constexpr int V = kVecOf<DT>;
   const Elem<DT>* x;
@@ -459,8 +458,8 @@ struct RowPart {
         blocks(static_cast<int>(size_)),
         log2_blocks(log2_of(size_)) {
     const int t = threadIdx.x;
-    first = rank * kRowThreads + t;
-    whole = sl.nvec >> (kLog2RowThreads + log2_blocks);
+    first = rank * T + t;
+    whole = sl.nvec / T >> log2_blocks;
     edge = -1;
     if (rank == 0) {
       const int after = t - 8;
@@ -468,7 +467,7 @@ struct RowPart {
       else if (after >= 0 && after < sl.n - sl.tail()) edge = sl.tail() + after;
     }
   }
-  __device__ __forceinline__ int step() const { return blocks * kRowThreads; }
+  __device__ __forceinline__ int step() const { return blocks * T; }
   __device__ __forceinline__ int64_t step_bytes() const { return static_cast<int64_t>(step()) * 16; }
   // Vectors of the thread that has most.
   __device__ __forceinline__ int vectors() const { return whole + (whole * step() < sl.nvec ? 1 : 0); }
@@ -491,8 +490,8 @@ struct RowPart {
       *thread = o < 0 ? id : id - sl.tail() + 8;
       return rank == 0;
     }
-    const int i = o / V, q = i / kRowThreads;
-    *thread = i % kRowThreads;
+    const int i = o / V, q = i / T;
+    *thread = i % T;
     *j = q >> log2_blocks;
     return (q & (blocks - 1)) == rank;
   }

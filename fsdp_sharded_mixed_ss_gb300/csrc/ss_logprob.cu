@@ -43,7 +43,12 @@ struct LogprobArgs {
 constexpr int kAheadBytes = 32768;  // of the row that comes after (0, 32, 64, 128 KB measured: 129.5, 126.4, 127.9, 132.9 us)
 constexpr int kUnits = 16;      // maxima kept per thread
 constexpr int kFlagged = 1024;  // units that are read again
-constexpr int kUnitPairs = kUnits * kRowThreads / 2;  // the units' memory as a buffer of pairs, once they are done with
+constexpr int kKeys = 256;
+constexpr int kManyThreads = 128;  // threads of a block that selects alternatives of one of many rows
+#ifndef SS_MANY
+#define SS_MANY 6
+#endif
+constexpr int kManyRows = SS_MANY;  // that many rows an SM
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
 
 using RunningSum = Running<RowSum, 8>;
@@ -89,14 +94,24 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, Runni
   return m;
 }
 
-// The pass over a thread's vectors; `unit` (with TOPS) receives its units' maxima. `units`: how many, `unit_batches`:
-// of how many batches each (both the same for all threads).
-template <int DT, bool TOPS>
-__device__ __forceinline__ RowSum stream_row(const RowPart<DT>& part, float c, float edge, float (*unit)[kRowThreads],
+// Batches in a unit, and units of each thread (the same for all).
+template <class Part>
+__device__ __forceinline__ int part_unit_batches(const Part& part) {
+  return ((part.vectors() + kBatch - 1) / kBatch + kUnits - 1) / kUnits;
+}
+template <class Part>
+__device__ __forceinline__ int part_units(const Part& part) {
+  const int batches = (part.vectors() + kBatch - 1) / kBatch, each = part_unit_batches(part);
+  return each > 0 ? (batches + each - 1) / each : 0;
+}
+
+// The pass over a thread's vectors; `unit` (with TOPS) receives its units' maxima.
+template <int DT, bool TOPS, int T>
+__device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c, float edge, float (*unit)[T],
                                              float* thread_max) {
   const int full = part.whole / kBatch;  // batches that every thread has whole
   const int batches = (part.vectors() + kBatch - 1) / kBatch;
-  const int unit_batches = (batches + kUnits - 1) / kUnits;
+  const int unit_batches = part_unit_batches(part);
   const int64_t sb = part.step_bytes();
   const char* src = part.at();
   RunningSum run(one_element<RowSum>(edge), c);
@@ -128,15 +143,16 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT>& part, float c, f
   return run.done(c);
 }
 
-constexpr int kCand = 2048;
+template <int T>
 struct TopShared {
-  float unit[kUnits][kRowThreads];
+  static constexpr int kCand = 8 * T;
+  float unit[kUnits][T];
   uint64_t cand[kCand];  // block 0's is used, shared out over the cluster's blocks
   uint64_t best[SS_MAX_TOP];
-  uint32_t keys[kRowThreads];
+  uint32_t keys[kKeys];
   uint16_t flagged[kFlagged];
   int count[kMaxCluster];  // candidates of every block
-  int warp_sums[kRowWarps];
+  int warp_sums[T / 32];
   uint32_t tau;
   int n, n_flagged;
 };
@@ -147,9 +163,9 @@ struct NoTops {};
 template <int DT>
 __device__ __forceinline__ uint32_t find_threshold(const uint32_t* key, uint32_t top_key, int k) {
   constexpr int kLowBit = DT == SS_BF16 ? 16 : (DT == SS_FP16 ? 13 : 0);
-  uint32_t keys[kRowWarps];
+  uint32_t keys[kKeys / 32];
 #pragma unroll
-  for (int i = 0; i < kRowWarps; ++i) keys[i] = key[(threadIdx.x & 31) + 32 * i];
+  for (int i = 0; i < kKeys / 32; ++i) keys[i] = key[(threadIdx.x & 31) + 32 * i];
   uint32_t t = 0;
 #pragma unroll 1
   for (int bit = 31; bit >= kLowBit; --bit) {
@@ -157,7 +173,7 @@ __device__ __forceinline__ uint32_t find_threshold(const uint32_t* key, uint32_t
     if (next > top_key) continue;
     int c[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kRowWarps; ++i) c[i & 1] += keys[i] >= next ? 1 : 0;
+    for (int i = 0; i < kKeys / 32; ++i) c[i & 1] += keys[i] >= next ? 1 : 0;
     const int all = __reduce_add_sync(0xFFFFFFFFu, c[0] + c[1]);
     if (all >= k) {
       t = next;
@@ -180,14 +196,12 @@ struct Wanted {
 
 // The part's candidates into out[0, room); returns their number, to all threads (above `room`: they did not fit).
 // s.n and s.n_flagged are zero before; s is the caller's again when this returns.
-template <int DT>
-__device__ __forceinline__ int collect(const RowPart<DT>& part, const Wanted& wanted, TopShared& s, uint64_t* out,
+template <int DT, int T>
+__device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted& wanted, TopShared<T>& s, uint64_t* out,
                                        int room) {
   constexpr int V = kVecOf<DT>;
   const int tt = threadIdx.x, lane = tt & 31;
-  const int batches = (part.vectors() + kBatch - 1) / kBatch;
-  const int unit_batches = (batches + kUnits - 1) / kUnits;
-  const int units = unit_batches > 0 ? (batches + unit_batches - 1) / unit_batches : 0;
+  const int unit_batches = part_unit_batches(part), units = part_units(part);
   unsigned mask = 0u;  // this thread's flagged units
   for (int u = 0; u < units; ++u) mask |= wanted(s.unit[u][tt]) ? 1u << u : 0u;
   int before = __popc(mask);
@@ -200,7 +214,7 @@ __device__ __forceinline__ int collect(const RowPart<DT>& part, const Wanted& wa
   if (lane == 31 && before > 0) base = atomicAdd(&s.n_flagged, before);
   base = __shfl_sync(0xFFFFFFFFu, base, 31) + before - __popc(mask);
   for (; mask != 0u; mask &= mask - 1u, ++base)
-    if (base < kFlagged) s.flagged[base] = static_cast<uint16_t>((__ffs(mask) - 1) * kRowThreads + tt);
+    if (base < kFlagged) s.flagged[base] = static_cast<uint16_t>((__ffs(mask) - 1) * T + tt);
   if (part.rank == 0 && tt < 16) {  // the elements outside the vectors
     const int id = tt < 8 ? (tt < part.sl.head ? tt : -1)
                           : (tt - 8 < part.sl.n - part.sl.tail() ? part.sl.tail() + tt - 8 : -1);
@@ -218,17 +232,17 @@ __device__ __forceinline__ int collect(const RowPart<DT>& part, const Wanted& wa
   const int per_unit = unit_batches * kBatch;
   const int items = min(s.n_flagged, kFlagged) * per_unit;
 #pragma unroll 1
-  for (int i0 = tt; i0 < items; i0 += kAgain * kRowThreads) {
+  for (int i0 = tt; i0 < items; i0 += kAgain * T) {
     uint4 w[kAgain];
     int at[kAgain];
 #pragma unroll
     for (int q = 0; q < kAgain; ++q) {
-      const int i = i0 + q * kRowThreads;
+      const int i = i0 + q * T;
       at[q] = -1;
       if (i < items) {
         const int f = s.flagged[i / per_unit];
-        const int64_t vec = static_cast<int64_t>((f / kRowThreads) * per_unit + i % per_unit) * part.step() +
-                            part.rank * kRowThreads + f % kRowThreads;
+        const int64_t vec = static_cast<int64_t>((f / T) * per_unit + i % per_unit) * part.step() +
+                            part.rank * T + f % T;
         if (vec < part.sl.nvec) {
           at[q] = static_cast<int>(vec);
           w[q] = __ldg(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec);
@@ -261,13 +275,14 @@ __device__ __forceinline__ int collect(const RowPart<DT>& part, const Wanted& wa
 }
 
 // The k largest of the part's pairs that reach the threshold, into s.best[0, k) in order: the elements go through a
-// buffer of kUnitPairs (the units' memory), which is cut to its k best, and the bound raised to the last of them,
+// buffer of pairs (the units' memory), which is cut to its k best, and the bound raised to the last of them,
 // whenever it is full. At least k of the part's pairs reach the threshold. Ascending ids make ties cheap: a later one
 // is below the bound. How full the buffer is, each thread counts for itself (`n`, from block-wide counts), so all
 // decide alike; s.n only hands out places.
-template <int DT>
-__device__ __noinline__ void select_through_buffer(const RowPart<DT>& part, TopShared& s, uint32_t tau, int k) {
+template <int DT, int T>
+__device__ __noinline__ void select_through_buffer(const RowPart<DT, T>& part, TopShared<T>& s, uint32_t tau, int k) {
   constexpr int V = kVecOf<DT>;
+  constexpr int kUnitPairs = kUnits * T / 2;
   const int tt = threadIdx.x;
   uint64_t* buffer = reinterpret_cast<uint64_t*>(s.unit);
   uint64_t bound = static_cast<uint64_t>(tau) << 32;  // pairs above it are wanted
@@ -275,21 +290,21 @@ __device__ __noinline__ void select_through_buffer(const RowPart<DT>& part, TopS
   if (tt == 0) s.n = 0;
   __syncthreads();
   auto cut = [&] {  // the buffer to its k best (n >= k), the bound to the k-th
-    for (int i = tt; i < n; i += kRowThreads) {
+    for (int i = tt; i < n; i += T) {
       const uint64_t mine = buffer[i];
       int above = 0;
       for (int j = 0; j < n; ++j) above += buffer[j] > mine ? 1 : 0;
       if (above < k) s.best[above] = mine;
     }
     __syncthreads();
-    for (int i = tt; i < k; i += kRowThreads) buffer[i] = s.best[i];
+    for (int i = tt; i < k; i += T) buffer[i] = s.best[i];
     if (tt == 0) s.n = k;
     bound = s.best[k - 1];
     n = k;
     __syncthreads();
   };
   auto step = [&](bool there, float f, int id) {  // one element of every thread
-    if (n + kRowThreads > kUnitPairs) cut();
+    if (n + T > kUnitPairs) cut();
     const uint64_t pair = order_pair(f, id);
     const bool enters = there && pair > bound;
     if (enters) buffer[atomicAdd(&s.n, 1)] = pair;
@@ -361,11 +376,11 @@ struct RowValues {
 };
 
 // Masked tokens by ascending id into the places from `have` on.
-template <int DT>
+template <int DT, int T>
 __device__ __forceinline__ void put_masked(const Elem<DT>* x, int64_t vocab, int have, int k, const TopOut& out,
                                            int* warp_sums) {
   const int tt = threadIdx.x;
-  for (int64_t base = 0; base < vocab && have < k; base += kRowThreads) {
+  for (int64_t base = 0; base < vocab && have < k; base += T) {
     const int64_t i = base + tt;
     const bool masked = i < vocab && to_float<DT>(x[i]) == -kInf;
     const unsigned votes = __ballot_sync(0xFFFFFFFFu, masked);
@@ -373,7 +388,7 @@ __device__ __forceinline__ void put_masked(const Elem<DT>* x, int64_t vocab, int
     if ((tt & 31) == 0) warp_sums[tt >> 5] = __popc(votes);
     __syncthreads();
     int before = have;
-    for (int w = 0; w < kRowWarps; ++w) {
+    for (int w = 0; w < (T / 32); ++w) {
       if (w < tt >> 5) before += warp_sums[w];
       have += warp_sums[w];
     }
@@ -382,28 +397,29 @@ __device__ __forceinline__ void put_masked(const Elem<DT>* x, int64_t vocab, int
   }
 }
 
-template <int DT, bool TOPS>
-__global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_constant__ LogprobArgs a) {
-  __shared__ RowSum red[kRowWarps];
+// T: threads of a block; 128 for alternatives of many rows, without clusters.
+template <int DT, bool TOPS, int T>
+__global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+  __shared__ RowSum red[T / 32];
   __shared__ RowSum parts[kMaxCluster];
-  __shared__ std::conditional_t<TOPS, TopShared, NoTops> tops;
-  const Cluster cl = Cluster::start();
+  __shared__ std::conditional_t<TOPS, TopShared<T>, NoTops> tops;
+  const Cluster cl = T == kRowThreads ? Cluster::start() : Cluster{1, 0};
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / cl.size;
-  const RowPart<DT> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl.rank, cl.size);
+  const RowPart<DT, T> part(static_cast<const Elem<DT>*>(a.x) + row * a.ld, a.vocab, cl.rank, cl.size);
   const float edge = part.edge >= 0 ? to_float<DT>(part.x[part.edge]) : -kInf;
   // the row's token comes beside the pass, its logit beside the sums
-  const bool writes = cl.rank == 0 && tid == kRowThreads - 1;
+  const bool writes = cl.rank == 0 && tid == T - 1;
   int64_t token = -1;
   if (writes && a.logprob) token = load_id(a.tokens, row, a.wide);
   float thread_max;
-  float(*unit)[kRowThreads] = nullptr;
+  float(*unit)[T] = nullptr;
   if constexpr (TOPS) unit = tops.unit;
-  const RowSum mine_sum = stream_row<DT, TOPS>(part, a.c, edge, unit, &thread_max);
+  const RowSum mine_sum = stream_row<DT, TOPS, T>(part, a.c, edge, unit, &thread_max);
   const Elem<DT> token_x = token >= 0 && token < a.vocab ? part.x[token] : Elem<DT>(0);
-  RowSum acc = block_merge(mine_sum, a.c, red);
+  RowSum acc = block_merge<T / 32>(mine_sum, a.c, red);
   if (TOPS && cl.size == 1 && tid == 0 && row + a.resident < a.rows)
     prefetch_row<DT>(static_cast<const Elem<DT>*>(a.x) + (row + a.resident) * a.ld, a.vocab, kAheadBytes);
   cl.started();
@@ -411,12 +427,23 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     if (tid < cl.size) cl.at(parts, tid)[cl.rank] = acc;
   }
   if constexpr (TOPS) {
-    // 256 keys of the whole row: the maxima of groups of `size` neighbouring threads of every block
-    uint32_t key = order_key(thread_max);
-    for (unsigned off = 1; off < cl.size; off <<= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
-    if (tid % cl.size == 0) {
-      const unsigned at = cl.rank * (kRowThreads / cl.size) + tid / cl.size;
-      for (unsigned r = 0; r < cl.size; ++r) cl.at(tops.keys, r)[at] = key;
+    if constexpr (T == kRowThreads) {
+      // 256 keys of the whole row: the maxima of groups of `size` neighbouring threads of every block
+      uint32_t key = order_key(thread_max);
+      for (unsigned off = 1; off < cl.size; off <<= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+      if (tid % cl.size == 0) {
+        const unsigned at = cl.rank * (kKeys / cl.size) + tid / cl.size;
+        for (unsigned r = 0; r < cl.size; ++r) cl.at(tops.keys, r)[at] = key;
+      }
+    } else {
+      // kKeys / T keys a thread, of every so many units
+      const int units = part_units(part);
+#pragma unroll
+      for (int s = 0; s < kKeys / T; ++s) {
+        float m = s == 0 ? edge : -kInf;
+        for (int u = s; u < units; u += kKeys / T) m = fmaxf(m, tops.unit[u][tid]);
+        tops.keys[s * T + tid] = order_key(m);
+      }
     }
     if (tid == 0) tops.n = tops.n_flagged = 0;
   }
@@ -439,12 +466,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     }
     __syncthreads();
     const Wanted wanted(tops.tau);
-    const int room = kCand / static_cast<int>(cl.size);
+    const int room = TopShared<T>::kCand / static_cast<int>(cl.size);
     uint64_t* mine = cl.at(tops.cand, 0) + cl.rank * room;
-    int found = collect<DT>(part, wanted, tops, mine, room);
+    int found = collect<DT, T>(part, wanted, tops, mine, room);
     if (writes) v.write(a, row, token, to_float<DT>(token_x));
     if (found > room) {  // this block's own k best instead
-      select_through_buffer<DT>(part, tops, wanted.few ? kMaskedKey + 1 : tops.tau, k);
+      select_through_buffer<DT, T>(part, tops, wanted.few ? kMaskedKey + 1 : tops.tau, k);
       if (tid < k) mine[tid] = tops.best[tid];
       found = k;
     }
@@ -453,7 +480,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
     if (cl.rank != 0) return;
     int total = 0;
     for (unsigned r = 0; r < cl.size; ++r) total += tops.count[r];
-    for (int i = tid; i < total; i += kRowThreads) {
+    for (int i = tid; i < total; i += T) {
       int r = 0, at = i;
       while (at >= tops.count[r]) at -= tops.count[r++];
       const uint64_t pair = tops.cand[r * room + at];
@@ -464,7 +491,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_co
         out.put(place, static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(pair)),
                 v.logp(key_value(static_cast<uint32_t>(pair >> 32))));
     }
-    if (wanted.few && total < k) put_masked<DT>(part.x, a.vocab, total, k, out, tops.warp_sums);
+    if (wanted.few && total < k) put_masked<DT, T>(part.x, a.vocab, total, k, out, tops.warp_sums);
   }
 }
 
@@ -606,17 +633,24 @@ ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype id
   ranges.add(out->top_logprob, rows * top_k * 4, true);
   ranges.add(out->top_id, rows * top_k * ib, true);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
-  const LogprobArgs a = {x->data, tokens, out->logprob, out->entropy, out->lse,
+  LogprobArgs a = {x->data, tokens, out->logprob, out->entropy, out->lse,
                          reinterpret_cast<float2*>(out->norm), out->top_logprob, out->top_id,
                          rows, x->vocab, x->ld, x->scale * kLog2e, x->scale, top_k, idtype == SS_I64, 4 * sm_count()};
-  const auto pick = [&](auto tops) {
+  const auto pick = [&](auto tops, auto threads) {
     constexpr bool kTops = decltype(tops)::value;
-    return x->dtype == SS_BF16 ? logprob_kernel<SS_BF16, kTops>
-                               : (x->dtype == SS_FP16 ? logprob_kernel<SS_FP16, kTops> : logprob_kernel<SS_FP32, kTops>);
+    constexpr int T = decltype(threads)::value;
+    return x->dtype == SS_BF16 ? logprob_kernel<SS_BF16, kTops, T>
+                               : (x->dtype == SS_FP16 ? logprob_kernel<SS_FP16, kTops, T> : logprob_kernel<SS_FP32, kTops, T>);
   };
-  const int cluster = cluster_for(rows, x->vocab, x->dtype == SS_FP32 ? 4 : 8);
-  auto* fn = top_k > 0 ? pick(std::true_type()) : pick(std::false_type());
+  constexpr std::integral_constant<int, kRowThreads> wide_block;
+  constexpr std::integral_constant<int, kManyThreads> small_block;
+  const int vec = x->dtype == SS_FP32 ? 4 : 8, cluster = cluster_for(rows, x->vocab, vec);
   if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
+  if (top_k > 0 && rows >= kManyRows * sm_count() && x->vocab / vec >= 8 * kBatch * kManyThreads) {
+    a.resident = 8 * sm_count();
+    return launch_rows(pick(std::true_type(), small_block), rows, 1, kManyThreads, 0, a, stream);
+  }
+  auto* fn = top_k > 0 ? pick(std::true_type(), wide_block) : pick(std::false_type(), wide_block);
   return launch_rows(fn, rows, cluster, kRowThreads, 0, a, stream);
 }
 

@@ -162,6 +162,24 @@ def test_logprobs_ties_everywhere(ss, rows, dtype):
     _check_logprobs(ss, x, torch.full((rows,), 40001, device="cuda"), 128)
 
 
+@pytest.mark.parametrize("dtype,vocab,k", [("bf16", 33001, 128), ("fp16", 40007, 5), ("fp32", 16390, 64)])
+def test_logprobs_many_rows(ss, dtype, vocab, k):
+    """More rows than the GPU has places for, with rows among them that are masked, all ties or hold NaN."""
+    rows = 1300
+    x = _logits(rows, vocab, dtype, pad=3, seed=9)
+    x[10] = -float("inf")
+    x[11] = torch.finfo(TYPES[dtype]).min
+    x[12, 7:] = -float("inf")
+    x[13] = 0.0
+    x[14, ::3] = -float("inf")
+    x[15, 5] = float("nan")
+    x[16] = (torch.arange(vocab, device="cuda") % 3).to(x.dtype)
+    x[17] = torch.linspace(-9, 9, vocab, device="cuda").to(x.dtype)
+    x[1299, : vocab // 2] = -float("inf")
+    tok = torch.arange(rows, device="cuda") * 31 % vocab
+    _check_logprobs(ss, x, tok, k)
+
+
 def test_logprobs_optional_outputs(ss):
     x = _logits(6, 777, "bf16")
     tok = torch.arange(6, device="cuda")
