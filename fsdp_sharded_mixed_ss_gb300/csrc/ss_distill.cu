@@ -24,7 +24,7 @@ struct DistillArgs {
   float* tail;
   void* d;
   int64_t rows, vocab, ld, d_ld;
-  float c, scale, t_scale;
+  float c, eps, scale, t_scale;
   int32_t k, mode, t_dtype;
   bool wide, vec, in_place;
   uint32_t split;    // gradient from saved normalisers: blocks that share a row
@@ -45,6 +45,10 @@ __device__ __forceinline__ float load_teacher(const void* p, int64_t i, int dtyp
 
 constexpr int kListThreads = kRowThreads + 32;  // the row's warps and the list's
 constexpr int kSlots = SS_MAX_TOP / 32;
+
+struct RowMass {
+  float m, s;
+};
 
 template <int DT>
 struct RowList {
@@ -124,24 +128,27 @@ struct RowList {
     }
   }
 
-  __device__ __forceinline__ static RowMass mass(const float (&v)[kSlots], float c) {
-    RowMass m = one_element<RowMass>(v[0]);
+  // max and sum of exp(scale (v - max)) over the list; -inf for masked or unused slots, NaN sum for NaN and +inf.
+  __device__ __forceinline__ static RowMass mass(const float (&v)[kSlots], float scale) {
+    float m = v[0];
 #pragma unroll
-    for (int i = 1; i < kSlots; ++i) {
-      RowMass o = one_element<RowMass>(v[i]);
-      if (o.m > m.m) m.move(o.m, c);
-      else if (m.m > o.m) o.move(m.m, c);
-      m.s += o.s;
-    }
-    return merge_lanes(m, c);
+    for (int i = 1; i < kSlots; ++i) m = fmaxf(m, v[i]);
+    m = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(m == m ? m : -kInf)));
+    const float ref = m == -kInf ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) s += expf((v[i] - ref) * scale);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    return {m, s};
   }
 
-  __device__ __forceinline__ void mass_in(const DistillArgs& a) { in = mass(x, a.c); }
+  __device__ __forceinline__ void mass_in(const DistillArgs& a) { in = mass(x, a.scale); }
   // log q, q, Q and q_t.
   __device__ __forceinline__ void sums(const DistillArgs& a) {
     q_sum = q_tail = 0.0f;
     if (a.mode == SS_TAIL_RENORM) {
-      const RowMass t = mass(lq, kLog2e);
+      const RowMass t = mass(lq, 1.0f);
       const float shift = t.s == 0.0f ? 0.0f : t.m + logf(t.s);
       q_sum = t.s == t.s ? (t.s == 0.0f ? 0.0f : 1.0f) : t.s;
 #pragma unroll
@@ -209,7 +216,7 @@ __device__ __forceinline__ void mask_elements(uint4& w, uint32_t bits) {
   }
 }
 
-using RunningMass = Running<RowMass, 40>;
+using RunningMass = Running<40>;
 
 // A batch of vectors into the running sum.
 template <int DT>
@@ -218,20 +225,26 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
 #pragma unroll
   for (int u = 1; u < kBatch; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
   acc.see(m, c);
-  Pair s = Pair::both(0.0f);
+  Pair s = Pair::both(0.0f), t = s;
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
     Pair f[kPairsOf<DT>];
     unpack_pairs<DT>(w[u], f);
 #pragma unroll
-    for (int j = 0; j < kPairsOf<DT>; ++j) s = add2(s, ex2_pair(acc.ref.arg(f[j])));
+    for (int j = 0; j < kPairsOf<DT>; ++j) {
+      const Pair d = acc.ref.arg(f[j]), e = ex2_pair(d);
+      s = add2(s, e);
+      t = fma2(e, d, t);
+    }
   }
   acc.at.s = fmaf(s.sum(), acc.ref.k, acc.at.s);
+  const float tt = t.sum();  // NaN with masked elements: the batch goes without its part of the (tiny) mending
+  acc.at.t += tt == tt ? tt : 0.0f;
 }
 
 struct DistillShared {
-  RowMass red[kRowWarps];
-  RowMass parts[kMaxCluster];
+  RowSum red[kRowWarps];
+  RowSum parts[kMaxCluster];
   int4 list_ids[SS_MAX_TOP / 4];
   float factor[3];
   uint32_t edge_listed;
@@ -276,25 +289,26 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
   barrier_sync<kAdded, kListThreads>();
   if (!GRAD && lane == 0 && after < a.rows)  // HBM has little else to do while the blocks exchange their sums
     prefetch_row<DT>(static_cast<const Elem<DT>*>(a.x) + after * a.ld, a.vocab, kAheadBytes, cl.rank, cl.size);
-  RowMass out = merge_lanes(sh.red[lane % kRowWarps], c, kRowWarps);
+  RowSum out = merge_lanes(sh.red[lane % kRowWarps], c, kRowWarps);
   if (cl.size > 1) {
     if (lane < cl.size) cl.at(sh.parts, lane)[cl.rank] = out;
     cl.arrive();
     cl.wait();
     out = merge_lanes(sh.parts[lane % cl.size], c, static_cast<int>(cl.size));
   }
-  RowMass all = l.in, o = out;
-  if (o.m > all.m) all.move(o.m, c);
-  else if (all.m > o.m) o.move(all.m, c);
-  all.s += o.s;
+  out.mend(a.eps);
+  // the row's mass: the listed tokens' and the unlisted ones', around the larger of their maxima
+  RowMass all = {fmaxf(l.in.m, out.m), 0.0f};
+  all.s = (l.in.m == all.m ? l.in.s : l.in.s * expf((l.in.m - all.m) * a.scale)) +
+          (out.m == all.m ? out.s : out.s * expf((out.m - all.m) * a.scale));
   const bool empty = all.s == 0.0f;
   // all unlisted tokens masked, by -inf or by values so low that no p_t is left
   const bool no_tail = out.s == 0.0f || (out.m - all.m) * c <= kFloor;
+  const float p_t = no_tail ? 0.0f : expf((out.m - all.m) * a.scale) * (out.s / all.s);
   const float ws = l.bad ? nan_f() : w * a.scale;
   const float b = l.q_sum + l.q_tail;
   if constexpr (GRAD) {
     // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
-    const float p_t = no_tail ? 0.0f : ex2((out.m - all.m) * c) * (out.s / all.s);
     const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - l.q_tail) / out.s;
     const ExpRef ref(out.m, c);
     if (lane == 0) {
@@ -306,12 +320,16 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
   }
   if (cl.rank == 0) {
     const float ln_s = logf(all.s);
-    const float tail = no_tail ? -kInf : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s);
+    // logs of p_t and p themselves while there is something of them: log s is a few units, and its rounding would be
+    // in every digit of a small divergence
+    const float tail = no_tail ? -kInf
+                               : (p_t > 1e-30f ? logf(p_t) : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s));
     float loss = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       if (l.id[i] >= 0 && l.q[i] != 0.0f) {
-        const float lp = empty ? -kInf : fmaf(l.x[i] - all.m, a.scale, -ln_s);
+        const float z = (l.x[i] - all.m) * a.scale, p = expf(z) / all.s;
+        const float lp = empty ? -kInf : (p > 1e-30f ? logf(p) : z - ln_s);
         loss += l.q[i] * (l.lq[i] - lp);
       }
     }
@@ -403,7 +421,7 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
   const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
   barrier_sync<kReady, kListThreads>();
   const bool edge_out = part.edge >= 0 && !((sh.edge_listed >> tid) & 1u);
-  RunningMass out(one_element<RowMass>(edge_out ? edge : -kInf), c);
+  RunningMass out(one_element(edge_out ? edge : -kInf), c);
   const uint32_t* listed = marks + tid;
 #pragma unroll 1
   for (int j = 0; j < vectors; j += kBatch, listed += kRowThreads) {
@@ -415,7 +433,7 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) v[u] = next[u];
   }
-  const RowMass warp_out = merge_lanes(out.done(c), c);
+  const RowSum warp_out = merge_lanes(out.done(c), c);
   if ((tid & 31) == 0) sh.red[tid >> 5] = warp_out;
   barrier_arrive<kAdded, kListThreads>();
   cl.started();
@@ -547,9 +565,10 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
   const int split = split_for(nvec, 32);
+  const Scale2 s2(x->scale);
   DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
                          reinterpret_cast<const float2*>(norm_in), tail_in, loss, reinterpret_cast<float2*>(norm),
-                         tail, d_logits, rows, x->vocab, x->ld, d_ld, x->scale * kLog2e, x->scale, t->scale, t->k,
+                         tail, d_logits, rows, x->vocab, x->ld, d_ld, s2.c, s2.eps, x->scale, t->scale, t->k,
                          t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld), d_logits == x->data,
                          static_cast<uint32_t>(split), 0};
   if (saved) {

@@ -227,22 +227,11 @@ struct RowSum {
     }
     m = to;
   }
-};
-
-// The same without t: m = max x, s = sum 2^((x - m) c).
-struct RowMass {
-  float m, s;
-
-  __device__ __forceinline__ static RowMass none() { return {-kInf, 0.0f}; }
-  __device__ __forceinline__ void move(float to, float c) {
-    if (s != 0.0f) s *= ex2((m - to) * c);
-    m = to;
-  }
-  __device__ __forceinline__ void merge(RowMass b, float c) {
-    if (b.m > m) move(b.m, c);
-    else if (m > b.m) b.move(m, c);
-    s += b.s;
-  }
+  // Two small systematic errors of s, mended to first order. c is the scale's product with log2(e) rounded to 24 bits,
+  // which is a slightly different temperature: eps ln 2 t (eps: its relative error, 2^-25 at most). And ex2.approx
+  // falls short by 9e-8 on average, but for the maximum's own 2^0 (sums of 9291 to 128256 terms against float64, over
+  // four spreads and three scales: 4e-8 to 1.6e-7); a loss of a few hundredths would lose its sixth digit to that.
+  __device__ __forceinline__ void mend(float eps) { s += fmaf(eps * kLn2, t, 9e-8f * fmaxf(s - 1.0f, 0.0f)); }
 };
 
 // Order of logits as unsigned integers (-0 counts as +0; NaN rows do not come here).
@@ -260,14 +249,14 @@ __device__ __forceinline__ uint64_t order_pair(float x, int64_t id) {
 
 // A thread's running sums around a reference that stays where it is while the elements are at most 2^SLACK times its
 // exponential: the reference is the first batch's maximum for nearly all threads, and `top` the maximum.
-template <class Sum, int SLACK>
+template <int SLACK>
 struct Running {
-  Sum at;        // around the reference at.m
+  RowSum at;     // around the reference at.m
   float top;     // max x
   float limit;   // elements above it move the reference
   ExpRef ref;    // of at.m
 
-  __device__ __forceinline__ Running(Sum first, float c) : at(first), top(first.m), ref(first.m, c) {
+  __device__ __forceinline__ Running(RowSum first, float c) : at(first), top(first.m), ref(first.m, c) {
     limit = first.m + SLACK / c;
   }
   __device__ __forceinline__ void see(float m, float c) {
@@ -279,16 +268,15 @@ struct Running {
     }
   }
   // The sums around the maximum.
-  __device__ __forceinline__ Sum done(float c) {
+  __device__ __forceinline__ RowSum done(float c) {
     if (top > at.m) at.move(top, c);
     return at;
   }
 };
 
 // One element as a sum: 2^0 (0 when masked, NaN for NaN and +inf, with any maximum that is a number).
-template <class Sum>
-__device__ __forceinline__ Sum one_element(float x) {
-  Sum a = Sum::none();
+__device__ __forceinline__ RowSum one_element(float x) {
+  RowSum a = RowSum::none();
   if (x == -kInf) return a;
   if (x <= 3.402823466e38f) {
     a.m = x;
@@ -301,13 +289,12 @@ __device__ __forceinline__ Sum one_element(float x) {
 
 // Merged over the `width` (a power of two) lanes of each aligned group, the groups being copies of one another;
 // the same in every lane. One rescale a lane: first the maximum, then plain sums.
-template <class Sum>
-__device__ __forceinline__ Sum merge_lanes(Sum a, float c, int width = 32) {
+__device__ __forceinline__ RowSum merge_lanes(RowSum a, float c, int width = 32) {
   const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(a.m)));
   if (top > a.m) a.move(top, c);
   for (int off = width >> 1; off > 0; off >>= 1) {
     a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, off);
-    if constexpr (std::is_same_v<Sum, RowSum>) a.t += __shfl_xor_sync(0xFFFFFFFFu, a.t, off);
+    a.t += __shfl_xor_sync(0xFFFFFFFFu, a.t, off);
   }
   return a;
 }
@@ -315,8 +302,8 @@ __device__ __forceinline__ Sum merge_lanes(Sum a, float c, int width = 32) {
 constexpr int kRowWarps = kRowThreads / 32;
 
 // Merged over the block, the same in every thread. `red`: a slot per warp, used by one call only.
-template <int WARPS = kRowWarps, class Sum>
-__device__ __forceinline__ Sum block_merge(Sum a, float c, Sum* red) {
+template <int WARPS = kRowWarps>
+__device__ __forceinline__ RowSum block_merge(RowSum a, float c, RowSum* red) {
   a = merge_lanes(a, c);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
   __syncthreads();
@@ -641,6 +628,16 @@ ss_status launch_rows(void (*fn)(Args), int64_t clusters, int cluster, int threa
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args);
   return e == cudaSuccess ? SS_OK : cuda_fail(e);
 }
+
+// scale * log2(e) as c (1 + eps), c in fp32.
+struct Scale2 {
+  float c, eps;
+  explicit Scale2(float scale) {
+    const double exact = static_cast<double>(scale) * 1.4426950408889634;
+    c = static_cast<float>(exact);
+    eps = static_cast<float>((exact - static_cast<double>(c)) / static_cast<double>(c));
+  }
+};
 
 // True when every row of the gradient starts at its logits row's 16-byte phase, so both take the same vectors.
 inline bool same_phase(const ss_logits* x, const void* d, int64_t d_ld) {

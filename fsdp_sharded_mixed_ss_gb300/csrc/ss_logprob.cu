@@ -15,7 +15,7 @@ struct LogprobArgs {
   float* top_logprob;
   void* top_id;
   int64_t rows, vocab, ld;
-  float c, scale;
+  float c, eps, scale;
   int32_t top_k;
   bool wide;         // int64 ids
   int32_t resident;  // rows in flight at a time
@@ -51,7 +51,7 @@ constexpr int kManyThreads = 128;  // threads of a block that selects alternativ
 constexpr int kManyRows = SS_MANY;  // that many rows an SM
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
 
-using RunningSum = Running<RowSum, 8>;
+using RunningSum = Running<8>;
 
 // N vectors into the running sums; returns their maximum.
 template <int DT, int N>
@@ -114,7 +114,7 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c
   const int unit_batches = part_unit_batches(part);
   const int64_t sb = part.step_bytes();
   const char* src = part.at();
-  RunningSum run(one_element<RowSum>(edge), c);
+  RunningSum run(one_element(edge), c);
   float best = -kInf;
   int in_unit = 0, units = 0;
   for (int b = 0; b < batches; ++b, src += kBatch * sb) {
@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
   }
   if (TOPS || cl.size > 1) cl.sync();
   if (cl.size > 1) acc = merge_lanes(parts[tid % cl.size], a.c, static_cast<int>(cl.size));
+  acc.mend(a.eps);
   const RowValues v(acc, a.scale);
   if constexpr (!TOPS) {
     if (writes) v.write(a, row, token, to_float<DT>(token_x));
@@ -633,9 +634,10 @@ ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype id
   ranges.add(out->top_logprob, rows * top_k * 4, true);
   ranges.add(out->top_id, rows * top_k * ib, true);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
+  const Scale2 s2(x->scale);
   LogprobArgs a = {x->data, tokens, out->logprob, out->entropy, out->lse,
                          reinterpret_cast<float2*>(out->norm), out->top_logprob, out->top_id,
-                         rows, x->vocab, x->ld, x->scale * kLog2e, x->scale, top_k, idtype == SS_I64, 4 * sm_count()};
+                         rows, x->vocab, x->ld, s2.c, s2.eps, x->scale, top_k, idtype == SS_I64, 4 * sm_count()};
   const auto pick = [&](auto tops, auto threads) {
     constexpr bool kTops = decltype(tops)::value;
     constexpr int T = decltype(threads)::value;
@@ -691,7 +693,7 @@ ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idty
   if (rows * split > INT32_MAX) return SS_ERR_OVERFLOW;
   const LogprobGradArgs a = {x->data, tokens, top_id, reinterpret_cast<const float2*>(norm), entropy, up->d_logprob,
                              up->d_entropy, up->d_lse, up->d_top_logprob, d_logits, rows, x->vocab, x->ld, d_ld,
-                             x->scale * kLog2e, x->scale, top_k, idtype == SS_I64, same_phase(x, d_logits, d_ld),
+                             Scale2(x->scale).c, x->scale, top_k, idtype == SS_I64, same_phase(x, d_logits, d_ld),
                              static_cast<uint32_t>(split)};
   auto* fn = x->dtype == SS_BF16
                  ? logprob_grad_kernel<SS_BF16>
