@@ -6,10 +6,9 @@
 namespace ss {
 namespace {
 
-#ifndef SS_PART_VECTORS
-#define SS_PART_VECTORS 32
-#endif
-constexpr int kPartVectors = SS_PART_VECTORS;
+// Vectors a thread in a block's part of a row shared by a cluster. 4096 x 128256 bf16 with 8, 16, 32, 64: 758, 522,
+// 403, 446 us (below, each part's fixed work shows; above, the rows in flight no longer fit L2).
+constexpr int kPartVectors = 32;
 
 struct DistillArgs {
   const void* x;
@@ -66,11 +65,13 @@ struct RowList {
     const int64_t at = row * a.k + lane;
     int64_t given[kSlots];
     if (a.wide) {
+      const int64_t* p = static_cast<const int64_t*>(a.ids) + at;
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) given[i] = lane + 32 * i < a.k ? static_cast<const int64_t*>(a.ids)[at + 32 * i] : -1;
+      for (int i = 0; i < kSlots; ++i) given[i] = lane + 32 * i < a.k ? p[32 * i] : -1;
     } else {
+      const int32_t* p = static_cast<const int32_t*>(a.ids) + at;
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) given[i] = lane + 32 * i < a.k ? static_cast<const int32_t*>(a.ids)[at + 32 * i] : -1;
+      for (int i = 0; i < kSlots; ++i) given[i] = lane + 32 * i < a.k ? p[32 * i] : -1;
     }
     if (a.t_dtype == SS_FP32) {
 #pragma unroll
@@ -185,7 +186,18 @@ struct RowList {
 // The gradient needs the row's sums and then the row again. A row is shared by
 // the blocks of a cluster: small enough parts that all the rows in flight stay
 // in L2, so the second pass reads them from there, and HBM sees each logit read
-// once and each gradient written once.
+// once (1.06 times, by the counters) and each gradient written once. With
+// z = scale x, p over the whole row, p_t over its unlisted tokens, b = Q + q_t:
+//   unlisted  d = w scale (p / p_t) (p_t b - q_t)    listed  d = w scale (p b - q)
+// where without a bucket q_t = 0 and the first is p b.
+//
+// 4096 x 128256 bf16, 64 listed: 372 us, 5.65 TB/s of the bytes that have to move,
+// 0.83 of the measured copy. What is left is the time from a part's last sum to its
+// first gradient and from its start to the list's marks, a fifth of a block's life,
+// which two other blocks on the SM cover in part: more of them (4: 409 us against
+// 390 then) put L2 over its size. A row held in shared memory (445 us) or in
+// registers (495) between the passes leaves room for fewer blocks. The loss alone
+// (1024 x 50257 fp16: 22 us, 0.70) is one pass, four blocks an SM.
 //
 // Eight warps go through the elements and do as little else as can be; the ninth
 // has the row's list, the exchange between the blocks and the row's loss:
@@ -250,7 +262,9 @@ struct DistillShared {
   uint32_t edge_listed;
 };
 
-constexpr int kAheadBytes = 65536;  // of the row that comes after (loss alone; 0, 16, 32, 64 KB: 24.6, 24.3, 23.6, 22.9 us)
+// Of the row that comes after, with the loss alone: 0, 16, 32, 64 KB: 24.6, 24.3, 23.6, 22.9 us. (With a gradient: 385,
+// 398, 404, 434 us; the rows in flight need the L2.)
+constexpr int kAheadBytes = 65536;
 
 // The ninth warp's part in a row. `marks`: a word of listed bits for each batch of vectors, by thread.
 template <int DT, bool GRAD>
@@ -275,9 +289,9 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
   barrier_arrive<kReady, kListThreads>();
   const int64_t after = row + a.resident;
   if (after < a.rows) {  // the list that comes after on this SM
-    const int64_t id_bytes = a.wide ? 8 : 4, t_bytes = a.t_dtype == SS_FP32 ? 4 : 2;
-    if (lane * 128 < a.k * id_bytes) prefetch_line(static_cast<const char*>(a.ids) + after * a.k * id_bytes + lane * 128);
-    if (lane * 128 < a.k * t_bytes) prefetch_line(static_cast<const char*>(a.teacher) + after * a.k * t_bytes + lane * 128);
+    const int64_t id_bytes = a.k * (a.wide ? 8 : 4), t_bytes = a.k * (a.t_dtype == SS_FP32 ? 4 : 2);
+    if (lane * 128 < id_bytes) prefetch_line(static_cast<const char*>(a.ids) + after * id_bytes + lane * 128);
+    if (lane * 128 < t_bytes) prefetch_line(static_cast<const char*>(a.teacher) + after * t_bytes + lane * 128);
   }
   l.drop_repeated(a, sh.list_ids);
 #pragma unroll
@@ -451,7 +465,9 @@ __global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(con
 // ------------------------------------------------------------------ the gradient from saved normalisers
 //
 // One pass: blocks share a row as above, but nothing is exchanged between them.
-// A ninth warp has the list while the first vectors are on their way.
+// A ninth warp has the list while the first vectors are on their way. Bound by HBM:
+// 2048 x 128256 bf16 165 us, 6.4 TB/s, 0.94 of the copy (parts of 16, 32, 64 vectors
+// a thread: 185, 171, 173 us: every part looks its list up).
 template <int DT>
 __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ int4 list_ids[SS_MAX_TOP / 4];
@@ -566,11 +582,10 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   const int64_t vec = x->dtype == SS_FP32 ? 4 : 8, nvec = x->vocab / vec;
   const int split = split_for(nvec, 32);
   const Scale2 s2(x->scale);
-  DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss,
-                         reinterpret_cast<const float2*>(norm_in), tail_in, loss, reinterpret_cast<float2*>(norm),
-                         tail, d_logits, rows, x->vocab, x->ld, d_ld, s2.c, s2.eps, x->scale, t->scale, t->k,
-                         t->tail, t->dtype, t->idtype == SS_I64, d_logits && same_phase(x, d_logits, d_ld), d_logits == x->data,
-                         static_cast<uint32_t>(split), 0};
+  DistillArgs a = {x->data, t->ids, t->logprob, t->row_weight, d_loss, reinterpret_cast<const float2*>(norm_in),
+                   tail_in, loss, reinterpret_cast<float2*>(norm), tail, d_logits, rows, x->vocab, x->ld, d_ld, s2.c,
+                   s2.eps, x->scale, t->scale, t->k, t->tail, t->dtype, t->idtype == SS_I64,
+                   d_logits && same_phase(x, d_logits, d_ld), d_logits == x->data, static_cast<uint32_t>(split), 0};
   if (saved) {
     auto* fn = x->dtype == SS_BF16
                    ? distill_grad_kernel<SS_BF16>
@@ -581,7 +596,8 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
   const auto pick = [&](auto grad) {
     constexpr bool kGrad = decltype(grad)::value;
     return x->dtype == SS_BF16 ? distill_kernel<SS_BF16, kGrad>
-                               : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16, kGrad> : distill_kernel<SS_FP32, kGrad>);
+                               : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16, kGrad>
+                                                      : distill_kernel<SS_FP32, kGrad>);
   };
   const auto vectors = [&](int n) { return (nvec + n * kRowThreads - 1) / (n * kRowThreads); };
   int cluster = 1;

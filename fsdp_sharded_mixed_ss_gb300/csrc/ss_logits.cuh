@@ -414,9 +414,10 @@ __device__ __forceinline__ void zero_part(Elem<DT>* d, int64_t n, unsigned rank,
 // Asks the L2 for the first `bytes` bytes of block `rank`'s of `size` equal runs of a row (as many of its whole
 // vectors as that is).
 template <int DT>
-__device__ __forceinline__ void prefetch_row(const Elem<DT>* row, int64_t vocab, int bytes, int rank = 0, int size = 1) {
+__device__ __forceinline__ void prefetch_row(const Elem<DT>* row, int64_t vocab, int bytes, int rank = 0,
+                                             int size = 1) {
   const Slice<DT> sl(row, vocab);
-  const int64_t first = static_cast<int64_t>(sl.nvec) * rank / size, last = static_cast<int64_t>(sl.nvec) * (rank + 1) / size;
+  const int64_t vecs = sl.nvec, first = vecs * rank / size, last = vecs * (rank + 1) / size;
   const char* p = reinterpret_cast<const char*>(row + sl.head) + first * 16;
   const int64_t n = min(static_cast<int64_t>(bytes), (last - first) * 16);
   constexpr int64_t kPiece = 16384;
