@@ -9,6 +9,7 @@ namespace {
 // Vectors a thread in a block's part of a row shared by a cluster. 4096 x 128256 bf16 with 8, 16, 32, 64: 758, 522,
 // 403, 446 us (below, each part's fixed work shows; above, the rows in flight no longer fit L2).
 constexpr int kPartVectors = 32;
+constexpr int kFewVectors = 8;  // with few rows (64 x 128256 fp32: parts of 31 vectors 20.4 us, of 16 16.1 us)
 
 struct DistillArgs {
   const void* x;
@@ -397,8 +398,9 @@ __device__ __forceinline__ void mask_batch(uint4* v, uint32_t bits) {
   }
 }
 
-template <int DT, bool GRAD>
-__global__ void __launch_bounds__(kListThreads, GRAD ? 3 : 4) distill_kernel(const __grid_constant__ DistillArgs a) {
+// BLOCKS: blocks an SM.
+template <int DT, bool GRAD, int BLOCKS>
+__global__ void __launch_bounds__(kListThreads, BLOCKS) distill_kernel(const __grid_constant__ DistillArgs a) {
   extern __shared__ uint32_t marks[];
   __shared__ DistillShared sh;
   const Cluster cl = Cluster::start();
@@ -593,19 +595,28 @@ ss_status distill_impl(const ss_logits* x, const ss_teacher* t, const float* nor
     if (rows * split > INT32_MAX) return SS_ERR_OVERFLOW;
     return launch(fn, static_cast<unsigned>(rows * split), a, stream, kListThreads);
   }
-  const auto pick = [&](auto grad) {
+  const auto pick = [&](auto grad, auto blocks) {
     constexpr bool kGrad = decltype(grad)::value;
-    return x->dtype == SS_BF16 ? distill_kernel<SS_BF16, kGrad>
-                               : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16, kGrad>
-                                                      : distill_kernel<SS_FP32, kGrad>);
+    constexpr int kBlocks = decltype(blocks)::value;
+    return x->dtype == SS_BF16 ? distill_kernel<SS_BF16, kGrad, kBlocks>
+                               : (x->dtype == SS_FP16 ? distill_kernel<SS_FP16, kGrad, kBlocks>
+                                                      : distill_kernel<SS_FP32, kGrad, kBlocks>);
   };
+  constexpr std::integral_constant<int, 3> three;
+  constexpr std::integral_constant<int, 4> four;
   const auto vectors = [&](int n) { return (nvec + n * kRowThreads - 1) / (n * kRowThreads); };
   int cluster = 1;
-  auto* fn = d_logits ? pick(std::true_type()) : pick(std::false_type());
   while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
+  // few rows: smaller parts, as long as all of them run at once
+  const int64_t places = 4 * sm_count();
+  const bool few = rows * cluster * 2 <= places;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= places && vectors(cluster) > kFewVectors) cluster *= 2;
+  const int blocks = d_logits && !few ? 3 : 4;
+  auto* fn = !d_logits ? pick(std::false_type(), four)
+                       : (few ? pick(std::true_type(), four) : pick(std::true_type(), three));
   const size_t smem = static_cast<size_t>((vectors(cluster) + kBatch - 1) / kBatch) * kRowThreads * sizeof(uint32_t);
   if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
-  a.resident = (d_logits ? 3 : 4) * sm_count() / cluster;
+  a.resident = blocks * sm_count() / cluster;
   return launch_rows(fn, rows, cluster, kListThreads, smem, a, stream);
 }
 
