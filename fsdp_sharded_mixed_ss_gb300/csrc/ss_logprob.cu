@@ -17,8 +17,7 @@ struct LogprobArgs {
   int64_t rows, vocab, ld;
   float c, eps, scale;
   int32_t top_k;
-  bool wide;         // int64 ids
-  int32_t resident;  // rows in flight at a time
+  bool wide;  // int64 ids
 };
 
 // ------------------------------------------------------------------ forward
@@ -29,33 +28,34 @@ struct LogprobArgs {
 // alternatives 166 us, 6.3 TB/s, 0.93 of the measured copy.
 //
 // The alternatives come from the same pass: the maximum of every unit (4 vectors of
-// a thread, more in rows longer than 16 units a thread) stays in shared memory,
-// and the threads' maxima are 256 keys. Some threshold that k of the keys reach
-// is a bound that at least k elements of the row reach, and few more: for k of
-// 256 keys drawn at random -256 ln(1 - k / 256) elements, 21 for k = 20 and 177
-// for k = 128. Only units whose maximum reaches it are read again, their elements
-// at or above it are the candidates, and a candidate's place is the number of
+// a thread, more in rows longer than 4096 units a block) stays in shared memory,
+// and threads' maxima are 256 keys. Some threshold that k of the keys reach is a
+// bound that at least k elements of the row reach, and few more: for k of 256
+// keys drawn at random -256 ln(1 - k / 256) elements, 21 for k = 20 and 177 for
+// k = 128. Only units whose maximum reaches it are read again, their elements at
+// or above it are the candidates, and a candidate's place is the number of
 // candidates above it. Where the candidates pass the buffer (ties), the part's
 // elements go through the buffer once more, which is cut to the k best whenever
 // it is full.
 //
 // The selection is a chain of small dependent reads beside a loaded memory system,
 // as long as a third of a 128256-token row's stream, and what bounds the kernel
-// with alternatives (2048 x 128256 bf16, 64 of them: 119 us, 4.4 TB/s, 0.65 of the
-// copy). Two things hide some of it: blocks of 128 threads, eight to an SM, where
-// there are rows enough (119 us against 127, and 1021 x 50257 fp32 44 against 49);
-// and a block that begins its selection asks for the start of the row that will
-// take its place, so that HBM does not idle. A ninth warp that selects while eight
-// stream the next row measured 139 us, a threshold counted by all threads instead
-// of a search in one warp 131.
+// with alternatives (2048 x 128256 bf16, 64 of them: 114 us, 4.6 TB/s, 0.68 of the
+// copy). Blocks of 128 threads, eight to an SM, hide some of it where there are
+// rows enough (at 16 maxima a thread in 32 bits 119 us against 127, and 1021 x 50257
+// fp32 44 against 49), and the less shared memory they take the more L1 is left to
+// the loads in flight (32 maxima in 32 bits: 128 and 57 us; in 16 bits, rounded up
+// so that no unit is missed: 114 and 43). A ninth warp
+// that selects while eight stream the next row measured 139 us, a threshold counted
+// by all threads instead of a search in one warp 131.
 //
 // A call on a few rows is bound by latencies: 8 x 128256 takes 9 us, of which the
 // stream is a fifth, the cluster's two barriers a third.
 
-constexpr int kAheadBytes = 32768;  // of the row that comes after (0, 32, 64, 128 KB: 129.5, 126.4, 127.9, 132.9 us)
-constexpr int kUnits = 16;      // maxima kept per thread
-constexpr int kFlagged = 1024;  // units that are read again
-constexpr int kKeys = 256;      // threads' maxima that the threshold is taken from
+template <int T>
+constexpr int kUnits = 4096 / T;   // maxima kept per thread
+constexpr int kFlagged = 1024;     // units that are read again
+constexpr int kKeys = 256;         // threads' maxima that the threshold is taken from
 constexpr int kManyThreads = 128;  // threads of a block that selects alternatives of one of many rows
 constexpr int kManyRows = 6;       // so many rows an SM (1021 rows are 6.7)
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
@@ -104,20 +104,27 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, Runni
 }
 
 // Batches in a unit, and units of each thread (the same for all).
-template <class Part>
-__device__ __forceinline__ int part_unit_batches(const Part& part) {
-  return ((part.vectors() + kBatch - 1) / kBatch + kUnits - 1) / kUnits;
+template <int DT, int T>
+__device__ __forceinline__ int part_unit_batches(const RowPart<DT, T>& part) {
+  return ((part.vectors() + kBatch - 1) / kBatch + kUnits<T> - 1) / kUnits<T>;
 }
-template <class Part>
-__device__ __forceinline__ int part_units(const Part& part) {
+template <int DT, int T>
+__device__ __forceinline__ int part_units(const RowPart<DT, T>& part) {
   const int batches = (part.vectors() + kBatch - 1) / kBatch, each = part_unit_batches(part);
   return each > 0 ? (batches + each - 1) / each : 0;
 }
 
-// The pass over a thread's vectors; `unit` (with TOPS) receives its units' maxima.
+// A unit's maximum as the upper half of its key, rounded up (masked: down): 16 bits of shared memory, which is the L1
+// that the loads in flight need. Compared with a threshold rounded up, no unit is missed.
+__device__ __forceinline__ uint16_t upper_key(uint32_t key) {
+  return static_cast<uint16_t>((key > kMaskedKey ? key + 0xFFFFu : key) >> 16);
+}
+
+// The pass over a thread's vectors; `unit` (with TOPS) receives its units' maxima, `maxima` those of its even and its
+// odd units (the even ones' with the edge element).
 template <int DT, bool TOPS, int T>
-__device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c, float edge, float (*unit)[T],
-                                             float* thread_max) {
+__device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c, float edge, uint16_t (*unit)[T],
+                                             float (&maxima)[2]) {
   const int full = part.whole / kBatch;  // batches that every thread has whole
   const int batches = (part.vectors() + kBatch - 1) / kBatch;
   const int unit_batches = part_unit_batches(part);
@@ -125,6 +132,8 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c
   const char* src = part.at();
   RunningSum run(one_element(edge), c);
   float best = -kInf;
+  maxima[0] = edge;
+  maxima[1] = -kInf;
   int in_unit = 0, units = 0;
   for (int b = 0; b < batches; ++b, src += kBatch * sb) {
     uint4 w[kBatch];
@@ -142,20 +151,22 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c
     if constexpr (TOPS) {
       best = fmaxf(best, m);
       if (++in_unit == unit_batches || b + 1 == batches) {
-        unit[units++][threadIdx.x] = best;
+        unit[units][threadIdx.x] = upper_key(order_key(best));
+        if (units & 1) maxima[1] = fmaxf(maxima[1], best);
+        else maxima[0] = fmaxf(maxima[0], best);
+        ++units;
         in_unit = 0;
         best = -kInf;
       }
     }
   }
-  *thread_max = run.top;
   return run.done(c);
 }
 
 template <int T>
 struct TopShared {
-  static constexpr int kCand = 8 * T;
-  float unit[kUnits][T];
+  static constexpr int kCand = T == kRowThreads ? 1024 : 512;
+  alignas(8) uint16_t unit[kUnits<T>][T];
   uint64_t cand[kCand];  // block 0's is used, shared out over the cluster's blocks
   uint64_t best[SS_MAX_TOP];
   uint32_t keys[kKeys];
@@ -206,13 +217,14 @@ struct Wanted {
 // The part's candidates into out[0, room); returns their number, to all threads (above `room`: they did not fit).
 // s.n and s.n_flagged are zero before; s is the caller's again when this returns.
 template <int DT, int T>
-__device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted& wanted, TopShared<T>& s, uint64_t* out,
-                                       int room) {
+__device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted& wanted, uint32_t tau, TopShared<T>& s,
+                                       uint64_t* out, int room) {
   constexpr int V = kVecOf<DT>;
   const int tt = threadIdx.x, lane = tt & 31;
   const int unit_batches = part_unit_batches(part), units = part_units(part);
   unsigned mask = 0u;  // this thread's flagged units
-  for (int u = 0; u < units; ++u) mask |= wanted(s.unit[u][tt]) ? 1u << u : 0u;
+  const uint16_t least = upper_key(tau);
+  for (int u = 0; u < units; ++u) mask |= s.unit[u][tt] >= least ? 1u << u : 0u;
   int before = __popc(mask);
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -285,20 +297,22 @@ __device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted&
 
 // The k largest of the part's pairs that reach the threshold, into s.best[0, k) in order: the elements go through a
 // buffer of pairs (the units' memory), which is cut to its k best, and the bound raised to the last of them,
-// whenever it is full. At least k of the part's pairs reach the threshold. Ascending ids make ties cheap: a later one
-// is below the bound. How full the buffer is, each thread counts for itself (`n`, from block-wide counts), so all
+// whenever it is full. Returns how many there are (k, or all that reach the threshold). Ascending ids make ties cheap:
+// a later one is below the bound. How full the buffer is, each thread counts for itself (`n`, from block-wide counts), so all
 // decide alike; s.n only hands out places.
 template <int DT, int T>
-__device__ __noinline__ void select_through_buffer(const RowPart<DT, T>& part, TopShared<T>& s, uint32_t tau, int k) {
+__device__ __noinline__ int select_through_buffer(const RowPart<DT, T>& part, TopShared<T>& s, uint32_t tau, int k) {
   constexpr int V = kVecOf<DT>;
-  constexpr int kUnitPairs = kUnits * T / 2;
+  constexpr int kUnitPairs = static_cast<int>(sizeof(s.unit) / sizeof(uint64_t));
+  static_assert(kUnitPairs >= SS_MAX_TOP + T, "a step fits after a cut");
   const int tt = threadIdx.x;
   uint64_t* buffer = reinterpret_cast<uint64_t*>(s.unit);
   uint64_t bound = static_cast<uint64_t>(tau) << 32;  // pairs above it are wanted
   int n = 0;
   if (tt == 0) s.n = 0;
   __syncthreads();
-  auto cut = [&] {  // the buffer to its k best (n >= k), the bound to the k-th
+  auto cut = [&] {  // the buffer to its k best, the bound to the k-th
+    const int kept = min(n, k);
     for (int i = tt; i < n; i += T) {
       const uint64_t mine = buffer[i];
       int above = 0;
@@ -306,10 +320,10 @@ __device__ __noinline__ void select_through_buffer(const RowPart<DT, T>& part, T
       if (above < k) s.best[above] = mine;
     }
     __syncthreads();
-    for (int i = tt; i < k; i += T) buffer[i] = s.best[i];
-    if (tt == 0) s.n = k;
-    bound = s.best[k - 1];
-    n = k;
+    for (int i = tt; i < kept; i += T) buffer[i] = s.best[i];
+    if (tt == 0) s.n = kept;
+    if (kept == k) bound = s.best[k - 1];
+    n = kept;
     __syncthreads();
   };
   auto step = [&](bool there, float f, int id) {  // one element of every thread
@@ -346,6 +360,7 @@ __device__ __noinline__ void select_through_buffer(const RowPart<DT, T>& part, T
     step(there, there ? to_float<DT>(part.x[id]) : 0.0f, id);
   }
   cut();
+  return n;
 }
 
 // Where a row's alternatives go.
@@ -423,14 +438,12 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
   const bool writes = cl.rank == 0 && tid == T - 1;
   int64_t token = -1;
   if (writes && a.logprob) token = load_id(a.tokens, row, a.wide);
-  float thread_max;
-  float(*unit)[T] = nullptr;
+  float maxima[2];
+  uint16_t(*unit)[T] = nullptr;
   if constexpr (TOPS) unit = tops.unit;
-  const RowSum mine_sum = stream_row<DT, TOPS, T>(part, a.c, edge, unit, &thread_max);
+  const RowSum mine_sum = stream_row<DT, TOPS, T>(part, a.c, edge, unit, maxima);
   const Elem<DT> token_x = token >= 0 && token < a.vocab ? part.x[token] : Elem<DT>(0);
   RowSum acc = block_merge<T / 32>(mine_sum, a.c, red);
-  if (TOPS && cl.size == 1 && tid == 0 && row + a.resident < a.rows)
-    prefetch_row<DT>(static_cast<const Elem<DT>*>(a.x) + (row + a.resident) * a.ld, a.vocab, kAheadBytes);
   cl.started();
   if (cl.size > 1) {
     if (tid < cl.size) cl.at(parts, tid)[cl.rank] = acc;
@@ -438,21 +451,16 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
   if constexpr (TOPS) {
     if constexpr (T == kRowThreads) {
       // 256 keys of the whole row: the maxima of groups of `size` neighbouring threads of every block
-      uint32_t key = order_key(thread_max);
+      uint32_t key = order_key(fmaxf(maxima[0], maxima[1]));
       for (unsigned off = 1; off < cl.size; off <<= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
       if (tid % cl.size == 0) {
         const unsigned at = cl.rank * (kKeys / cl.size) + tid / cl.size;
         for (unsigned r = 0; r < cl.size; ++r) cl.at(tops.keys, r)[at] = key;
       }
     } else {
-      // kKeys / T keys a thread, of every so many units
-      const int units = part_units(part);
-#pragma unroll
-      for (int s = 0; s < kKeys / T; ++s) {
-        float m = s == 0 ? edge : -kInf;
-        for (int u = s; u < units; u += kKeys / T) m = fmaxf(m, tops.unit[u][tid]);
-        tops.keys[s * T + tid] = order_key(m);
-      }
+      static_assert(kKeys == 2 * T || T == kRowThreads, "two keys a thread");
+      tops.keys[tid] = order_key(maxima[0]);
+      tops.keys[T + tid] = order_key(maxima[1]);
     }
     if (tid == 0) tops.n = tops.n_flagged = 0;
   }
@@ -475,15 +483,16 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
       if (tid == 0) tops.tau = t;
     }
     __syncthreads();
-    const Wanted wanted(tops.tau);
+    const uint32_t tau = tops.tau;
+    const Wanted wanted(tau);
     const int room = TopShared<T>::kCand / static_cast<int>(cl.size);
     uint64_t* mine = cl.at(tops.cand, 0) + cl.rank * room;
-    int found = collect<DT, T>(part, wanted, tops, mine, room);
+    const uint32_t least = wanted.few ? kMaskedKey + 1 : tau;
+    int found = collect<DT, T>(part, wanted, least, tops, mine, room);
     if (writes) v.write(a, row, token, to_float<DT>(token_x));
     if (found > room) {  // this block's own k best instead
-      select_through_buffer<DT, T>(part, tops, wanted.few ? kMaskedKey + 1 : tops.tau, k);
-      if (tid < k) mine[tid] = tops.best[tid];
-      found = k;
+      found = select_through_buffer<DT, T>(part, tops, least, k);
+      if (tid < found) mine[tid] = tops.best[tid];
     }
     if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = found;
     cl.sync();
@@ -649,9 +658,9 @@ ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype id
   ranges.add(out->top_id, rows * top_k * ib, true);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const Scale2 s2(x->scale);
-  LogprobArgs a = {x->data, tokens, out->logprob, out->entropy, out->lse,
+  const LogprobArgs a = {x->data, tokens, out->logprob, out->entropy, out->lse,
                          reinterpret_cast<float2*>(out->norm), out->top_logprob, out->top_id,
-                         rows, x->vocab, x->ld, s2.c, s2.eps, x->scale, top_k, idtype == SS_I64, 4 * sm_count()};
+                         rows, x->vocab, x->ld, s2.c, s2.eps, x->scale, top_k, idtype == SS_I64};
   const auto pick = [&](auto tops, auto threads) {
     constexpr bool kTops = decltype(tops)::value;
     constexpr int T = decltype(threads)::value;
@@ -664,7 +673,6 @@ ss_status ss_token_logprobs(const ss_logits* x, const void* tokens, ss_idtype id
   const int vec = x->dtype == SS_FP32 ? 4 : 8, cluster = cluster_for(rows, x->vocab, vec);
   if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
   if (top_k > 0 && rows >= kManyRows * sm_count() && x->vocab / vec >= 8 * kBatch * kManyThreads) {
-    a.resident = 8 * sm_count();
     return launch_rows(pick(std::true_type(), small_block), rows, 1, kManyThreads, 0, a, stream);
   }
   auto* fn = top_k > 0 ? pick(std::true_type(), wide_block) : pick(std::false_type(), wide_block);
