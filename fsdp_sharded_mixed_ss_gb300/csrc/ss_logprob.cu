@@ -40,12 +40,15 @@ struct LogprobArgs {
 //
 // The selection is a chain of small dependent reads beside a loaded memory system,
 // as long as a third of a 128256-token row's stream, and what bounds the kernel
-// with alternatives (2048 x 128256 bf16, 64 of them: 114 us, 4.6 TB/s, 0.68 of the
+// with alternatives (2048 x 128256 bf16, 64 of them: 105 us, 5.0 TB/s, 0.74 of the
 // copy). Blocks of 128 threads, eight to an SM, hide some of it where there are
 // rows enough (at 16 maxima a thread in 32 bits 119 us against 127, and 1021 x 50257
 // fp32 44 against 49), and the less shared memory they take the more L1 is left to
-// the loads in flight (32 maxima in 32 bits: 128 and 57 us; in 16 bits, rounded up
-// so that no unit is missed: 114 and 43). A ninth warp
+// the loads in flight (32 maxima in 32 bits: 128 and 57 us; in 16 bits 114 and 43).
+// What a row's selection issues counts as well: a batch instead of a vector a thread
+// when units are read again (no division, one place taken for all its candidates),
+// the bits that all keys share skipped in the search, eight candidates compared a
+// step: 108 to 105 us. A ninth warp
 // that selects while eight stream the next row measured 139 us, a threshold counted
 // by all threads instead of a search in one warp 131.
 //
@@ -114,11 +117,9 @@ __device__ __forceinline__ int part_units(const RowPart<DT, T>& part) {
   return each > 0 ? (batches + each - 1) / each : 0;
 }
 
-// A unit's maximum as the upper half of its key, rounded up (masked: down): 16 bits of shared memory, which is the L1
-// that the loads in flight need. Compared with a threshold rounded up, no unit is missed.
-__device__ __forceinline__ uint16_t upper_key(uint32_t key) {
-  return static_cast<uint16_t>((key > kMaskedKey ? key + 0xFFFFu : key) >> 16);
-}
+// A unit's maximum as the upper half of its key: 16 bits of shared memory, which is the L1 that the loads in flight
+// need. Compared with a threshold cut likewise, no unit is missed.
+__device__ __forceinline__ uint16_t upper_key(uint32_t key) { return static_cast<uint16_t>(key >> 16); }
 
 // The pass over a thread's vectors; `unit` (with TOPS) receives its units' maxima, `maxima` those of its even and its
 // odd units (the even ones' with the edge element).
@@ -128,23 +129,24 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c
   const int full = part.whole / kBatch;  // batches that every thread has whole
   const int batches = (part.vectors() + kBatch - 1) / kBatch;
   const int unit_batches = part_unit_batches(part);
-  const int64_t sb = part.step_bytes();
-  const char* src = part.at();
+  const uint4* src = reinterpret_cast<const uint4*>(part.x + part.sl.head);
+  const int step = part.step();
+  int at = part.first;
   RunningSum run(one_element(edge), c);
   float best = -kInf;
   maxima[0] = edge;
   maxima[1] = -kInf;
   int in_unit = 0, units = 0;
-  for (int b = 0; b < batches; ++b, src += kBatch * sb) {
+  for (int b = 0; b < batches; ++b, at += kBatch * step) {
     uint4 w[kBatch];
     if (b < full) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) w[u] = __ldg(reinterpret_cast<const uint4*>(src + u * sb));
+      for (int u = 0; u < kBatch; ++u) w[u] = __ldg(src + at + u * step);
     } else {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        w[u] = part.more(b * kBatch + u)
-                   ? __ldg(reinterpret_cast<const uint4*>(src + u * sb))
+        w[u] = at + u * step < part.sl.nvec
+                   ? __ldg(src + at + u * step)
                    : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
     }
     const float m = add_vectors<DT>(w, c, run);
@@ -167,7 +169,7 @@ template <int T>
 struct TopShared {
   static constexpr int kCand = T == kRowThreads ? 1024 : 512;
   alignas(8) uint16_t unit[kUnits<T>][T];
-  uint64_t cand[kCand];  // block 0's is used, shared out over the cluster's blocks
+  alignas(16) uint64_t cand[kCand];  // block 0's is used, shared out over the cluster's blocks
   uint64_t best[SS_MAX_TOP];
   uint32_t keys[kKeys];
   uint16_t flagged[kFlagged];
@@ -186,9 +188,13 @@ __device__ __forceinline__ uint32_t find_threshold(const uint32_t* key, uint32_t
   uint32_t keys[kKeys / 32];
 #pragma unroll
   for (int i = 0; i < kKeys / 32; ++i) keys[i] = key[(threadIdx.x & 31) + 32 * i];
-  uint32_t t = 0;
+  uint32_t low = keys[0];
+#pragma unroll
+  for (int i = 1; i < kKeys / 32; ++i) low = min(low, keys[i]);
+  const int differ = 32 - __clz(__reduce_min_sync(0xFFFFFFFFu, low) ^ top_key);  // above, all keys are alike
+  uint32_t t = differ < 32 ? top_key >> differ << differ : 0u;
 #pragma unroll 1
-  for (int bit = 31; bit >= kLowBit; --bit) {
+  for (int bit = differ - 1; bit >= kLowBit; --bit) {
     const uint32_t next = t | (1u << bit);
     if (next > top_key) continue;
     int c[2] = {0, 0};
@@ -248,45 +254,32 @@ __device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted&
     }
   }
   __syncthreads();
-  // one vector of a flagged unit a thread, four in flight
-  constexpr int kAgain = 4;
-  const int per_unit = unit_batches * kBatch;
-  const int items = min(s.n_flagged, kFlagged) * per_unit;
+  // one batch of a flagged unit a thread
+  const int items = min(s.n_flagged, kFlagged) * unit_batches;
 #pragma unroll 1
-  for (int i0 = tt; i0 < items; i0 += kAgain * T) {
-    uint4 w[kAgain];
-    int at[kAgain];
+  for (int i = tt; i < items; i += T) {
+    const int q = unit_batches == 1 ? i : i / unit_batches;
+    const int f = s.flagged[q];
+    const int vec = ((f / T) * unit_batches + i - q * unit_batches) * kBatch * part.step() + part.rank * T + f % T;
+    uint4 w[kBatch];
 #pragma unroll
-    for (int q = 0; q < kAgain; ++q) {
-      const int i = i0 + q * T;
-      at[q] = -1;
-      if (i < items) {
-        const int f = s.flagged[i / per_unit];
-        const int64_t vec = static_cast<int64_t>((f / T) * per_unit + i % per_unit) * part.step() +
-                            part.rank * T + f % T;
-        if (vec < part.sl.nvec) {
-          at[q] = static_cast<int>(vec);
-          w[q] = __ldg(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec);
-        }
-      }
-    }
+    for (int u = 0; u < kBatch; ++u)
+      w[u] = vec + u * part.step() < part.sl.nvec
+                 ? __ldg(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec + u * part.step())
+                 : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+    unsigned hits = 0u;
 #pragma unroll
-    for (int q = 0; q < kAgain; ++q) {
-      if (at[q] < 0) continue;
+    for (int u = 0; u < kBatch; ++u) {
       float e[V];
-      unpack<DT>(w[q], e);
-      unsigned hits = 0u;
+      unpack<DT>(w[u], e);
 #pragma unroll
-      for (int j = 0; j < V; ++j) hits |= wanted(e[j]) ? 1u << j : 0u;
-      if (hits != 0u) {
-        int n = atomicAdd(&s.n, __popc(hits));
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if ((hits >> j) & 1u) {
-            if (n < room) out[n] = order_pair(e[j], part.sl.head + at[q] * V + j);
-            ++n;
-          }
-      }
+      for (int j = 0; j < V; ++j) hits |= wanted(e[j]) ? 1u << (u * V + j) : 0u;
+    }
+    int n = hits != 0u ? atomicAdd(&s.n, __popc(hits)) : 0;
+    for (; hits != 0u; hits &= hits - 1u, ++n) {
+      const int bit = __ffs(hits) - 1;
+      const int id = part.sl.head + (vec + bit / V * part.step()) * V + bit % V;
+      if (n < room) out[n] = order_pair(to_float<DT>(part.x[id]), id);
     }
   }
   __syncthreads();
@@ -494,6 +487,7 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
       found = select_through_buffer<DT, T>(part, tops, least, k);
       if (tid < found) mine[tid] = tops.best[tid];
     }
+    if (tid < (-found & 7)) mine[found + tid] = 0;  // below every pair: eight are read at a time
     if (tid < cl.size) cl.at(tops.count, tid)[cl.rank] = found;
     cl.sync();
     if (cl.rank != 0) return;
@@ -505,7 +499,14 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
       const uint64_t pair = tops.cand[r * room + at];
       int place = 0;
       for (unsigned q = 0; q < cl.size; ++q)
-        for (int j = 0; j < tops.count[q]; ++j) place += tops.cand[q * room + j] > pair ? 1 : 0;
+        for (int j = 0; j < tops.count[q]; j += 8) {
+          const auto* four = reinterpret_cast<const ulonglong2*>(tops.cand + q * room + j);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const ulonglong2 two = four[h];
+            place += (two.x > pair ? 1 : 0) + (two.y > pair ? 1 : 0);
+          }
+        }
       if (place < k)
         out.put(place, static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(pair)),
                 v.logp(key_value(static_cast<uint32_t>(pair >> 32))));
