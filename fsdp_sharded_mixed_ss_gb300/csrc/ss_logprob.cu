@@ -25,7 +25,7 @@ struct LogprobArgs {
 // One pass over the row gives m = max x, s = sum 2^d and t = sum 2^d d over
 // d = (x - m) c: the normaliser, log p_i = (x_i - m) scale - ln s, and the entropy
 // H = ln s - ln 2 t / s. It is bound by HBM: 4096 x 128256 bf16 without
-// alternatives 166 us, 6.3 TB/s, 0.93 of the measured copy.
+// alternatives 164 us, 6.4 TB/s, 0.94 of the measured copy.
 //
 // The alternatives come from the same pass: the maximum of every unit (4 vectors of
 // a thread, more in rows longer than 4096 units a block) stays in shared memory,
@@ -40,11 +40,13 @@ struct LogprobArgs {
 //
 // The selection is a chain of small dependent reads beside a loaded memory system,
 // as long as a third of a 128256-token row's stream, and what bounds the kernel
-// with alternatives (2048 x 128256 bf16, 64 of them: 105 us, 5.0 TB/s, 0.74 of the
+// with alternatives (2048 x 128256 bf16, 64 of them: 104 us, 5.1 TB/s, 0.75 of the
 // copy). Blocks of 128 threads, eight to an SM, hide some of it where there are
 // rows enough (at 16 maxima a thread in 32 bits 119 us against 127, and 1021 x 50257
 // fp32 44 against 49), and the less shared memory they take the more L1 is left to
-// the loads in flight (32 maxima in 32 bits: 128 and 57 us; in 16 bits 114 and 43).
+// the loads in flight (32 maxima in 32 bits: 128 and 57 us; in 16 bits 114 and 43;
+// candidates in the units' place, 11 KB a block instead of 16: 105 to 104, 42.2 to
+// 41.5).
 // What a row's selection issues counts as well: a batch instead of a vector a thread
 // when units are read again (no division, one place taken for all its candidates),
 // the bits that all keys share skipped in the search, eight candidates compared a
@@ -57,7 +59,8 @@ struct LogprobArgs {
 
 template <int T>
 constexpr int kUnits = 4096 / T;   // maxima kept per thread
-constexpr int kFlagged = 1024;     // units that are read again
+template <int T>
+constexpr int kFlagged = 4 * T;    // units that are read again
 constexpr int kKeys = 256;         // threads' maxima that the threshold is taken from
 constexpr int kManyThreads = 128;  // threads of a block that selects alternatives of one of many rows
 constexpr int kManyRows = 6;       // so many rows an SM (1021 rows are 6.7)
@@ -172,15 +175,26 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c
 template <int T>
 struct TopShared {
   static constexpr int kCand = T == kRowThreads ? 1024 : 512;
-  alignas(8) uint16_t unit[kUnits<T>][T];
-  alignas(16) uint64_t cand[kCand];  // block 0's is used, shared out over the cluster's blocks
+  static constexpr bool kCandInUnits = T != kRowThreads;  // no cluster: nobody writes before the units are read
+  alignas(16) uint16_t unit[kUnits<T>][T];
+  alignas(16) uint64_t own_cand[kCandInUnits ? 2 : kCand];
   uint64_t best[SS_MAX_TOP];
   uint32_t keys[kKeys];
-  uint16_t flagged[kFlagged];
+  uint16_t flagged[kFlagged<T>];
   int count[kMaxCluster];  // candidates of every block
   int warp_sums[T / 32];
   uint32_t tau;
   int n, n_flagged;
+
+  // Candidates; block 0's are used, shared out over the cluster's blocks.
+  __device__ __forceinline__ uint64_t* cand() {
+    if constexpr (kCandInUnits) {
+      static_assert(sizeof(unit) >= kCand * sizeof(uint64_t), "they fit");
+      return reinterpret_cast<uint64_t*>(unit);
+    } else {
+      return own_cand;
+    }
+  }
 };
 struct NoTops {};
 
@@ -245,7 +259,8 @@ __device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted&
   if (lane == 31 && before > 0) base = atomicAdd(&s.n_flagged, before);
   base = __shfl_sync(0xFFFFFFFFu, base, 31) + before - __popc(mask);
   for (; mask != 0u; mask &= mask - 1u, ++base)
-    if (base < kFlagged) s.flagged[base] = static_cast<uint16_t>((__ffs(mask) - 1) * T + tt);
+    if (base < kFlagged<T>) s.flagged[base] = static_cast<uint16_t>((__ffs(mask) - 1) * T + tt);
+  __syncthreads();  // the units have been read: candidates may take their place
   if (part.rank == 0 && tt < 16) {  // the elements outside the vectors
     const int id = tt < 8 ? (tt < part.sl.head ? tt : -1)
                           : (tt - 8 < part.sl.n - part.sl.tail() ? part.sl.tail() + tt - 8 : -1);
@@ -257,9 +272,8 @@ __device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted&
       }
     }
   }
-  __syncthreads();
   // one batch of a flagged unit a thread
-  const int items = min(s.n_flagged, kFlagged) * unit_batches;
+  const int items = min(s.n_flagged, kFlagged<T>) * unit_batches;
 #pragma unroll 1
   for (int i = tt; i < items; i += T) {
     const int q = unit_batches == 1 ? i : i / unit_batches;
@@ -287,7 +301,7 @@ __device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted&
     }
   }
   __syncthreads();
-  const int n = s.n_flagged > kFlagged ? room + 1 : s.n;
+  const int n = s.n_flagged > kFlagged<T> ? room + 1 : s.n;
   __syncthreads();  // every thread has read them
   return n;
 }
@@ -483,7 +497,7 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
     const uint32_t tau = tops.tau;
     const Wanted wanted(tau);
     const int room = TopShared<T>::kCand / static_cast<int>(cl.size);
-    uint64_t* mine = cl.at(tops.cand, 0) + cl.rank * room;
+    uint64_t* mine = cl.at(tops.cand(), 0) + cl.rank * room;
     const uint32_t least = wanted.few ? kMaskedKey + 1 : tau;
     int found = collect<DT, T>(part, wanted, least, tops, mine, room);
     if (writes) v.write(a, row, token, to_float<DT>(token_x));
@@ -500,11 +514,11 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
     for (int i = tid; i < total; i += T) {
       int r = 0, at = i;
       while (at >= tops.count[r]) at -= tops.count[r++];
-      const uint64_t pair = tops.cand[r * room + at];
+      const uint64_t pair = tops.cand()[r * room + at];
       int place = 0;
       for (unsigned q = 0; q < cl.size; ++q)
         for (int j = 0; j < tops.count[q]; j += 8) {
-          const auto* four = reinterpret_cast<const ulonglong2*>(tops.cand + q * room + j);
+          const auto* four = reinterpret_cast<const ulonglong2*>(tops.cand() + q * room + j);
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const ulonglong2 two = four[h];
