@@ -192,13 +192,13 @@ struct RowList {
 //   unlisted  d = w scale (p / p_t) (p_t b - q_t)    listed  d = w scale (p b - q)
 // where without a bucket q_t = 0 and the first is p b.
 //
-// 4096 x 128256 bf16, 64 listed: 372 us, 5.65 TB/s of the bytes that have to move,
-// 0.83 of the measured copy. What is left is the time from a part's last sum to its
+// 4096 x 128256 bf16, 64 listed: 378 us, 5.56 TB/s of the bytes that have to move,
+// 0.82 of the measured copy. What is left is the time from a part's last sum to its
 // first gradient and from its start to the list's marks, a fifth of a block's life,
 // which two other blocks on the SM cover in part: more of them (4: 409 us against
 // 390 then) put L2 over its size. A row held in shared memory (445 us) or in
 // registers (495) between the passes leaves room for fewer blocks. The loss alone
-// (1024 x 50257 fp16: 22 us, 0.70) is one pass, four blocks an SM.
+// (1024 x 50257 fp16: 24 us, 0.63) is one pass, four blocks an SM.
 //
 // Eight warps go through the elements and do as little else as can be; the ninth
 // has the row's list, the exchange between the blocks and the row's loss:

@@ -25,7 +25,7 @@ struct LogprobArgs {
 // One pass over the row gives m = max x, s = sum 2^d and t = sum 2^d d over
 // d = (x - m) c: the normaliser, log p_i = (x_i - m) scale - ln s, and the entropy
 // H = ln s - ln 2 t / s. It is bound by HBM: 4096 x 128256 bf16 without
-// alternatives 164 us, 6.4 TB/s, 0.94 of the measured copy.
+// alternatives 166 us, 6.3 TB/s, 0.93 of the measured copy.
 //
 // The alternatives come from the same pass: the maximum of every unit (4 vectors of
 // a thread, more in rows longer than 4096 units a block) stays in shared memory,
@@ -39,20 +39,20 @@ struct LogprobArgs {
 // it is full.
 //
 // The selection is a chain of small dependent reads beside a loaded memory system,
-// as long as a third of a 128256-token row's stream, and what bounds the kernel
-// with alternatives (2048 x 128256 bf16, 64 of them: 104 us, 5.1 TB/s, 0.75 of the
-// copy). Blocks of 128 threads, eight to an SM, hide some of it where there are
-// rows enough (at 16 maxima a thread in 32 bits 119 us against 127, and 1021 x 50257
-// fp32 44 against 49), and the less shared memory they take the more L1 is left to
-// the loads in flight (32 maxima in 32 bits: 128 and 57 us; in 16 bits 114 and 43;
-// candidates in the units' place, 11 KB a block instead of 16: 105 to 104, 42.2 to
-// 41.5).
-// What a row's selection issues counts as well: a batch instead of a vector a thread
-// when units are read again (no division, one place taken for all its candidates),
-// the bits that all keys share skipped in the search, eight candidates compared a
-// step: 108 to 105 us. A ninth warp that selects while eight stream the next row
-// measured 139 us, a threshold counted by all threads instead of a search in one
-// warp 131.
+// as long as a quarter of a 128256-token row's stream, and what bounds the kernel
+// with alternatives (2048 x 128256 bf16, 64 of them: 105 us, 5.0 TB/s, 0.74 of the
+// copy; the units read again are a tenth more of DRAM traffic). Blocks of 128
+// threads, eight to an SM, hide some of it where there are rows enough (105 us
+// against 122, and 1021 x 50257 fp32 42 against 48), and the less shared memory
+// they take the more L1 is left to the loads in flight (32 maxima a thread in 32
+// bits: 128 and 57 us; in 16 bits 114 and 43; candidates in the units' place, 11 KB
+// a block instead of 16: a last 1%). What a row issues counts as well: maxima cut
+// instead of rounded and a 32-bit index took 114 to 108 us; a batch instead of a
+// vector a thread when units are read again (no division, one place taken for all
+// its candidates), the bits that all keys share skipped in the search and eight
+// candidates compared a step 108 to 105. A ninth warp that selects while eight
+// stream the next row measured 139 us, a threshold counted by all threads instead of
+// a search in one warp 131, both against 119 then.
 //
 // A call on a few rows is bound by latencies: 8 x 128256 takes 9 us, of which the
 // stream is a fifth, the cluster's two barriers a third.
