@@ -250,9 +250,9 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
       t = fma2(e, d, t);
     }
   }
-  acc.at.s = fmaf(s.sum(), acc.ref.k, acc.at.s);
+  acc.s += s.sum();
   const float tt = t.sum();  // NaN with masked elements: the batch goes without its part of the (tiny) mending
-  acc.at.t += tt == tt ? tt : 0.0f;
+  acc.t += tt == tt ? tt : 0.0f;
 }
 
 struct DistillShared {

@@ -251,26 +251,37 @@ __device__ __forceinline__ uint64_t order_pair(float x, int64_t id) {
 // exponential: the reference is the first batch's maximum for nearly all threads, and `top` the maximum.
 template <int SLACK>
 struct Running {
-  RowSum at;     // around the reference at.m
-  float top;     // max x
-  float limit;   // elements above it move the reference
-  ExpRef ref;    // of at.m
+  float m;      // the reference
+  float s, t;   // sums of 2^a and 2^a a, a = ref.arg(x): those around m when m moves and at the end
+  float top;    // max x
+  float limit;  // elements above it move the reference
+  ExpRef ref;   // of m
 
-  __device__ __forceinline__ Running(RowSum first, float c) : at(first), top(first.m), ref(first.m, c) {
-    limit = first.m + SLACK / c;
-  }
-  __device__ __forceinline__ void see(float m, float c) {
-    top = fmaxf(top, m);
-    if (m > limit) {
-      at.move(m, c);
-      ref = ExpRef(m, c);
-      limit = m + SLACK / c;
+  __device__ __forceinline__ Running(RowSum first, float c) : top(first.m), ref(first.m, c) { put(first, c); }
+  __device__ __forceinline__ void see(float to, float c) {
+    top = fmaxf(top, to);
+    if (to > limit) {
+      RowSum a = around();
+      a.move(to, c);
+      put(a, c);
     }
   }
   // The sums around the maximum.
-  __device__ __forceinline__ RowSum done(float c) {
-    if (top > at.m) at.move(top, c);
-    return at;
+  __device__ __forceinline__ RowSum done(float c) const {
+    RowSum a = around();
+    if (top > m) a.move(top, c);
+    return a;
+  }
+
+ private:
+  __device__ __forceinline__ RowSum around() const { return {m, s * ref.k, fmaf(ref.shift, s, t) * ref.k}; }
+  __device__ __forceinline__ void put(const RowSum& a, float c) {
+    ref = ExpRef(a.m, c);
+    const float back = ex2(-ref.shift);
+    m = a.m;
+    s = a.s * back;
+    t = fmaf(-ref.shift, s, a.t * back);
+    limit = m + SLACK / c;
   }
 };
 

@@ -104,8 +104,8 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, Runni
       }
     }
   }
-  acc.at.s = fmaf(ss, ref.k, acc.at.s);
-  acc.at.t = fmaf(fmaf(ref.shift, ss, tt), ref.k, acc.at.t);
+  acc.s += ss;
+  acc.t += tt;
   return m;
 }
 
