@@ -205,7 +205,7 @@ struct RowList {
 //   clear   row -> list    the marks are zero
 //   ready   list -> row    the listed tokens are marked
 //   added   row -> list    the warps' sums are in `red`
-//   scales  list -> row    the gradient's factors are in `factor`
+//   scales  list -> row    the gradient's factors are in `unlisted`
 //   written row -> list    the gradient is written; the list's own goes on top
 // The listed tokens are left out of the sums (a bit per element of the part says
 // which they are), so the unlisted mass is a sum of its own terms and not a
@@ -255,11 +255,30 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
   acc.t += tt == tt ? tt : 0.0f;
 }
 
+// The gradient's factors for the unlisted tokens: a 2^(arg(x) + lift), arg as ExpRef has it. The lift is added to the
+// argument: in r it would be rounded to r's digits.
+struct Unlisted {
+  float c, r, a, lift;
+
+  // The gradient of the part's elements, the listed ones' to be written over.
+  template <int DT>
+  __device__ __forceinline__ void map(const RowPart<DT>& part, uint4 (&w)[kBatch], Elem<DT>* d, bool vec,
+                                      float edge) const {
+    const Pair c2 = Pair::both(c), r2 = Pair::both(-r), a2 = Pair::both(a);
+    if (lift == 0.0f) {
+      part.map(w, d, vec, edge, [&](Pair x) { return mul2(ex2_pair(fma2(x, c2, r2)), a2); });
+    } else {
+      const Pair up = Pair::both(lift);
+      part.map(w, d, vec, edge, [&](Pair x) { return mul2(ex2_pair(add2(fma2(x, c2, r2), up)), a2); });
+    }
+  }
+};
+
 struct DistillShared {
   RowSum red[kRowWarps];
   RowSum parts[kMaxCluster];
   int4 list_ids[SS_MAX_TOP / 4];
-  float factor[3];
+  Unlisted unlisted;
   uint32_t edge_listed;
 };
 
@@ -326,11 +345,7 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
     // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
     const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - l.q_tail) / out.s;
     const ExpRef ref(out.m, c);
-    if (lane == 0) {
-      sh.factor[0] = ref.c;
-      sh.factor[1] = ref.r;
-      sh.factor[2] = A * ref.k;
-    }
+    if (lane == 0) sh.unlisted = {ref.c, ref.r, A * ref.k, 0.0f};
     barrier_arrive<kScales, kListThreads>();
   }
   if (cl.rank == 0) {
@@ -457,8 +472,7 @@ __global__ void __launch_bounds__(kListThreads, BLOCKS) distill_kernel(const __g
   if constexpr (GRAD) {
     part.load(0, v);
     barrier_sync<kScales, kListThreads>();
-    const Pair f_c = Pair::both(sh.factor[0]), f_r = Pair::both(-sh.factor[1]), f_a = Pair::both(sh.factor[2]);
-    part.map(v, d, a.vec, edge, [&](Pair f) { return mul2(ex2_pair(fma2(f, f_c, f_r)), f_a); });
+    sh.unlisted.map<DT>(part, v, d, a.vec, edge);
     barrier_arrive<kWritten, kListThreads>();
   }
   if (cl.size > 1) cl.wait();
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kListThreads, BLOCKS) distill_kernel(const __g
 template <int DT>
 __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ int4 list_ids[SS_MAX_TOP / 4];
-  __shared__ float factor[3];
+  __shared__ Unlisted unlisted;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
@@ -495,8 +509,7 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
   if (tid < kRowThreads) {
     const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : 0.0f;
     barrier_sync<kScales, kListThreads>();
-    const Pair c = Pair::both(factor[0]), r = Pair::both(-factor[1]), A = Pair::both(factor[2]);
-    part.map(first, d, a.vec, edge, [&](Pair f) { return mul2(ex2_pair(fma2(f, c, r)), A); });
+    unlisted.map<DT>(part, first, d, a.vec, edge);
     barrier_arrive<kWritten, kListThreads>();
     return;
   }
@@ -509,7 +522,7 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
   // so small that the exponentials without it would vanish
   const ExpRef ref(norm.x, a.c);
   const float over = ref.k / norm.y;
-  float A = ws * b * over, r = ref.r;
+  float A = ws * b * over, lift = 0.0f;
   if (a.mode == SS_TAIL_BUCKET) {
     const float tail = a.tail_in[row], p_t = expf(tail);
     if (tail == -kInf) {
@@ -518,14 +531,10 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
       A = ws * (p_t * b - l.q_tail) * (over / p_t);
     } else {
       A = ws * (p_t * b - l.q_tail) * over;
-      r = fmaf(tail, kLog2e, r);
+      lift = -tail * kLog2e;
     }
   }
-  if ((tid & 31) == 0) {
-    factor[0] = ref.c;
-    factor[1] = r;
-    factor[2] = A;
-  }
+  if ((tid & 31) == 0) unlisted = {ref.c, ref.r, A, lift};
   float g[kSlots];
   if (a.in_place) {  // the logits have to be here before the other warps write over them
 #pragma unroll
