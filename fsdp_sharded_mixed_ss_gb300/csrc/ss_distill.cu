@@ -239,17 +239,22 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
   for (int u = 1; u < kBatch; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
   acc.see(m, c);
   Pair s = Pair::both(0.0f), t = s;
+  const auto add = [&](auto far) {
+    const ExpArg ref = acc.reference(c);
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    Pair f[kPairsOf<DT>];
-    unpack_pairs<DT>(w[u], f);
+    for (int u = 0; u < kBatch; ++u) {
+      Pair f[kPairsOf<DT>];
+      unpack_pairs<DT>(w[u], f);
 #pragma unroll
-    for (int j = 0; j < kPairsOf<DT>; ++j) {
-      const Pair d = acc.ref.arg(f[j]), e = ex2_pair(d);
-      s = add2(s, e);
-      t = fma2(e, d, t);
+      for (int j = 0; j < kPairsOf<DT>; ++j) {
+        const Pair d = ref.template arg<decltype(far)::value>(f[j]), e = ex2_pair(d);
+        s = add2(s, e);
+        t = fma2(e, d, t);
+      }
     }
-  }
+  };
+  if (acc.r == acc.r) add(std::false_type());
+  else add(std::true_type());
   acc.s += s.sum();
   const float tt = t.sum();  // NaN with masked elements: the batch goes without its part of the (tiny) mending
   acc.t += tt == tt ? tt : 0.0f;
@@ -258,18 +263,20 @@ __device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, Runn
 // The gradient's factors for the unlisted tokens: a 2^(arg(x) + lift), arg as ExpRef has it. The lift is added to the
 // argument: in r it would be rounded to r's digits.
 struct Unlisted {
-  float c, r, a, lift;
+  float r, a, lift;
+  bool far;
 
   // The gradient of the part's elements, the listed ones' to be written over.
   template <int DT>
-  __device__ __forceinline__ void map(const RowPart<DT>& part, uint4 (&w)[kBatch], Elem<DT>* d, bool vec,
+  __device__ __forceinline__ void map(const RowPart<DT>& part, float scale2, uint4 (&w)[kBatch], Elem<DT>* d, bool vec,
                                       float edge) const {
-    const Pair c2 = Pair::both(c), r2 = Pair::both(-r), a2 = Pair::both(a);
-    if (lift == 0.0f) {
-      part.map(w, d, vec, edge, [&](Pair x) { return mul2(ex2_pair(fma2(x, c2, r2)), a2); });
+    const Pair c = Pair::both(scale2), a2 = Pair::both(a), r2 = Pair::both(-r);
+    if (!far && lift == 0.0f) {
+      part.map(w, d, vec, edge, [&](Pair x) { return mul2(ex2_pair(fma2(x, c, r2)), a2); });
     } else {
-      const Pair up = Pair::both(lift);
-      part.map(w, d, vec, edge, [&](Pair x) { return mul2(ex2_pair(add2(fma2(x, c2, r2), up)), a2); });
+      const Pair from = Pair::both(far ? -r : 0.0f), back = Pair::both(far ? 0.0f : -r), up = Pair::both(lift);
+      part.map(w, d, vec, edge,
+               [&](Pair x) { return mul2(ex2_pair(add2(fma2(add2(x, from), c, back), up)), a2); });
     }
   }
 };
@@ -345,7 +352,7 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
     // unlisted: (p / p_t) (p_t b - q_t) = 2^((x - m_out) c) / s_out (p_t b - q_t)
     const float A = no_tail ? ws * 0.0f * all.s : ws * (p_t * b - l.q_tail) / out.s;
     const ExpRef ref(out.m, c);
-    if (lane == 0) sh.unlisted = {ref.c, ref.r, A * ref.k, 0.0f};
+    if (lane == 0) sh.unlisted = {ref.r, A * ref.k, 0.0f, ref.far};
     barrier_arrive<kScales, kListThreads>();
   }
   if (cl.rank == 0) {
@@ -472,7 +479,7 @@ __global__ void __launch_bounds__(kListThreads, BLOCKS) distill_kernel(const __g
   if constexpr (GRAD) {
     part.load(0, v);
     barrier_sync<kScales, kListThreads>();
-    sh.unlisted.map<DT>(part, v, d, a.vec, edge);
+    sh.unlisted.map<DT>(part, c, v, d, a.vec, edge);
     barrier_arrive<kWritten, kListThreads>();
   }
   if (cl.size > 1) cl.wait();
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
   if (tid < kRowThreads) {
     const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : 0.0f;
     barrier_sync<kScales, kListThreads>();
-    unlisted.map<DT>(part, first, d, a.vec, edge);
+    unlisted.map<DT>(part, a.c, first, d, a.vec, edge);
     barrier_arrive<kWritten, kListThreads>();
     return;
   }
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
       lift = -tail * kLog2e;
     }
   }
-  if ((tid & 31) == 0) unlisted = {ref.c, ref.r, A, lift};
+  if ((tid & 31) == 0) unlisted = {ref.r, A, lift, ref.far};
   float g[kSlots];
   if (a.in_place) {  // the logits have to be here before the other warps write over them
 #pragma unroll

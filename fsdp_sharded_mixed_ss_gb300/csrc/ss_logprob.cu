@@ -76,7 +76,7 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, Runni
 #pragma unroll
   for (int u = 1; u < N; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
   acc.see(m, c);
-  const ExpRef& ref = acc.ref;
+  const Pair scale2 = Pair::both(c), back = Pair::both(-acc.r);
   Pair s = Pair::both(0.0f), t = s;
 #pragma unroll
   for (int u = 0; u < N; ++u) {
@@ -84,25 +84,27 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, Runni
     unpack_pairs<DT>(w[u], f);
 #pragma unroll
     for (int j = 0; j < kPairsOf<DT>; ++j) {
-      const Pair d = ref.arg(f[j]), e = ex2_pair(d);
+      const Pair d = fma2(f[j], scale2, back), e = ex2_pair(d);
       s = add2(s, e);
       t = fma2(e, d, t);
     }
   }
-  const float ss = s.sum();
-  float tt = t.sum();
-  if (!(tt == tt)) {  // masked elements (0 * -inf): the same sum with them at kFloor
-    tt = 0.0f;
+  float ss = s.sum(), tt = t.sum();
+  if (!(tt == tt)) {  // masked elements (0 * -inf), or a far reference: the sums one by one, masked arguments at kFloor
+    const ExpArg ref = acc.reference(c);
+    float again = tt = 0.0f;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       float f[V];
       unpack<DT>(w[u], f);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float d = fmaxf(ref.arg(f[j]), kFloor);
-        tt = fmaf(ex2(d), d, tt);
+        const float d = ref.arg(f[j]), e = ex2(d);
+        again += e;
+        tt = fmaf(e, fmaxf(d, kFloor), tt);
       }
     }
+    if (ref.far) ss = again;
   }
   acc.s += ss;
   acc.t += tt;
@@ -616,13 +618,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_grad_kernel(const __gr
   const float lift = ref.shift - log2f(norm.y), over = ref.k / norm.y;
   const float B = -a.scale * dh * kLn2 * over;
   const float A = a.scale * (dl - sum - (a.d_entropy ? dh * h : 0.0f)) * over;
-  auto grad = [&](Pair f) {
-    const Pair l = ref.arg(f);
+  auto from_arg = [&](Pair l) {
     const float2 g = add2(l, Pair::both(lift)).split();
     const Pair clear = Pair::of(fmaxf(g.x, kFloor), fmaxf(g.y, kFloor));
     return mul2(ex2_pair(l), fma2(Pair::both(B), clear, Pair::both(A)));
   };
-  auto grad_flat = [&](Pair f) { return mul2(ex2_pair(ref.arg(f)), Pair::both(A)); };  // no entropy
+  auto grad = [&](Pair f) { return from_arg(ref.arg<false>(f)); };
+  auto grad_flat = [&](Pair f) { return mul2(ex2_pair(ref.arg<false>(f)), Pair::both(A)); };  // no entropy
+  auto grad_far = [&](Pair f) { return from_arg(ref.arg<true>(f)); };
   // a listed element's whole gradient, by the thread that holds its slot: several slots may name one id, and all
   // of them write the same
   float whole = 0.0f;
@@ -632,10 +635,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_grad_kernel(const __gr
     float v = 0.0f;
     for (int j = 0; j < n_ids; ++j)
       if (ids[j] == static_cast<int32_t>(id)) v += up[j];
-    whole = fmaf(a.scale, v, grad(Pair::both(to_float<DT>(x[id]))).split().x);
+    whole = fmaf(a.scale, v, from_arg(Pair::both(ref.arg(to_float<DT>(x[id])))).split().x);
   }
   __syncthreads();
-  if (dh != 0.0f) part.map(first, d, a.vec, edge, grad);
+  if (ref.far) part.map(first, d, a.vec, edge, grad_far);
+  else if (dh != 0.0f) part.map(first, d, a.vec, edge, grad);
   else part.map(first, d, a.vec, edge, grad_flat);
   __syncthreads();
   if (mine) d[id] = from_float<DT>(whole);

@@ -11,8 +11,9 @@ adds the roundings of (x - m) scale - log s, a few of its own EPS32.
 import numpy as np
 import pytest
 
-from logits_ref import REL, grad_bound, row_distill, row_softmax
-from test_gpu_logits_ops import MODES, _check_distill, _close, _logits, _np, _tail, _teacher
+from logits_ref import REL, grad_bound, row_distill, row_logprobs_grad, row_softmax
+from test_gpu_logits_ops import (MODES, TYPES, _check_distill, _check_logprobs, _close, _logits, _np, _outputs,
+                                 _same_layout, _tail, _teacher)
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -73,3 +74,163 @@ def test_saved_gradient_of_small_tails(ss, gap, offset):
         bound = grad_bound(g, size, "fp32")
         _close(_np(d[r]), g, bound, ("fused", r))
         _close(_np(e[r]), g, bound + 4 * 2.0 ** -24 * abs(lpt) * np.abs(g), ("saved", r))
+
+
+FILLS = [-1e9, -2e9, -3e9, -1e10, -1e12, -1e15, -1e20, -1e29, -1e30, -1e35, 3e9, 1e10, 1e20]
+SCALES = [1.0, 0.5, 1.0 / 0.7, 10.0]
+
+
+def _filled(dtype, vocab, fills, **kw):
+    """For each fill a row of nothing else, one with all but ten tokens filled, one with a contiguous half filled, one
+    with every third token filled, and one whose first tokens and last one are left."""
+    x = _logits(5 * len(fills), vocab, dtype, **kw)
+    for i, f in enumerate(fills):
+        r = x[5 * i:5 * i + 5]
+        keep = torch.arange(10, device="cuda") * (vocab // 11) + 3
+        kept = r[1, keep].clone()
+        r[0] = f
+        r[1] = f
+        r[1, keep] = kept
+        r[2, vocab // 3:vocab // 3 + vocab // 2] = f
+        r[3, ::3] = f
+        r[4, 3:-1] = f
+    return x
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_logprobs_filled_rows(ss, dtype, scale):
+    x = _filled(dtype, 3001, FILLS, pad=7, off=1)
+    tok = torch.arange(x.shape[0], device="cuda") * 37 % 3001
+    _check_logprobs(ss, x, tok, 0, scale)
+    _check_logprobs(ss, x, tok, 17, scale)
+
+
+@pytest.mark.parametrize("vocab", [50257, 128256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_logprobs_filled_rows_shared_by_blocks(ss, dtype, vocab):
+    """Whole threads and blocks of a row that see fills only."""
+    x = _filled(dtype, vocab, [-1e10], pad=1)
+    tok = torch.arange(x.shape[0], device="cuda") * 37
+    _check_logprobs(ss, x, tok, 20)
+    _check_logprobs(ss, x, tok, 0, 1.0 / 0.7)
+
+
+@pytest.mark.parametrize("dtype,vocab,k", [("bf16", 33001, 20), ("fp32", 16390, 50)])
+def test_logprobs_filled_many_rows(ss, dtype, vocab, k):
+    rows = 1000
+    x = _logits(rows, vocab, dtype, pad=3, seed=9)
+    fills = [-1e9, -2e9, -1e10, -1e15, -1e29]
+    for i, f in enumerate(fills):
+        x[10 * i, :] = f
+        x[10 * i + 1, : vocab // 2] = f
+        x[10 * i + 2, vocab // 2:] = f
+        x[10 * i + 3, ::2] = f
+        x[10 * i + 4, 50:] = f
+    x[60:, -vocab // 4:] = -1e10
+    _check_logprobs(ss, x, torch.arange(rows, device="cuda") * 31 % vocab, k)
+
+
+@pytest.mark.parametrize("scale", [1e3, 1e5, 1e7, 1e10, 1e20])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_logprobs_low_temperatures(ss, dtype, scale):
+    """Temperatures at which a row's largest logit has all the mass, or shares it with its equals."""
+    x = _logits(12, 5001, dtype, pad=1, seed=3)
+    x[3] -= 40.0
+    x[4] = x[4].abs() * -1.0
+    x[5, 7:900:31] = x[5].max()
+    x[6] = 17.25
+    x[7] = 0.0
+    _check_logprobs(ss, x, torch.arange(12, device="cuda") * 400, 9, scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("offset", [-3e2, 1e4, -1e6, 1e7, 3e7, -2e8, 4e9])
+def test_logprobs_logits_far_from_zero(ss, dtype, offset):
+    """Ordinary differences (as far as the type holds them) around a large offset."""
+    vocab, digits = 4001, 8 if dtype == "bf16" else 24
+    base = float(torch.tensor(offset, dtype=TYPES[dtype]))
+    step = 2.0 ** (np.frexp(abs(base))[1] - digits)  # between neighbouring numbers of the type
+    x = torch.empty((6, vocab), dtype=TYPES[dtype], device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    x.copy_((base + torch.randint(-6, 1, x.shape, generator=g, device="cuda").double() * step))
+    for scale in (1.0, 0.25, 1.0 / step, 3.0 / step):
+        _check_logprobs(ss, x, torch.arange(6, device="cuda") * 11, 5, scale)
+
+
+def _check_logprobs_grad(ss, x, tok, dtype, scale):
+    rows, k = x.shape[0], 4
+    out = _outputs(rows, k)
+    ss.ss_token_logprobs(x, tok, scale=scale, **out)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    up = {n: torch.randn(rows, generator=g, device="cuda") for n in ("d_logprob", "d_entropy", "d_lse")}
+    up["d_top_logprob"] = torch.randn((rows, k), generator=g, device="cuda")
+    d = torch.full_like(x, 9.0)
+    X, s32 = _np(x), float(np.float32(scale))
+    for names in [("d_logprob",), ("d_entropy",), tuple(up)]:
+        ss.ss_token_logprobs_grad(x, out["norm"], d, tokens=tok, entropy=out["entropy"], top_id=out["top_id"],
+                                  scale=scale, **{n: up[n] for n in names})
+        torch.cuda.synchronize()
+        got = _np(d)
+        for i in range(rows):
+            u = {n: float(up[n][i]) for n in names if n != "d_top_logprob"}
+            if "d_top_logprob" in names:
+                u["top_id"], u["d_top"] = out["top_id"][i].tolist(), up["d_top_logprob"][i].tolist()
+            ref, size = row_logprobs_grad(X[i], s32, token=int(tok[i]) if "d_logprob" in names else None, **u)
+            # ex2 gives 0 for probabilities below 2^-126; log p and H near 0 are off by what the forward call's may be
+            least = s32 * 2.0 ** -126 * (1e3 if "d_entropy" in names else 20.0)
+            logs = 3 * REL * s32 * abs(u.get("d_entropy", 0.0)) * np.exp(row_softmax(X[i], s32)[0])
+            _close(got[i], ref, grad_bound(ref, size, dtype) + least + logs, (names, i))
+    y = _same_layout(x)
+    ss.ss_token_logprobs_grad(y, out["norm"], y, tokens=tok, entropy=out["entropy"], top_id=out["top_id"], scale=scale,
+                              **up)
+    torch.cuda.synchronize()
+    assert torch.equal(y, d)
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_logprobs_grad_filled_rows(ss, dtype, scale):
+    x = _filled(dtype, 1501, FILLS, pad=3, off=2)
+    _check_logprobs_grad(ss, x, torch.arange(x.shape[0], device="cuda") * 37 % 1501, dtype, scale)
+
+
+@pytest.mark.parametrize("scale", [1e3, 1e5, 1e7, 1e10])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_logprobs_grad_low_temperatures(ss, dtype, scale):
+    x = _logits(6, 2001, dtype, seed=3)
+    x[3] -= 40.0
+    x[4, 7:900:31] = x[4].max()
+    x[5] = 17.25
+    _check_logprobs_grad(ss, x, torch.arange(6, device="cuda") * 300, dtype, scale)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mode", MODES)
+def test_distill_filled_rows(ss, mode, dtype, scale):
+    x = _filled(dtype, 1203, FILLS, pad=5)
+    ids, t = _teacher(x, 12, scale, idt=torch.int64)
+    _check_norms(ss, x, ids, t, mode, scale)
+    _check_distill(ss, x, ids, t, mode, scale=scale, dtype=dtype, dpad=5)
+
+
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 128256), ("fp32", 50257)])
+def test_distill_filled_rows_shared_by_blocks(ss, dtype, vocab):
+    x = _filled(dtype, vocab, [-1e10], pad=1)
+    ids, t = _teacher(x, 64, 1.0)
+    _check_norms(ss, x, ids, t, "bucket", 1.0)
+    _check_distill(ss, x, ids, t, "bucket", dtype=dtype, dpad=1)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("scale", [1e7, 1e10])
+def test_distill_low_temperatures(ss, scale, mode):
+    x = _logits(5, 2001, "fp32", seed=3)
+    x[3] -= 40.0
+    x[4] = 17.25
+    ids, t = _teacher(x, 9, 1.0)
+    _check_norms(ss, x, ids, t, mode, scale)
+    _check_distill(ss, x, ids, t, mode, scale=scale, dtype="fp32")
