@@ -298,7 +298,7 @@ struct Running {
     r = e.far ? nan_f() : e.r;
     s = a.s * back;
     t = fmaf(-e.shift, s, a.t * back);
-    limit = m + SLACK / c;
+    limit = m == -kInf ? m : m + SLACK / c;  // SLACK / c may be infinite
   }
 };
 

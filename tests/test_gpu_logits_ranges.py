@@ -234,3 +234,19 @@ def test_distill_low_temperatures(ss, scale, mode):
     ids, t = _teacher(x, 9, 1.0)
     _check_norms(ss, x, ids, t, mode, scale)
     _check_distill(ss, x, ids, t, mode, scale=scale, dtype="fp32")
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-37, 1e-38, 1e-39, 1.5e-45])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_smallest_scales(ss, dtype, scale):
+    """Rows that a scale near zero makes uniform over their unmasked tokens."""
+    x = _logits(4, 3001, dtype, pad=3, off=1)
+    x[1, 5:2000] = -float("inf")
+    x[2] = -float("inf")
+    tok = torch.tensor([7, 2500, 0, 3000], device="cuda")
+    _check_logprobs(ss, x, tok, 17, scale)
+    _check_logprobs(ss, x, tok, 0, scale)
+    ids, t = _teacher(x, 12, 1.0)
+    ids[1] = torch.arange(12, device="cuda") + 2900
+    for mode in MODES:
+        _check_distill(ss, x, ids, t, mode, scale=scale, dtype=dtype, dpad=3, doff=1)
