@@ -139,7 +139,7 @@ struct RowList {
     const float ref = m == -kInf ? 0.0f : m;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) s += expf((v[i] - ref) * scale);
+    for (int i = 0; i < kSlots; ++i) s += expf(scaled_gap(v[i], ref, scale));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
     return {m, s};
@@ -340,12 +340,12 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
   out.mend(a.eps);
   // the row's mass: the listed tokens' and the unlisted ones', around the larger of their maxima
   RowMass all = {fmaxf(l.in.m, out.m), 0.0f};
-  all.s = (l.in.m == all.m ? l.in.s : l.in.s * expf((l.in.m - all.m) * a.scale)) +
-          (out.m == all.m ? out.s : out.s * expf((out.m - all.m) * a.scale));
+  all.s = (l.in.m == all.m ? l.in.s : l.in.s * expf(scaled_gap(l.in.m, all.m, a.scale))) +
+          (out.m == all.m ? out.s : out.s * expf(scaled_gap(out.m, all.m, a.scale)));
   const bool empty = all.s == 0.0f;
   // all unlisted tokens masked, by -inf or by values so low that no p_t is left
-  const bool no_tail = out.s == 0.0f || (out.m - all.m) * c <= kFloor;
-  const float p_t = no_tail ? 0.0f : expf((out.m - all.m) * a.scale) * (out.s / all.s);
+  const bool no_tail = out.s == 0.0f || scaled_gap(out.m, all.m, c) <= kFloor;
+  const float p_t = no_tail ? 0.0f : expf(scaled_gap(out.m, all.m, a.scale)) * (out.s / all.s);
   const float ws = l.bad ? nan_f() : w * a.scale;
   const float b = l.q_sum + l.q_tail;
   if constexpr (GRAD) {
@@ -360,12 +360,12 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
     // logs of p_t and p themselves while there is something of them: log s is a few units, and its rounding would be
     // in every digit of a small divergence
     const float tail = no_tail ? -kInf
-                               : (p_t > 1e-30f ? logf(p_t) : fmaf(out.m - all.m, a.scale, logf(out.s) - ln_s));
+                               : (p_t > 1e-30f ? logf(p_t) : scaled_gap(out.m, all.m, a.scale, logf(out.s) - ln_s));
     float loss = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       if (l.id[i] >= 0 && l.q[i] != 0.0f) {
-        const float z = (l.x[i] - all.m) * a.scale, p = expf(z) / all.s;
+        const float z = scaled_gap(l.x[i], all.m, a.scale), p = expf(z) / all.s;
         const float lp = empty ? -kInf : (p > 1e-30f ? logf(p) : z - ln_s);
         loss += l.q[i] * (l.lq[i] - lp);
       }

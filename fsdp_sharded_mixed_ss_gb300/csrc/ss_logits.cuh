@@ -223,6 +223,11 @@ struct ExpRef : ExpArg {
   }
 };
 
+// (x - m) scale + add, also where x - m passes fp32's range and the product does not.
+__device__ __forceinline__ float scaled_gap(float x, float m, float scale, float add = 0.0f) {
+  return fmaf(fmaf(0.5f, x, -0.5f * m), 2.0f * scale, add);
+}
+
 // m = max x (-inf before the first unmasked element), s = sum 2^d and
 // t = sum 2^d d over d = (x - m) c.
 struct RowSum {
@@ -232,7 +237,7 @@ struct RowSum {
   // Moves the maximum up to `to` (> m).
   __device__ __forceinline__ void move(float to, float c) {
     if (s != 0.0f) {  // NaN sums move too
-      const float d = fmaxf((m - to) * c, kFloor), f = ex2(d);
+      const float d = fmaxf(scaled_gap(m, to, c), kFloor), f = ex2(d);
       t = f * fmaf(s, d, t);
       s *= f;
     }

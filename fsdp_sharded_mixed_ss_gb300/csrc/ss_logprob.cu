@@ -399,7 +399,7 @@ struct RowValues {
       : all(a), scale(scale_), ln_s(logf(a.s)), nan(!(a.s == a.s)), empty(a.s == 0.0f) {}
   __device__ __forceinline__ float logp(float x) const {
     if (nan) return nan_f();
-    return empty ? -kInf : fmaf(x - all.m, scale, -ln_s);
+    return empty ? -kInf : scaled_gap(x, all.m, scale, -ln_s);
   }
   __device__ __forceinline__ void write(const LogprobArgs& a, int64_t row, int64_t token, float token_x) const {
     if (a.norm) a.norm[row] = make_float2(all.m, all.s);

@@ -250,3 +250,22 @@ def test_smallest_scales(ss, dtype, scale):
     ids[1] = torch.arange(12, device="cuda") + 2900
     for mode in MODES:
         _check_distill(ss, x, ids, t, mode, scale=scale, dtype=dtype, dpad=3, doff=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_differences_past_the_types_range(ss, dtype):
+    """x - max x passes what the type holds, and the scale brings it back."""
+    lowest, big = torch.finfo(TYPES[dtype]).min, torch.finfo(TYPES[dtype]).max
+    vocab = 2003
+    x = torch.full((3, vocab), lowest, dtype=TYPES[dtype], device="cuda")
+    x[0, 7] = big
+    x[1, ::2] = big
+    x[2] = (torch.linspace(-0.99, 0.99, vocab, device="cuda", dtype=torch.float64) * big).to(x.dtype)
+    tok = torch.tensor([3, 1, 0], device="cuda")
+    for scale in (0.25, 0.4, 1e-20, 2e-37, 1e-37, 2e-38, 5e-39):
+        _check_logprobs(ss, x, tok, 9, scale)
+    ids, t = _teacher(x, 12, 1.0)
+    ids[2] = torch.arange(12, device="cuda") * 150
+    for mode in MODES:
+        for scale in (0.25, 2e-37, 1e-37, 2e-38, 5e-39):
+            _check_distill(ss, x, ids, t, mode, scale=scale, dtype=dtype)
