@@ -383,23 +383,37 @@ def _rows_of(x, shape, ld, dtype, scale):
         if dtype is None:
             dtype = -1
         return _LOGITS.pack(x, rows, vocab, vocab if ld is None else ld, dtype, scale), rows, vocab, dtype
-    if _ID_DTYPES is None:
-        _load_dtypes()
     rows, vocab = x.shape
     ld, one = x.stride()
     if one != 1 and vocab > 1:
         raise SSError(1, "logits: the vocabulary must have stride 1")
     if ld < vocab and rows == 1:  # torch gives a single row any stride
         ld = vocab
-    dtype = _DTYPES.get(x.dtype, -1)
+    dtype = _float_type(x)
     return _LOGITS.pack(x.data_ptr(), rows, vocab, ld, dtype, scale), rows, vocab, dtype
 
 
 def _load_dtypes():
+    """The tables of torch's types: whichever helper sees the process's first tensor loads them, since a call may have
+    addresses in any of its other places."""
     global _ID_DTYPES, _F32
     torch = _t()
     _F32 = torch.float32
     _ID_DTYPES = {torch.int32: SS_I32, torch.int64: SS_I64}
+
+
+def _float_type(t):
+    """The ss_dtype of a tensor, -1 for another type."""
+    if _DTYPES is None:
+        _load_dtypes()
+    return _DTYPES.get(t.dtype, -1)
+
+
+def _id_type(t):
+    """The ss_idtype of a tensor, -1 for another type."""
+    if _ID_DTYPES is None:
+        _load_dtypes()
+    return _ID_DTYPES.get(t.dtype, -1)
 
 
 def _grad_rows(d, rows, vocab, dtype, d_ld):
@@ -411,7 +425,7 @@ def _grad_rows(d, rows, vocab, dtype, d_ld):
     ld, one = d.stride()
     if tuple(d.shape) != (rows, vocab) or (one != 1 and vocab > 1):
         raise SSError(1, "d_logits: the logits' shape, with stride 1 along the vocabulary")
-    if _DTYPES.get(d.dtype, -1) != dtype:
+    if _float_type(d) != dtype:
         raise SSError(4, "d_logits")
     return d.data_ptr(), (vocab if ld < vocab and rows == 1 else ld)
 
@@ -422,6 +436,8 @@ def _f32(t, n, where):
         return 0
     if isinstance(t, int):
         return t
+    if _F32 is None:
+        _load_dtypes()
     if t.dtype is not _F32:
         raise SSError(4, where)
     if t.numel() != n or not t.is_contiguous():
@@ -435,7 +451,7 @@ def _ids(t, n, idtype, where):
         return 0
     if isinstance(t, int):
         return t
-    if _ID_DTYPES.get(t.dtype, -1) != idtype:
+    if _id_type(t) != idtype:
         raise SSError(4, where)
     if t.numel() != n or not t.is_contiguous():
         raise SSError(1, f"{where}: a dense array of {n} elements")
@@ -446,9 +462,7 @@ def _idtype(ids, idtype):
     """The ss_idtype of the call: the tensor's, or `idtype` for an address."""
     if ids is None or isinstance(ids, int):
         return SS_I64 if idtype is None else idtype
-    if _ID_DTYPES is None:
-        _load_dtypes()
-    return _ID_DTYPES.get(ids.dtype, -1)
+    return _id_type(ids)
 
 
 def _call(fn, where, like, stream, *args) -> None:
@@ -514,7 +528,7 @@ def _teacher_of(r, ids, logprob, row_weight, tail, teacher_scale, k, idtype, tdt
     if isinstance(logprob, int):
         at, td = logprob, -1 if tdtype is None else tdtype
     else:
-        at, td = logprob.data_ptr(), _DTYPES.get(logprob.dtype, -1)
+        at, td = logprob.data_ptr(), _float_type(logprob)
         if logprob.numel() != r * k or not logprob.is_contiguous():
             raise SSError(1, f"teacher: a dense array of {r * k} elements")
     return _TEACHER.pack(_ids(ids, r * k, it, "ids"), at, _f32(row_weight, r, "row_weight"), k, it, td, tail,
