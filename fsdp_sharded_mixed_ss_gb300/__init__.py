@@ -375,14 +375,26 @@ _ID_DTYPES = None
 _F32 = None
 
 
+def _pack(form, where, *values) -> bytes:
+    try:
+        return form.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise SSError(1, f"{where}: {e}") from None
+
+
 def _rows_of(x, shape, ld, dtype, scale):
     """(ss_logits, rows, vocab, dtype) of a 2-D tensor (unit stride along the vocabulary), or of an address with shape
     = (rows, vocab), ld (default: vocab) and dtype."""
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
+        if shape is None:
+            raise SSError(1, "logits: an address needs its shape")
         rows, vocab = shape
         if dtype is None:
             dtype = -1
-        return _LOGITS.pack(x, rows, vocab, vocab if ld is None else ld, dtype, scale), rows, vocab, dtype
+        return (_pack(_LOGITS, "logits", x or 0, rows, vocab, vocab if ld is None else ld, dtype, scale), rows, vocab,
+                dtype)
+    if x.dim() != 2:
+        raise SSError(1, "logits: (rows, vocab)")
     rows, vocab = x.shape
     ld, one = x.stride()
     if one != 1 and vocab > 1:
@@ -390,7 +402,7 @@ def _rows_of(x, shape, ld, dtype, scale):
     if ld < vocab and rows == 1:  # torch gives a single row any stride
         ld = vocab
     dtype = _float_type(x)
-    return _LOGITS.pack(x.data_ptr(), rows, vocab, ld, dtype, scale), rows, vocab, dtype
+    return _pack(_LOGITS, "logits", x.data_ptr(), rows, vocab, ld, dtype, scale), rows, vocab, dtype
 
 
 def _load_dtypes():
@@ -422,9 +434,9 @@ def _grad_rows(d, rows, vocab, dtype, d_ld):
         return None, 0
     if isinstance(d, int):
         return d, (vocab if d_ld is None else d_ld)
-    ld, one = d.stride()
-    if tuple(d.shape) != (rows, vocab) or (one != 1 and vocab > 1):
+    if tuple(d.shape) != (rows, vocab) or (d.stride(1) != 1 and vocab > 1):
         raise SSError(1, "d_logits: the logits' shape, with stride 1 along the vocabulary")
+    ld = d.stride(0)
     if _float_type(d) != dtype:
         raise SSError(4, "d_logits")
     return d.data_ptr(), (vocab if ld < vocab and rows == 1 else ld)
@@ -467,7 +479,7 @@ def _idtype(ids, idtype):
 
 def _call(fn, where, like, stream, *args) -> None:
     """fn(*args, stream) with `like`'s device current."""
-    dev = -1 if isinstance(like, int) else like.get_device()
+    dev = -1 if like is None or isinstance(like, int) else like.get_device()
     if _RAW_STREAM is not None and dev >= 0 and dev == _GET_DEVICE():
         rc = fn(*args, _RAW_STREAM(dev) if stream is None else _stream(stream))
     else:
@@ -524,15 +536,17 @@ def ss_token_logprobs_grad(logits, norm, d_logits, *, tokens=None, d_logprob=Non
 def _teacher_of(r, ids, logprob, row_weight, tail, teacher_scale, k, idtype, tdtype):
     it = _idtype(ids, idtype)
     if k is None:
+        if ids is None or isinstance(ids, int):
+            raise SSError(1, "ids: an address needs k")
         k = ids.shape[-1]
-    if isinstance(logprob, int):
-        at, td = logprob, -1 if tdtype is None else tdtype
+    if logprob is None or isinstance(logprob, int):
+        at, td = logprob or 0, -1 if tdtype is None else tdtype
     else:
         at, td = logprob.data_ptr(), _float_type(logprob)
         if logprob.numel() != r * k or not logprob.is_contiguous():
             raise SSError(1, f"teacher: a dense array of {r * k} elements")
-    return _TEACHER.pack(_ids(ids, r * k, it, "ids"), at, _f32(row_weight, r, "row_weight"), k, it, td, tail,
-                         teacher_scale, 0)
+    return _pack(_TEACHER, "teacher", _ids(ids, r * k, it, "ids"), at, _f32(row_weight, r, "row_weight"), k, it, td,
+                 tail, teacher_scale, 0)
 
 
 def ss_distill_topk(logits, ids, teacher, loss=None, *, norm=None, tail_logprob=None, d_logits=None, row_weight=None,

@@ -32,3 +32,31 @@ def test_addresses_with_tensors_in_the_first_call(call):
             "X = torch.zeros((0, 1000), dtype=torch.bfloat16)\n" + CALLS[call])
     p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert p.returncode == 0, p.stderr
+
+
+def test_what_the_binding_cannot_pass_on_is_refused():
+    """With the library's own error, before anything is launched."""
+    import torch
+
+    import fsdp_sharded_mixed_ss_gb300 as ss
+
+    x = torch.zeros(4, 10, dtype=torch.bfloat16)
+    f, t, ids = torch.zeros(4), torch.zeros(4, 3), torch.zeros(4, 3, dtype=torch.int32)
+    at = 0x10000000
+    for call in [lambda: ss.ss_token_logprobs(x[0], lse=f, stream=0),
+                 lambda: ss.ss_token_logprobs(x.view(2, 2, 10), lse=f, stream=0),
+                 lambda: ss.ss_token_logprobs(None, lse=f, stream=0),
+                 lambda: ss.ss_token_logprobs(None, shape=(4, 10), dtype=ss.SS_BF16, lse=f, stream=0),
+                 lambda: ss.ss_token_logprobs(at, lse=f, dtype=ss.SS_BF16, stream=0),
+                 lambda: ss.ss_token_logprobs(at, lse=f, dtype=ss.SS_BF16, shape=(4, 1 << 70), stream=0),
+                 lambda: ss.ss_token_logprobs(x, lse=f, scale=1e39, stream=0),
+                 lambda: ss.ss_token_logprobs_grad(x, torch.zeros(4, 2), x[0], d_lse=f, stream=0),
+                 lambda: ss.ss_distill_topk(x, None, t, f, stream=0),
+                 lambda: ss.ss_distill_topk(x, None, t, f, k=3, stream=0),
+                 lambda: ss.ss_distill_topk(x, ids, None, f, stream=0),
+                 lambda: ss.ss_distill_topk(x, at, t, f, idtype=ss.SS_I32, stream=0),
+                 lambda: ss.ss_distill_topk(x, ids, t, f, teacher_scale=1e39, stream=0),
+                 lambda: ss.ss_distill_topk(x, ids, t, f, tail=1 << 40, stream=0)]:
+        with pytest.raises(ss.SSError) as e:
+            call()
+        assert e.value.status == 1
