@@ -269,3 +269,33 @@ def test_differences_past_the_types_range(ss, dtype):
     for mode in MODES:
         for scale in (0.25, 2e-37, 1e-37, 2e-38, 5e-39):
             _check_distill(ss, x, ids, t, mode, scale=scale, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("mode", MODES)
+def test_saved_gradient_over_its_logits(ss, mode, dtype):
+    """The gradient from saved normalisers written over the logits: the same bits as apart from them, with rows in one
+    part and in several, and listed tokens in every part and at both ends."""
+    for rows, vocab, pad, off, k in [(3, 7, 0, 0, 5), (4, 9, 1, 1, 9), (7, 1000, 0, 3, 128), (9, 33001, 5, 3, 100),
+                                     (40, 128256, 3, 1, 128), (300, 70001, 0, 0, 64)]:
+        x = _logits(rows, vocab, dtype, pad=pad, off=off, seed=k)
+        ids, t = _teacher(x, k, 1.0, seed=k)
+        if vocab > 2 * k:  # a third of the slots over the whole row, the edges among them
+            n = k // 3
+            ids[:, :n] = (torch.arange(n, device="cuda") * ((vocab - 1) // (n - 1))).to(ids.dtype)
+            ids[:, 0], ids[:, 1], ids[:, n - 1] = 0, vocab - 1, vocab - 2
+        w = torch.linspace(0.25, 2.0, rows, device="cuda")
+        w[rows // 2] = 0.0
+        norm, tail, loss = (torch.empty(s, device="cuda") for s in ((rows, 2), (rows,), (rows,)))
+        kw = dict(row_weight=w, tail=_tail(ss, mode))
+        ss.ss_distill_topk(x, ids, t, loss, norm=norm, tail_logprob=tail, **kw)
+        up = torch.linspace(0.5, 2.0, rows, device="cuda")
+        up[0] = 0.0 if rows > 4 else 1.0
+        kw.update(tail_logprob=tail, d_loss=up)
+        apart = torch.full_like(x, 3.0)
+        ss.ss_distill_topk_grad(x, ids, t, norm, apart, **kw)
+        y = _same_layout(x)
+        ss.ss_distill_topk_grad(y, ids, t, norm, y, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(y, apart), (rows, vocab)
+        assert not bool(apart.isnan().any())
