@@ -266,15 +266,18 @@ ss_status ss_reshard(const void* flat, const int64_t* shard_bounds, int32_t n_ra
  *   - `norm` [rows][2] is a row's normaliser as the pair (max x, sum exp(scale
  *     (x - max x))): lse = scale * norm[0] + log norm[1]. The forward calls
  *     write it, the gradient calls take it. Kept as a pair it has all its digits
- *     whatever the size of the logits (a row that a mask filled with the type's
- *     lowest value is the uniform distribution that the formulas say).
+ *     whatever the size of the logits and of the scale (a row that a mask
+ *     filled with a finite value, the type's lowest or -1e10, is the uniform
+ *     distribution that the formulas say).
  *   - A row all of whose logits are -inf (a mask that leaves nothing) has
  *     p = 0 everywhere, lse = -inf and norm = (-inf, 0); the calls below say
  *     what they write.
  *   - A row with a NaN or +inf logit has a NaN sum and lse, and everything
  *     computed from it is NaN.
- *   - Logits of -inf elsewhere are masked tokens: p = 0, log p = -inf, and
- *     nothing flows back to them.
+ *   - Logits of -inf elsewhere are masked tokens: p = 0 and log p = -inf. Their
+ *     gradient is what the formulas leave with p = 0: nothing, but for a masked
+ *     token that is itself given or listed, which keeps its own term (scale
+ *     times its upstream gradient, -row_weight scale q).
  * x: element i of row r is data[r * ld + i]; ld >= vocab (elements), so a view
  *   of the first `vocab` columns of a padded head's output needs no copy.
  *   Any element alignment; 16-byte vector accesses are used from each row's
@@ -346,6 +349,10 @@ ss_status ss_token_logprobs_grad(const ss_logits* x, const void* tokens, ss_idty
  *                   one more outcome, against the student's mass p_t of all
  *                   unlisted tokens. */
 typedef enum ss_tail { SS_TAIL_DROP = 0, SS_TAIL_RENORM = 1, SS_TAIL_BUCKET = 2 } ss_tail;
+/* Longest rows of the distillation calls: a bit per element marks the listed
+ * tokens in the shared memory of the at most 8 blocks that share a row (12 KB in
+ * each at this length), and the rows in flight are read twice and have to stay
+ * in L2 in between. */
 #define SS_MAX_DISTILL_VOCAB 393216
 
 /* A teacher's top k tokens of every row; device arrays. */
