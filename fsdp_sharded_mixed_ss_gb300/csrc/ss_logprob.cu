@@ -90,21 +90,33 @@ __device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, Runni
     }
   }
   float ss = s.sum(), tt = t.sum();
-  if (!(tt == tt)) {  // masked elements (0 * -inf), or a far reference: the sums one by one, masked arguments at kFloor
-    const ExpArg ref = acc.reference(c);
-    float again = tt = 0.0f;
+  if (!(tt == tt)) {  // two loops: in one for both, 4096 x 128256 without alternatives 166.5 us against 164.1
+    tt = 0.0f;
+    if (acc.r == acc.r) {  // masked elements (0 * -inf): the same sum with them at kFloor
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      float f[V];
-      unpack<DT>(w[u], f);
+      for (int u = 0; u < N; ++u) {
+        float f[V];
+        unpack<DT>(w[u], f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float d = ref.arg(f[j]), e = ex2(d);
-        again += e;
-        tt = fmaf(e, fmaxf(d, kFloor), tt);
+        for (int j = 0; j < V; ++j) {
+          const float d = fmaxf(fmaf(f[j], c, -acc.r), kFloor);
+          tt = fmaf(ex2(d), d, tt);
+        }
+      }
+    } else {  // a far reference: both sums, the difference first
+      ss = 0.0f;
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        float f[V];
+        unpack<DT>(w[u], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = acc.reference(c).arg(f[j]), e = ex2(d);
+          ss += e;
+          tt = fmaf(e, fmaxf(d, kFloor), tt);
+        }
       }
     }
-    if (ref.far) ss = again;
   }
   acc.s += ss;
   acc.t += tt;
