@@ -365,9 +365,11 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       if (l.id[i] >= 0 && l.q[i] != 0.0f) {
-        const float z = scaled_gap(l.x[i], all.m, a.scale), p = expf(z) / all.s;
-        const float lp = empty ? -kInf : (p > 1e-30f ? logf(p) : z - ln_s);
-        loss += l.q[i] * (l.lq[i] - lp);
+        const float half = half_gap(l.x[i], all.m), p = expf(half * (2.0f * a.scale)) / all.s;
+        // a small p's log by its logit, times q before the scale, which may take the log alone past fp32's range
+        if (empty) loss += kInf;
+        else if (p > 1e-30f) loss += l.q[i] * (l.lq[i] - logf(p));
+        else loss += fmaf(-l.q[i] * half, 2.0f * a.scale, l.q[i] * (l.lq[i] + ln_s));
       }
     }
 #pragma unroll

@@ -223,9 +223,10 @@ struct ExpRef : ExpArg {
   }
 };
 
-// (x - m) scale + add, also where x - m passes fp32's range and the product does not.
+// (x - m) / 2, which does not overflow, and (x - m) scale + add from it.
+__device__ __forceinline__ float half_gap(float x, float m) { return fmaf(0.5f, x, -0.5f * m); }
 __device__ __forceinline__ float scaled_gap(float x, float m, float scale, float add = 0.0f) {
-  return fmaf(fmaf(0.5f, x, -0.5f * m), 2.0f * scale, add);
+  return fmaf(half_gap(x, m), 2.0f * scale, add);
 }
 
 // m = max x (-inf before the first unmasked element), s = sum 2^d and

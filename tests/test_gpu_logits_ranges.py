@@ -299,3 +299,26 @@ def test_saved_gradient_over_its_logits(ss, mode, dtype):
         torch.cuda.synchronize()
         assert torch.equal(y, apart), (rows, vocab)
         assert not bool(apart.isnan().any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mode", MODES)
+def test_losses_whose_logs_pass_the_types_range(ss, mode, dtype):
+    """A listed token at the type's lowest value, and a scale that takes its log p, not its part of the loss, past what
+    fp32 holds."""
+    lowest, vocab, k = torch.finfo(TYPES[dtype]).min, 1203, 12
+    x = _logits(4, vocab, dtype, pad=5)
+    ids, t = _teacher(x, k, 1.0)
+    for r in range(4):
+        x[r, ids[r, 3 + r].long()] = lowest
+    t = (torch.arange(k, device="cuda") * -0.3 - 2.5).repeat(4, 1)  # q of 0.08 and less, 0.3 in all
+    loss, alone, d = torch.empty(4, device="cuda"), torch.empty(4, device="cuda"), torch.empty_like(x)
+    for scale in (1.0 / 0.7, 2.0, 5.0):
+        kw = dict(tail=_tail(ss, mode), scale=scale)
+        ss.ss_distill_topk(x, ids, t, loss, d_logits=d, **kw)
+        ss.ss_distill_topk(x, ids, t, alone, **kw)
+        torch.cuda.synchronize()
+        X, I, T, s32 = _np(x), ids.tolist(), _np(t), float(np.float32(scale))
+        for r in range(4):
+            ref, _, _, _, size = row_distill(X[r], s32, I[r], T[r], 1.0, mode, 1.0)
+            _close([loss[r].item(), alone[r].item()], [ref, ref], 4 * REL * size, ("loss", mode, scale, r))
