@@ -359,8 +359,8 @@ __device__ __forceinline__ void list_warp(const DistillArgs& a, const Cluster& c
     const float ln_s = logf(all.s);
     // logs of p_t and p themselves while there is something of them: log s is a few units, and its rounding would be
     // in every digit of a small divergence
-    const float tail = no_tail ? -kInf
-                               : (p_t > 1e-30f ? logf(p_t) : scaled_gap(out.m, all.m, a.scale, logf(out.s) - ln_s));
+    float tail = p_t > 1e-30f ? logf(p_t) : scaled_gap(out.m, all.m, a.scale, logf(out.s) - ln_s);
+    if (no_tail) tail = all.s == all.s ? -kInf : nan_f();
     float loss = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __g
   if (a.mode == SS_TAIL_BUCKET) {
     const float tail = a.tail_in[row], p_t = expf(tail);
     if (tail == -kInf) {
-      A = ws * 0.0f;
+      A = ws * 0.0f * norm.y;  // NaN for a row that is
     } else if (tail > -60.0f) {
       A = ws * (p_t * b - l.q_tail) * (over / p_t);
     } else {

@@ -322,3 +322,23 @@ def test_losses_whose_logs_pass_the_types_range(ss, mode, dtype):
         for r in range(4):
             ref, _, _, _, size = row_distill(X[r], s32, I[r], T[r], 1.0, mode, 1.0)
             _close([loss[r].item(), alone[r].item()], [ref, ref], 4 * REL * size, ("loss", mode, scale, r))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("mode", MODES)
+def test_distill_listed_tokens_that_are_not_numbers(ss, mode, dtype):
+    """NaN or +inf at a listed token, whatever the unlisted ones are: loss, log p_t and both gradients are NaN."""
+    inf, lowest = float("inf"), torch.finfo(TYPES[dtype]).min
+    x = _logits(8, 1203, dtype, pad=5)
+    ids, t = _teacher(x, 12, 1.0)
+    for r, rest in enumerate([None, -inf, lowest, -1e4]):
+        for row, value in ((r, float("nan")), (4 + r, inf)):
+            if rest is not None:
+                kept = x[row, ids[row].long()].clone()
+                x[row] = rest
+                x[row, ids[row].long()] = kept
+            x[row, ids[row, 5].long()] = value
+    _check_distill(ss, x, ids, t, mode, dtype=dtype, dpad=5)
+    tail = torch.zeros(8, device="cuda")
+    ss.ss_distill_topk(x, ids, t, tail_logprob=tail, tail=_tail(ss, mode))
+    assert bool(tail.isnan().all())
