@@ -561,26 +561,6 @@ struct RowPart {
       for (int u = 0; u < kBatch; ++u) w[u] = next[u];
     }
   }
-  // f(value, id) of every element of this thread's vectors numbered [j0, j1).
-  template <class F>
-  __device__ __forceinline__ void each(int j0, int j1, const F& f) const {
-    for (int j = j0; j < j1; j += kBatch) {
-      uint4 w[kBatch];
-      const char* p = at() + j * step_bytes();
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (j + u < j1 && more(j + u)) w[u] = __ldg(reinterpret_cast<const uint4*>(p + u * step_bytes()));
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (j + u < j1 && more(j + u)) {
-          float e[V];
-          unpack<DT>(w[u], e);
-#pragma unroll
-          for (int q = 0; q < V; ++q) f(e[q], sl.head + (first + (j + u) * step()) * V + q);
-        }
-      }
-    }
-  }
 };
 
 // ------------------------------------------------------------------ host checks
