@@ -6,10 +6,10 @@
 namespace ss {
 namespace {
 
-// Vectors a thread in a block's part of a row shared by a cluster. 4096 x 128256 bf16 with 8, 16, 32, 64: 758, 522,
-// 403, 446 us (below, each part's fixed work shows; above, the rows in flight no longer fit L2).
+// Vectors a thread in a block's part of a row shared by a cluster. 4096 x 128256 bf16 with 8, 16, 32, 64: 620, 458,
+// 375, 428 us (below, each part's fixed work shows; above, the rows in flight no longer fit L2).
 constexpr int kPartVectors = 32;
-constexpr int kFewVectors = 8;  // with few rows (64 x 128256 fp32: parts of 31 vectors 20.4 us, of 16 16.1 us)
+constexpr int kFewVectors = 8;  // with few rows (64 x 128256 fp32: parts of 32 vectors 18.3 us, of 16 16.4 us)
 
 struct DistillArgs {
   const void* x;
@@ -192,7 +192,7 @@ struct RowList {
 //   unlisted  d = w scale (p / p_t) (p_t b - q_t)    listed  d = w scale (p b - q)
 // where without a bucket q_t = 0 and the first is p b.
 //
-// 4096 x 128256 bf16, 64 listed: 378 us, 5.56 TB/s of the bytes that have to move,
+// 4096 x 128256 bf16, 64 listed: 376 us, 5.59 TB/s of the bytes that have to move,
 // 0.82 of the measured copy. What is left is the time from a part's last sum to its
 // first gradient and from its start to the list's marks, a fifth of a block's life,
 // which two other blocks on the SM cover in part: more of them (4: 409 us against
@@ -289,8 +289,9 @@ struct DistillShared {
   uint32_t edge_listed;
 };
 
-// Of the row that comes after, with the loss alone: 0, 16, 32, 64 KB: 24.6, 24.3, 23.6, 22.9 us. (With a gradient: 385,
-// 398, 404, 434 us; the rows in flight need the L2.)
+// Of the row that comes after, with the loss alone: 0, 16, 32, 64 KB: 24.6, 24.3, 23.6, 22.9 us when it was chosen,
+// 23.4, 23.3, 23.5, 24.1 with the loop as it is now. (With a gradient: 385, 398, 404, 434 us; the rows in flight need
+// the L2.)
 constexpr int kAheadBytes = 65536;
 
 // The ninth warp's part in a row. `marks`: a word of listed bits for each batch of vectors, by thread.
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kListThreads, BLOCKS) distill_kernel(const __g
 // One pass: blocks share a row as above, but nothing is exchanged between them.
 // A ninth warp has the list while the first vectors are on their way. Bound by HBM:
 // 2048 x 128256 bf16 165 us, 6.4 TB/s, 0.94 of the copy (parts of 16, 32, 64 vectors
-// a thread: 185, 171, 173 us: every part looks its list up).
+// a thread: 172, 166, 170 us: every part looks its list up).
 template <int DT>
 __global__ void __launch_bounds__(kListThreads, 4) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ int4 list_ids[SS_MAX_TOP / 4];

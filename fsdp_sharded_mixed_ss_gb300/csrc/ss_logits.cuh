@@ -247,7 +247,9 @@ struct RowSum {
   // Two small systematic errors of s, mended to first order. c is the scale's product with log2(e) rounded to 24 bits,
   // which is a slightly different temperature: eps ln 2 t (eps: its relative error, 2^-25 at most). And ex2.approx
   // falls short by 9e-8 on average, but for the maximum's own 2^0 (sums of 9291 to 128256 terms against float64, over
-  // four spreads and three scales: 4e-8 to 1.6e-7); a loss of a few hundredths would lose its sixth digit to that.
+  // four spreads and three scales: 4e-8 to 1.7e-7; mended, 9e-8 at most on average over rows); a loss of a few
+  // hundredths would lose its sixth digit to that. The price: sums whose terms are exactly 2^0, of rows without any
+  // spread, come out up to a unit in their last place too large (6e-8 to 1.1e-7).
   __device__ __forceinline__ void mend(float eps) { s += fmaf(eps * kLn2, t, 9e-8f * fmaxf(s - 1.0f, 0.0f)); }
 };
 
@@ -272,8 +274,8 @@ struct Running {
   float s, t;   // sums of 2^a and 2^a a, a = reference().arg(x): those around m when m moves and at the end
   float top;    // max x
   float limit;  // elements above it move the reference
-  float r;      // a = x c - r; NaN where m is far: a loop that looks at its sums for NaN, as masked elements give it, has
-                // this for nothing (a look of its own: 2048 x 128256 with 64 alternatives 108.5 us against 104.5)
+  float r;      // a = x c - r; NaN where m is far: a loop that looks at its sums for NaN, as masked elements give it,
+                // has this for nothing (a look of its own: 2048 x 128256 with 64 alternatives 108.5 us against 104.5)
 
   __device__ __forceinline__ Running(RowSum first, float c) : top(first.m) { put(first, c); }
   __device__ __forceinline__ void see(float to, float c) {

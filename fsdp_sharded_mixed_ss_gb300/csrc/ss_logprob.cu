@@ -25,7 +25,7 @@ struct LogprobArgs {
 // One pass over the row gives m = max x, s = sum 2^d and t = sum 2^d d over
 // d = (x - m) c: the normaliser, log p_i = (x_i - m) scale - ln s, and the entropy
 // H = ln s - ln 2 t / s. It is bound by HBM: 4096 x 128256 bf16 without
-// alternatives 166 us, 6.3 TB/s, 0.93 of the measured copy.
+// alternatives 164 us, 6.4 TB/s, 0.94 of the measured copy.
 //
 // The alternatives come from the same pass: the maximum of every unit (4 vectors of
 // a thread, more in rows longer than 4096 units a block) stays in shared memory,
@@ -40,10 +40,10 @@ struct LogprobArgs {
 //
 // The selection is a chain of small dependent reads beside a loaded memory system,
 // as long as a quarter of a 128256-token row's stream, and what bounds the kernel
-// with alternatives (2048 x 128256 bf16, 64 of them: 105 us, 5.0 TB/s, 0.74 of the
+// with alternatives (2048 x 128256 bf16, 64 of them: 103 us, 5.1 TB/s, 0.75 of the
 // copy; the units read again are a tenth more of DRAM traffic). Blocks of 128
-// threads, eight to an SM, hide some of it where there are rows enough (105 us
-// against 122, and 1021 x 50257 fp32 42 against 48), and the less shared memory
+// threads, eight to an SM, hide some of it where there are rows enough (103 us
+// against 121, and 1021 x 50257 fp32 42 against 48), and the less shared memory
 // they take the more L1 is left to the loads in flight (32 maxima a thread in 32
 // bits: 128 and 57 us; in 16 bits 114 and 43; candidates in the units' place, 11 KB
 // a block instead of 16: a last 1%). What a row issues counts as well: maxima cut
@@ -63,7 +63,12 @@ template <int T>
 constexpr int kFlagged = 4 * T;    // units that are read again
 constexpr int kKeys = 256;         // threads' maxima that the threshold is taken from
 constexpr int kManyThreads = 128;  // threads of a block that selects alternatives of one of many rows
-constexpr int kManyRows = 6;       // so many rows an SM (1021 rows are 6.7)
+// So many rows an SM. 256 and 128 threads, us: 50257 bf16 with 20 alternatives, 608 rows 20.0 21.1, 684 rows 30.1 25.1,
+// 836 rows 32.1 25.7, 912 rows 33.3 26.4; 128256 bf16 with 64, 36.7 41.6, 55.0 50.2, 58.0 51.7, 60.4 52.7; 50257 fp32
+// with 20, 28.7 31.5, 42.6 34.3, 44.6 36.6, 46.1 38.5. Up to 4 rows an SM, one wave of the larger blocks, those are
+// ahead; beyond, where they need a second wave, the smaller ones: the rule is never wrong where it takes them, and
+// leaves 609 to 911 rows to the slower form.
+constexpr int kManyRows = 6;
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
 
 using RunningSum = Running<8>;
@@ -548,8 +553,8 @@ __global__ void __launch_bounds__(T, 1024 / T) logprob_kernel(const __grid_const
 }
 
 // Blocks that share a row: rows alone fill the GPU from about 4 blocks on each SM; fewer rows are split while
-// every thread keeps half a batch of vectors. 1, 2, 4, 8 blocks: 8 x 128256 bf16 16.2, 13.8, 11.6, 11.0 us; 2048 rows
-// of it (64 alternatives) 146, 156, 217 us for 1, 2, 4.
+// every thread keeps half a batch of vectors. 1, 2, 4, 8 blocks: 8 x 128256 bf16 14.3, 11.4, 9.4, 9.1 us; 4096 rows
+// of it (no alternatives) 164, 177, 213 us for 1, 2, 4.
 int cluster_for(int64_t rows, int64_t vocab, int vec) {
   const int64_t blocks = 4 * std::max(1, sm_count());
   int c = 1;
@@ -580,9 +585,9 @@ struct LogprobGradArgs {
 // One pass, each row shared by blocks that exchange nothing. Every element is
 // p (A + B log2 p); the listed ids, whose logits are read before anything is
 // written (the gradient may replace the logits), get their own terms on top.
-// Bound by HBM: 2048 x 128256 bf16 155 us, 6.77 TB/s, as fast as the copy (parts
-// of 8, 16, 32, 64 vectors a thread: 167, 156, 160, 165 us); 509 x 50257 fp32 35 us,
-// 0.86 of it, a row and a half of such parts an SM slot.
+// Bound by HBM: 2048 x 128256 bf16 156 us, 6.74 TB/s, as fast as the copy (parts
+// of 8, 16, 32, 64 vectors a thread: 165, 156, 160, 165 us); 509 x 50257 fp32 36 us,
+// 0.85 of it, a row and a half of such parts an SM slot.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 4) logprob_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
   __shared__ int32_t ids[SS_MAX_TOP + 1];
