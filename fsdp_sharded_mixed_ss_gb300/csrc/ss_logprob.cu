@@ -151,6 +151,8 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c
   const int full = part.whole / kBatch;  // batches that every thread has whole
   const int batches = (part.vectors() + kBatch - 1) / kBatch;
   const int unit_batches = part_unit_batches(part);
+  // ordinary loads, kept in L1 for the units that are read again: the kernel may start while the one ahead still writes
+  // the logits, which loads by way of the read-only path do not allow for (they take as long)
   // a 32-bit index beside the units' work, a pointer that advances without it: 2048 x 128256 with 64 alternatives 105 us
   // against 109, 4096 x 128256 without 166 against 168
   const int step = part.step();
@@ -165,12 +167,12 @@ __device__ __forceinline__ RowSum stream_row(const RowPart<DT, T>& part, float c
     uint4 w[kBatch];
     if (b < full) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) w[u] = __ldg(src + at + u * step);
+      for (int u = 0; u < kBatch; ++u) w[u] = __ldca(src + at + u * step);
     } else {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         w[u] = part.more(b * kBatch + u)
-                   ? __ldg(src + at + u * step)
+                   ? __ldca(src + at + u * step)
                    : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
     }
     if constexpr (TOPS) at += kBatch * step;
@@ -302,7 +304,7 @@ __device__ __forceinline__ int collect(const RowPart<DT, T>& part, const Wanted&
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       w[u] = vec + u * part.step() < part.sl.nvec
-                 ? __ldg(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec + u * part.step())
+                 ? __ldca(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec + u * part.step())
                  : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
     unsigned hits = 0u;
 #pragma unroll
@@ -373,7 +375,7 @@ __device__ __noinline__ int select_through_buffer(const RowPart<DT, T>& part, To
     const int vec = part.first + j * part.step();
     const bool there = vec < part.sl.nvec;
     uint4 w = make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
-    if (there) w = __ldg(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec);
+    if (there) w = __ldca(reinterpret_cast<const uint4*>(part.x + part.sl.head) + vec);
     float e[V];
     unpack<DT>(w, e);
     unsigned hits = 0u;

@@ -342,3 +342,28 @@ def test_distill_listed_tokens_that_are_not_numbers(ss, mode, dtype):
     tail = torch.zeros(8, device="cuda")
     ss.ss_distill_topk(x, ids, t, tail_logprob=tail, tail=_tail(ss, mode))
     assert bool(tail.isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_calls_read_what_the_call_before_wrote(ss, dtype):
+    """A call's kernel starts before the one ahead of it in the stream has ended: logits that the one ahead writes (a
+    gradient in their place) are read after it, also where the same blocks have read them before."""
+    for rows, vocab, k in [(1500, 33001, 8), (300, 20011, 0), (12, 128256, 20)]:
+        x = _logits(rows, vocab, dtype, seed=2)
+        ids, t = _teacher(x, 16, 1.0)
+        tok = torch.arange(rows, device="cuda")
+        y = x.clone()
+        loss = torch.empty(rows, device="cuda")
+        ss.ss_distill_topk(y, ids, t, loss, d_logits=y)
+        torch.cuda.synchronize()
+        want = _outputs(rows, k)
+        ss.ss_token_logprobs(y, tok, scale=100.0, **want)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            z, got, first = x.clone(), _outputs(rows, k), _outputs(rows, k)
+            torch.cuda.synchronize()
+            ss.ss_token_logprobs(z, tok, **first)
+            ss.ss_distill_topk(z, ids, t, loss, d_logits=z)
+            ss.ss_token_logprobs(z, tok, scale=100.0, **got)
+            torch.cuda.synchronize()
+            assert all(torch.equal(got[n], want[n]) for n in want), (rows, vocab)
