@@ -187,7 +187,7 @@ struct RowList {
 // The gradient needs the row's sums and then the row again. A row is shared by
 // the blocks of a cluster: small enough parts that all the rows in flight stay
 // in L2, so the second pass reads them from there, and HBM sees each logit read
-// once (1.06 times, by the counters) and each gradient written once. With
+// once (1.09 times, by the counters) and each gradient written once. With
 // z = scale x, p over the whole row, p_t over its unlisted tokens, b = Q + q_t:
 //   unlisted  d = w scale (p / p_t) (p_t b - q_t)    listed  d = w scale (p b - q)
 // where without a bucket q_t = 0 and the first is p b.
