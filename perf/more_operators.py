@@ -319,7 +319,7 @@ def run(s):
     if op.startswith("policy"):
         kl = {"none": ss.SS_KL_K3, "k1": ss.SS_KL_K1, "k2": ss.SS_KL_K2, "k3": ss.SS_KL_K3}[case["kl"]]
         ss.ss_policy_loss(s["x"], s["tokens"], s["advantage"], old_logprob=s["old"], ref_logprob=s["ref"],
-                          row_weight=s["weight"], clip_low=CLIP_LOW, clip_high=CLIP_HIGH, clip_max=case["dual"], kl=kl,
+                          row_weight=s["weight"], clip_low=CLIP_LOW, clip_high=CLIP_HIGH, clip_max=case["dual"], kl_kind=kl,
                           kl_coef=case["kl_coef"], entropy_coef=case["entropy"], scale=case["scale"],
                           d_logits=s.get("d_logits"), **s["out"])
         return {**s["out"], "d_logits": s["d_logits"]} if op == "policy" else s["out"]
