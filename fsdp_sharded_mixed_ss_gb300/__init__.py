@@ -30,6 +30,7 @@ SS_BF16, SS_FP16, SS_FP32 = 0, 1, 2
 SS_MAX_RANKS = 1024
 SS_I32, SS_I64 = 0, 1
 SS_TAIL_DROP, SS_TAIL_RENORM, SS_TAIL_BUCKET = 0, 1, 2
+SS_KL_K1, SS_KL_K2, SS_KL_K3 = 0, 1, 2
 SS_MAX_TOP = 128
 SS_MAX_DISTILL_VOCAB = 393216
 
@@ -73,12 +74,14 @@ class _Options(ctypes.Structure):
                 ("dev_grad_scale", ctypes.c_void_p), ("dev_skip_flag", ctypes.c_void_p)]
 
 
-# ss_logits, ss_logprob_out, ss_logprob_grad and ss_teacher as bytes: packing them costs a quarter of building a
+# ss_logits, ss_logprob_out, ss_logprob_grad, ss_teacher and the structures of the losses as bytes: packing them costs a quarter of building a
 # ctypes structure, which calls on a few rows feel
 _LOGITS = struct.Struct("@Pqqqif")
 _LOGPROB_OUT = struct.Struct("@6P")
 _LOGPROB_GRAD = struct.Struct("@4P")
 _TEACHER = struct.Struct("@3P4ifi")
+_POLICY = struct.Struct("@5P5f3i")
+_POLICY_OUT = struct.Struct("@8P")
 
 
 _NO_OPTIONS = _Options(None, None, None, None)
@@ -113,6 +116,7 @@ def _load():
                                            vp, vp, i64, vp]
     lib.ss_distill_topk.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
     lib.ss_distill_topk_grad.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.ss_policy_loss.argtypes = [vp, vp, vp, vp, i64, vp]
     lib.ss_grad_sumsq_noalloc.argtypes = [i64, vp, vp, i32, i32, f32, vp, vp, vp, vp]
     return lib
 
@@ -581,3 +585,31 @@ def ss_distill_topk_grad(logits, ids, teacher, norm, d_logits, *, tail_logprob=N
     d, dl = _grad_rows(d_logits, r, v, dt, d_ld)
     _call(_lib.ss_distill_topk_grad, "ss_distill_topk_grad", logits, stream, x, t, _f32(norm, 2 * r, "norm"),
           _f32(tail_logprob, r, "tail_logprob"), _f32(d_loss, r, "d_loss"), d, dl)
+
+
+def ss_policy_loss(logits, tokens, advantage, loss=None, *, old_logprob=None, ref_logprob=None, row_weight=None,
+                   clip_low: float = 0.2, clip_high: float = 0.2, clip_max: float = 0.0, kl_kind: int = SS_KL_K3,
+                   kl_coef: float = 0.0, entropy_coef: float = 0.0, scale: float = 1.0, logprob=None, entropy=None,
+                   ratio=None, kl=None, norm=None, d_logprob=None, d_entropy=None, d_logits=None, shape=None,
+                   ld: int | None = None, d_ld: int | None = None, dtype: int | None = None,
+                   idtype: int | None = None, stream=None) -> None:
+    """loss[r] = row_weight[r] * (-advantage clamp(ratio) + kl_coef KL - entropy_coef H) of the row's token, and, when
+    d_logits is given, the gradient of loss.sum() in the same call (d_logits may be the logits themselves).
+
+    ratio = exp(log p - old_logprob), 1 without old_logprob. It is clamped from above at 1 + clip_high for advantages
+    >= 0, from below at 1 - clip_low and (clip_max > 1) from above at clip_max for negative ones. KL is the estimate
+    SS_KL_* of the distance from ref_logprob. tokens: (rows,) int32 or int64, negative where a row has none. Every output
+    is optional and written into the given tensor: loss, logprob, entropy, ratio, kl (rows,); norm (rows, 2), d_logprob
+    and d_entropy (rows,) are what ss_token_logprobs_grad takes for a backward pass of its own. Rows of weight 0 or
+    without a token give zeros, whatever their logits.
+    """
+    x, r, v, dt = _rows_of(logits, shape, ld, dtype, scale)
+    it = _idtype(tokens, idtype)
+    d, dl = _grad_rows(d_logits, r, v, dt, d_ld)
+    p = _pack(_POLICY, "policy", _ids(tokens, r, it, "tokens"), _f32(advantage, r, "advantage"),
+              _f32(old_logprob, r, "old_logprob"), _f32(ref_logprob, r, "ref_logprob"),
+              _f32(row_weight, r, "row_weight"), clip_low, clip_high, clip_max, kl_coef, entropy_coef, kl_kind, it, 0)
+    out = _POLICY_OUT.pack(_f32(loss, r, "loss"), _f32(logprob, r, "logprob"), _f32(entropy, r, "entropy"),
+                           _f32(ratio, r, "ratio"), _f32(kl, r, "kl"), _f32(norm, 2 * r, "norm"),
+                           _f32(d_logprob, r, "d_logprob"), _f32(d_entropy, r, "d_entropy"))
+    _call(_lib.ss_policy_loss, "ss_policy_loss", logits, stream, x, p, out, d, dl)

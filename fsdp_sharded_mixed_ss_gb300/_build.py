@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libss.so")
 
 SOURCES = ["ss_layout.cpp", "ss_util.cu", "ss_step.cu", "ss_step_shift.cu", "ss_reduce.cu", "ss_norm.cu", "ss_copy.cu",
-           "ss_logprob.cu", "ss_distill.cu"]
+           "ss_logprob.cu", "ss_distill.cu", "ss_policy.cu"]
 
 
 def nvcc() -> str:

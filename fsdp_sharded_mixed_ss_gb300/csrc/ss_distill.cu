@@ -229,37 +229,6 @@ __device__ __forceinline__ void mask_elements(uint4& w, uint32_t bits) {
   }
 }
 
-using RunningMass = Running<40>;
-
-// A batch of vectors into the running sum.
-template <int DT>
-__device__ __forceinline__ void add_mass(const uint4 (&w)[kBatch], float c, RunningMass& acc) {
-  float m = vec_max<DT>(w[0]);
-#pragma unroll
-  for (int u = 1; u < kBatch; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
-  acc.see(m, c);
-  Pair s = Pair::both(0.0f), t = s;
-  const auto add = [&](auto far) {
-    const ExpArg ref = acc.reference(c);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      Pair f[kPairsOf<DT>];
-      unpack_pairs<DT>(w[u], f);
-#pragma unroll
-      for (int j = 0; j < kPairsOf<DT>; ++j) {
-        const Pair d = ref.template arg<decltype(far)::value>(f[j]), e = ex2_pair(d);
-        s = add2(s, e);
-        t = fma2(e, d, t);
-      }
-    }
-  };
-  if (acc.r == acc.r) add(std::false_type());
-  else add(std::true_type());
-  acc.s += s.sum();
-  const float tt = t.sum();  // NaN with masked elements: the batch goes without its part of the (tiny) mending
-  acc.t += tt == tt ? tt : 0.0f;
-}
-
 // The gradient's factors for the unlisted tokens: a 2^(arg(x) + lift), arg as ExpRef has it. The lift is added to the
 // argument: in r it would be rounded to r's digits.
 struct Unlisted {

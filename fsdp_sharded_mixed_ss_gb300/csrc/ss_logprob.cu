@@ -71,63 +71,6 @@ constexpr int kManyThreads = 128;  // threads of a block that selects alternativ
 constexpr int kManyRows = 6;
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // order_key(-inf)
 
-using RunningSum = Running<8>;
-
-// N vectors into the running sums; returns their maximum.
-template <int DT, int N>
-__device__ __forceinline__ float add_vectors(const uint4 (&w)[N], float c, RunningSum& acc) {
-  constexpr int V = kVecOf<DT>;
-  float m = vec_max<DT>(w[0]);
-#pragma unroll
-  for (int u = 1; u < N; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
-  acc.see(m, c);
-  const Pair scale2 = Pair::both(c), back = Pair::both(-acc.r);
-  Pair s = Pair::both(0.0f), t = s;
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-    Pair f[kPairsOf<DT>];
-    unpack_pairs<DT>(w[u], f);
-#pragma unroll
-    for (int j = 0; j < kPairsOf<DT>; ++j) {
-      const Pair d = fma2(f[j], scale2, back), e = ex2_pair(d);
-      s = add2(s, e);
-      t = fma2(e, d, t);
-    }
-  }
-  float ss = s.sum(), tt = t.sum();
-  if (!(tt == tt)) {  // two loops: in one for both, 4096 x 128256 without alternatives 166.5 us against 164.1
-    tt = 0.0f;
-    if (acc.r == acc.r) {  // masked elements (0 * -inf): the same sum with them at kFloor
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        float f[V];
-        unpack<DT>(w[u], f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float d = fmaxf(fmaf(f[j], c, -acc.r), kFloor);
-          tt = fmaf(ex2(d), d, tt);
-        }
-      }
-    } else {  // a far reference: both sums, the difference first
-      ss = 0.0f;
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        float f[V];
-        unpack<DT>(w[u], f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float d = acc.reference(c).arg(f[j]), e = ex2(d);
-          ss += e;
-          tt = fmaf(e, fmaxf(d, kFloor), tt);
-        }
-      }
-    }
-  }
-  acc.s += ss;
-  acc.t += tt;
-  return m;
-}
-
 // Batches in a unit, and units of each thread (the same for all).
 template <int DT, int T>
 __device__ __forceinline__ int part_unit_batches(const RowPart<DT, T>& part) {

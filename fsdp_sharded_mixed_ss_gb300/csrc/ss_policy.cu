@@ -1,0 +1,381 @@
+// ss_policy.cu -- the clipped policy loss of rows of logits, with a KL term and an
+// entropy bonus, and its gradient in the same call (ss_policy_loss).
+#include "ss_logits.cuh"
+
+namespace ss {
+namespace {
+
+constexpr int kPartVectors = 32;  // vectors a thread in a block's part of a row shared by a cluster
+constexpr int kFewVectors = 8;    // with few rows
+
+struct PolicyArgs {
+  const void* x;
+  const void* tokens;
+  const float* old;
+  const float* advantage;
+  const float* ref;
+  const float* weight;
+  float* loss;
+  float* logprob;
+  float* entropy;
+  float* ratio;
+  float* kl;
+  float2* norm;
+  float* d_logprob;
+  float* d_entropy;
+  void* d;
+  int64_t rows, vocab, ld, d_ld;
+  float c, eps, scale;
+  float low, high, most;  // 1 - clip_low, 1 + clip_high, clip_max (infinite: none)
+  float kl_coef, entropy_coef;
+  int32_t kl_kind;
+  bool wide, vec;
+};
+
+// ------------------------------------------------------------------ a row's scalars
+//
+// Ratios stand next to the borders of the clipping and KL terms are small
+// differences, so log p is kept as a pair: (x_t - m) scale exactly, and log s as
+// e ln 2 + log f with f in [0.7, 1.41], whose rounding is 3e-8 at most where that
+// of log s itself is 5e-7. What is left is s's own error.
+
+__device__ __forceinline__ dd plus(dd a, float b) {
+  const dd s = two_sum(a.hi, b);
+  return {s.hi, s.lo + a.lo};
+}
+
+// log of the probability of an element, as a pair; an infinity or NaN stands in hi alone.
+__device__ __forceinline__ dd pair_logp(float x, const RowSum& all, float scale) {
+  if (!(all.s == all.s)) return {nan_f(), 0.0f};
+  if (all.s == 0.0f || x == -kInf) return {-kInf, 0.0f};
+  // halves, which do not overflow
+  const dd gap = two_sum(0.5f * x, -0.5f * all.m);
+  dd z = two_prod(gap.hi, 2.0f * scale);
+  if (!finite(z.hi)) return {z.hi, 0.0f};
+  z.lo = fmaf(gap.lo, 2.0f * scale, z.lo);
+  int e;
+  float f = frexpf(all.s, &e);  // [0.5, 1)
+  if (f < 0.70710678f) {
+    f *= 2.0f;
+    e -= 1;
+  }
+  constexpr float kLn2Hi = 0.693145751953125f, kLn2Lo = 1.42860682e-6f;  // the first has 17 bits: e times it is exact
+  z = plus(z, -static_cast<float>(e) * kLn2Hi);
+  z.lo -= fmaf(static_cast<float>(e), kLn2Lo, logf(f));
+  return z;
+}
+
+// a - b of a log probability and another, which may both be infinite.
+__device__ __forceinline__ float log_ratio(dd a, float b) {
+  if (!finite(a.hi) || !finite(b)) return a.hi - b;
+  const dd s = plus(a, -b);
+  return s.hi + s.lo;
+}
+
+// exp(-g) + g - 1, without the cancellation near 0.
+__device__ __forceinline__ float excess(float g) {
+  if (fabsf(g) >= 0.5f) return g == -kInf ? kInf : expm1f(-g) + g;
+  // g^2 (1/2 - g/6 + g^2/24 - ...), the next term 2e-8 of the sum
+  float s = 1.0f / 362880.0f;
+  s = fmaf(-g, s, 1.0f / 40320.0f);
+  s = fmaf(-g, s, 1.0f / 5040.0f);
+  s = fmaf(-g, s, 1.0f / 720.0f);
+  s = fmaf(-g, s, 1.0f / 120.0f);
+  s = fmaf(-g, s, 1.0f / 24.0f);
+  s = fmaf(-g, s, 1.0f / 6.0f);
+  s = fmaf(-g, s, 0.5f);
+  return g * g * s;
+}
+
+// What the loss makes of a row.
+struct PolicyRow {
+  float loss, logprob, entropy, ratio, kl;
+  float d_logprob, d_entropy;  // the loss's derivatives with respect to log p of the token and the entropy
+
+  __device__ __forceinline__ PolicyRow(const PolicyArgs& a, const RowSum& all, float token_x, float adv, float old,
+                                       float ref, float w, bool past) {
+    const bool nan = !(all.s == all.s) || past;
+    const dd lp = past ? dd{nan_f(), 0.0f} : pair_logp(token_x, all, a.scale);
+    logprob = lp.hi + lp.lo;
+    const float h = all.s == 0.0f ? 0.0f : logf(all.s) - all.t / all.s * kLn2;
+    entropy = h < 0.0f ? 0.0f : h;
+    ratio = nan ? nan_f() : (a.old ? expf(log_ratio(lp, old)) : 1.0f);
+    const float low = adv < 0.0f ? a.low : 0.0f, high = adv < 0.0f ? a.most : a.high;
+    const float held = ratio < low ? low : (ratio > high ? high : ratio);  // NaN stays
+    loss = -adv * held;
+    d_logprob = ratio < low || ratio > high ? 0.0f : -adv * ratio;
+    kl = 0.0f;
+    if (a.ref) {
+      const float g = nan ? nan_f() : log_ratio(lp, ref);
+      kl = a.kl_kind == SS_KL_K1 ? g : (a.kl_kind == SS_KL_K2 ? 0.5f * g * g : excess(g));
+      if (a.kl_coef != 0.0f) {
+        loss = fmaf(a.kl_coef, kl, loss);
+        d_logprob = fmaf(a.kl_coef, a.kl_kind == SS_KL_K1 ? 1.0f : (a.kl_kind == SS_KL_K2 ? g : -expm1f(-g)), d_logprob);
+      }
+    }
+    d_entropy = -a.entropy_coef * w;
+    if (a.entropy_coef != 0.0f) loss = fmaf(-a.entropy_coef, entropy, loss);
+    loss *= w;
+    d_logprob = nan ? nan_f() : d_logprob * w;
+    if (nan) loss = nan_f();
+  }
+  __device__ __forceinline__ void write(const PolicyArgs& a, int64_t row, const RowSum& all) const {
+    if (a.loss) a.loss[row] = loss;
+    if (a.logprob) a.logprob[row] = logprob;
+    if (a.entropy) a.entropy[row] = entropy;
+    if (a.ratio) a.ratio[row] = ratio;
+    if (a.kl) a.kl[row] = kl;
+    if (a.norm) a.norm[row] = make_float2(all.m, all.s);
+    if (a.d_logprob) a.d_logprob[row] = d_logprob;
+    if (a.d_entropy) a.d_entropy[row] = d_entropy;
+  }
+};
+
+// The gradient of a row's elements but its token's: p (A + B log2 p), with p = 2^l and l = arg + lift.
+struct RowFactors {
+  ExpArg ref;
+  float a, b, lift;
+  bool zero;
+
+  __device__ __forceinline__ Pair from_arg(Pair l) const {
+    const float2 g = add2(l, Pair::both(lift)).split();
+    const Pair clear = Pair::of(fmaxf(g.x, kFloor), fmaxf(g.y, kFloor));
+    return mul2(ex2_pair(l), fma2(Pair::both(b), clear, Pair::both(a)));
+  }
+  __device__ __forceinline__ float at(float x) const { return from_arg(Pair::both(ref.arg(x))).split().x; }
+  template <int DT>
+  __device__ __forceinline__ void map(const RowPart<DT>& part, uint4 (&w)[kBatch], Elem<DT>* d, bool vec,
+                                      float edge) const {
+    if (ref.far) {
+      part.map(w, d, vec, edge, [&](Pair x) { return from_arg(ref.arg<true>(x)); });
+    } else if (b != 0.0f) {
+      part.map(w, d, vec, edge, [&](Pair x) { return from_arg(ref.arg<false>(x)); });
+    } else {
+      const Pair c = Pair::both(ref.c), back = Pair::both(-ref.r), a2 = Pair::both(a);
+      part.map(w, d, vec, edge, [&](Pair x) { return mul2(ex2_pair(fma2(x, c, back)), a2); });
+    }
+  }
+};
+
+// ------------------------------------------------------------------ loss and gradient
+//
+// Two passes over a row, like the distillation's: the sums, then the gradient,
+// with the rows in flight small enough to stay in L2 in between. Eight warps go
+// through the elements; the ninth has the row's scalars, the exchange between the
+// blocks of a cluster and the loss:
+//   added   row -> scalars   the warps' sums are in `red`
+//   factors scalars -> row   the gradient's factors are in `factors`
+//   written row -> scalars   the gradient is written; the token's own goes on top
+
+enum Barrier : int { kAdded = 1, kFactors = 2, kWritten = 3 };
+constexpr int kPolicyThreads = kRowThreads + 32;
+
+struct PolicyShared {
+  RowSum red[kRowWarps];
+  RowSum parts[kMaxCluster];
+  RowFactors factors;
+};
+
+template <int DT, bool GRAD>
+__device__ __forceinline__ void scalar_warp(const PolicyArgs& a, const Cluster& cl, const RowPart<DT>& part,
+                                            int64_t row, int64_t token, float w, const Elem<DT>* x, Elem<DT>* d,
+                                            PolicyShared& sh) {
+  const int lane = threadIdx.x & 31;
+  const bool past = token >= a.vocab;
+  const int id = past ? 0 : static_cast<int>(token);
+  const float token_x = to_float<DT>(x[id]);  // before anything is written: the gradient may replace the logits
+  const float adv = a.advantage[row], old = a.old ? a.old[row] : 0.0f, ref = a.ref ? a.ref[row] : 0.0f;
+  cl.started();
+  barrier_sync<kAdded, kPolicyThreads>();
+  RowSum all = merge_lanes(sh.red[lane % kRowWarps], a.c, kRowWarps);
+  if (cl.size > 1) {
+    if (lane < cl.size) cl.at(sh.parts, lane)[cl.rank] = all;
+    cl.arrive();
+    cl.wait();
+    all = merge_lanes(sh.parts[lane % cl.size], a.c, static_cast<int>(cl.size));
+  }
+  all.mend(a.eps);
+  const PolicyRow v(a, all, token_x, adv, old, ref, w, past);
+  if constexpr (GRAD) {
+    const ExpRef e(all.m, a.c);
+    const float over = all.s == 0.0f ? 0.0f : e.k / all.s;
+    RowFactors f;
+    f.ref = e;
+    f.lift = e.shift - log2f(all.s);
+    f.b = -a.scale * v.d_entropy * kLn2 * over;
+    f.a = -a.scale * (v.d_logprob + (v.d_entropy != 0.0f ? v.d_entropy * v.entropy : 0.0f)) * over;
+    f.zero = all.s == 0.0f || (v.d_logprob == 0.0f && v.d_entropy == 0.0f);
+    if (lane == 0) sh.factors = f;
+    barrier_arrive<kFactors, kPolicyThreads>();
+    if (cl.rank == 0 && lane == 0) v.write(a, row, all);
+    int owner, slot;
+    const float own = f.zero ? 0.0f : fmaf(a.scale, v.d_logprob, f.at(token_x));
+    barrier_sync<kWritten, kPolicyThreads>();
+    if (lane == 0 && !f.zero && !past && part.owns(id, &owner, &slot)) d[id] = from_float<DT>(own);
+  } else {
+    if (cl.rank == 0 && lane == 0) v.write(a, row, all);
+  }
+}
+
+// A row that carries nothing: its zeros, by every block of its cluster.
+template <int DT, bool GRAD>
+__device__ __forceinline__ void skip_row(const PolicyArgs& a, const Cluster& cl, int64_t row, Elem<DT>* d) {
+  if (GRAD && threadIdx.x < kRowThreads) zero_part<DT>(d, a.vocab, cl.rank, cl.size);
+  if (cl.rank == 0 && threadIdx.x == kRowThreads) {
+    if (a.loss) a.loss[row] = 0.0f;
+    if (a.logprob) a.logprob[row] = 0.0f;
+    if (a.entropy) a.entropy[row] = 0.0f;
+    if (a.ratio) a.ratio[row] = 0.0f;
+    if (a.kl) a.kl[row] = 0.0f;
+    if (a.norm) a.norm[row] = make_float2(0.0f, 0.0f);
+    if (a.d_logprob) a.d_logprob[row] = 0.0f;
+    if (a.d_entropy) a.d_entropy[row] = 0.0f;
+  }
+  cl.started();
+}
+
+// ENTROPY: the sum that it takes is exact with masked elements, too. BLOCKS: blocks an SM.
+template <int DT, bool GRAD, bool ENTROPY, int BLOCKS>
+__global__ void __launch_bounds__(kPolicyThreads, BLOCKS) policy_kernel(const __grid_constant__ PolicyArgs a) {
+  __shared__ PolicyShared sh;
+  const Cluster cl = Cluster::start();
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / cl.size;
+  const Elem<DT>* x = static_cast<const Elem<DT>*>(a.x) + row * a.ld;
+  Elem<DT>* d = static_cast<Elem<DT>*>(a.d) + row * a.d_ld;
+  const int64_t token = load_id(a.tokens, row, a.wide);
+  const float w = a.weight ? a.weight[row] : 1.0f;
+  const RowPart<DT> part(x, a.vocab, cl.rank, cl.size);
+  const int vectors = part.vectors();
+  const int64_t sb = part.step_bytes();
+  const char* src = part.at();
+  auto fetch = [&](const char* p, int j, uint4 (&v)[kBatch]) {
+    if (j + kBatch <= part.whole) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) v[u] = load_row<GRAD>(p + u * sb);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        v[u] = part.more(j + u) ? load_row<GRAD>(p + u * sb)
+                                : make_uint4(kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>, kMaskedWord<DT>);
+    }
+  };
+  uint4 v[kBatch];
+  if (tid < kRowThreads) fetch(src, 0, v);  // on its way while the token and the weight are
+  if (w == 0.0f || token < 0) return skip_row<DT, GRAD>(a, cl, row, d);
+  if (tid >= kRowThreads) return scalar_warp<DT, GRAD>(a, cl, part, row, token, w, x, d, sh);
+  const float edge = part.edge >= 0 ? to_float<DT>(x[part.edge]) : -kInf;
+  std::conditional_t<ENTROPY, RunningSum, RunningMass> run(one_element(edge), a.c);
+#pragma unroll 1
+  for (int j = 0; j < vectors; j += kBatch) {
+    uint4 next[kBatch];
+    src += kBatch * sb;
+    fetch(src, j + kBatch, next);
+    if constexpr (ENTROPY) add_vectors<DT>(v, a.c, run);
+    else add_mass<DT>(v, a.c, run);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) v[u] = next[u];
+  }
+  const RowSum mine = merge_lanes(run.done(a.c), a.c);
+  if ((tid & 31) == 0) sh.red[tid >> 5] = mine;
+  barrier_arrive<kAdded, kPolicyThreads>();
+  cl.started();
+  if (cl.size > 1) cl.arrive();
+  if constexpr (GRAD) {
+    part.load(0, v);
+    barrier_sync<kFactors, kPolicyThreads>();
+    const RowFactors f = sh.factors;
+    if (f.zero) zero_part<DT>(d, a.vocab, cl.rank, cl.size);
+    else f.map<DT>(part, v, d, a.vec, edge);
+    barrier_arrive<kWritten, kPolicyThreads>();
+  }
+  if (cl.size > 1) cl.wait();
+}
+
+ss_status policy_impl(const ss_logits* x, const ss_policy* p, const ss_policy_out* out, void* d_logits, int64_t d_ld,
+                      void* stream) {
+  int64_t x_bytes = 0;
+  ss_status st = check_logits(x, &x_bytes);
+  if (st != SS_OK) return st;
+  if (!p->tokens || !p->advantage) return SS_ERR_INVALID_ARG;
+  if (p->kl != SS_KL_K1 && p->kl != SS_KL_K2 && p->kl != SS_KL_K3) return SS_ERR_INVALID_ARG;
+  if (!(p->clip_low >= 0.0f) || !(p->clip_low <= 1.0f)) return SS_ERR_INVALID_ARG;
+  if (!(p->clip_high >= 0.0f) || !std::isfinite(p->clip_high)) return SS_ERR_INVALID_ARG;
+  if (p->clip_max != 0.0f && (!(p->clip_max > 1.0f) || !std::isfinite(p->clip_max))) return SS_ERR_INVALID_ARG;
+  if (!std::isfinite(p->kl_coef) || !std::isfinite(p->entropy_coef)) return SS_ERR_INVALID_ARG;
+  if ((p->kl_coef != 0.0f || out->kl) && !p->ref_logprob) return SS_ERR_INVALID_ARG;
+  if (p->idtype != SS_I32 && p->idtype != SS_I64) return SS_ERR_DTYPE;
+  if (x->rows > INT32_MAX) return SS_ERR_OVERFLOW;
+  const int64_t rows = x->rows, ib = p->idtype == SS_I64 ? 8 : 4;
+  const float* in[] = {p->old_logprob, p->advantage, p->ref_logprob, p->row_weight};
+  float* const to[] = {out->loss, out->logprob, out->entropy, out->ratio, out->kl, out->d_logprob, out->d_entropy};
+  if (misaligned(p->tokens, ib) || misaligned(out->norm, 8)) return SS_ERR_ALIGN;
+  for (const float* q : in)
+    if (misaligned(q, 4)) return SS_ERR_ALIGN;
+  for (const float* q : to)
+    if (misaligned(q, 4)) return SS_ERR_ALIGN;
+  Ranges ranges;
+  if (d_logits) {
+    st = check_grad_out(x, x_bytes, d_logits, d_ld, &ranges);
+    if (st != SS_OK) return st;
+  } else {
+    ranges.add(x->data, x_bytes, false);
+  }
+  ranges.add(p->tokens, rows * ib, false);
+  for (const float* q : in) ranges.add(q, rows * 4, false);
+  for (const float* q : to) ranges.add(q, rows * 4, true);
+  ranges.add(out->norm, rows * 8, true);
+  if (ranges.overlap()) return SS_ERR_OVERLAP;
+  const Scale2 s2(x->scale);
+  const PolicyArgs a = {x->data, p->tokens, p->old_logprob, p->advantage, p->ref_logprob, p->row_weight,
+                        out->loss, out->logprob, out->entropy, out->ratio, out->kl,
+                        reinterpret_cast<float2*>(out->norm), out->d_logprob, out->d_entropy, d_logits,
+                        rows, x->vocab, x->ld, d_ld, s2.c, s2.eps, x->scale,
+                        1.0f - p->clip_low, 1.0f + p->clip_high, p->clip_max != 0.0f ? p->clip_max : HUGE_VALF,
+                        p->kl_coef, p->entropy_coef, p->kl, p->idtype == SS_I64,
+                        d_logits && same_phase(x, d_logits, d_ld)};
+  const auto pick = [&](auto grad, auto entropy, auto blocks) {
+    constexpr bool kGrad = decltype(grad)::value, kEntropy = decltype(entropy)::value;
+    constexpr int kBlocks = decltype(blocks)::value;
+    return x->dtype == SS_BF16 ? policy_kernel<SS_BF16, kGrad, kEntropy, kBlocks>
+                               : (x->dtype == SS_FP16 ? policy_kernel<SS_FP16, kGrad, kEntropy, kBlocks>
+                                                      : policy_kernel<SS_FP32, kGrad, kEntropy, kBlocks>);
+  };
+  constexpr std::integral_constant<int, 3> three;
+  constexpr std::integral_constant<int, 4> four;
+  const int64_t nvec = x->vocab / (x->dtype == SS_FP32 ? 4 : 8);
+  const auto vectors = [&](int n) { return (nvec + n * kRowThreads - 1) / (n * kRowThreads); };
+  int cluster = 1;
+  while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
+  // few rows: smaller parts, as long as all of them run at once
+  const int64_t places = 4 * sm_count();
+  const bool few = rows * cluster * 2 <= places;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= places && vectors(cluster) > kFewVectors) cluster *= 2;
+  const bool entropy = p->entropy_coef != 0.0f || out->entropy;
+  const auto with = [&](auto e) {
+    return !d_logits ? pick(std::false_type(), e, four)
+                     : (few ? pick(std::true_type(), e, four) : pick(std::true_type(), e, three));
+  };
+  auto* fn = entropy ? with(std::true_type()) : with(std::false_type());
+  if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;
+  return launch_rows(fn, rows, cluster, kPolicyThreads, 0, a, stream);
+}
+
+}  // namespace
+}  // namespace ss
+
+extern "C" {
+
+ss_status ss_policy_loss(const ss_logits* x, const ss_policy* policy, const ss_policy_out* out, void* d_logits,
+                         int64_t d_ld, void* stream) {
+  if (!x || !policy || !out || x->rows < 0) return SS_ERR_INVALID_ARG;
+  if (x->rows == 0) return SS_OK;
+  if (!out->loss && !out->logprob && !out->entropy && !out->ratio && !out->kl && !out->norm && !out->d_logprob &&
+      !out->d_entropy && !d_logits)
+    return SS_ERR_INVALID_ARG;
+  return ss::policy_impl(x, policy, out, d_logits, d_ld, stream);
+}
+
+}  // extern "C"

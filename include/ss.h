@@ -396,6 +396,60 @@ ss_status ss_distill_topk_grad(const ss_logits* x, const ss_teacher* teacher, co
                                const float* tail_logprob, const float* d_loss, void* d_logits, int64_t d_ld,
                                void* stream);
 
+/* How far a policy is from its reference, of d = log p - log p_ref of a sampled
+ * token: SS_KL_K1 d; SS_KL_K2 d^2 / 2; SS_KL_K3 exp(-d) + d - 1. */
+typedef enum ss_kl { SS_KL_K1 = 0, SS_KL_K2 = 1, SS_KL_K3 = 2 } ss_kl;
+
+/* What ss_policy_loss takes beside the logits; device arrays. */
+typedef struct ss_policy {
+  const void* tokens;       /* [rows] idtype: the sampled token; negative: the row has none; >= vocab: NaN */
+  const float* advantage;   /* [rows] */
+  const float* old_logprob; /* [rows] log p under the policy that sampled, or NULL: this one (ratio 1) */
+  const float* ref_logprob; /* [rows] log p under the reference, or NULL: no KL term */
+  const float* row_weight;  /* [rows] or NULL (all 1) */
+  float clip_low;           /* 0 .. 1 */
+  float clip_high;          /* >= 0 */
+  float clip_max;           /* > 1, or 0: none */
+  float kl_coef;            /* not 0 only with ref_logprob */
+  float entropy_coef;
+  int32_t kl;               /* ss_kl */
+  int32_t idtype;           /* ss_idtype */
+  int32_t pad_;
+} ss_policy;
+
+/* Outputs of ss_policy_loss, [rows] fp32 each; each is optional (NULL), one of
+ * them or d_logits is given. */
+typedef struct ss_policy_out {
+  float* loss;
+  float* logprob;   /* log p of the token */
+  float* entropy;   /* of the row, in nats */
+  float* ratio;     /* exp(log p - old_logprob), not clipped */
+  float* kl;        /* the estimate, without its coefficient; needs ref_logprob */
+  float* norm;      /* [rows][2], 8-byte aligned: see above */
+  float* d_logprob; /* the loss's derivative with respect to logprob, and to entropy: with norm and entropy */
+  float* d_entropy; /* what ss_token_logprobs_grad takes for a backward pass of its own */
+} ss_policy_out;
+
+/* ss_policy_loss: the clipped policy loss of every row's token, with a KL term and
+ * an entropy bonus, and, when d_logits is given, the gradient of sum_r loss_r with
+ * respect to x in the same call. With A the advantage, ratio = exp(log p - old):
+ *   loss_r = row_weight_r (-A clamp(ratio, lo, hi) + kl_coef KL - entropy_coef H),
+ *   [lo, hi] = [0, 1 + clip_high] for A >= 0, [1 - clip_low, clip_max] for A < 0,
+ * which is -min(ratio A, clip(ratio) A), bounded by clip_max |A| where that is
+ * given. A ratio on a border counts as inside. With
+ *   d_logprob = row_weight (-A ratio [lo <= ratio <= hi] + kl_coef dKL/dlog p),
+ *   d_entropy = -row_weight entropy_coef:
+ *   d_x = scale (d_logprob (1[i = t] - p) - d_entropy p (log p + H)).
+ * d_logits, d_ld: as in ss_token_logprobs_grad; may be x itself.
+ * A row of weight 0 or without a token, whatever its logits: every output and the
+ * gradient 0. A masked-out row: log p -inf, the loss as the formula, gradient 0.
+ * A masked token: log p -inf and ratio 0 (SS_KL_K2 and SS_KL_K3 are +inf then, and
+ * with their term the row's gradient is infinite or NaN). A row whose
+ * derivatives are both 0 (all clipped) has gradient 0; a NaN row is NaN, loss and
+ * derivatives, whatever its advantage. */
+ss_status ss_policy_loss(const ss_logits* x, const ss_policy* policy, const ss_policy_out* out, void* d_logits,
+                         int64_t d_ld, void* stream);
+
 /* ------------------------------------------------------------------- misc */
 const char* ss_status_string(ss_status s);      /* static string, never NULL */
 const char* ss_last_cuda_error(void);           /* last CUDA error text of this thread ("" if none) */
