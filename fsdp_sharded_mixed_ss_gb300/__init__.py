@@ -31,8 +31,10 @@ SS_MAX_RANKS = 1024
 SS_I32, SS_I64 = 0, 1
 SS_TAIL_DROP, SS_TAIL_RENORM, SS_TAIL_BUCKET = 0, 1, 2
 SS_KL_K1, SS_KL_K2, SS_KL_K3 = 0, 1, 2
+SS_PREF_SIGMOID, SS_PREF_HINGE, SS_PREF_SQUARE = 0, 1, 2
 SS_MAX_TOP = 128
 SS_MAX_DISTILL_VOCAB = 393216
+SS_MAX_DIM = 16777216
 
 STATUS = {0: "SS_OK", 1: "SS_ERR_INVALID_ARG", 2: "SS_ERR_ALIGN", 3: "SS_ERR_OVERLAP", 4: "SS_ERR_DTYPE",
           5: "SS_ERR_OVERFLOW", 6: "SS_ERR_CUDA"}
@@ -74,7 +76,7 @@ class _Options(ctypes.Structure):
                 ("dev_grad_scale", ctypes.c_void_p), ("dev_skip_flag", ctypes.c_void_p)]
 
 
-# ss_logits, ss_logprob_out, ss_logprob_grad, ss_teacher and the structures of the losses as bytes: packing them costs a quarter of building a
+# ss_logits, ss_logprob_out, ss_logprob_grad, ss_teacher ss_policy, ss_policy_out, ss_preference and ss_table as bytes: packing them costs a quarter of building a
 # ctypes structure, which calls on a few rows feel
 _LOGITS = struct.Struct("@Pqqqif")
 _LOGPROB_OUT = struct.Struct("@6P")
@@ -82,6 +84,8 @@ _LOGPROB_GRAD = struct.Struct("@4P")
 _TEACHER = struct.Struct("@3P4ifi")
 _POLICY = struct.Struct("@5P5f3i")
 _POLICY_OUT = struct.Struct("@8P")
+_PREFERENCE = struct.Struct("@4P3f5i")
+_TABLE = struct.Struct("@Pqqqii")
 
 
 _NO_OPTIONS = _Options(None, None, None, None)
@@ -117,6 +121,11 @@ def _load():
     lib.ss_distill_topk.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
     lib.ss_distill_topk_grad.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
     lib.ss_policy_loss.argtypes = [vp, vp, vp, vp, i64, vp]
+    lib.ss_preference_loss.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.ss_embedding.argtypes = [vp, vp, i32, i64, f32, vp, i32, i64, vp]
+    lib.ss_embedding_grad_workspace.argtypes = [i64, i64, i64]
+    lib.ss_embedding_grad_workspace.restype = i64
+    lib.ss_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, f32, vp, vp, vp, i64, vp]
     lib.ss_grad_sumsq_noalloc.argtypes = [i64, vp, vp, i32, i32, f32, vp, vp, vp, vp]
     return lib
 
@@ -613,3 +622,134 @@ def ss_policy_loss(logits, tokens, advantage, loss=None, *, old_logprob=None, re
                            _f32(ratio, r, "ratio"), _f32(kl, r, "kl"), _f32(norm, 2 * r, "norm"),
                            _f32(d_logprob, r, "d_logprob"), _f32(d_entropy, r, "d_entropy"))
     _call(_lib.ss_policy_loss, "ss_policy_loss", logits, stream, x, p, out, d, dl)
+
+
+def ss_preference_loss(logprob, offsets, loss=None, *, ref_logprob=None, row_weight=None, pair_weight=None,
+                       kind: int = SS_PREF_SIGMOID, beta: float = 0.1, margin: float = 0.0,
+                       label_smoothing: float = 0.0, average: bool = False, halves: bool = False, reward=None,
+                       d_logprob=None, rows: int | None = None, pairs: int | None = None, idtype: int | None = None,
+                       stream=None) -> None:
+    """loss[i] = pair_weight[i] * the preference loss (SS_PREF_*) of pair i, and its gradient with respect to the tokens'
+    log probabilities.
+
+    logprob (rows,): the tokens' log probabilities; offsets (2 pairs + 1,) int32 or int64: sequence j is rows
+    offsets[j]:offsets[j + 1]. Pair i is sequences 2i (chosen) and 2i + 1 (rejected), with `halves` i and pairs + i. A
+    sequence counts by its sum of row_weight (logprob - ref_logprob), with `average` by its mean; h = beta (chosen -
+    rejected) - margin. Outputs, each optional: loss (pairs,), reward (pairs, 2) = beta times the sequences' scores,
+    d_logprob (rows,), of which rows outside the sequences are left as they are. include/ss.h says what empty sequences,
+    weights of 0, bad offsets and NaN give.
+    """
+    if rows is None:
+        if logprob is None or isinstance(logprob, int):
+            raise SSError(1, "logprob: an address needs rows")
+        rows = logprob.numel()
+    if pairs is None:
+        if offsets is None or isinstance(offsets, int):
+            raise SSError(1, "offsets: an address needs pairs")
+        pairs = (offsets.numel() - 1) // 2
+    it = _idtype(offsets, idtype)
+    p = _pack(_PREFERENCE, "preference", _ids(offsets, 2 * pairs + 1, it, "offsets"),
+              _f32(ref_logprob, rows, "ref_logprob"), _f32(row_weight, rows, "row_weight"),
+              _f32(pair_weight, pairs, "pair_weight"), beta, margin, label_smoothing, kind, int(bool(average)),
+              int(bool(halves)), it, 0)
+    _call(_lib.ss_preference_loss, "ss_preference_loss", logprob, stream, _f32(logprob, rows, "logprob"), rows, p,
+          pairs, _f32(loss, pairs, "loss"), _f32(reward, 2 * pairs, "reward"), _f32(d_logprob, rows, "d_logprob"))
+
+
+# ----------------------------------------------------------------------------- embedding
+
+def _table_of(t, shape, ld, dtype, where):
+    """(ss_table, vocab, dim) of a 2-D tensor (unit stride along a row), or of an address with shape = (vocab, dim), ld
+    (default: dim) and dtype."""
+    if t is None or isinstance(t, int):
+        if shape is None:
+            raise SSError(1, f"{where}: an address needs its shape")
+        vocab, dim = shape
+        if dtype is None:
+            dtype = -1
+        return _pack(_TABLE, where, t or 0, vocab, dim, dim if ld is None else ld, dtype, 0), vocab, dim
+    if t.dim() != 2:
+        raise SSError(1, f"{where}: (vocab, dim)")
+    vocab, dim = t.shape
+    ld, one = t.stride()
+    if one != 1 and dim > 1:
+        raise SSError(1, f"{where}: a row must have stride 1")
+    if ld < dim and vocab == 1:  # torch gives a single row any stride
+        ld = dim
+    return _pack(_TABLE, where, t.data_ptr(), vocab, dim, ld, _float_type(t), 0), vocab, dim
+
+
+def _position_rows(t, n, dim, ld, dtype, where):
+    """(address, ld, dtype) of the rows of n positions: a tensor (..., dim) whose positions lie evenly spaced, or an
+    address with ld (default: dim) and dtype."""
+    if t is None or isinstance(t, int):
+        return t or 0, dim if ld is None else ld, -1 if dtype is None else dtype
+    if t.dim() == 0 or t.shape[-1] != dim or t.numel() != n * dim:
+        raise SSError(1, f"{where}: {n} rows of {dim}")
+    if t.dim() != 2:
+        if not t.is_contiguous():
+            raise SSError(1, f"{where}: more than two dimensions have to be dense")
+        return t.data_ptr(), dim, _float_type(t)
+    ld, one = t.stride()
+    if one != 1 and dim > 1:
+        raise SSError(1, f"{where}: a row must have stride 1")
+    return t.data_ptr(), dim if ld < dim and n == 1 else ld, _float_type(t)
+
+
+def _positions(ids, n, where):
+    if n is not None:
+        return n
+    if ids is None or isinstance(ids, int):
+        raise SSError(1, f"{where}: an address needs n")
+    return ids.numel()
+
+
+def ss_embedding(table, ids, out, *, scale: float = 1.0, shape=None, ld: int | None = None, dtype: int | None = None,
+                 out_ld: int | None = None, out_dtype: int | None = None, n: int | None = None,
+                 idtype: int | None = None, stream=None) -> None:
+    """out[r] = scale * table[ids[r]], rounded once to out's type.
+
+    table (vocab, dim), any row stride and alignment (a view of the flat unit); ids: n positions of int32 or int64,
+    negative: a row of zeros, >= vocab: a row of NaN; out (..., dim). bf16, fp16 or fp32 each.
+    """
+    n = _positions(ids, n, "ids")
+    t, _, dim = _table_of(table, shape, ld, dtype, "table")
+    it = _idtype(ids, idtype)
+    o, ol, od = _position_rows(out, n, dim, out_ld, out_dtype, "out")
+    _call(_lib.ss_embedding, "ss_embedding", table, stream, t, _ids(ids, n, it, "ids"), it, n, float(scale), o, od,
+          ol)
+
+
+def ss_embedding_grad_workspace(n: int, vocab: int, dim: int) -> int:
+    """Bytes of device workspace ss_embedding_grad needs for n positions (-1: sizes out of range)."""
+    return int(_lib.ss_embedding_grad_workspace(n, vocab, dim))
+
+
+def ss_embedding_grad(d_out, ids, d_table, workspace, *, base=None, scale: float = 1.0, shape=None,
+                      ld: int | None = None, dtype: int | None = None, base_ld: int | None = None,
+                      base_dtype: int | None = None, d_ld: int | None = None, d_dtype: int | None = None,
+                      n: int | None = None, idtype: int | None = None, workspace_bytes: int | None = None,
+                      stream=None) -> None:
+    """d_table[v] = base[v] + scale * the sum of d_out[r] over the positions r with ids[r] == v, summed in fp32 in the
+    positions' order and rounded once to d_table's type.
+
+    base: None (zeros), another table of any type (the tied head's gradient), or d_table itself: then only the rows of
+    tokens that occur are read and written. Negative ids, and ids past the table, carry nothing. workspace: device
+    scratch of ss_embedding_grad_workspace(n, vocab, dim) bytes.
+    """
+    n = _positions(ids, n, "ids")
+    t, vocab, dim = _table_of(d_table, shape, ld, dtype, "d_table")
+    if base is None:
+        b = None
+    elif base is d_table or (isinstance(base, int) and isinstance(d_table, int) and base == d_table):
+        b = t
+    else:
+        b, _, _ = _table_of(base, (vocab, dim), base_ld, base_dtype, "base")
+    it = _idtype(ids, idtype)
+    d, dl, dd = _position_rows(d_out, n, dim, d_ld, d_dtype, "d_out")
+    if workspace_bytes is None:
+        if isinstance(workspace, int):
+            raise SSError(1, "workspace: an address needs workspace_bytes")
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(_lib.ss_embedding_grad, "ss_embedding_grad", d_table, stream, d, dd, dl, _ids(ids, n, it, "ids"), it, n,
+          float(scale), b, t, _ptr(workspace), workspace_bytes)

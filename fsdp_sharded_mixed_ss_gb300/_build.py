@@ -2,7 +2,7 @@
 
 One translation unit per part of the ABI (host layout code; the fused step,
 in two parts by the arrays' alignment; the reduce; the norm clip; the copies; the operators on rows
-of logits; shared host helpers), compiled in
+of logits, the losses on sampled tokens, the embedding; shared host helpers), compiled in
 parallel by nvcc and linked against the shared CUDA runtime so the library
 shares the runtime instance of the process that loads it (e.g. PyTorch's).
 """
@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libss.so")
 
 SOURCES = ["ss_layout.cpp", "ss_util.cu", "ss_step.cu", "ss_step_shift.cu", "ss_reduce.cu", "ss_norm.cu", "ss_copy.cu",
-           "ss_logprob.cu", "ss_distill.cu", "ss_policy.cu"]
+           "ss_logprob.cu", "ss_distill.cu", "ss_policy.cu", "ss_preference.cu", "ss_embed.cu"]
 
 
 def nvcc() -> str:

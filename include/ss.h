@@ -450,6 +450,86 @@ typedef struct ss_policy_out {
 ss_status ss_policy_loss(const ss_logits* x, const ss_policy* policy, const ss_policy_out* out, void* d_logits,
                          int64_t d_ld, void* stream);
 
+/* The loss of a pair of sequences as a function of h, their scaled distance:
+ *   SS_PREF_SIGMOID -(1 - label_smoothing) log sigmoid(h) - label_smoothing log sigmoid(-h)
+ *   SS_PREF_HINGE   max(0, 1 - h) (derivative 0 at h = 1)
+ *   SS_PREF_SQUARE  ((h - 1/2) / beta)^2 */
+typedef enum ss_pref { SS_PREF_SIGMOID = 0, SS_PREF_HINGE = 1, SS_PREF_SQUARE = 2 } ss_pref;
+
+/* What ss_preference_loss takes beside the log probabilities; device arrays. */
+typedef struct ss_preference {
+  const void* offsets;      /* [2 pairs + 1] idtype: sequence j is rows offsets[j] .. offsets[j + 1] - 1 */
+  const float* ref_logprob; /* [rows] log p under the reference, or NULL: 0 */
+  const float* row_weight;  /* [rows] or NULL (all 1); 0: the token is not counted, whatever its log probability */
+  const float* pair_weight; /* [pairs] or NULL (all 1) */
+  float beta;               /* finite and > 0 */
+  float margin;             /* finite */
+  float label_smoothing;    /* 0 .. 1; not 0 only with SS_PREF_SIGMOID */
+  int32_t kind;             /* ss_pref */
+  int32_t average;          /* sequences count by their mean instead of their sum */
+  int32_t halves;           /* 0: pair i is sequences 2i (chosen) and 2i + 1; else i and pairs + i */
+  int32_t idtype;           /* ss_idtype of the offsets */
+  int32_t pad_;
+} ss_preference;
+
+/* ss_preference_loss: the loss of pairs of sequences from their tokens' log
+ * probabilities (ss_token_logprobs), and its gradient with respect to them, which
+ * ss_token_logprobs_grad takes as d_logprob:
+ *   s = sum_t row_weight_t (logprob_t - ref_t) [/ sum_t row_weight_t if average],
+ *   h = beta (s_chosen - s_rejected) - margin,  loss = pair_weight loss(h).
+ * logprob [rows] fp32. loss [pairs], reward [pairs][2] (beta s_chosen, beta
+ * s_rejected; 8-byte aligned), d_logprob [rows]: each optional, one of them given.
+ * Sums are kept as pairs of fp32 and added in a fixed order.
+ *   - A sequence may be empty; one without weight has the mean 0 and no gradient.
+ *   - d_logprob of rows outside the sequences is left as it is.
+ *   - A pair of weight 0, whatever its log probabilities: loss, reward and
+ *     gradient 0.
+ *   - Offsets outside 0 .. rows, or descending: the pair's loss and reward are NaN
+ *     and its rows are neither read nor written.
+ *   - A counted -inf is the formula's: -inf for its sequence. NaN goes into its
+ *     pair's loss and gradient, and no other's.
+ * rows below 2^61, pairs below 2^28. One launch. */
+ss_status ss_preference_loss(const float* logprob, int64_t rows, const ss_preference* preference, int64_t pairs,
+                             float* loss, float* reward, float* d_logprob, void* stream);
+
+/* -------------------------------------------------------------- embedding
+ * No counterpart on the pages: the other end of a model's vocabulary, whose table
+ * is the first tensor of a language model's unit. The lookup reads its rows out of
+ * the flat 16-bit unit; the gradient goes into the 16-bit gradient that the calls
+ * above reduce, on top of the head's where the two are tied. */
+typedef struct ss_table {
+  void* data;              /* device: row i, column j at data[i * ld + j]; any element alignment */
+  int64_t vocab, dim, ld;  /* 1 <= vocab < 2^31 - 1, 1 <= dim <= SS_MAX_DIM, ld >= dim */
+  int32_t dtype;           /* ss_dtype */
+  int32_t pad_;
+} ss_table;
+#define SS_MAX_DIM 16777216
+
+/* ss_embedding: out[r] = scale table[ids[r]], r = 0 .. n - 1, rounded once to out's
+ * type; row r at out[r * out_ld]. ids [n] (device, idtype): negative: a row of
+ * zeros; >= vocab: a row of NaN. scale finite. n < 2^31. out must not overlap the
+ * table or the ids. One launch. */
+ss_status ss_embedding(const ss_table* table, const void* ids, ss_idtype idtype, int64_t n, float scale, void* out,
+                       int32_t out_dtype, int64_t out_ld, void* stream);
+
+/* ss_embedding_grad: the table's gradient,
+ *   d_table[v] = base[v] + scale sum over r with ids[r] = v of d_out[r],
+ * rounded once to d_table's type. base: the same vocab and dim, any type; NULL: 0;
+ * the same array as d_table (data, ld and type): added in place, and only rows of
+ * tokens that occur are read and written. Otherwise it must not overlap d_table.
+ * d_out: row r at d_out[r * d_ld], of d_dtype. Negative ids and ids >= vocab carry
+ * nothing (their rows are not read).
+ * The sums are fp32, over a token's rows in ascending order, in parts that n alone
+ * decides: results do not depend on the launch.
+ * workspace: device scratch of at least ss_embedding_grad_workspace(n, vocab, dim)
+ *   bytes, 16-byte aligned, owned by the caller, overwritten (no initial contents
+ *   needed). Calls that share it have to be ordered, captured ones included.
+ * n < 2^31; n == 0 is valid (d_table = base) and needs no workspace. */
+int64_t ss_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
+ss_status ss_embedding_grad(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype,
+                            int64_t n, float scale, const ss_table* base, const ss_table* d_table, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------- misc */
 const char* ss_status_string(ss_status s);      /* static string, never NULL */
 const char* ss_last_cuda_error(void);           /* last CUDA error text of this thread ("" if none) */
