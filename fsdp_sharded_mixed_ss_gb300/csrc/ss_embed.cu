@@ -42,6 +42,44 @@ __device__ __forceinline__ void store8(void* row, int e, int dim, const float (&
   }
 }
 
+// Eight elements as they lie in memory.
+template <int DT>
+struct Raw8 {
+  uint4 w[DT == SS_FP32 ? 2 : 1];
+
+  template <bool VEC>
+  __device__ __forceinline__ void load(const void* row, int e, int dim) {
+    const Elem<DT>* p = static_cast<const Elem<DT>*>(row) + e;
+    if (VEC && e + 8 <= dim) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(w) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+      uint32_t* q = &w[0].x;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const Elem<DT> v = e + j < dim ? p[j] : Elem<DT>(0);
+        if constexpr (DT == SS_FP32) q[j] = __float_as_uint(v);
+        else q[j / 2] = j % 2 ? q[j / 2] | static_cast<uint32_t>(v) << 16 : v;
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    if constexpr (DT == SS_FP32) {
+      const uint32_t* q = &w[0].x;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(q[j]);
+    } else {
+      widen8<DT>(w[0], f);
+    }
+  }
+  __device__ __forceinline__ void add_to(float (&sum)[8]) const {
+    float f[8];
+    unpack(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += f[j];
+  }
+};
+
 // The same of a type known at run time (a branch that all threads take alike).
 template <bool VEC>
 __device__ __forceinline__ void load8(int dt, const void* row, int e, int dim, float (&f)[8]) {
@@ -87,29 +125,43 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32), tasks = a.n * a.pieces;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); task < tasks;
-       task += warps) {
-    const int64_t pos = task / a.pieces;
-    const int from = static_cast<int>(task - pos * a.pieces) * kRowPiece;
-    const int64_t id = load_id(a.ids, pos, a.wide);
-    char* out = a.out.row(pos);
+  int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  // the next task's row is on its way while this one's is written, and the id of the one after
+  auto id_at = [&](int64_t t) { return t < tasks ? load_id(a.ids, t / a.pieces, a.wide) : -1; };
+  auto fetch = [&](int64_t t, int64_t id, Raw8<DT> (&raw)[4]) {
+    if (id < 0 || id >= a.vocab) return;
+    const char* row = a.table.row(id);
+    const int from = static_cast<int>(t % a.pieces) * kRowPiece;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = from + (u * 32 + lane) * 8;
+      if (e < a.dim) raw[u].template load<VEC>(row, e, a.dim);
+    }
+  };
+  int64_t id = id_at(task), next_id = id_at(task + warps);
+  Raw8<DT> raw[4];
+  fetch(task, id, raw);
+  for (; task < tasks; task += warps) {
+    Raw8<DT> next[4];
+    fetch(task + warps, next_id, next);
+    const int64_t after = id_at(task + 2 * warps);
+    char* out = a.out.row(task / a.pieces);
+    const int from = static_cast<int>(task % a.pieces) * kRowPiece;
     const bool there = id >= 0 && id < a.vocab;
-    const char* row = a.table.row(there ? id : 0);
     const float none = id < 0 ? 0.0f : nan_f();
-    float f[4][8];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = from + (u * 32 + lane) * 8;
-      if (there && e < a.dim) load8<DT, VEC>(row, e, a.dim, f[u]);
+      float f[8];
+      raw[u].unpack(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = there ? f[j] * a.scale : none;
+      if (e < a.dim) store8<OT, VEC>(out, e, a.dim, f);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = from + (u * 32 + lane) * 8;
-      if (e >= a.dim) continue;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[u][j] = there ? f[u][j] * a.scale : none;
-      store8<OT, VEC>(out, e, a.dim, f[u]);
-    }
+    for (int u = 0; u < 4; ++u) raw[u] = next[u];
+    id = next_id;
+    next_id = after;
   }
 }
 
@@ -129,19 +181,36 @@ constexpr int kSortBlocks = 8;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 
+// What the sums are made of: up to kChunk sorted positions of one token, those of one aligned run of kChunk.
+constexpr int kChunk = 32;  // a warp's lanes: a warp that goes through the sorted positions sees a whole run at a time
+struct Task {
+  int32_t at;        // first sorted position
+  uint32_t token;
+  int32_t count;     // positions; negative where the token has positions in other runs as well
+  int32_t first;     // its first position's row; its token's number among those that occur where count is negative
+};
+
 struct SortArgs {
   const void* ids;
   uint64_t* pairs[2];  // token << 32 | position; the sorted ones are in pairs[passes & 1 ? 0 : 1]
-  int64_t vocab;
+  Task* tasks;
+  int32_t* first_task;  // of every token that occurs; then their number
+  int32_t* n_tasks;
+  uint32_t* arrived;    // n_arrived counters, to be cleared
+  int64_t n_arrived, vocab;
   int32_t n, passes, bits;  // bits of a digit
   bool wide;
 };
+
+__device__ __forceinline__ uint32_t token_of(uint64_t pair) { return static_cast<uint32_t>(pair >> 32); }
 
 struct SortShared {
   uint32_t count[kSortWarps][kDigits];  // of a warp's digits; then the next place of each
   uint32_t total[kDigits];              // of the block's digits
   uint32_t base[kDigits];
   uint32_t warp_sum[kSortWarps];
+  uint2 warp_tasks[kSortWarps];  // tasks and tokens that begin in a warp's run
+  uint2 block_tasks;
 };
 
 __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared& s) {
@@ -152,6 +221,8 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
   const int64_t first = (static_cast<int64_t>(cl.rank) * kSortWarps + warp) * each;
   const int64_t last = min(first + each, static_cast<int64_t>(n));
   const uint32_t none = static_cast<uint32_t>(a.vocab);
+  for (int64_t i = static_cast<int64_t>(cl.rank) * kSortThreads + tid; i < a.n_arrived; i += kSortBlocks * kSortThreads)
+    a.arrived[i] = 0u;
   for (int pass = 0; pass < a.passes; ++pass) {
     const uint64_t* from = a.pairs[(pass & 1) ^ 1];
     uint64_t* to = a.pairs[pass & 1];
@@ -219,6 +290,66 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
     __threadfence();
     cl.sync();
   }
+  // the tasks, in the order of their positions: counted, then written
+  const auto* sorted = reinterpret_cast<const unsigned long long*>(a.pairs[a.passes & 1 ? 0 : 1]);
+  auto over_runs = [&](const auto& f) {
+    uint32_t before = first > 0 && first < last ? token_of(__ldcg(sorted + first - 1)) : ~0u;
+    for (int64_t i = first; i < last; i += kChunk) {
+      const uint64_t pair = i + lane < last ? __ldcg(sorted + i + lane) : ~0ull;
+      const uint32_t token = token_of(pair);
+      uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, token, 1);
+      if (lane == 0) prev = before;
+      before = __shfl_sync(0xFFFFFFFFu, token, 31);
+      const bool live = token < none, begins = live && token != prev;
+      f(i, pair, live, begins, __ballot_sync(0xFFFFFFFFu, begins), __ballot_sync(0xFFFFFFFFu, begins || (live && lane == 0)));
+    }
+  };
+  uint2 here = make_uint2(0, 0);
+  over_runs([&](int64_t, uint64_t, bool, bool, unsigned tokens, unsigned tasks) {
+    here.x += __popc(tasks);
+    here.y += __popc(tokens);
+  });
+  if (lane == 0) s.warp_tasks[warp] = here;
+  __syncthreads();
+  if (warp == 0) {  // sums before each warp, and the block's
+    const uint2 own = s.warp_tasks[lane];
+    uint2 upto = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto.x, off), y = __shfl_up_sync(0xFFFFFFFFu, upto.y, off);
+      if (lane >= off) upto = make_uint2(upto.x + x, upto.y + y);
+    }
+    s.warp_tasks[lane] = make_uint2(upto.x - own.x, upto.y - own.y);
+    if (lane == 31) s.block_tasks = upto;
+  }
+  cl.sync();
+  uint2 at = s.warp_tasks[warp], all = make_uint2(0, 0);
+  for (unsigned r = 0; r < cl.size; ++r) {
+    const uint2 b = *cl.at(&s.block_tasks, r);
+    if (r < cl.rank) at = make_uint2(at.x + b.x, at.y + b.y);
+    all = make_uint2(all.x + b.x, all.y + b.y);
+  }
+  over_runs([&](int64_t i, uint64_t pair, bool live, bool begins, unsigned tokens, unsigned tasks) {
+    const uint32_t token = token_of(pair);
+    const unsigned below = (1u << lane) - 1u, behind = lane == 31 ? 0u : tasks >> (lane + 1) << (lane + 1);
+    const int in_run = __popc(__ballot_sync(0xFFFFFFFFu, live));
+    if ((tasks >> lane) & 1u) {
+      const int end = behind ? __ffs(behind) - 1 : in_run;
+      const bool goes_on = end == kChunk && i + kChunk < n && token_of(__ldcg(sorted + i + kChunk)) == token;
+      const uint32_t task = at.x + __popc(tasks & below), number = at.y + __popc(tokens & (below | 1u << lane)) - 1u;
+      const bool parts = goes_on || !begins;
+      a.tasks[task] = {static_cast<int32_t>(i) + lane, token, parts ? lane - end : end - lane,
+                       parts ? static_cast<int32_t>(number) : static_cast<int32_t>(static_cast<uint32_t>(pair))};
+      if (begins) a.first_task[number] = static_cast<int32_t>(task);
+    }
+    at.x += __popc(tasks);
+    at.y += __popc(tokens);
+  });
+  if (cl.rank == 0 && tid == 0) {
+    *a.n_tasks = static_cast<int32_t>(all.x);
+    a.first_task[all.y] = static_cast<int32_t>(all.x);
+  }
+  cl.sync();  // the other blocks have read this one's totals
 }
 
 struct FillArgs {
@@ -264,6 +395,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_fill_kernel(const __grid
   pdl_trigger();
   cl.started();
   if (blockIdx.x < kSortBlocks) {
+    if (a.sort.n == 0) return;  // there is no workspace then
     sort_positions(a.sort, cl, *reinterpret_cast<SortShared*>(shared));
   } else {
     const int64_t warp = static_cast<int64_t>(blockIdx.x - kSortBlocks) * kSortWarps + (threadIdx.x >> 5);
@@ -273,119 +405,202 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_fill_kernel(const __grid
 
 // ------------------------------------------------------------------ the sums
 //
-// A block takes kChunk consecutive sorted positions and 1024 columns: a thread adds
-// its eight columns of one position after another and writes them out where the
-// token changes. A token whose positions reach into other chunks leaves its sum of
-// each chunk in the workspace; the join adds them in the chunks' order.
+// A warp takes a task's positions and up to 512 columns. A token with one task is
+// finished by it. A token with more leaves each task's sum in the workspace, and
+// whichever warp is the last to do so of kGroup neighbouring runs adds these up, and the
+// last of those the groups' sums: the order of the sums is that of the positions
+// whichever warp adds them.
 
-constexpr int kChunk = 32;
-constexpr int kSumThreads = 128;
-constexpr int kSumColumns = kSumThreads * 8;
-constexpr int kInFlight = 8;  // rows that a thread has in flight
+constexpr int kGroup = 16;
+constexpr int kSumThreads = 256;
+constexpr int kVecs = 2;                   // groups of eight columns that a lane has
+constexpr int kSumPiece = kVecs * 32 * 8;  // columns that a warp takes at a time
 
 struct SumArgs {
   const uint64_t* pairs;
+  const Task* tasks;
+  const int32_t* first_task;
+  const int32_t* n_tasks;
+  uint32_t* arrived;  // [2][2 runs][pieces]: of a token's tasks in a group of runs, of its groups
+  float* partial;     // [2 runs][pitch]: of the token that a run begins with, of the one that it ends with
   Rows d_out, base, table;
-  float* partial;  // [chunks][2][pitch]: of the token that began before the chunk, of the one that goes on behind it
-  int64_t pitch, vocab;
-  int32_t n, dim;
+  int64_t pitch;
+  int32_t runs, dim, pieces;
   float scale;
 };
 
-__device__ __forceinline__ uint32_t token_of(uint64_t pair) { return static_cast<uint32_t>(pair >> 32); }
+struct Columns {
+  int from, dim, lane;
+  __device__ __forceinline__ int at(int u) const { return from + (u * 32 + lane) * 8; }
+};
 
 // A token's row from its sum.
 template <bool VEC>
-__device__ __forceinline__ void finish_row(const SumArgs& a, uint32_t token, int e, const float (&sum)[8]) {
-  float f[8] = {};
-  if (a.base.data) load8<VEC>(a.base.dtype, a.base.row(token), e, a.dim, f);
+__device__ __forceinline__ void finish_row(const SumArgs& a, uint32_t token, const Columns& c, const float (&sum)[kVecs][8]) {
+  char* out = a.table.row(token);
+  float f[kVecs][8] = {};
+  if (a.base.data) {
+    const char* base = a.base.row(token);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = fmaf(sum[j], a.scale, f[j]);
-  store8<VEC>(a.table.dtype, a.table.row(token), e, a.dim, f);
+    for (int u = 0; u < kVecs; ++u)
+      if (c.at(u) < c.dim) load8<VEC>(a.base.dtype, base, c.at(u), c.dim, f[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[u][j] = fmaf(sum[u][j], a.scale, f[u][j]);
+    if (c.at(u) < c.dim) store8<VEC>(a.table.dtype, out, c.at(u), c.dim, f[u]);
+  }
 }
 
-template <int DT, bool VEC, bool TVEC>
-__global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ SumArgs a) {
-  __shared__ uint64_t pairs[kChunk + 2];
-  pdl_wait();
-  pdl_trigger();
-  const int64_t chunk = blockIdx.x, first = chunk * kChunk;
-  const int cnt = static_cast<int>(min(static_cast<int64_t>(kChunk), a.n - first));
-  const uint32_t none = static_cast<uint32_t>(a.vocab);
-  for (int i = threadIdx.x; i < cnt + 2; i += kSumThreads) {
-    const int64_t at = first + i - 1;
-    pairs[i] = at < 0 || at >= a.n ? ~0ull : a.pairs[at];
-  }
-  __syncthreads();
-  const int e = (blockIdx.y * kSumThreads + threadIdx.x) * 8;
-  if (e >= a.dim) return;
-  float sum[8] = {};
-  bool began = token_of(pairs[0]) != token_of(pairs[1]);  // in this chunk
-  for (int i0 = 0; i0 < cnt; i0 += kInFlight) {
-    float f[kInFlight][8];
+// The sums of a token's tasks: one in each of the runs from `first` to `last`.
+struct TokenParts {
+  int first, last;  // runs
+  bool inside;      // it begins inside its first run
+
+  __device__ __forceinline__ int64_t slot(int run) const { return 2 * static_cast<int64_t>(run) + (run == first && inside); }
+};
+
+__device__ __forceinline__ void add_partial(const SumArgs& a, int64_t slot, const Columns& c, float (&sum)[kVecs][8]) {
+  const float* p = a.partial + slot * a.pitch;
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u)
-      if (i0 + u < cnt && token_of(pairs[i0 + u + 1]) < none)
-        load8<DT, VEC>(a.d_out.row(static_cast<uint32_t>(pairs[i0 + u + 1])), e, a.dim, f[u]);
+  for (int u = 0; u < kVecs; ++u) {
+    const int e = c.at(u);
+    if (e < c.dim) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + e)), y = __ldcg(reinterpret_cast<const float4*>(p + e + 4));
+      const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      const int i = i0 + u;
-      if (i >= cnt) break;
-      const uint32_t token = token_of(pairs[i + 1]);
-      if (token >= none) return;  // and all behind it
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += f[u][j];
-      const bool ends = token_of(pairs[i + 2]) != token;
-      if (ends && began) {
-        finish_row<TVEC>(a, token, e, sum);
-      } else if (ends || i + 1 == cnt) {
-        float* p = a.partial + (2 * chunk + (began ? 1 : 0)) * a.pitch;
-        store8<SS_FP32, true>(p, e, static_cast<int>(a.pitch), sum);
-      }
-      if (ends) {
-        began = true;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-      }
+      for (int j = 0; j < 8; ++j) sum[u][j] += f[j];
     }
   }
 }
 
-// The tokens that begin in a chunk and go on behind it.
-template <bool TVEC>
-__global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant__ SumArgs a) {
+__device__ __forceinline__ void put_partial(const SumArgs& a, int64_t slot, const Columns& c, const float (&sum)[kVecs][8]) {
+  float* p = a.partial + slot * a.pitch;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u)
+    if (c.at(u) < c.dim) store8<SS_FP32, true>(p, c.at(u), static_cast<int>(a.pitch), sum[u]);
+}
+
+// Whether this warp is the last of `of` that arrive at a counter; what the others wrote before they did is then seen.
+__device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int of, int lane) {
+  __threadfence();
+  __syncwarp();
+  uint32_t before = 0;
+  if (lane == 0) before = atomicAdd(counter, 1u);
+  const bool last = __shfl_sync(0xFFFFFFFFu, before, 0) == static_cast<uint32_t>(of - 1);
+  __threadfence();
+  return last;
+}
+
+// A part's sum on its way to its token's row.
+template <bool VEC>
+__device__ __forceinline__ void join_parts(const SumArgs& a, const Task& task, int piece, const Columns& c,
+                                           float (&sum)[kVecs][8]) {
+  const int begin = a.first_task[task.first], parts = a.first_task[task.first + 1] - begin;
+  const int start = a.tasks[begin].at;
+  TokenParts t;
+  t.first = start / kChunk;
+  t.last = t.first + parts - 1;
+  t.inside = start % kChunk != 0;
+  const int run = task.at / kChunk;
+  put_partial(a, t.slot(run), c, sum);
+  // this group's parts
+  const int lo = max(t.first, run / kGroup * kGroup), hi = min(t.last, run / kGroup * kGroup + kGroup - 1);
+  uint32_t* arrived = a.arrived + t.slot(lo) * a.pieces + piece;
+  if (!last_to_arrive(arrived, hi - lo + 1, c.lane)) return;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
+#pragma unroll 2
+  for (int r = lo; r <= hi; ++r) add_partial(a, t.slot(r), c, sum);
+  const int groups = t.last / kGroup - t.first / kGroup + 1;
+  if (groups > 1) {
+    put_partial(a, t.slot(lo), c, sum);
+    arrived = a.arrived + (2 * static_cast<int64_t>(a.runs) + t.slot(t.first)) * a.pieces + piece;
+    if (!last_to_arrive(arrived, groups, c.lane)) return;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
+#pragma unroll 2
+    for (int g = t.first / kGroup; g <= t.last / kGroup; ++g) add_partial(a, t.slot(max(t.first, g * kGroup)), c, sum);
+  }
+  finish_row<VEC>(a, task.token, c, sum);
+}
+
+template <int DT>
+constexpr int kInFlight = DT == SS_FP32 ? 1 : 2;  // rows that a warp has in flight
+
+template <int DT, bool VEC, bool TVEC>
+__global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(const __grid_constant__ SumArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int64_t chunk = blockIdx.x, end = (chunk + 1) * kChunk;
-  if (end >= a.n) return;
-  const uint32_t token = token_of(a.pairs[end - 1]);
-  if (token >= static_cast<uint32_t>(a.vocab) || token_of(a.pairs[end]) != token) return;
-  if (chunk > 0 && token_of(a.pairs[end - kChunk - 1]) == token) return;  // it began before
-  const int e = (blockIdx.y * kSumThreads + threadIdx.x) * 8;
-  if (e >= a.dim) return;
-  float sum[8];
-  load8<SS_FP32, true>(a.partial + (2 * chunk + 1) * a.pitch, e, static_cast<int>(a.pitch), sum);
-  for (int64_t c = chunk + 1;; ++c) {
-    float f[8];
-    load8<SS_FP32, true>(a.partial + 2 * c * a.pitch, e, static_cast<int>(a.pitch), f);
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kSumThreads / 32);
+  const int64_t items = static_cast<int64_t>(*a.n_tasks) * a.pieces;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5); item < items;
+       item += warps) {
+    const int64_t j = item / a.pieces;
+    const int piece = static_cast<int>(item - j * a.pieces);
+    const int4 words = *reinterpret_cast<const int4*>(a.tasks + j);
+    const Task task = {words.x, static_cast<uint32_t>(words.y), words.z, words.w};
+    const int count = abs(task.count);
+    const Columns c = {piece * kSumPiece, a.dim, lane};
+    // lane i has the row of the task's i-th position
+    const int32_t row = task.count == 1 ? task.first
+                                        : static_cast<int32_t>(static_cast<uint32_t>(a.pairs[task.at + min(lane, count - 1)]));
+    float sum[kVecs][8] = {};
+    for (int i = 0; i < count; i += kInFlight<DT>) {
+      Raw8<DT> f[kInFlight<DT>][kVecs];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += f[j];
-    const int64_t next = (c + 1) * kChunk;
-    if (next >= a.n || token_of(a.pairs[next]) != token) break;
+      for (int r = 0; r < kInFlight<DT>; ++r) {
+        const char* p = a.d_out.row(__shfl_sync(0xFFFFFFFFu, row, min(i + r, count - 1)));
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+          if (i + r < count && c.at(u) < c.dim) f[r][u].template load<VEC>(p, c.at(u), c.dim);
+      }
+#pragma unroll
+      for (int r = 0; r < kInFlight<DT>; ++r)
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+          if (i + r < count && c.at(u) < c.dim) f[r][u].add_to(sum[u]);
+    }
+    if (task.count > 0) finish_row<TVEC>(a, task.token, c, sum);
+    else join_parts<TVEC>(a, task, piece, c, sum);
   }
-  finish_row<TVEC>(a, token, e, sum);
 }
 
 // ------------------------------------------------------------------ host
 
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
 int64_t pitch_of(int64_t dim) { return (dim + 7) / 8 * 8; }
+int pieces_of(int64_t dim, int piece) { return static_cast<int>((dim + piece - 1) / piece); }
 
-// Bytes of the workspace, or -1 where they do not fit in int64.
-int64_t workspace_bytes_of(int64_t n, int64_t dim) {
-  const __int128 v = static_cast<__int128>(n) * 16 + static_cast<__int128>(chunks_of(n)) * 2 * pitch_of(dim) * 4 + 16;
-  return v > INT64_MAX ? -1 : static_cast<int64_t>(v);
-}
+// The workspace's parts, each on a 16-byte boundary: where they begin, and its bytes (-1: more than int64 holds).
+struct Workspace {
+  int64_t runs, n_arrived;
+  int64_t pairs[2], tasks, first_task, n_tasks, arrived, partial, bytes;
+
+  Workspace(int64_t n, int64_t dim) {
+    runs = (n + kChunk - 1) / kChunk;
+    n_arrived = 4 * runs * pieces_of(dim, kSumPiece);
+    __int128 at = 0;
+    const auto take = [&](__int128 size) {
+      const __int128 from = at;
+      at += (size + 15) / 16 * 16;
+      return static_cast<int64_t>(from);
+    };
+    pairs[0] = take(static_cast<__int128>(n) * 8);
+    pairs[1] = take(static_cast<__int128>(n) * 8);
+    tasks = take(static_cast<__int128>(n) * static_cast<int64_t>(sizeof(Task)));
+    first_task = take((static_cast<__int128>(n) + 1) * 4);
+    n_tasks = take(4);
+    arrived = take(static_cast<__int128>(n_arrived) * 4);
+    partial = take(static_cast<__int128>(runs) * 2 * pitch_of(dim) * 4);
+    bytes = at > INT64_MAX ? -1 : static_cast<int64_t>(at);
+  }
+};
 
 ss_status check_table(const ss_table* t, int64_t* bytes) {
   if (!t->data || t->vocab < 1 || t->dim < 1 || t->ld < t->dim) return SS_ERR_INVALID_ARG;
@@ -409,8 +624,6 @@ ss_status check_rows(const void* p, int64_t n, int64_t dim, int64_t ld, int32_t 
 bool aligned_rows(const Rows& r) {
   return !misaligned(r.data, 16) && r.ld * dtype_bytes(r.dtype) % 16 == 0;
 }
-
-int pieces_of(int64_t dim) { return static_cast<int>((dim + kRowPiece - 1) / kRowPiece); }
 
 template <int DT, bool VEC>
 auto pick_lookup(int32_t out) {
@@ -441,11 +654,10 @@ ss_status lookup_impl(const ss_table* t, const void* ids, ss_idtype idtype, int6
   ranges.add(out, o_bytes, true);
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const LookupArgs a = {ids, {t->data, t->ld, t->dtype}, {out, out_ld, out_dtype}, n, t->vocab,
-                        static_cast<int32_t>(t->dim), pieces_of(t->dim), scale, idtype == SS_I64};
+                        static_cast<int32_t>(t->dim), pieces_of(t->dim, kRowPiece), scale, idtype == SS_I64};
   auto* fn = aligned_rows(a.table) && aligned_rows(a.out) ? pick_lookup<true>(t->dtype, out_dtype)
                                                           : pick_lookup<false>(t->dtype, out_dtype);
-  const int64_t blocks = (n * a.pieces + kThreads / 32 - 1) / (kThreads / 32);
-  return launch(fn, static_cast<unsigned>(std::min<int64_t>(blocks, INT32_MAX)), a, stream);
+  return launch(fn, grid_for(reinterpret_cast<const void*>(fn), n * a.pieces * 32), a, stream);
 }
 
 template <int DT>
@@ -475,15 +687,15 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   if (!std::isfinite(scale)) return SS_ERR_INVALID_ARG;
   if (idtype != SS_I32 && idtype != SS_I64) return SS_ERR_DTYPE;
   const int64_t ib = idtype == SS_I64 ? 8 : 4;
+  const Workspace ws(std::min<int64_t>(n, INT32_MAX), t->dim);
   if (n > 0) {
     if (!ids || !workspace) return SS_ERR_INVALID_ARG;
     st = check_rows(d_out, n, t->dim, d_ld, d_dtype, &d_bytes);
     if (st != SS_OK) return st;
     if (misaligned(ids, ib) || misaligned(workspace, 16)) return SS_ERR_ALIGN;
     if (n > INT32_MAX) return SS_ERR_OVERFLOW;
-    const int64_t need = workspace_bytes_of(n, t->dim);
-    if (need < 0) return SS_ERR_OVERFLOW;
-    if (workspace_bytes < need) return SS_ERR_INVALID_ARG;
+    if (ws.bytes < 0) return SS_ERR_OVERFLOW;
+    if (workspace_bytes < ws.bytes) return SS_ERR_INVALID_ARG;
   }
   const bool in_place = base && base->data == t->data && base->ld == t->ld && base->dtype == t->dtype;
   Ranges ranges;
@@ -492,7 +704,7 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   if (n > 0) {
     ranges.add(d_out, d_bytes, false);
     ranges.add(ids, n * ib, false);
-    ranges.add(workspace, workspace_bytes_of(n, t->dim), true);
+    ranges.add(workspace, ws.bytes, true);
   }
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   if (n == 0 && in_place) return SS_OK;
@@ -501,31 +713,33 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   const Rows from = base ? Rows{base->data, base->ld, base->dtype} : Rows{nullptr, 0, SS_FP32};
   const bool tvec = aligned_rows(table) && (!base || aligned_rows(from));
   SortFillArgs sf = {};
-  uint64_t* pairs = static_cast<uint64_t*>(workspace);
+  char* w = static_cast<char*>(workspace);
   if (n > 0) {
     int bits = 1;  // of the keys 0 .. vocab
     while ((t->vocab >> bits) != 0) ++bits;
     const int passes = (bits + kDigitBits - 1) / kDigitBits;
-    sf.sort = {ids, {pairs, pairs + n}, t->vocab, static_cast<int32_t>(n), passes, (bits + passes - 1) / passes,
-               idtype == SS_I64};
+    sf.sort = {ids, {reinterpret_cast<uint64_t*>(w + ws.pairs[0]), reinterpret_cast<uint64_t*>(w + ws.pairs[1])},
+               reinterpret_cast<Task*>(w + ws.tasks), reinterpret_cast<int32_t*>(w + ws.first_task),
+               reinterpret_cast<int32_t*>(w + ws.n_tasks), reinterpret_cast<uint32_t*>(w + ws.arrived), ws.n_arrived,
+               t->vocab, static_cast<int32_t>(n), passes, (bits + passes - 1) / passes, idtype == SS_I64};
   }
-  sf.fill = {from, table, in_place ? 0 : t->vocab, dim, pieces_of(dim)};
+  sf.fill = {from, table, in_place ? 0 : t->vocab, dim, pieces_of(dim, kRowPiece)};
   auto* sort_fill = tvec ? sort_fill_kernel<true> : sort_fill_kernel<false>;
   st = allow_shared(sort_fill, sizeof(SortShared));
   if (st != SS_OK) return st;
   const int fill_clusters = in_place ? 0 : std::max(1, 2 * sm_count() / kSortBlocks);
   st = launch_rows(sort_fill, 1 + fill_clusters, kSortBlocks, kSortThreads, sizeof(SortShared), sf, stream);
   if (st != SS_OK || n == 0) return st;
-  const SumArgs a = {sf.sort.pairs[sf.sort.passes & 1 ? 0 : 1], {const_cast<void*>(d_out), d_ld, d_dtype}, from, table,
-                     reinterpret_cast<float*>(pairs + 2 * n), pitch_of(dim), t->vocab, static_cast<int32_t>(n), dim,
-                     scale};
+  // tasks: one for each token, and one more at most for each run that a token's positions pass into
+  const int64_t most = std::min(n, t->vocab + ws.runs);
+  const SumArgs a = {sf.sort.pairs[sf.sort.passes & 1 ? 0 : 1], sf.sort.tasks, sf.sort.first_task, sf.sort.n_tasks,
+                     sf.sort.arrived, reinterpret_cast<float*>(w + ws.partial), {const_cast<void*>(d_out), d_ld, d_dtype},
+                     from, table, pitch_of(dim), static_cast<int32_t>(ws.runs), dim, pieces_of(dim, kSumPiece), scale};
   const bool vec = aligned_rows(a.d_out);
   auto* fn = d_dtype == SS_BF16 ? pick_sum<SS_BF16>(vec, tvec)
                                 : (d_dtype == SS_FP16 ? pick_sum<SS_FP16>(vec, tvec) : pick_sum<SS_FP32>(vec, tvec));
-  const dim3 grid(static_cast<unsigned>(chunks_of(n)), static_cast<unsigned>((dim + kSumColumns - 1) / kSumColumns));
-  st = launch_dependent(fn, grid, dim3(kSumThreads), 0, stream, a);
-  if (st != SS_OK) return st;
-  return launch_dependent(tvec ? join_kernel<true> : join_kernel<false>, grid, dim3(kSumThreads), 0, stream, a);
+  const unsigned grid = grid_for(reinterpret_cast<const void*>(fn), most * a.pieces * 32, kSumThreads);
+  return launch(fn, grid, a, stream, kSumThreads);
 }
 
 }  // namespace
@@ -542,7 +756,7 @@ ss_status ss_embedding(const ss_table* table, const void* ids, ss_idtype idtype,
 
 int64_t ss_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
   if (n < 0 || n > INT32_MAX || vocab < 1 || vocab >= INT32_MAX || dim < 1 || dim > SS_MAX_DIM) return -1;
-  return ss::workspace_bytes_of(n, dim);
+  return ss::Workspace(n, dim).bytes;
 }
 
 ss_status ss_embedding_grad(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype,

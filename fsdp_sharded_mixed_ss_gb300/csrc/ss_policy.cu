@@ -270,13 +270,17 @@ __global__ void __launch_bounds__(kPolicyThreads, BLOCKS) policy_kernel(const __
   std::conditional_t<ENTROPY, RunningSum, RunningMass> run(one_element(edge), a.c);
 #pragma unroll 1
   for (int j = 0; j < vectors; j += kBatch) {
-    uint4 next[kBatch];
     src += kBatch * sb;
-    fetch(src, j + kBatch, next);
-    if constexpr (ENTROPY) add_vectors<DT>(v, a.c, run);
-    else add_mass<DT>(v, a.c, run);
+    if constexpr (ENTROPY) {
+      add_vectors<DT>(v, a.c, run);
+      fetch(src, j + kBatch, v);
+    } else {
+      uint4 next[kBatch];
+      fetch(src, j + kBatch, next);
+      add_mass<DT>(v, a.c, run);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) v[u] = next[u];
+      for (int u = 0; u < kBatch; ++u) v[u] = next[u];
+    }
   }
   const RowSum mine = merge_lanes(run.done(a.c), a.c);
   if ((tid & 31) == 0) sh.red[tid >> 5] = mine;
@@ -348,7 +352,7 @@ ss_status policy_impl(const ss_logits* x, const ss_policy* p, const ss_policy_ou
   const int64_t nvec = x->vocab / (x->dtype == SS_FP32 ? 4 : 8);
   const auto vectors = [&](int n) { return (nvec + n * kRowThreads - 1) / (n * kRowThreads); };
   int cluster = 1;
-  while (cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
+  while (d_logits && cluster < kMaxCluster && vectors(cluster) > kPartVectors) cluster *= 2;
   // few rows: smaller parts, as long as all of them run at once
   const int64_t places = 4 * sm_count();
   const bool few = rows * cluster * 2 <= places;

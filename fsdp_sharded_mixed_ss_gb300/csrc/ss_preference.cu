@@ -49,13 +49,14 @@ struct Span {
   int64_t lo, hi;
 };
 
-// f(i, weight) over block `rank`'s of `size` parts of a sequence, four of a thread's tokens in flight.
+constexpr int kTokens = 4;  // of a thread in flight
+
+// f(i, step) over block `rank`'s of `size` parts of a sequence: the thread's tokens i, i + step, ... below q.hi, kTokens
+// of them a call.
 template <class F>
 __device__ __forceinline__ void over_tokens(const Span& q, unsigned rank, unsigned size, const F& f) {
   const int64_t step = static_cast<int64_t>(size) * blockDim.x;
-  int64_t i = q.lo + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x;
-  for (; i + 3 * step < q.hi; i += 4 * step) f(i, step, std::integral_constant<int, 4>());
-  for (; i < q.hi; i += step) f(i, step, std::integral_constant<int, 1>());
+  for (int64_t i = q.lo + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; i < q.hi; i += kTokens * step) f(i, step);
 }
 
 // A block of `blockDim.x` threads a pair, or the blocks of a cluster: the two sums, the pair's loss, and its derivative
@@ -88,9 +89,10 @@ __global__ void __launch_bounds__(kMaxThreads) preference_kernel(const __grid_co
     if (!bad && a.d) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step, auto n) {
+        over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step) {
 #pragma unroll
-          for (int u = 0; u < decltype(n)::value; ++u) a.d[i + u * step] = 0.0f;
+          for (int u = 0; u < kTokens; ++u)
+            if (i + u * step < at[k].hi) a.d[i + u * step] = 0.0f;
         });
     }
     return;
@@ -98,17 +100,17 @@ __global__ void __launch_bounds__(kMaxThreads) preference_kernel(const __grid_co
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     SeqSum sum = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-    over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step, auto n) {
-      constexpr int N = decltype(n)::value;
-      float lp[N], ref[N], w[N];
+    over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step) {
+      float lp[kTokens], ref[kTokens], w[kTokens];
 #pragma unroll
-      for (int u = 0; u < N; ++u) {
-        lp[u] = a.logprob[i + u * step];
-        ref[u] = a.ref ? a.ref[i + u * step] : 0.0f;
-        w[u] = a.weight ? a.weight[i + u * step] : 1.0f;
+      for (int u = 0; u < kTokens; ++u) {
+        const bool there = i + u * step < at[k].hi;
+        lp[u] = there ? a.logprob[i + u * step] : 0.0f;
+        ref[u] = there && a.ref ? a.ref[i + u * step] : 0.0f;
+        w[u] = !there ? 0.0f : (a.weight ? a.weight[i + u * step] : 1.0f);
       }
 #pragma unroll
-      for (int u = 0; u < N; ++u) {
+      for (int u = 0; u < kTokens; ++u) {
         if (w[u] == 0.0f) continue;  // whatever the token's log probability
         SeqSum::add(sum.s, {w[u] * (lp[u] - ref[u]), 0.0f});
         SeqSum::add(sum.w, {w[u], 0.0f});
@@ -164,13 +166,13 @@ __global__ void __launch_bounds__(kMaxThreads) preference_kernel(const __grid_co
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const float g = slope[k];
-    over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step, auto n) {
-      constexpr int N = decltype(n)::value;
-      float w[N];
+    over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step) {
+      float w[kTokens];
 #pragma unroll
-      for (int u = 0; u < N; ++u) w[u] = a.weight ? a.weight[i + u * step] : 1.0f;
+      for (int u = 0; u < kTokens; ++u) w[u] = a.weight && i + u * step < at[k].hi ? a.weight[i + u * step] : 1.0f;
 #pragma unroll
-      for (int u = 0; u < N; ++u) a.d[i + u * step] = w[u] == 0.0f ? 0.0f : w[u] * g;
+      for (int u = 0; u < kTokens; ++u)
+        if (i + u * step < at[k].hi) a.d[i + u * step] = w[u] == 0.0f ? 0.0f : w[u] * g;
     });
   }
 }
@@ -202,10 +204,10 @@ ss_status preference_impl(const float* logprob, int64_t rows, const ss_preferenc
   const PreferenceArgs a = {logprob, p->ref_logprob, p->row_weight, p->pair_weight, p->offsets, loss,
                             reinterpret_cast<float2*>(reward), d_logprob, rows, pairs, p->beta, p->margin,
                             p->label_smoothing, p->kind, p->idtype == SS_I64, p->halves != 0, p->average != 0};
-  // threads and blocks by the tokens of a pair, on average: four of each sequence a thread
+  // threads and blocks by the tokens of a pair, on average: eight of each sequence a thread
   const int64_t each = rows / pairs;
   int threads = 64;
-  while (threads < kMaxThreads && each > 8 * threads) threads *= 2;
+  while (threads < kMaxThreads && each > 16 * threads) threads *= 2;
   int cluster = 1;
   while (cluster < kMaxCluster && each > 16 * cluster * threads && pairs * cluster * threads * 2 <= 1024 * sm_count())
     cluster *= 2;
