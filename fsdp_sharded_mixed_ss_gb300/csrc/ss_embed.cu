@@ -139,29 +139,32 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
     }
   };
   int64_t id = id_at(task), next_id = id_at(task + warps);
-  Raw8<DT> raw[4];
-  fetch(task, id, raw);
-  for (; task < tasks; task += warps) {
-    Raw8<DT> next[4];
-    fetch(task + warps, next_id, next);
+  Raw8<DT> f[4], g[4];
+  fetch(task, id, f);
+  // two buffers by name: a copy from one to the other would wait for the loads
+  auto step = [&](const Raw8<DT> (&here)[4], Raw8<DT> (&there)[4]) {
+    if (task >= tasks) return false;
+    fetch(task + warps, next_id, there);
     const int64_t after = id_at(task + 2 * warps);
     char* out = a.out.row(task / a.pieces);
     const int from = static_cast<int>(task % a.pieces) * kRowPiece;
-    const bool there = id >= 0 && id < a.vocab;
+    const bool row = id >= 0 && id < a.vocab;
     const float none = id < 0 ? 0.0f : nan_f();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = from + (u * 32 + lane) * 8;
-      float f[8];
-      raw[u].unpack(f);
+      float v[8];
+      here[u].unpack(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = there ? f[j] * a.scale : none;
-      if (e < a.dim) store8<OT, VEC>(out, e, a.dim, f);
+      for (int j = 0; j < 8; ++j) v[j] = row ? v[j] * a.scale : none;
+      if (e < a.dim) store8<OT, VEC>(out, e, a.dim, v);
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) raw[u] = next[u];
     id = next_id;
     next_id = after;
+    task += warps;
+    return true;
+  };
+  while (step(f, g) && step(g, f)) {
   }
 }
 
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 //
 // A stable radix sort of (token, position) by one cluster of blocks, so that a
 // token's positions stand together and in ascending order: that order is the order
-// of the sums. Every warp has a run of consecutive pairs. A pass counts each warp's
+// of the sums. Every warp has a part of consecutive pairs. A pass counts each warp's
 // digits, turns the counts into places (by digit, then by warp) and moves the pairs
 // there, 32 at a time; the places of equal digits within them come from a match over
 // the lanes. Positions without a token (a negative id, or one past the vocabulary)
@@ -178,27 +181,26 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBlocks = 8;
+constexpr int kAloneMost = 8192;  // positions that one block sorts alone
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 
-// What the sums are made of: up to kChunk sorted positions of one token, those of one aligned run of kChunk.
-constexpr int kChunk = 32;  // a warp's lanes: a warp that goes through the sorted positions sees a whole run at a time
-struct Task {
-  int32_t at;        // first sorted position
-  uint32_t token;
-  int32_t count;     // positions; negative where the token has positions in other runs as well
-  int32_t first;     // its first position's row; its token's number among those that occur where count is negative
+// The sums are over runs of `run` (a divisor of 32) sorted positions. What a run has to know of a token that reaches
+// into other runs:
+struct Crossing {
+  int32_t* before;  // [runs] tokens that begin in an earlier run than the one they end in, and before this run
+  int32_t* at;      // of each of those, in order: its first sorted position,
+  int32_t* last;    // and its last run
 };
 
 struct SortArgs {
   const void* ids;
   uint64_t* pairs[2];  // token << 32 | position; the sorted ones are in pairs[passes & 1 ? 0 : 1]
-  Task* tasks;
-  int32_t* first_task;  // of every token that occurs; then their number
-  int32_t* n_tasks;
+  Crossing crossing;
   uint32_t* arrived;    // n_arrived counters, to be cleared
   int64_t n_arrived, vocab;
   int32_t n, passes, bits;  // bits of a digit
+  int32_t run;
   bool wide;
 };
 
@@ -209,25 +211,25 @@ struct SortShared {
   uint32_t total[kDigits];              // of the block's digits
   uint32_t base[kDigits];
   uint32_t warp_sum[kSortWarps];
-  uint2 warp_tasks[kSortWarps];  // tasks and tokens that begin in a warp's run
-  uint2 block_tasks;
+  uint32_t crossing[kSortWarps + 1];  // tokens that cross a run's end and begin in a warp's part; the block's at the end
 };
 
 __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n;
-  // this warp's run
-  const int64_t each = (static_cast<int64_t>(n) + kSortBlocks * kSortWarps * 32 - 1) / (kSortBlocks * kSortWarps * 32) * 32;
+  // this warp's part
+  const int64_t warps = static_cast<int64_t>(cl.size) * kSortWarps;
+  const int64_t each = (n + warps * 32 - 1) / (warps * 32) * 32;
   const int64_t first = (static_cast<int64_t>(cl.rank) * kSortWarps + warp) * each;
   const int64_t last = min(first + each, static_cast<int64_t>(n));
   const uint32_t none = static_cast<uint32_t>(a.vocab);
-  for (int64_t i = static_cast<int64_t>(cl.rank) * kSortThreads + tid; i < a.n_arrived; i += kSortBlocks * kSortThreads)
-    a.arrived[i] = 0u;
+  const int digits = 1 << a.bits;
+  for (int64_t i = static_cast<int64_t>(cl.rank) * kSortThreads + tid; i < a.n_arrived; i += warps * 32) a.arrived[i] = 0u;
   for (int pass = 0; pass < a.passes; ++pass) {
     const uint64_t* from = a.pairs[(pass & 1) ^ 1];
     uint64_t* to = a.pairs[pass & 1];
     const int shift = pass * a.bits;
-    const uint32_t mask = (1u << a.bits) - 1u;
+    const uint32_t mask = digits - 1u;
     auto pair_at = [&](int64_t i) -> uint64_t {
       if (pass > 0) return __ldcg(reinterpret_cast<const unsigned long long*>(from) + i);
       const int64_t id = load_id(a.ids, i, a.wide);
@@ -235,12 +237,13 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
       return static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(i);
     };
     auto digit_of = [&](uint64_t pair) { return static_cast<uint32_t>(pair >> (32 + shift)) & mask; };
-    for (int d = lane; d < kDigits; d += 32) s.count[warp][d] = 0;
+    for (int d = lane; d < digits; d += 32) s.count[warp][d] = 0;
     __syncwarp();
     for (int64_t i = first + lane; i < last; i += 32) atomicAdd(&s.count[warp][digit_of(pair_at(i))], 1u);
     __syncthreads();
-    if (tid < kDigits) {
+    if (tid < digits) {
       uint32_t sum = 0;
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) sum += s.count[w][tid];
       s.total[tid] = sum;
     }
@@ -249,7 +252,7 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
     if (tid < kDigits) {
       uint32_t all = 0, before = 0;
       for (unsigned r = 0; r < cl.size; ++r) {
-        const uint32_t t = cl.at(s.total, r)[tid];
+        const uint32_t t = tid < digits ? cl.at(s.total, r)[tid] : 0u;
         before += r < cl.rank ? t : 0u;
         all += t;
       }
@@ -263,9 +266,10 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
       s.base[tid] = upto - all + before;
     }
     __syncthreads();
-    if (tid < kDigits) {
+    if (tid < digits) {
       uint32_t at = s.base[tid];
       for (int w = 0; w < warp; ++w) at += s.warp_sum[w];
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = s.count[w][tid];
         s.count[w][tid] = at;
@@ -290,66 +294,54 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
     __threadfence();
     cl.sync();
   }
-  // the tasks, in the order of their positions: counted, then written
+  // the tokens that cross runs: counted, then listed
   const auto* sorted = reinterpret_cast<const unsigned long long*>(a.pairs[a.passes & 1 ? 0 : 1]);
+  const int run = a.run, base = lane / run * run;  // this lane's run of the warp's 32 positions
+  const unsigned of_run = (run == 32 ? ~0u : (1u << run) - 1u) << base;
+  const bool speaks = lane % run == run - 1;       // for its run
   auto over_runs = [&](const auto& f) {
     uint32_t before = first > 0 && first < last ? token_of(__ldcg(sorted + first - 1)) : ~0u;
-    for (int64_t i = first; i < last; i += kChunk) {
-      const uint64_t pair = i + lane < last ? __ldcg(sorted + i + lane) : ~0ull;
-      const uint32_t token = token_of(pair);
-      uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, token, 1);
+    for (int64_t i = first; i < last; i += 32) {
+      const uint32_t token = i + lane < n ? token_of(__ldcg(sorted + i + lane)) : ~0u;
+      const uint32_t behind = i + 32 < n ? token_of(__ldcg(sorted + i + 32)) : ~0u;
+      uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, token, 1), next = __shfl_down_sync(0xFFFFFFFFu, token, 1);
       if (lane == 0) prev = before;
+      if (lane == 31) next = behind;
       before = __shfl_sync(0xFFFFFFFFu, token, 31);
-      const bool live = token < none, begins = live && token != prev;
-      f(i, pair, live, begins, __ballot_sync(0xFFFFFFFFu, begins), __ballot_sync(0xFFFFFFFFu, begins || (live && lane == 0)));
+      const unsigned begin = __ballot_sync(0xFFFFFFFFu, token < none && token != prev) & of_run;
+      const bool comes = __shfl_sync(0xFFFFFFFFu, token < none && token == prev, base);  // into the run
+      const bool goes = token < none && token == next;                                   // out of it
+      const bool starts = speaks && goes && begin, ends = speaks && comes && !(goes && !begin);
+      f(i, begin, starts, ends, __ballot_sync(0xFFFFFFFFu, starts));
     }
   };
-  uint2 here = make_uint2(0, 0);
-  over_runs([&](int64_t, uint64_t, bool, bool, unsigned tokens, unsigned tasks) {
-    here.x += __popc(tasks);
-    here.y += __popc(tokens);
-  });
-  if (lane == 0) s.warp_tasks[warp] = here;
+  uint32_t at = 0;
+  over_runs([&](int64_t, unsigned, bool, bool, unsigned starts) { at += __popc(starts); });
+  if (lane == 0) s.crossing[warp] = at;
   __syncthreads();
   if (warp == 0) {  // sums before each warp, and the block's
-    const uint2 own = s.warp_tasks[lane];
-    uint2 upto = own;
+    const uint32_t own = s.crossing[lane];
+    uint32_t upto = own;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto.x, off), y = __shfl_up_sync(0xFFFFFFFFu, upto.y, off);
-      if (lane >= off) upto = make_uint2(upto.x + x, upto.y + y);
+      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += o;
     }
-    s.warp_tasks[lane] = make_uint2(upto.x - own.x, upto.y - own.y);
-    if (lane == 31) s.block_tasks = upto;
+    s.crossing[lane] = upto - own;
+    if (lane == 31) s.crossing[kSortWarps] = upto;
   }
   cl.sync();
-  uint2 at = s.warp_tasks[warp], all = make_uint2(0, 0);
-  for (unsigned r = 0; r < cl.size; ++r) {
-    const uint2 b = *cl.at(&s.block_tasks, r);
-    if (r < cl.rank) at = make_uint2(at.x + b.x, at.y + b.y);
-    all = make_uint2(all.x + b.x, all.y + b.y);
-  }
-  over_runs([&](int64_t i, uint64_t pair, bool live, bool begins, unsigned tokens, unsigned tasks) {
-    const uint32_t token = token_of(pair);
-    const unsigned below = (1u << lane) - 1u, behind = lane == 31 ? 0u : tasks >> (lane + 1) << (lane + 1);
-    const int in_run = __popc(__ballot_sync(0xFFFFFFFFu, live));
-    if ((tasks >> lane) & 1u) {
-      const int end = behind ? __ffs(behind) - 1 : in_run;
-      const bool goes_on = end == kChunk && i + kChunk < n && token_of(__ldcg(sorted + i + kChunk)) == token;
-      const uint32_t task = at.x + __popc(tasks & below), number = at.y + __popc(tokens & (below | 1u << lane)) - 1u;
-      const bool parts = goes_on || !begins;
-      a.tasks[task] = {static_cast<int32_t>(i) + lane, token, parts ? lane - end : end - lane,
-                       parts ? static_cast<int32_t>(number) : static_cast<int32_t>(static_cast<uint32_t>(pair))};
-      if (begins) a.first_task[number] = static_cast<int32_t>(task);
-    }
-    at.x += __popc(tasks);
-    at.y += __popc(tokens);
+  at = s.crossing[warp];
+  for (unsigned r = 0; r < cl.rank; ++r) at += *cl.at(&s.crossing[kSortWarps], r);
+  over_runs([&](int64_t i, unsigned begin, bool starts, bool ends, unsigned all) {
+    const uint32_t here = at + __popc(all & ((1u << base) - 1u));
+    const int64_t r = (i + base) / run;
+    if (speaks && i + base < n) a.crossing.before[r] = static_cast<int32_t>(here);
+    if (starts) a.crossing.at[here] = static_cast<int32_t>(i) + 31 - __clz(static_cast<int>(begin));
+    if (ends) a.crossing.last[here - 1] = static_cast<int32_t>(r);
+    at += __popc(all);
   });
-  if (cl.rank == 0 && tid == 0) {
-    *a.n_tasks = static_cast<int32_t>(all.x);
-    a.first_task[all.y] = static_cast<int32_t>(all.x);
-  }
-  cl.sync();  // the other blocks have read this one's totals
+  cl.sync();  // the other blocks have read this one's total
 }
 
 struct FillArgs {
@@ -387,6 +379,7 @@ struct SortFillArgs {
 };
 
 // Cluster 0 sorts; the others fill the table meanwhile.
+// (A cluster is the sort's blocks.)
 template <bool VEC>
 __global__ void __launch_bounds__(kSortThreads, 1) sort_fill_kernel(const __grid_constant__ SortFillArgs a) {
   extern __shared__ char shared[];
@@ -394,38 +387,41 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_fill_kernel(const __grid
   pdl_wait();
   pdl_trigger();
   cl.started();
-  if (blockIdx.x < kSortBlocks) {
+  if (blockIdx.x < cl.size) {
     if (a.sort.n == 0) return;  // there is no workspace then
     sort_positions(a.sort, cl, *reinterpret_cast<SortShared*>(shared));
   } else {
-    const int64_t warp = static_cast<int64_t>(blockIdx.x - kSortBlocks) * kSortWarps + (threadIdx.x >> 5);
-    fill_rows<VEC>(a.fill, warp, static_cast<int64_t>(gridDim.x - kSortBlocks) * kSortWarps);
+    const int64_t warp = static_cast<int64_t>(blockIdx.x - cl.size) * kSortWarps + (threadIdx.x >> 5);
+    fill_rows<VEC>(a.fill, warp, static_cast<int64_t>(gridDim.x - cl.size) * kSortWarps);
   }
 }
 
 // ------------------------------------------------------------------ the sums
 //
-// A warp takes a task's positions and up to 512 columns. A token with one task is
-// finished by it. A token with more leaves each task's sum in the workspace, and
-// whichever warp is the last to do so of kGroup neighbouring runs adds these up, and the
-// last of those the groups' sums: the order of the sums is that of the positions
-// whichever warp adds them.
+// A warp takes a run of sorted positions and up to 512 columns, adds one row after
+// another and writes the sum out where the token changes. The next kStages - 1 rows,
+// and the base's where a token ends, are on their way to shared memory meanwhile
+// (registers for as many would halve the warps); a lane copies and reads its own
+// columns only, so nothing is waited for but its own copies. A token that reaches into
+// other runs leaves each run's sum in the workspace, and whichever warp is the last to
+// do so of kGroup neighbouring runs adds these up, and the last of those the groups'
+// sums: the order of the sums is that of the positions whichever warp adds them.
 
 constexpr int kGroup = 16;
+constexpr int kStages = 4;
 constexpr int kSumThreads = 256;
 constexpr int kVecs = 2;                   // groups of eight columns that a lane has
 constexpr int kSumPiece = kVecs * 32 * 8;  // columns that a warp takes at a time
 
 struct SumArgs {
   const uint64_t* pairs;
-  const Task* tasks;
-  const int32_t* first_task;
-  const int32_t* n_tasks;
-  uint32_t* arrived;  // [2][2 runs][pieces]: of a token's tasks in a group of runs, of its groups
+  Crossing crossing;
+  uint32_t* arrived;  // [2][2 runs][pieces]: of a token's runs in a group, of its groups
   float* partial;     // [2 runs][pitch]: of the token that a run begins with, of the one that it ends with
   Rows d_out, base, table;
-  int64_t pitch;
-  int32_t runs, dim, pieces;
+  int64_t pitch, vocab;
+  int32_t n, run, runs, dim, pieces;
+  int32_t stage_bytes;  // of a warp, for a row and the base's
   float scale;
 };
 
@@ -434,29 +430,62 @@ struct Columns {
   __device__ __forceinline__ int at(int u) const { return from + (u * 32 + lane) * 8; }
 };
 
-// A token's row from its sum.
-template <bool VEC>
-__device__ __forceinline__ void finish_row(const SumArgs& a, uint32_t token, const Columns& c, const float (&sum)[kVecs][8]) {
-  char* out = a.table.row(token);
-  float f[kVecs][8] = {};
-  if (a.base.data) {
-    const char* base = a.base.row(token);
+__device__ __forceinline__ void copy16(void* shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+               "l"(global)
+               : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {  // all but the latest N
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A lane's columns of a row on their way to shared memory: group u of the lane at place(u), 16 bytes every 512.
+template <int DT, bool VEC>
+__device__ __forceinline__ void copy_row(char* shared, const char* row, const Columns& c) {
+  constexpr int W = DT == SS_FP32 ? 2 : 1;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      if (c.at(u) < c.dim) load8<VEC>(a.base.dtype, base, c.at(u), c.dim, f[u]);
+  for (int u = 0; u < kVecs; ++u) {
+    const int e = c.at(u);
+    char* to = shared + u * W * 512 + c.lane * 16;
+    if (VEC && e + 8 <= c.dim) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) copy16(to + i * 512, row + static_cast<int64_t>(e) * sizeof(Elem<DT>) + i * 16);
+    } else if (e < c.dim) {
+      Raw8<DT> f;
+      f.template load<false>(row, e, c.dim);
+#pragma unroll
+      for (int i = 0; i < W; ++i) *reinterpret_cast<uint4*>(to + i * 512) = f.w[i];
+    }
   }
+}
+template <int DT>
+__device__ __forceinline__ Raw8<DT> copied(const char* shared, int u, int lane) {
+  constexpr int W = DT == SS_FP32 ? 2 : 1;
+  Raw8<DT> f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) f.w[i] = *reinterpret_cast<const uint4*>(shared + (u * W + i) * 512 + lane * 16);
+  return f;
+}
+
+// A token's row: its sum on `base`.
+template <bool VEC>
+__device__ __forceinline__ void put_row(const SumArgs& a, uint32_t token, const Columns& c, const float (&sum)[kVecs][8],
+                                        float (&base)[kVecs][8]) {
+  char* out = a.table.row(token);
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[u][j] = fmaf(sum[u][j], a.scale, f[u][j]);
-    if (c.at(u) < c.dim) store8<VEC>(a.table.dtype, out, c.at(u), c.dim, f[u]);
+    for (int j = 0; j < 8; ++j) base[u][j] = fmaf(sum[u][j], a.scale, base[u][j]);
+    if (c.at(u) < c.dim) store8<VEC>(a.table.dtype, out, c.at(u), c.dim, base[u]);
   }
 }
 
-// The sums of a token's tasks: one in each of the runs from `first` to `last`.
-struct TokenParts {
-  int first, last;  // runs
-  bool inside;      // it begins inside its first run
+// The runs of a token that reaches into several.
+struct TokenRuns {
+  int first, last;
+  bool inside;  // it begins inside its first run
 
   __device__ __forceinline__ int64_t slot(int run) const { return 2 * static_cast<int64_t>(run) + (run == first && inside); }
 };
@@ -493,82 +522,164 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int of, int la
   return last;
 }
 
-// A part's sum on its way to its token's row.
-template <bool VEC>
-__device__ __forceinline__ void join_parts(const SumArgs& a, const Task& task, int piece, const Columns& c,
-                                           float (&sum)[kVecs][8]) {
-  const int begin = a.first_task[task.first], parts = a.first_task[task.first + 1] - begin;
-  const int start = a.tasks[begin].at;
-  TokenParts t;
-  t.first = start / kChunk;
-  t.last = t.first + parts - 1;
-  t.inside = start % kChunk != 0;
-  const int run = task.at / kChunk;
-  put_partial(a, t.slot(run), c, sum);
-  // this group's parts
-  const int lo = max(t.first, run / kGroup * kGroup), hi = min(t.last, run / kGroup * kGroup + kGroup - 1);
-  uint32_t* arrived = a.arrived + t.slot(lo) * a.pieces + piece;
-  if (!last_to_arrive(arrived, hi - lo + 1, c.lane)) return;
+__device__ __forceinline__ void clear(float (&sum)[kVecs][8]) {
 #pragma unroll
   for (int u = 0; u < kVecs; ++u)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
+}
+
+// A run's sum of a token that reaches into others, on its way to the token's row. `number`: the token's among those.
+template <bool VEC>
+__device__ __forceinline__ void join_runs(const SumArgs& a, uint32_t token, int number, int run, int piece, const Columns& c,
+                                          float (&sum)[kVecs][8]) {
+  const int start = a.crossing.at[number];
+  const TokenRuns t = {start / a.run, a.crossing.last[number], start % a.run != 0};
+  put_partial(a, t.slot(run), c, sum);
+  // this group's runs
+  const int lo = max(t.first, run / kGroup * kGroup), hi = min(t.last, run / kGroup * kGroup + kGroup - 1);
+  if (!last_to_arrive(a.arrived + t.slot(lo) * a.pieces + piece, hi - lo + 1, c.lane)) return;
+  clear(sum);
 #pragma unroll 2
   for (int r = lo; r <= hi; ++r) add_partial(a, t.slot(r), c, sum);
   const int groups = t.last / kGroup - t.first / kGroup + 1;
   if (groups > 1) {
     put_partial(a, t.slot(lo), c, sum);
-    arrived = a.arrived + (2 * static_cast<int64_t>(a.runs) + t.slot(t.first)) * a.pieces + piece;
-    if (!last_to_arrive(arrived, groups, c.lane)) return;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
+    if (!last_to_arrive(a.arrived + (2 * static_cast<int64_t>(a.runs) + t.slot(t.first)) * a.pieces + piece, groups, c.lane))
+      return;
+    clear(sum);
 #pragma unroll 2
     for (int g = t.first / kGroup; g <= t.last / kGroup; ++g) add_partial(a, t.slot(max(t.first, g * kGroup)), c, sum);
   }
-  finish_row<VEC>(a, task.token, c, sum);
+  float base[kVecs][8] = {};
+  if (a.base.data) {
+    const char* row = a.base.row(token);
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (c.at(u) < c.dim) load8<VEC>(a.base.dtype, row, c.at(u), c.dim, base[u]);
+  }
+  put_row<VEC>(a, token, c, sum, base);
 }
 
-template <int DT>
-constexpr int kInFlight = DT == SS_FP32 ? 1 : 2;  // rows that a warp has in flight
+// A run of sorted positions as a warp sees it: lane i has the i-th one's token and row.
+struct RunView {
+  uint32_t token;
+  int32_t row;
+  int live;       // positions with a token
+  unsigned ends;  // bit i: the token of position i ends there
+  bool comes;     // the first token begins in an earlier run
+  int index, piece;
+
+  // The loads, and what is made of them: apart, so that the next run's are on their way while this one is added.
+  struct Loads {
+    uint64_t pair, before, behind;
+  };
+  __device__ __forceinline__ static Loads load(const SumArgs& a, int64_t item, int64_t items) {
+    const int lane = threadIdx.x & 31;
+    Loads l = {~0ull, ~0ull, ~0ull};
+    if (item < items) {
+      const int64_t from = item / a.pieces * a.run, at = from + lane;
+      if (lane < a.run && at < a.n) l.pair = a.pairs[at];
+      if (from > 0) l.before = a.pairs[from - 1];
+      if (from + a.run < a.n) l.behind = a.pairs[from + a.run];
+    }
+    return l;
+  }
+  __device__ __forceinline__ RunView(const SumArgs& a, const Loads& l, int64_t item)
+      : token(token_of(l.pair)),
+        row(static_cast<int32_t>(static_cast<uint32_t>(l.pair))),
+        index(static_cast<int>(item / a.pieces)),
+        piece(static_cast<int>(item - static_cast<int64_t>(index) * a.pieces)) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t none = static_cast<uint32_t>(a.vocab);
+    uint32_t next = __shfl_down_sync(0xFFFFFFFFu, token, 1);
+    if (lane == a.run - 1) next = token_of(l.behind);
+    live = __popc(__ballot_sync(0xFFFFFFFFu, token < none));
+    ends = __ballot_sync(0xFFFFFFFFu, token < none && token != next);
+    comes = __shfl_sync(0xFFFFFFFFu, token, 0) == token_of(l.before);
+  }
+  // Whether position i is the last of a token that is this run's alone.
+  __device__ __forceinline__ bool completes(int i) const {
+    return ((ends >> i) & 1u) && !(comes && (ends & ((1u << i) - 1u)) == 0u);
+  }
+};
 
 template <int DT, bool VEC, bool TVEC>
-__global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_constant__ SumArgs a) {
+  extern __shared__ __align__(16) char shared[];
   pdl_wait();
   pdl_trigger();
+  constexpr int kRowBytes = kSumPiece * sizeof(Elem<DT>);
   const int lane = threadIdx.x & 31;
+  char* stages = shared + (threadIdx.x >> 5) * kStages * a.stage_bytes;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kSumThreads / 32);
-  const int64_t items = static_cast<int64_t>(*a.n_tasks) * a.pieces;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5); item < items;
-       item += warps) {
-    const int64_t j = item / a.pieces;
-    const int piece = static_cast<int>(item - j * a.pieces);
-    const int4 words = *reinterpret_cast<const int4*>(a.tasks + j);
-    const Task task = {words.x, static_cast<uint32_t>(words.y), words.z, words.w};
-    const int count = abs(task.count);
-    const Columns c = {piece * kSumPiece, a.dim, lane};
-    // lane i has the row of the task's i-th position
-    const int32_t row = task.count == 1 ? task.first
-                                        : static_cast<int32_t>(static_cast<uint32_t>(a.pairs[task.at + min(lane, count - 1)]));
-    float sum[kVecs][8] = {};
-    for (int i = 0; i < count; i += kInFlight<DT>) {
-      Raw8<DT> f[kInFlight<DT>][kVecs];
-#pragma unroll
-      for (int r = 0; r < kInFlight<DT>; ++r) {
-        const char* p = a.d_out.row(__shfl_sync(0xFFFFFFFFu, row, min(i + r, count - 1)));
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-          if (i + r < count && c.at(u) < c.dim) f[r][u].template load<VEC>(p, c.at(u), c.dim);
+  const int64_t items = static_cast<int64_t>(a.runs) * a.pieces;
+  int64_t item = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5);
+  if (item >= items) return;
+  auto issue = [&](const RunView& v, int i, int stage) {
+    if (i < v.live) {
+      const Columns c = {v.piece * kSumPiece, a.dim, lane};
+      char* to = stages + stage * a.stage_bytes;
+      copy_row<DT, VEC>(to, a.d_out.row(__shfl_sync(0xFFFFFFFFu, v.row, i)), c);
+      if (a.base.data && v.completes(i)) {
+        const char* base = a.base.row(__shfl_sync(0xFFFFFFFFu, v.token, i));
+        if (a.base.dtype == SS_FP32) copy_row<SS_FP32, TVEC>(to + kRowBytes, base, c);
+        else copy_row<SS_BF16, TVEC>(to + kRowBytes, base, c);  // the bits, of either 16-bit type
       }
-#pragma unroll
-      for (int r = 0; r < kInFlight<DT>; ++r)
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-          if (i + r < count && c.at(u) < c.dim) f[r][u].add_to(sum[u]);
     }
-    if (task.count > 0) finish_row<TVEC>(a, task.token, c, sum);
-    else join_parts<TVEC>(a, task, piece, c, sum);
+    commit_copies();
+  };
+  RunView now(a, RunView::load(a, item, items), item);
+  RunView::Loads ahead = RunView::load(a, item + warps, items);
+  int stage = 0;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(now, i, i);
+  while (true) {
+    // a run of fewer positions than stages has empty groups of copies behind it
+    const int steps = max(now.live, kStages - 1);
+    const RunView next(a, ahead, item + warps);
+    ahead = RunView::load(a, item + 2 * warps, items);
+    const bool more = item + warps < items;
+    const Columns c = {now.piece * kSumPiece, a.dim, lane};
+    float sum[kVecs][8];
+    clear(sum);
+    for (int i = 0; i < steps; ++i) {
+      const int ahead_i = i + kStages - 1, to = (stage + kStages - 1) % kStages;
+      if (ahead_i < steps) issue(now, ahead_i, to);
+      else if (more) issue(next, ahead_i - steps, to);
+      else commit_copies();
+      wait_copies<kStages - 1>();
+      const char* from = stages + stage * a.stage_bytes;
+      stage = (stage + 1) % kStages;
+      if (i >= now.live) continue;
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (c.at(u) < c.dim) copied<DT>(from, u, lane).add_to(sum[u]);
+      const bool ends = (now.ends >> i) & 1u;
+      if (!ends && i + 1 < now.live) continue;
+      const uint32_t token = __shfl_sync(0xFFFFFFFFu, now.token, i);
+      if (now.completes(i)) {
+        float base[kVecs][8] = {};
+        if (a.base.data) {
+#pragma unroll
+          for (int u = 0; u < kVecs; ++u) {
+            if (c.at(u) >= c.dim) continue;
+            if (a.base.dtype == SS_FP32) copied<SS_FP32>(from + kRowBytes, u, lane).unpack(base[u]);
+            else if (a.base.dtype == SS_BF16) copied<SS_BF16>(from + kRowBytes, u, lane).unpack(base[u]);
+            else copied<SS_FP16>(from + kRowBytes, u, lane).unpack(base[u]);
+          }
+        }
+        put_row<TVEC>(a, token, c, sum, base);
+      } else {
+        // the run's first token is the last that began before it
+        const bool first = now.comes && (now.ends & ((1u << i) - 1u)) == 0u;
+        join_runs<TVEC>(a, token, a.crossing.before[now.index] - (first ? 1 : 0), now.index, now.piece, c, sum);
+      }
+      clear(sum);
+    }
+    if (!more) break;
+    now = next;
+    item += warps;
   }
 }
 
@@ -577,28 +688,33 @@ __global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(const __grid_consta
 int64_t pitch_of(int64_t dim) { return (dim + 7) / 8 * 8; }
 int pieces_of(int64_t dim, int piece) { return static_cast<int>((dim + piece - 1) / piece); }
 
+// Positions of a run: short ones where there are few, so that there are warps enough.
+int64_t most_short(int64_t dim) { return (4096 + pieces_of(dim, kSumPiece) - 1) / pieces_of(dim, kSumPiece) * 32 - 1; }
+int run_of(int64_t n, int64_t dim) { return n <= most_short(dim) ? 8 : 32; }
+
 // The workspace's parts, each on a 16-byte boundary: where they begin, and its bytes (-1: more than int64 holds).
 struct Workspace {
-  int64_t runs, n_arrived;
-  int64_t pairs[2], tasks, first_task, n_tasks, arrived, partial, bytes;
+  int64_t run, runs, n_arrived;
+  int64_t pairs[2], before, at, last, arrived, partial, bytes;
 
   Workspace(int64_t n, int64_t dim) {
-    runs = (n + kChunk - 1) / kChunk;
+    run = run_of(n, dim);
+    runs = (n + run - 1) / run;
     n_arrived = 4 * runs * pieces_of(dim, kSumPiece);
-    __int128 at = 0;
+    __int128 end = 0;
     const auto take = [&](__int128 size) {
-      const __int128 from = at;
-      at += (size + 15) / 16 * 16;
+      const __int128 from = end;
+      end += (size + 15) / 16 * 16;
       return static_cast<int64_t>(from);
     };
     pairs[0] = take(static_cast<__int128>(n) * 8);
     pairs[1] = take(static_cast<__int128>(n) * 8);
-    tasks = take(static_cast<__int128>(n) * static_cast<int64_t>(sizeof(Task)));
-    first_task = take((static_cast<__int128>(n) + 1) * 4);
-    n_tasks = take(4);
+    before = take(runs * 4);
+    at = take(runs * 4);  // one token at most crosses each run's end
+    last = take(runs * 4);
     arrived = take(static_cast<__int128>(n_arrived) * 4);
     partial = take(static_cast<__int128>(runs) * 2 * pitch_of(dim) * 4);
-    bytes = at > INT64_MAX ? -1 : static_cast<int64_t>(at);
+    bytes = end > INT64_MAX ? -1 : static_cast<int64_t>(end);
   }
 };
 
@@ -719,27 +835,34 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
     while ((t->vocab >> bits) != 0) ++bits;
     const int passes = (bits + kDigitBits - 1) / kDigitBits;
     sf.sort = {ids, {reinterpret_cast<uint64_t*>(w + ws.pairs[0]), reinterpret_cast<uint64_t*>(w + ws.pairs[1])},
-               reinterpret_cast<Task*>(w + ws.tasks), reinterpret_cast<int32_t*>(w + ws.first_task),
-               reinterpret_cast<int32_t*>(w + ws.n_tasks), reinterpret_cast<uint32_t*>(w + ws.arrived), ws.n_arrived,
-               t->vocab, static_cast<int32_t>(n), passes, (bits + passes - 1) / passes, idtype == SS_I64};
+               {reinterpret_cast<int32_t*>(w + ws.before), reinterpret_cast<int32_t*>(w + ws.at),
+                reinterpret_cast<int32_t*>(w + ws.last)},
+               reinterpret_cast<uint32_t*>(w + ws.arrived), ws.n_arrived, t->vocab, static_cast<int32_t>(n), passes,
+               (bits + passes - 1) / passes, static_cast<int32_t>(ws.run), idtype == SS_I64};
   }
   sf.fill = {from, table, in_place ? 0 : t->vocab, dim, pieces_of(dim, kRowPiece)};
   auto* sort_fill = tvec ? sort_fill_kernel<true> : sort_fill_kernel<false>;
   st = allow_shared(sort_fill, sizeof(SortShared));
   if (st != SS_OK) return st;
-  const int fill_clusters = in_place ? 0 : std::max(1, 2 * sm_count() / kSortBlocks);
-  st = launch_rows(sort_fill, 1 + fill_clusters, kSortBlocks, kSortThreads, sizeof(SortShared), sf, stream);
+  const int cluster = n > kAloneMost ? kSortBlocks : 1;
+  const int fill_clusters = in_place ? 0 : std::max(1, 2 * sm_count() / cluster);
+  st = launch_rows(sort_fill, 1 + fill_clusters, cluster, kSortThreads, sizeof(SortShared), sf, stream);
   if (st != SS_OK || n == 0) return st;
-  // tasks: one for each token, and one more at most for each run that a token's positions pass into
-  const int64_t most = std::min(n, t->vocab + ws.runs);
-  const SumArgs a = {sf.sort.pairs[sf.sort.passes & 1 ? 0 : 1], sf.sort.tasks, sf.sort.first_task, sf.sort.n_tasks,
-                     sf.sort.arrived, reinterpret_cast<float*>(w + ws.partial), {const_cast<void*>(d_out), d_ld, d_dtype},
-                     from, table, pitch_of(dim), static_cast<int32_t>(ws.runs), dim, pieces_of(dim, kSumPiece), scale};
+  const int stage_bytes = kSumPiece * static_cast<int>(dtype_bytes(d_dtype) + (base ? dtype_bytes(base->dtype) : 0));
+  const SumArgs a = {sf.sort.pairs[sf.sort.passes & 1 ? 0 : 1], sf.sort.crossing, sf.sort.arrived,
+                     reinterpret_cast<float*>(w + ws.partial), {const_cast<void*>(d_out), d_ld, d_dtype}, from, table,
+                     pitch_of(dim), t->vocab, static_cast<int32_t>(n), static_cast<int32_t>(ws.run),
+                     static_cast<int32_t>(ws.runs), dim, pieces_of(dim, kSumPiece), stage_bytes, scale};
   const bool vec = aligned_rows(a.d_out);
   auto* fn = d_dtype == SS_BF16 ? pick_sum<SS_BF16>(vec, tvec)
                                 : (d_dtype == SS_FP16 ? pick_sum<SS_FP16>(vec, tvec) : pick_sum<SS_FP32>(vec, tvec));
-  const unsigned grid = grid_for(reinterpret_cast<const void*>(fn), most * a.pieces * 32, kSumThreads);
-  return launch(fn, grid, a, stream, kSumThreads);
+  const size_t smem = static_cast<size_t>(stage_bytes) * kStages * (kSumThreads / 32);
+  st = allow_shared(fn, smem);
+  if (st != SS_OK) return st;
+  const int64_t blocks = (ws.runs * a.pieces + kSumThreads / 32 - 1) / (kSumThreads / 32);
+  const int64_t places = static_cast<int64_t>(sm_count()) * std::min<int64_t>(3, (224 * 1024) / static_cast<int64_t>(smem + 1024));
+  return launch_dependent(fn, dim3(static_cast<unsigned>(std::min(blocks, std::max<int64_t>(places, 1)))),
+                          dim3(kSumThreads), smem, stream, a);
 }
 
 }  // namespace
@@ -756,7 +879,8 @@ ss_status ss_embedding(const ss_table* table, const void* ids, ss_idtype idtype,
 
 int64_t ss_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
   if (n < 0 || n > INT32_MAX || vocab < 1 || vocab >= INT32_MAX || dim < 1 || dim > SS_MAX_DIM) return -1;
-  return ss::Workspace(n, dim).bytes;
+  // as much as any fewer positions need
+  return std::max(ss::Workspace(n, dim).bytes, ss::Workspace(std::min(n, ss::most_short(dim)), dim).bytes);
 }
 
 ss_status ss_embedding_grad(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype,

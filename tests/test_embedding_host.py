@@ -61,8 +61,10 @@ def test_workspace_sizes(ss):
     assert ss.ss_embedding_grad_workspace(1, 1, 1) > 0
     for bad in ((-1, 10, 10), (1 << 31, 10, 10), (5, 0, 10), (5, 10, 0), (5, 10, (1 << 24) + 1), (5, (1 << 31) - 1, 4)):
         assert ss.ss_embedding_grad_workspace(*bad) == -1
-    sizes = [ss.ss_embedding_grad_workspace(n, 1000, 64) for n in range(200)]
-    assert sizes == sorted(sizes)
+    for dim in (1, 64, 768, 4096, 8192):                    # one for n positions does for fewer
+        ns = sorted({*range(200), *(int(1.01 ** i) for i in range(2160)), *range(8000, 8400), 131071, 131072})
+        sizes = [ss.ss_embedding_grad_workspace(n, 1000, dim) for n in ns]
+        assert sizes == sorted(sizes)
 
 
 def test_binding_checks_tensors(ss):
