@@ -72,11 +72,11 @@ struct Raw8 {
       widen8<DT>(w[0], f);
     }
   }
-  __device__ __forceinline__ void add_to(float (&sum)[8]) const {
+  __device__ __forceinline__ void add_to(Pair (&sum)[4]) const {
     float f[8];
     unpack(f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += f[j];
+    for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], Pair::of(f[2 * j], f[2 * j + 1]));
   }
 };
 
@@ -174,14 +174,15 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 // token's positions stand together and in ascending order: that order is the order
 // of the sums. Every warp has a part of consecutive pairs. A pass counts each warp's
 // digits, turns the counts into places (by digit, then by warp) and moves the pairs
-// there, 32 at a time; the places of equal digits within them come from a match over
-// the lanes. Positions without a token (a negative id, or one past the vocabulary)
+// there, 32 at a time; the places of equal digits within them come from votes on
+// their bits. Positions without a token (a negative id, or one past the vocabulary)
 // go behind the last one.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBlocks = 8;
-constexpr int kAloneMost = 8192;  // positions that one block sorts alone
+constexpr int kSortLoads = 8;  // pairs that a lane has in flight
+constexpr int kAloneMost = 2048;  // positions that one block sorts alone
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 
@@ -239,7 +240,15 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
     auto digit_of = [&](uint64_t pair) { return static_cast<uint32_t>(pair >> (32 + shift)) & mask; };
     for (int d = lane; d < digits; d += 32) s.count[warp][d] = 0;
     __syncwarp();
-    for (int64_t i = first + lane; i < last; i += 32) atomicAdd(&s.count[warp][digit_of(pair_at(i))], 1u);
+    for (int64_t i = first + lane; i < last; i += 32 * kSortLoads) {
+      uint64_t pair[kSortLoads];
+#pragma unroll
+      for (int u = 0; u < kSortLoads; ++u)
+        if (i + 32 * u < last) pair[u] = pair_at(i + 32 * u);
+#pragma unroll
+      for (int u = 0; u < kSortLoads; ++u)
+        if (i + 32 * u < last) atomicAdd(&s.count[warp][digit_of(pair[u])], 1u);
+    }
     __syncthreads();
     if (tid < digits) {
       uint32_t sum = 0;
@@ -277,18 +286,28 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
       }
     }
     __syncthreads();
-    for (int64_t i = first; i < last; i += 32) {
-      const bool there = i + lane < last;
-      const uint64_t pair = there ? pair_at(i + lane) : 0u;
-      const uint32_t digit = there ? digit_of(pair) : kDigits;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
-      if (there) {
-        const uint32_t at = s.count[warp][digit] + __popc(same & ((1u << lane) - 1u));
-        to[at] = pair;
+    for (int64_t i = first + lane; i - lane < last; i += 32 * kSortLoads) {
+      uint64_t pair[kSortLoads];
+#pragma unroll
+      for (int u = 0; u < kSortLoads; ++u)
+        if (i + 32 * u < last) pair[u] = pair_at(i + 32 * u);
+#pragma unroll
+      for (int u = 0; u < kSortLoads; ++u) {
+        if (i - lane + 32 * u >= last) break;
+        const bool there = i + 32 * u < last;
+        const uint32_t digit = there ? digit_of(pair[u]) : 0u;
+        // the lanes of the same digit, bit by bit
+        unsigned same = __ballot_sync(0xFFFFFFFFu, there);
+        for (int bit = 0; bit < a.bits; ++bit) {
+          const bool set = (digit >> bit) & 1u;
+          const unsigned with = __ballot_sync(0xFFFFFFFFu, set);
+          same &= set ? with : ~with;
+        }
+        if (there) to[s.count[warp][digit] + __popc(same & ((1u << lane) - 1u))] = pair[u];
+        __syncwarp();
+        if (there && (same >> lane) == 1u) s.count[warp][digit] += __popc(same);  // the last of its digit
+        __syncwarp();
       }
-      __syncwarp();
-      if (there && (same >> lane) == 1u) s.count[warp][digit] += __popc(same);  // the last of its digit
-      __syncwarp();
     }
     // the pairs, and the reads of this block's totals, are over before the next pass begins in any block
     __threadfence();
@@ -301,18 +320,27 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
   const bool speaks = lane % run == run - 1;       // for its run
   auto over_runs = [&](const auto& f) {
     uint32_t before = first > 0 && first < last ? token_of(__ldcg(sorted + first - 1)) : ~0u;
-    for (int64_t i = first; i < last; i += 32) {
-      const uint32_t token = i + lane < n ? token_of(__ldcg(sorted + i + lane)) : ~0u;
-      const uint32_t behind = i + 32 < n ? token_of(__ldcg(sorted + i + 32)) : ~0u;
-      uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, token, 1), next = __shfl_down_sync(0xFFFFFFFFu, token, 1);
-      if (lane == 0) prev = before;
-      if (lane == 31) next = behind;
-      before = __shfl_sync(0xFFFFFFFFu, token, 31);
-      const unsigned begin = __ballot_sync(0xFFFFFFFFu, token < none && token != prev) & of_run;
-      const bool comes = __shfl_sync(0xFFFFFFFFu, token < none && token == prev, base);  // into the run
-      const bool goes = token < none && token == next;                                   // out of it
-      const bool starts = speaks && goes && begin, ends = speaks && comes && !(goes && !begin);
-      f(i, begin, starts, ends, __ballot_sync(0xFFFFFFFFu, starts));
+    auto token_at = [&](int64_t i) { return i < n ? token_of(__ldcg(sorted + i)) : ~0u; };
+    for (int64_t j = first; j < last; j += 32 * kSortLoads) {
+      uint32_t tokens[kSortLoads + 1];  // with the window behind
+#pragma unroll
+      for (int u = 0; u <= kSortLoads; ++u) tokens[u] = token_at(j + 32 * u + lane);
+#pragma unroll
+      for (int u = 0; u < kSortLoads; ++u) {
+        const int64_t i = j + 32 * u;
+        if (i >= last) break;
+        const uint32_t token = tokens[u];
+        const uint32_t behind = __shfl_sync(0xFFFFFFFFu, tokens[u + 1], 0);
+        uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, token, 1), next = __shfl_down_sync(0xFFFFFFFFu, token, 1);
+        if (lane == 0) prev = before;
+        if (lane == 31) next = behind;
+        before = __shfl_sync(0xFFFFFFFFu, token, 31);
+        const unsigned begin = __ballot_sync(0xFFFFFFFFu, token < none && token != prev) & of_run;
+        const bool comes = __shfl_sync(0xFFFFFFFFu, token < none && token == prev, base);  // into the run
+        const bool goes = token < none && token == next;                                   // out of it
+        const bool starts = speaks && goes && begin, ends = speaks && comes && !(goes && !begin);
+        f(i, begin, starts, ends, __ballot_sync(0xFFFFFFFFu, starts));
+      }
     }
   };
   uint32_t at = 0;
@@ -407,11 +435,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_fill_kernel(const __grid
 // do so of kGroup neighbouring runs adds these up, and the last of those the groups'
 // sums: the order of the sums is that of the positions whichever warp adds them.
 
-constexpr int kGroup = 16;
+constexpr int kGroup = 8;
 constexpr int kStages = 4;
 constexpr int kSumThreads = 256;
-constexpr int kVecs = 2;                   // groups of eight columns that a lane has
-constexpr int kSumPiece = kVecs * 32 * 8;  // columns that a warp takes at a time
+
+// Columns that a warp takes at a time, VECS groups of eight a lane. One where rows are short: 16384 x 768 61 us against
+// 67 (a third of the lanes idle with two); two where they are long: 65536 x 4096 299 us against 325.
+template <int VECS>
+constexpr int kSumPiece = VECS * 32 * 8;
+int vecs_of(int64_t dim) { return dim < 2048 ? 1 : 2; }
 
 struct SumArgs {
   const uint64_t* pairs;
@@ -425,15 +457,28 @@ struct SumArgs {
   float scale;
 };
 
+// A lane's columns of a piece: groups of eight, 32 * 8 apart.
+template <int VECS>
 struct Columns {
-  int from, dim, lane;
-  __device__ __forceinline__ int at(int u) const { return from + (u * 32 + lane) * 8; }
+  int from, dim;
+  __device__ __forceinline__ Columns(int piece, int dim_)
+      : from(piece * kSumPiece<VECS> + (threadIdx.x & 31) * 8), dim(dim_) {}
+  __device__ __forceinline__ int at(int u) const { return from + u * 256; }
+  __device__ __forceinline__ bool has(int u) const { return at(u) < dim; }
 };
+template <int VECS>
+using Sum = Pair[VECS][4];
 
-__device__ __forceinline__ void copy16(void* shared, const void* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
-               "l"(global)
-               : "memory");
+template <int VECS>
+__device__ __forceinline__ void clear(Sum<VECS>& sum) {
+#pragma unroll
+  for (int u = 0; u < VECS; ++u)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[u][j] = Pair::both(0.0f);
+}
+
+__device__ __forceinline__ void copy16(uint32_t shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared), "l"(global) : "memory");
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -441,153 +486,158 @@ __device__ __forceinline__ void wait_copies() {  // all but the latest N
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's columns of a row on their way to shared memory: group u of the lane at place(u), 16 bytes every 512.
-template <int DT, bool VEC>
-__device__ __forceinline__ void copy_row(char* shared, const char* row, const Columns& c) {
+// A lane's columns of a row on their way to `shared` (the lane's own 16 bytes of every 512). VEC: the row is on a 16-byte
+// boundary and has whole groups only.
+template <int DT, bool VEC, int VECS>
+__device__ __forceinline__ void copy_row(char* shared, const char* row, const Columns<VECS>& c) {
   constexpr int W = DT == SS_FP32 ? 2 : 1;
+  if constexpr (VEC) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(shared));
+    const char* from = row + static_cast<int64_t>(c.from) * static_cast<int>(sizeof(Elem<DT>));
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    const int e = c.at(u);
-    char* to = shared + u * W * 512 + c.lane * 16;
-    if (VEC && e + 8 <= c.dim) {
+    for (int u = 0; u < VECS; ++u)
+      if (c.has(u)) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) copy16(to + i * 512, row + static_cast<int64_t>(e) * sizeof(Elem<DT>) + i * 16);
-    } else if (e < c.dim) {
-      Raw8<DT> f;
-      f.template load<false>(row, e, c.dim);
+        for (int i = 0; i < W; ++i) copy16(to + (u * W + i) * 512, from + u * 256 * sizeof(Elem<DT>) + i * 16);
+      }
+  } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) *reinterpret_cast<uint4*>(to + i * 512) = f.w[i];
-    }
+    for (int u = 0; u < VECS; ++u)
+      if (c.has(u)) {
+        Raw8<DT> f;
+        f.template load<false>(row, c.at(u), c.dim);
+#pragma unroll
+        for (int i = 0; i < W; ++i) *reinterpret_cast<uint4*>(shared + (u * W + i) * 512) = f.w[i];
+      }
   }
 }
 template <int DT>
-__device__ __forceinline__ Raw8<DT> copied(const char* shared, int u, int lane) {
+__device__ __forceinline__ Raw8<DT> copied(const char* shared, int u) {
   constexpr int W = DT == SS_FP32 ? 2 : 1;
   Raw8<DT> f;
 #pragma unroll
-  for (int i = 0; i < W; ++i) f.w[i] = *reinterpret_cast<const uint4*>(shared + (u * W + i) * 512 + lane * 16);
+  for (int i = 0; i < W; ++i) f.w[i] = *reinterpret_cast<const uint4*>(shared + (u * W + i) * 512);
   return f;
 }
 
-// A token's row: its sum on `base`.
+// Eight columns of a token's row: their sum on the base's.
 template <bool VEC>
-__device__ __forceinline__ void put_row(const SumArgs& a, uint32_t token, const Columns& c, const float (&sum)[kVecs][8],
-                                        float (&base)[kVecs][8]) {
-  char* out = a.table.row(token);
+__device__ __forceinline__ void put_group(const SumArgs& a, char* out, int e, const Pair (&sum)[4], float (&base)[8]) {
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) base[u][j] = fmaf(sum[u][j], a.scale, base[u][j]);
-    if (c.at(u) < c.dim) store8<VEC>(a.table.dtype, out, c.at(u), c.dim, base[u]);
+  for (int j = 0; j < 4; ++j) {
+    const float2 s = sum[j].split();
+    base[2 * j] = fmaf(s.x, a.scale, base[2 * j]);
+    base[2 * j + 1] = fmaf(s.y, a.scale, base[2 * j + 1]);
   }
+  store8<VEC>(a.table.dtype, out, e, a.dim, base);
 }
 
-// The runs of a token that reaches into several.
-struct TokenRuns {
-  int first, last;
-  bool inside;  // it begins inside its first run
-
-  __device__ __forceinline__ int64_t slot(int run) const { return 2 * static_cast<int64_t>(run) + (run == first && inside); }
-};
-
-__device__ __forceinline__ void add_partial(const SumArgs& a, int64_t slot, const Columns& c, float (&sum)[kVecs][8]) {
-  const float* p = a.partial + slot * a.pitch;
+template <int VECS>
+__device__ __forceinline__ void add_partial(const float* p, const Columns<VECS>& c, Sum<VECS>& sum) {
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    const int e = c.at(u);
-    if (e < c.dim) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + e)), y = __ldcg(reinterpret_cast<const float4*>(p + e + 4));
-      const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum[u][j] += f[j];
+  for (int u = 0; u < VECS; ++u)
+    if (c.has(u)) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + c.at(u)));
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p + c.at(u) + 4));
+      sum[u][0] = add2(sum[u][0], Pair::of(x.x, x.y));
+      sum[u][1] = add2(sum[u][1], Pair::of(x.z, x.w));
+      sum[u][2] = add2(sum[u][2], Pair::of(y.x, y.y));
+      sum[u][3] = add2(sum[u][3], Pair::of(y.z, y.w));
     }
-  }
 }
-
-__device__ __forceinline__ void put_partial(const SumArgs& a, int64_t slot, const Columns& c, const float (&sum)[kVecs][8]) {
-  float* p = a.partial + slot * a.pitch;
+template <int VECS>
+__device__ __forceinline__ void put_partial(float* p, const Columns<VECS>& c, const Sum<VECS>& sum) {
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u)
-    if (c.at(u) < c.dim) store8<SS_FP32, true>(p, c.at(u), static_cast<int>(a.pitch), sum[u]);
+  for (int u = 0; u < VECS; ++u)
+    if (c.has(u)) {
+      float4* q = reinterpret_cast<float4*>(p + c.at(u));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 s = sum[u][2 * i].split(), t = sum[u][2 * i + 1].split();
+        q[i] = make_float4(s.x, s.y, t.x, t.y);
+      }
+    }
 }
 
-// Whether this warp is the last of `of` that arrive at a counter; what the others wrote before they did is then seen.
-__device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int of, int lane) {
-  __threadfence();
+// Whether this warp is the last of `of` that arrive at a counter; what the others wrote before they did is then seen: the
+// lanes' stores come before lane 0's release, its acquire before the lanes' loads.
+__device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int of) {
   __syncwarp();
   uint32_t before = 0;
-  if (lane == 0) before = atomicAdd(counter, 1u);
-  const bool last = __shfl_sync(0xFFFFFFFFu, before, 0) == static_cast<uint32_t>(of - 1);
-  __threadfence();
-  return last;
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  before = __shfl_sync(0xFFFFFFFFu, before, 0);
+  __syncwarp();
+  return before == static_cast<uint32_t>(of - 1);
 }
 
-__device__ __forceinline__ void clear(float (&sum)[kVecs][8]) {
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
-}
-
-// A run's sum of a token that reaches into others, on its way to the token's row. `number`: the token's among those.
-template <bool VEC>
-__device__ __forceinline__ void join_runs(const SumArgs& a, uint32_t token, int number, int run, int piece, const Columns& c,
-                                          float (&sum)[kVecs][8]) {
-  const int start = a.crossing.at[number];
-  const TokenRuns t = {start / a.run, a.crossing.last[number], start % a.run != 0};
-  put_partial(a, t.slot(run), c, sum);
+// A run's sum of a token that reaches into others, on its way to the token's row. `start`: the token's first sorted
+// position, `last`: its last run.
+template <bool VEC, int VECS>
+__device__ __forceinline__ void join_runs(const SumArgs& a, uint32_t token, int start, int last, int run, int piece,
+                                          Sum<VECS>& sum) {
+  const Columns<VECS> c(piece, a.dim);
+  const int first = start / a.run;
+  const bool inside = start % a.run != 0;  // the token begins inside its first run
+  auto slot = [&](int r) { return 2 * static_cast<int64_t>(r) + (r == first && inside); };
+  put_partial<VECS>(a.partial + slot(run) * a.pitch, c, sum);
   // this group's runs
-  const int lo = max(t.first, run / kGroup * kGroup), hi = min(t.last, run / kGroup * kGroup + kGroup - 1);
-  if (!last_to_arrive(a.arrived + t.slot(lo) * a.pieces + piece, hi - lo + 1, c.lane)) return;
-  clear(sum);
+  const int lo = max(first, run / kGroup * kGroup), hi = min(last, run / kGroup * kGroup + kGroup - 1);
+  if (!last_to_arrive(a.arrived + slot(lo) * a.pieces + piece, hi - lo + 1)) return;
+  clear<VECS>(sum);
 #pragma unroll 2
-  for (int r = lo; r <= hi; ++r) add_partial(a, t.slot(r), c, sum);
-  const int groups = t.last / kGroup - t.first / kGroup + 1;
+  for (int r = lo; r <= hi; ++r) add_partial<VECS>(a.partial + slot(r) * a.pitch, c, sum);
+  const int groups = last / kGroup - first / kGroup + 1;
   if (groups > 1) {
-    put_partial(a, t.slot(lo), c, sum);
-    if (!last_to_arrive(a.arrived + (2 * static_cast<int64_t>(a.runs) + t.slot(t.first)) * a.pieces + piece, groups, c.lane))
-      return;
-    clear(sum);
+    put_partial<VECS>(a.partial + slot(lo) * a.pitch, c, sum);
+    if (!last_to_arrive(a.arrived + (2 * static_cast<int64_t>(a.runs) + slot(first)) * a.pieces + piece, groups)) return;
+    clear<VECS>(sum);
 #pragma unroll 2
-    for (int g = t.first / kGroup; g <= t.last / kGroup; ++g) add_partial(a, t.slot(max(t.first, g * kGroup)), c, sum);
+    for (int g = first / kGroup; g <= last / kGroup; ++g)
+      add_partial<VECS>(a.partial + slot(max(first, g * kGroup)) * a.pitch, c, sum);
   }
-  float base[kVecs][8] = {};
-  if (a.base.data) {
-    const char* row = a.base.row(token);
+  char* out = a.table.row(token);
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      if (c.at(u) < c.dim) load8<VEC>(a.base.dtype, row, c.at(u), c.dim, base[u]);
-  }
-  put_row<VEC>(a, token, c, sum, base);
+  for (int u = 0; u < VECS; ++u)
+    if (c.has(u)) {
+      float base[8] = {};
+      if (a.base.data) load8<VEC>(a.base.dtype, a.base.row(token), c.at(u), c.dim, base);
+      put_group<VEC>(a, out, c.at(u), sum[u], base);
+    }
 }
 
 // A run of sorted positions as a warp sees it: lane i has the i-th one's token and row.
 struct RunView {
   uint32_t token;
   int32_t row;
-  int live;       // positions with a token
-  unsigned ends;  // bit i: the token of position i ends there
-  bool comes;     // the first token begins in an earlier run
+  int32_t cross;   // lanes 0, 1: first position and last run of the token that comes into the run; 2, 3: that goes out of it
+  int live;        // positions with a token
+  bool comes;      // the first token begins in an earlier run
+  unsigned ends;   // bit i: the token of position i ends there
+  unsigned whole;  // the same of tokens that are this run's alone
   int index, piece;
 
   // The loads, and what is made of them: apart, so that the next run's are on their way while this one is added.
   struct Loads {
     uint64_t pair, before, behind;
+    int32_t crossing;
   };
   __device__ __forceinline__ static Loads load(const SumArgs& a, int64_t item, int64_t items) {
     const int lane = threadIdx.x & 31;
-    Loads l = {~0ull, ~0ull, ~0ull};
+    Loads l = {~0ull, ~0ull, ~0ull, 0};
     if (item < items) {
-      const int64_t from = item / a.pieces * a.run, at = from + lane;
+      const int64_t r = item / a.pieces, from = r * a.run, at = from + lane;
       if (lane < a.run && at < a.n) l.pair = a.pairs[at];
       if (from > 0) l.before = a.pairs[from - 1];
       if (from + a.run < a.n) l.behind = a.pairs[from + a.run];
+      l.crossing = a.crossing.before[r];
     }
     return l;
   }
   __device__ __forceinline__ RunView(const SumArgs& a, const Loads& l, int64_t item)
       : token(token_of(l.pair)),
         row(static_cast<int32_t>(static_cast<uint32_t>(l.pair))),
+        cross(0),
         index(static_cast<int>(item / a.pieces)),
         piece(static_cast<int>(item - static_cast<int64_t>(index) * a.pieces)) {
     const int lane = threadIdx.x & 31;
@@ -596,90 +646,94 @@ struct RunView {
     if (lane == a.run - 1) next = token_of(l.behind);
     live = __popc(__ballot_sync(0xFFFFFFFFu, token < none));
     ends = __ballot_sync(0xFFFFFFFFu, token < none && token != next);
-    comes = __shfl_sync(0xFFFFFFFFu, token, 0) == token_of(l.before);
-  }
-  // Whether position i is the last of a token that is this run's alone.
-  __device__ __forceinline__ bool completes(int i) const {
-    return ((ends >> i) & 1u) && !(comes && (ends & ((1u << i) - 1u)) == 0u);
+    comes = live > 0 && __shfl_sync(0xFFFFFFFFu, token, 0) == token_of(l.before);
+    const bool goes = live > 0 && !((ends >> (live - 1)) & 1u);
+    whole = comes ? ends & (ends - 1u) : ends;
+    // (a token that comes and goes is the one that came)
+    if (lane < 2 ? comes : (lane < 4 && goes && !(comes && ends == 0u)))
+      cross = (lane & 1 ? a.crossing.last : a.crossing.at)[l.crossing - (lane < 2 ? 1 : 0)];
   }
 };
 
-template <int DT, bool VEC, bool TVEC>
+template <int DT, bool VEC, bool TVEC, int VECS>
 __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_constant__ SumArgs a) {
   extern __shared__ __align__(16) char shared[];
   pdl_wait();
   pdl_trigger();
-  constexpr int kRowBytes = kSumPiece * sizeof(Elem<DT>);
+  constexpr int kRowBytes = kSumPiece<VECS> * sizeof(Elem<DT>);
   const int lane = threadIdx.x & 31;
-  char* stages = shared + (threadIdx.x >> 5) * kStages * a.stage_bytes;
+  const int ring = kStages * a.stage_bytes;
+  char* stages = shared + (threadIdx.x >> 5) * ring + lane * 16;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kSumThreads / 32);
   const int64_t items = static_cast<int64_t>(a.runs) * a.pieces;
+  const int64_t d_pitch = a.d_out.ld * static_cast<int>(sizeof(Elem<DT>));
   int64_t item = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5);
   if (item >= items) return;
-  auto issue = [&](const RunView& v, int i, int stage) {
+  int put = 0, get = 0;  // the stages' places in the ring
+  auto forth = [&](int at) { return at + a.stage_bytes == ring ? 0 : at + a.stage_bytes; };
+  auto issue = [&](const RunView& v, int i) {
     if (i < v.live) {
-      const Columns c = {v.piece * kSumPiece, a.dim, lane};
-      char* to = stages + stage * a.stage_bytes;
-      copy_row<DT, VEC>(to, a.d_out.row(__shfl_sync(0xFFFFFFFFu, v.row, i)), c);
-      if (a.base.data && v.completes(i)) {
+      const Columns<VECS> c(v.piece, a.dim);
+      copy_row<DT, VEC>(stages + put, static_cast<const char*>(a.d_out.data) + __shfl_sync(0xFFFFFFFFu, v.row, i) * d_pitch, c);
+      if (a.base.data && ((v.whole >> i) & 1u)) {
         const char* base = a.base.row(__shfl_sync(0xFFFFFFFFu, v.token, i));
-        if (a.base.dtype == SS_FP32) copy_row<SS_FP32, TVEC>(to + kRowBytes, base, c);
-        else copy_row<SS_BF16, TVEC>(to + kRowBytes, base, c);  // the bits, of either 16-bit type
+        if (a.base.dtype == SS_FP32) copy_row<SS_FP32, TVEC>(stages + put + kRowBytes, base, c);
+        else copy_row<SS_BF16, TVEC>(stages + put + kRowBytes, base, c);  // the bits, of either 16-bit type
       }
     }
     commit_copies();
+    put = forth(put);
   };
   RunView now(a, RunView::load(a, item, items), item);
   RunView::Loads ahead = RunView::load(a, item + warps, items);
-  int stage = 0;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(now, i, i);
+  for (int i = 0; i < kStages - 1; ++i) issue(now, i);
   while (true) {
     // a run of fewer positions than stages has empty groups of copies behind it
     const int steps = max(now.live, kStages - 1);
     const RunView next(a, ahead, item + warps);
     ahead = RunView::load(a, item + 2 * warps, items);
-    const bool more = item + warps < items;
-    const Columns c = {now.piece * kSumPiece, a.dim, lane};
-    float sum[kVecs][8];
-    clear(sum);
+    const Columns<VECS> c(now.piece, a.dim);
+    Sum<VECS> sum;
+    clear<VECS>(sum);
+#pragma unroll 1
     for (int i = 0; i < steps; ++i) {
-      const int ahead_i = i + kStages - 1, to = (stage + kStages - 1) % kStages;
-      if (ahead_i < steps) issue(now, ahead_i, to);
-      else if (more) issue(next, ahead_i - steps, to);
-      else commit_copies();
+      const int i_ahead = i + kStages - 1;
+      if (i_ahead < steps) issue(now, i_ahead);
+      else issue(next, i_ahead - steps);  // nothing, behind the last run
       wait_copies<kStages - 1>();
-      const char* from = stages + stage * a.stage_bytes;
-      stage = (stage + 1) % kStages;
+      const char* from = stages + get;
+      get = forth(get);
       if (i >= now.live) continue;
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-        if (c.at(u) < c.dim) copied<DT>(from, u, lane).add_to(sum[u]);
+      for (int u = 0; u < VECS; ++u)
+        if (c.has(u)) copied<DT>(from, u).add_to(sum[u]);
       const bool ends = (now.ends >> i) & 1u;
       if (!ends && i + 1 < now.live) continue;
       const uint32_t token = __shfl_sync(0xFFFFFFFFu, now.token, i);
-      if (now.completes(i)) {
-        float base[kVecs][8] = {};
-        if (a.base.data) {
+      if ((now.whole >> i) & 1u) {
+        char* out = a.table.row(token);
 #pragma unroll
-          for (int u = 0; u < kVecs; ++u) {
-            if (c.at(u) >= c.dim) continue;
-            if (a.base.dtype == SS_FP32) copied<SS_FP32>(from + kRowBytes, u, lane).unpack(base[u]);
-            else if (a.base.dtype == SS_BF16) copied<SS_BF16>(from + kRowBytes, u, lane).unpack(base[u]);
-            else copied<SS_FP16>(from + kRowBytes, u, lane).unpack(base[u]);
+        for (int u = 0; u < VECS; ++u)
+          if (c.has(u)) {
+            float base[8] = {};
+            if (a.base.data) {
+              if (a.base.dtype == SS_FP32) copied<SS_FP32>(from + kRowBytes, u).unpack(base);
+              else if (a.base.dtype == SS_BF16) copied<SS_BF16>(from + kRowBytes, u).unpack(base);
+              else copied<SS_FP16>(from + kRowBytes, u).unpack(base);
+            }
+            put_group<TVEC>(a, out, c.at(u), sum[u], base);
           }
-        }
-        put_row<TVEC>(a, token, c, sum, base);
       } else {
-        // the run's first token is the last that began before it
-        const bool first = now.comes && (now.ends & ((1u << i) - 1u)) == 0u;
-        join_runs<TVEC>(a, token, a.crossing.before[now.index] - (first ? 1 : 0), now.index, now.piece, c, sum);
+        const int which = now.comes && (now.ends & ((1u << i) - 1u)) == 0u ? 0 : 2;  // the run's first token, or its last
+        join_runs<TVEC, VECS>(a, token, __shfl_sync(0xFFFFFFFFu, now.cross, which), __shfl_sync(0xFFFFFFFFu, now.cross, which + 1),
+                        now.index, now.piece, sum);
       }
-      clear(sum);
+      clear<VECS>(sum);
     }
-    if (!more) break;
-    now = next;
     item += warps;
+    if (item >= items) break;
+    now = next;
   }
 }
 
@@ -688,9 +742,13 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
 int64_t pitch_of(int64_t dim) { return (dim + 7) / 8 * 8; }
 int pieces_of(int64_t dim, int piece) { return static_cast<int>((dim + piece - 1) / piece); }
 
-// Positions of a run: short ones where there are few, so that there are warps enough.
-int64_t most_short(int64_t dim) { return (4096 + pieces_of(dim, kSumPiece) - 1) / pieces_of(dim, kSumPiece) * 32 - 1; }
-int run_of(int64_t n, int64_t dim) { return n <= most_short(dim) ? 8 : 32; }
+int sum_pieces_of(int64_t dim) { return pieces_of(dim, vecs_of(dim) == 1 ? kSumPiece<1> : kSumPiece<2>); }
+
+// Positions of a run. Short runs give warps enough where there are few positions, long ones leave fewer sums to be joined.
+// 8, 16, 32: 1013 x 768 24.4, 25.7, 30.0 us; 4096 x 768 35.3, 36.1, 39.2; 16384 x 768 (on a base) 60.7, 55.0, 63.0;
+// 65536 x 256 74.5, 64.8, 62.0; 65536 x 4096 446, 350, 309 (with groups of 16 runs, not 8).
+constexpr int64_t kShortMost = 8191, kMiddleMost = 32767;
+int run_of(int64_t n) { return n <= kShortMost ? 8 : (n <= kMiddleMost ? 16 : 32); }
 
 // The workspace's parts, each on a 16-byte boundary: where they begin, and its bytes (-1: more than int64 holds).
 struct Workspace {
@@ -698,9 +756,9 @@ struct Workspace {
   int64_t pairs[2], before, at, last, arrived, partial, bytes;
 
   Workspace(int64_t n, int64_t dim) {
-    run = run_of(n, dim);
+    run = run_of(n);
     runs = (n + run - 1) / run;
-    n_arrived = 4 * runs * pieces_of(dim, kSumPiece);
+    n_arrived = 4 * runs * sum_pieces_of(dim);
     __int128 end = 0;
     const auto take = [&](__int128 size) {
       const __int128 from = end;
@@ -776,17 +834,15 @@ ss_status lookup_impl(const ss_table* t, const void* ids, ss_idtype idtype, int6
   return launch(fn, grid_for(reinterpret_cast<const void*>(fn), n * a.pieces * 32), a, stream);
 }
 
-template <int DT>
+template <int DT, int VECS>
 auto pick_sum(bool vec, bool tvec) {
-  return vec ? (tvec ? sum_kernel<DT, true, true> : sum_kernel<DT, true, false>)
-             : (tvec ? sum_kernel<DT, false, true> : sum_kernel<DT, false, false>);
+  return vec ? (tvec ? sum_kernel<DT, true, true, VECS> : sum_kernel<DT, true, false, VECS>)
+             : (tvec ? sum_kernel<DT, false, true, VECS> : sum_kernel<DT, false, false, VECS>);
 }
-
-// Shared memory past 48 KB has to be asked for, once a device.
-template <typename Fn>
-ss_status allow_shared(Fn* fn, size_t bytes) {
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  return e == cudaSuccess ? SS_OK : cuda_fail(e);
+template <int VECS>
+auto pick_sum(int32_t dtype, bool vec, bool tvec) {
+  return dtype == SS_BF16 ? pick_sum<SS_BF16, VECS>(vec, tvec)
+                          : (dtype == SS_FP16 ? pick_sum<SS_FP16, VECS>(vec, tvec) : pick_sum<SS_FP32, VECS>(vec, tvec));
 }
 
 ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype, int64_t n,
@@ -827,7 +883,8 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   const int32_t dim = static_cast<int32_t>(t->dim);
   const Rows table = {t->data, t->ld, t->dtype};
   const Rows from = base ? Rows{base->data, base->ld, base->dtype} : Rows{nullptr, 0, SS_FP32};
-  const bool tvec = aligned_rows(table) && (!base || aligned_rows(from));
+  const bool groups = dim % 8 == 0;
+  const bool tvec = groups && aligned_rows(table) && (!base || aligned_rows(from));
   SortFillArgs sf = {};
   char* w = static_cast<char*>(workspace);
   if (n > 0) {
@@ -848,14 +905,13 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   const int fill_clusters = in_place ? 0 : std::max(1, 2 * sm_count() / cluster);
   st = launch_rows(sort_fill, 1 + fill_clusters, cluster, kSortThreads, sizeof(SortShared), sf, stream);
   if (st != SS_OK || n == 0) return st;
-  const int stage_bytes = kSumPiece * static_cast<int>(dtype_bytes(d_dtype) + (base ? dtype_bytes(base->dtype) : 0));
+  const int stage_bytes = (vecs_of(dim) == 1 ? kSumPiece<1> : kSumPiece<2>) * static_cast<int>(dtype_bytes(d_dtype) + (base ? dtype_bytes(base->dtype) : 0));
   const SumArgs a = {sf.sort.pairs[sf.sort.passes & 1 ? 0 : 1], sf.sort.crossing, sf.sort.arrived,
                      reinterpret_cast<float*>(w + ws.partial), {const_cast<void*>(d_out), d_ld, d_dtype}, from, table,
                      pitch_of(dim), t->vocab, static_cast<int32_t>(n), static_cast<int32_t>(ws.run),
-                     static_cast<int32_t>(ws.runs), dim, pieces_of(dim, kSumPiece), stage_bytes, scale};
-  const bool vec = aligned_rows(a.d_out);
-  auto* fn = d_dtype == SS_BF16 ? pick_sum<SS_BF16>(vec, tvec)
-                                : (d_dtype == SS_FP16 ? pick_sum<SS_FP16>(vec, tvec) : pick_sum<SS_FP32>(vec, tvec));
+                     static_cast<int32_t>(ws.runs), dim, sum_pieces_of(dim), stage_bytes, scale};
+  const bool vec = groups && aligned_rows(a.d_out);
+  auto* fn = vecs_of(dim) == 1 ? pick_sum<1>(d_dtype, vec, tvec) : pick_sum<2>(d_dtype, vec, tvec);
   const size_t smem = static_cast<size_t>(stage_bytes) * kStages * (kSumThreads / 32);
   st = allow_shared(fn, smem);
   if (st != SS_OK) return st;
@@ -880,7 +936,8 @@ ss_status ss_embedding(const ss_table* table, const void* ids, ss_idtype idtype,
 int64_t ss_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
   if (n < 0 || n > INT32_MAX || vocab < 1 || vocab >= INT32_MAX || dim < 1 || dim > SS_MAX_DIM) return -1;
   // as much as any fewer positions need
-  return std::max(ss::Workspace(n, dim).bytes, ss::Workspace(std::min(n, ss::most_short(dim)), dim).bytes);
+  const auto bytes = [&](int64_t most) { return ss::Workspace(std::min(n, most), dim).bytes; };
+  return std::max({bytes(n), bytes(ss::kShortMost), bytes(ss::kMiddleMost)});
 }
 
 ss_status ss_embedding_grad(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype,

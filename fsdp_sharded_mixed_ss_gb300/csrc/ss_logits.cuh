@@ -714,6 +714,14 @@ inline int split_for(int64_t nvec, int vectors) {
   return static_cast<int>(split);
 }
 
+// Dynamic shared memory past 48 KB has to be asked for.
+template <typename Fn>
+ss_status allow_shared(Fn* fn, size_t bytes) {
+  if (bytes <= 48 * 1024) return SS_OK;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  return e == cudaSuccess ? SS_OK : cuda_fail(e);
+}
+
 // Launches `clusters` clusters of `cluster` blocks (a plain launch for 1).
 template <typename Args>
 ss_status launch_rows(void (*fn)(Args), int64_t clusters, int cluster, int threads, size_t smem, const Args& args,

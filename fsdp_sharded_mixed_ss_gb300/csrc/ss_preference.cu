@@ -5,8 +5,6 @@
 namespace ss {
 namespace {
 
-constexpr int kMaxThreads = 512;
-
 struct PreferenceArgs {
   const float* logprob;
   const float* ref;
@@ -22,26 +20,36 @@ struct PreferenceArgs {
   bool wide, halves, average;
 };
 
-// A sequence's weighted sum, as a pair (thousands of log ratios cancel against those of the other answer), and the
-// weights' sum.
+// Pairs of fp32. Once hi is infinite or NaN, lo is not used.
+__device__ __forceinline__ dd clean(dd a) { return finite(a.hi) ? a : dd{a.hi, 0.0f}; }
+__device__ __forceinline__ dd plus(dd a, float b) {
+  const dd t = two_sum(a.hi, b);
+  return {t.hi, t.lo + a.lo};
+}
+__device__ __forceinline__ dd plus(dd a, dd b) {
+  const dd t = two_sum(a.hi, b.hi);
+  return {t.hi, t.lo + (a.lo + b.lo)};
+}
+__device__ __forceinline__ dd times(dd a, float b) {
+  const dd t = two_prod(a.hi, b);
+  return clean({t.hi, fmaf(a.lo, b, t.lo)});
+}
+__device__ __forceinline__ dd over(dd a, dd b) {
+  const float q = a.hi / b.hi;
+  return clean({q, (fmaf(-q, b.hi, a.hi) + fmaf(-q, b.lo, a.lo)) / b.hi});
+}
+
+// A sequence's weighted sum (thousands of log ratios cancel against those of the other answer), and the weights' sum.
 struct SeqSum {
   dd s, w;
 
-  // lo is NaN once hi is infinite or NaN, and then not used
-  __device__ __forceinline__ static void add(dd& a, dd b) {
-    const dd t = two_sum(a.hi, b.hi);
-    a = {t.hi, t.lo + (a.lo + b.lo)};
-  }
   __device__ __forceinline__ void add(const SeqSum& o) {
-    add(s, o.s);
-    add(w, o.w);
+    s = plus(s, o.s);
+    w = plus(w, o.w);
   }
   __device__ __forceinline__ SeqSum from_lane(int off) const {
     return {{__shfl_xor_sync(0xFFFFFFFFu, s.hi, off), __shfl_xor_sync(0xFFFFFFFFu, s.lo, off)},
             {__shfl_xor_sync(0xFFFFFFFFu, w.hi, off), __shfl_xor_sync(0xFFFFFFFFu, w.lo, off)}};
-  }
-  __device__ __forceinline__ static double value(dd a) {
-    return finite(a.hi) ? static_cast<double>(a.hi) + static_cast<double>(a.lo) : static_cast<double>(a.hi);
   }
 };
 
@@ -49,35 +57,46 @@ struct Span {
   int64_t lo, hi;
 };
 
-constexpr int kTokens = 4;  // of a thread in flight
+constexpr int kTokens = 8;  // of a thread in flight
 
-// f(i, step) over block `rank`'s of `size` parts of a sequence: the thread's tokens i, i + step, ... below q.hi, kTokens
-// of them a call.
-template <class F>
-__device__ __forceinline__ void over_tokens(const Span& q, unsigned rank, unsigned size, const F& f) {
-  const int64_t step = static_cast<int64_t>(size) * blockDim.x;
-  for (int64_t i = q.lo + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; i < q.hi; i += kTokens * step) f(i, step);
+// f(i, n) over block `rank`'s of `size` shares of a sequence, for HALF threads of which this is number t: its tokens i, i +
+// HALF, ..., n of them: kTokens, but for the last. (Places at a constant distance: with the distance a variable the
+// addresses took more instructions than the sums.)
+template <int HALF, class F>
+__device__ __forceinline__ void over_tokens(const Span& q, unsigned rank, unsigned size, int t, const F& f) {
+  constexpr int64_t kShare = HALF * kTokens;
+  int64_t at = q.lo + rank * kShare;
+  for (; at + kShare <= q.hi; at += size * kShare) f(at + t, kTokens);
+  if (at < q.hi) f(at + t, static_cast<int>((q.hi - at - t + HALF - 1) / HALF));
 }
 
-// A block of `blockDim.x` threads a pair, or the blocks of a cluster: the two sums, the pair's loss, and its derivative
-// to every token.
-__global__ void __launch_bounds__(kMaxThreads) preference_kernel(const __grid_constant__ PreferenceArgs a) {
-  __shared__ SeqSum red[2][kMaxThreads / 32];
+__device__ __forceinline__ float sum8(const float (&v)[kTokens]) {
+  static_assert(kTokens == 8, "three levels");
+  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+// A block of 2 HALF threads a pair, or the blocks of a cluster: half of each has the chosen sequence, the other the
+// rejected one. Their sums, the pair's loss, and its derivative to every token. A thread's eight terms at a time are added
+// in fp32, the rest as pairs.
+template <int HALF>
+__global__ void __launch_bounds__(2 * HALF) preference_kernel(const __grid_constant__ PreferenceArgs a) {
+  __shared__ SeqSum red[HALF / 16];
   __shared__ SeqSum parts[2][kMaxCluster];
   __shared__ float slope[2];
   const Cluster cl = Cluster::start();
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+  const int tid = threadIdx.x, k = tid < HALF ? 0 : 1, t = tid - k * HALF;
   const int64_t pair = blockIdx.x / cl.size;
   const int64_t seq[2] = {a.halves ? pair : 2 * pair, a.halves ? a.pairs + pair : 2 * pair + 1};
-  Span at[2];
+  Span spans[2];
   bool bad = false;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    at[k] = {load_id(a.offsets, seq[k], a.wide), load_id(a.offsets, seq[k] + 1, a.wide)};
-    bad = bad || at[k].lo < 0 || at[k].hi < at[k].lo || at[k].hi > a.rows;
+  for (int q = 0; q < 2; ++q) {
+    spans[q] = {load_id(a.offsets, seq[q], a.wide), load_id(a.offsets, seq[q] + 1, a.wide)};
+    bad = bad || spans[q].lo < 0 || spans[q].hi < spans[q].lo || spans[q].hi > a.rows;
   }
+  const Span at = k == 0 ? spans[0] : spans[1];
   const float wp = a.pair_weight ? a.pair_weight[pair] : 1.0f;
   cl.started();
   if (bad || wp == 0.0f) {  // the same in all blocks of the cluster
@@ -86,58 +105,58 @@ __global__ void __launch_bounds__(kMaxThreads) preference_kernel(const __grid_co
       if (a.loss) a.loss[pair] = v;
       if (a.reward) a.reward[pair] = make_float2(v, v);
     }
-    if (!bad && a.d) {
+    if (!bad && a.d)
+      over_tokens<HALF>(at, cl.rank, cl.size, t, [&](int64_t i, int n) {
+        float* d = a.d + i;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step) {
-#pragma unroll
-          for (int u = 0; u < kTokens; ++u)
-            if (i + u * step < at[k].hi) a.d[i + u * step] = 0.0f;
-        });
-    }
+        for (int u = 0; u < kTokens; ++u)
+          if (u < n) d[u * HALF] = 0.0f;
+      });
     return;
   }
+  SeqSum mine = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+  over_tokens<HALF>(at, cl.rank, cl.size, t, [&](int64_t i, int n) {
+    const float *lp = a.logprob + i, *ref = a.ref + i, *weight = a.weight + i;
+    float v[kTokens], r[kTokens], w[kTokens];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    SeqSum sum = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-    over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step) {
-      float lp[kTokens], ref[kTokens], w[kTokens];
+    for (int u = 0; u < kTokens; ++u) {
+      v[u] = u < n ? lp[u * HALF] : 0.0f;
+      r[u] = u < n && a.ref ? ref[u * HALF] : 0.0f;
+      w[u] = u < n ? (a.weight ? weight[u * HALF] : 1.0f) : 0.0f;
+    }
 #pragma unroll
-      for (int u = 0; u < kTokens; ++u) {
-        const bool there = i + u * step < at[k].hi;
-        lp[u] = there ? a.logprob[i + u * step] : 0.0f;
-        ref[u] = there && a.ref ? a.ref[i + u * step] : 0.0f;
-        w[u] = !there ? 0.0f : (a.weight ? a.weight[i + u * step] : 1.0f);
-      }
+    for (int u = 0; u < kTokens; ++u)  // nothing of a token of weight 0, whatever its log probability
+      v[u] = w[u] == 0.0f ? 0.0f : w[u] * (v[u] - r[u]);
+    mine.s = plus(mine.s, sum8(v));
+    if (a.average) mine.w = plus(mine.w, sum8(w));
+  });
 #pragma unroll
-      for (int u = 0; u < kTokens; ++u) {
-        if (w[u] == 0.0f) continue;  // whatever the token's log probability
-        SeqSum::add(sum.s, {w[u] * (lp[u] - ref[u]), 0.0f});
-        SeqSum::add(sum.w, {w[u], 0.0f});
-      }
-    });
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum.add(sum.from_lane(off));
-    if (lane == 0) red[k][tid >> 5] = sum;
-  }
+  for (int off = 16; off > 0; off >>= 1) mine.add(mine.from_lane(off));
+  if ((tid & 31) == 0) red[tid >> 5] = mine;
   __syncthreads();
-  if (tid < 2) {  // one thread a sequence
-    SeqSum sum = red[tid][0];
-    for (int i = 1; i < warps; ++i) sum.add(red[tid][i]);
-    for (unsigned r = 0; r < cl.size; ++r) cl.at(&parts[tid][0], r)[cl.rank] = sum;
+  if (t == 0) {  // one thread a sequence
+#pragma unroll
+    for (int i = 1; i < HALF / 32; ++i) mine.add(red[(tid >> 5) + i]);
+    for (unsigned r = 0; r < cl.size; ++r) cl.at(&parts[k][0], r)[cl.rank] = mine;
   }
   cl.sync();
   if (tid == 0) {
-    double score[2], per[2];
+    dd score[2];
+    float per[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      SeqSum sum = parts[k][0];
-      for (unsigned r = 1; r < cl.size; ++r) sum.add(parts[k][r]);
-      const double w = SeqSum::value(sum.w);
-      per[k] = !a.average ? 1.0 : (w == 0.0 ? 0.0 : 1.0 / w);
-      score[k] = SeqSum::value(sum.s) * per[k];
+    for (int q = 0; q < 2; ++q) {
+      SeqSum sum = parts[q][0];
+      for (unsigned r = 1; r < cl.size; ++r) sum.add(parts[q][r]);
+      score[q] = clean(sum.s);
+      per[q] = 1.0f;
+      if (a.average) {
+        const bool none = sum.w.hi == 0.0f;
+        score[q] = none ? dd{0.0f, 0.0f} : over(score[q], sum.w);
+        per[q] = none ? 0.0f : 1.0f / (sum.w.hi + sum.w.lo);
+      }
     }
-    const float h = static_cast<float>(static_cast<double>(a.beta) * (score[0] - score[1]) - a.margin);
+    const dd far = plus(times(clean(plus(score[0], dd{-score[1].hi, -score[1].lo})), a.beta), -a.margin);
+    const float h = finite(far.hi) ? far.hi + far.lo : far.hi;
     float loss, d_h;
     if (a.kind == SS_PREF_SIGMOID) {
       const float e = expf(-fabsf(h)), soft = log1pf(e);
@@ -153,28 +172,30 @@ __global__ void __launch_bounds__(kMaxThreads) preference_kernel(const __grid_co
       d_h = 2.0f * q / a.beta;
     }
     if (!(h == h)) loss = d_h = nan_f();
-    slope[0] = static_cast<float>(static_cast<double>(wp * d_h) * a.beta * per[0]);
-    slope[1] = static_cast<float>(-static_cast<double>(wp * d_h) * a.beta * per[1]);
+    const float up = wp * d_h * a.beta;
+    slope[0] = up * per[0];
+    slope[1] = -up * per[1];
     if (cl.rank == 0) {
       if (a.loss) a.loss[pair] = wp * loss;
-      if (a.reward)
-        a.reward[pair] = make_float2(static_cast<float>(a.beta * score[0]), static_cast<float>(a.beta * score[1]));
+      if (a.reward) {
+        const dd c = times(score[0], a.beta), r = times(score[1], a.beta);
+        a.reward[pair] = make_float2(c.hi + c.lo, r.hi + r.lo);
+      }
     }
   }
   if (!a.d) return;
   __syncthreads();
+  const float g = slope[k];
+  over_tokens<HALF>(at, cl.rank, cl.size, t, [&](int64_t i, int n) {
+    const float* weight = a.weight + i;
+    float* d = a.d + i;
+    float w[kTokens];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float g = slope[k];
-    over_tokens(at[k], cl.rank, cl.size, [&](int64_t i, int64_t step) {
-      float w[kTokens];
+    for (int u = 0; u < kTokens; ++u) w[u] = u < n && a.weight ? weight[u * HALF] : 1.0f;
 #pragma unroll
-      for (int u = 0; u < kTokens; ++u) w[u] = a.weight && i + u * step < at[k].hi ? a.weight[i + u * step] : 1.0f;
-#pragma unroll
-      for (int u = 0; u < kTokens; ++u)
-        if (i + u * step < at[k].hi) a.d[i + u * step] = w[u] == 0.0f ? 0.0f : w[u] * g;
-    });
-  }
+    for (int u = 0; u < kTokens; ++u)
+      if (u < n) d[u * HALF] = w[u] == 0.0f ? 0.0f : w[u] * g;
+  });
 }
 
 ss_status preference_impl(const float* logprob, int64_t rows, const ss_preference* p, int64_t pairs, float* loss,
@@ -204,14 +225,14 @@ ss_status preference_impl(const float* logprob, int64_t rows, const ss_preferenc
   const PreferenceArgs a = {logprob, p->ref_logprob, p->row_weight, p->pair_weight, p->offsets, loss,
                             reinterpret_cast<float2*>(reward), d_logprob, rows, pairs, p->beta, p->margin,
                             p->label_smoothing, p->kind, p->idtype == SS_I64, p->halves != 0, p->average != 0};
-  // threads and blocks by the tokens of a pair, on average: eight of each sequence a thread
+  // threads and blocks by the tokens of a pair, on average
   const int64_t each = rows / pairs;
-  int threads = 64;
-  while (threads < kMaxThreads && each > 16 * threads) threads *= 2;
+  const int threads = each <= 512 ? 64 : (each <= 8192 ? 128 : 512);
   int cluster = 1;
   while (cluster < kMaxCluster && each > 16 * cluster * threads && pairs * cluster * threads * 2 <= 1024 * sm_count())
     cluster *= 2;
-  return launch_rows(preference_kernel, pairs, cluster, threads, 0, a, stream);
+  auto* fn = threads == 64 ? preference_kernel<32> : (threads == 128 ? preference_kernel<64> : preference_kernel<256>);
+  return launch_rows(fn, pairs, cluster, threads, 0, a, stream);
 }
 
 }  // namespace

@@ -1,8 +1,10 @@
 """Plain float64 form of the preference loss, pair by pair in numpy, and bounds of the fp32 kernel's errors.
 
-Bounds. A term w (lp - ref) rounds twice, 2^-24 each; the sums of pairs of fp32 add nothing that counts. With S the sum of
-the terms' absolute values a score is within 2^-23 S (divided by the weights' sum where it is a mean), h within beta times
-both scores' bounds, and its own rounding. The loss follows with its slope, its derivative with its curvature; exp, log1p,
+Bounds. A term w (lp - ref) rounds twice, 2^-24 each; eight of them are added in fp32 by three levels of sums, which round
+each term's share three times more; the sums of pairs of fp32 above add nothing that counts. With S the sum of the terms'
+absolute values a score is within 5 * 2^-24 S. The weights' sum is within 3 * 2^-24 of its own, so a mean (of weights that
+are not negative) within 9 * 2^-24 S over the weights' sum, with the quotient's rounding. h is within beta times both
+scores' bounds, and its own rounding. The loss follows with its slope, its derivative with its curvature; exp, log1p,
 the divisions and products round at most eight times.
 """
 import numpy as np
@@ -45,7 +47,7 @@ def preference(lp, offsets, *, ref=None, weight=None, pair_weight=None, kind="si
             total = w[a:b][on].sum()
             p = 1.0 if not average else (1.0 / total if total != 0 else 0.0)
             score.append(t.sum() * p if len(t) else 0.0)
-            err.append((2.0 ** -23 * np.abs(t).sum() + 1e-37) * abs(p))
+            err.append(((9 if average else 5) * 2.0 ** -24 * np.abs(t).sum() + 1e-37) * abs(p))
             per.append(p)
         with np.errstate(invalid="ignore"):
             h = beta * (score[0] - score[1]) - margin
