@@ -14,14 +14,14 @@ __device__ __forceinline__ void load8(const void* row, int e, int dim, float (&f
   const Elem<DT>* p = static_cast<const Elem<DT>*>(row) + e;
   if (VEC && e + 8 <= dim) {
     if constexpr (DT == SS_FP32) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
       f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     } else {
-      widen8<DT>(*reinterpret_cast<const uint4*>(p), f);
+      widen8<DT>(__ldcg(reinterpret_cast<const uint4*>(p)), f);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = e + j < dim ? to_float<DT>(p[j]) : 0.0f;
+    for (int j = 0; j < 8; ++j) f[j] = e + j < dim ? to_float<DT>(__ldcg(p + j)) : 0.0f;
   }
 }
 
@@ -89,6 +89,17 @@ __device__ __forceinline__ void store8(int dt, void* row, int e, int dim, const 
   if (dt == SS_BF16) store8<SS_BF16, VEC>(row, e, dim, f);
   else if (dt == SS_FP16) store8<SS_FP16, VEC>(row, e, dim, f);
   else store8<SS_FP32, VEC>(row, e, dim, f);
+}
+
+// One element.
+__device__ __forceinline__ float load1(int dt, const void* row, int e) {
+  if (dt == SS_FP32) return static_cast<const float*>(row)[e];
+  const uint16_t h = static_cast<const uint16_t*>(row)[e];
+  return dt == SS_BF16 ? widen1<SS_BF16>(h) : widen1<SS_FP16>(h);
+}
+__device__ __forceinline__ void put1(int dt, void* row, int e, float f) {
+  if (dt == SS_FP32) static_cast<float*>(row)[e] = f;
+  else static_cast<uint16_t*>(row)[e] = dt == SS_BF16 ? narrow1<SS_BF16>(f) : narrow1<SS_FP16>(f);
 }
 
 struct Rows {
@@ -179,7 +190,6 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBlocks = 8;
 constexpr int kSortLoads = 8;  // pairs that a lane has in flight
-constexpr int kAloneMost = 2048;  // positions that one block sorts alone
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 
@@ -216,7 +226,7 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n;
   // this warp's part
-  const int64_t warps = static_cast<int64_t>(cl.size) * kSortWarps;
+  constexpr int64_t warps = kSortBlocks * kSortWarps;
   const int64_t each = (n + warps * 32 - 1) / (warps * 32) * 32;
   const int64_t first = (static_cast<int64_t>(cl.rank) * kSortWarps + warp) * each;
   const int64_t last = min(first + each, static_cast<int64_t>(n));
@@ -257,7 +267,7 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
     // places: all smaller digits of all blocks, this digit of the blocks before, of the warps before
     if (tid < kDigits) {
       uint32_t all = 0, before = 0;
-      for (unsigned r = 0; r < cl.size; ++r) {
+      for (unsigned r = 0; r < kSortBlocks; ++r) {
         const uint32_t t = tid < digits ? cl.at(s.total, r)[tid] : 0u;
         before += r < cl.rank ? t : 0u;
         all += t;
@@ -372,53 +382,65 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
 struct FillArgs {
   Rows base, table;  // base.data null: zeros
   int64_t vocab;
-  int32_t dim, pieces;
+  int32_t dim;
 };
 
-// The table's rows as they are without any token: zeros, or the base's.
+// A table's row as it is without its token, by a warp: zeros, or the base's.
 template <bool VEC>
-__device__ __forceinline__ void fill_rows(const FillArgs& a, int64_t warp, int64_t warps) {
+__device__ __forceinline__ void fill_row(const Rows& base, const Rows& table, int64_t r, int dim) {
   const int lane = threadIdx.x & 31;
-  for (int64_t task = warp; task < a.vocab * a.pieces; task += warps) {
-    const int64_t r = task / a.pieces;
-    const int from = static_cast<int>(task - r * a.pieces) * kRowPiece;
-    char* out = a.table.row(r);
-    const char* base = a.base.data ? a.base.row(r) : nullptr;
-    float f[4][8] = {};
+  char* out = table.row(r);
+  const int vecs = VEC ? dim / (table.dtype == SS_FP32 ? 4 : 8) : 0;  // whole, as VEC is
+  if (VEC && !base.data) {
+    for (int i = lane; i < vecs; i += 32) __stcs(reinterpret_cast<uint4*>(out) + i, make_uint4(0u, 0u, 0u, 0u));
+  } else if (VEC && base.dtype == table.dtype) {
+    const uint4* from = reinterpret_cast<const uint4*>(base.row(r));
+    for (int i = lane; i < vecs; i += 128) {
+      uint4 w[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = from + (u * 32 + lane) * 8;
-      if (base && e < a.dim) load8<VEC>(a.base.dtype, base, e, a.dim, f[u]);
+      for (int u = 0; u < 4; ++u)
+        if (i + 32 * u < vecs) w[u] = __ldcg(from + i + 32 * u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + 32 * u < vecs) __stcs(reinterpret_cast<uint4*>(out) + i + 32 * u, w[u]);
     }
+  } else {
+    const char* row = base.data ? base.row(r) : nullptr;
+    for (int e = lane * 8; e < dim; e += 1024) {
+      float f[4][8] = {};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = from + (u * 32 + lane) * 8;
-      if (e < a.dim) store8<VEC>(a.table.dtype, out, e, a.dim, f[u]);
+      for (int u = 0; u < 4; ++u)
+        if (row && e + 256 * u < dim) load8<VEC>(base.dtype, row, e + 256 * u, dim, f[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (e + 256 * u < dim) store8<VEC>(table.dtype, out, e + 256 * u, dim, f[u]);
     }
   }
 }
 
-struct SortFillArgs {
-  SortArgs sort;
-  FillArgs fill;
-};
-
-// Cluster 0 sorts; the others fill the table meanwhile.
-// (A cluster is the sort's blocks.)
-template <bool VEC>
-__global__ void __launch_bounds__(kSortThreads, 1) sort_fill_kernel(const __grid_constant__ SortFillArgs a) {
-  extern __shared__ char shared[];
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ char sort_shared[];
   const Cluster cl = Cluster::start();
   pdl_wait();
   pdl_trigger();
   cl.started();
-  if (blockIdx.x < cl.size) {
-    if (a.sort.n == 0) return;  // there is no workspace then
-    sort_positions(a.sort, cl, *reinterpret_cast<SortShared*>(shared));
-  } else {
-    const int64_t warp = static_cast<int64_t>(blockIdx.x - cl.size) * kSortWarps + (threadIdx.x >> 5);
-    fill_rows<VEC>(a.fill, warp, static_cast<int64_t>(gridDim.x - cl.size) * kSortWarps);
-  }
+  sort_positions(a, cl, *reinterpret_cast<SortShared*>(sort_shared));
+}
+
+// The table's rows while the sort, which is launched before, goes on: it starts once the sort's blocks have waited for what
+// was ahead of them, so that is done (its writes are in L2, from where the base is read); its last block ends when the
+// sort has ended, and with it the grid, which is what the sums wait for. A block has a part of the rows, kFillBytes: 128256 x 4096 bf16 144 us, 7.3 TB/s;
+// rows dealt out to 304 blocks of 1024 threads that took turns 170.
+constexpr int kFillThreads = 256;
+constexpr int kFillBytes = 96 * 1024;
+
+template <bool VEC>
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constant__ FillArgs a) {
+  pdl_trigger();
+  const int64_t block = blockIdx.x, blocks = gridDim.x, last = a.vocab * (block + 1) / blocks;
+  for (int64_t r = a.vocab * block / blocks + (threadIdx.x >> 5); r < last; r += kFillThreads / 32)
+    fill_row<VEC>(a.base, a.table, r, a.dim);
+  if (block == blocks - 1) pdl_wait();
 }
 
 // ------------------------------------------------------------------ the sums
@@ -519,14 +541,15 @@ __device__ __forceinline__ Raw8<DT> copied(const char* shared, int u) {
 
 // Eight columns of a token's row: their sum on the base's.
 template <bool VEC>
-__device__ __forceinline__ void put_group(const SumArgs& a, char* out, int e, const Pair (&sum)[4], float (&base)[8]) {
+__device__ __forceinline__ void put_group(int dtype, char* out, int e, int dim, float scale, const Pair (&sum)[4],
+                                          float (&base)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 s = sum[j].split();
-    base[2 * j] = fmaf(s.x, a.scale, base[2 * j]);
-    base[2 * j + 1] = fmaf(s.y, a.scale, base[2 * j + 1]);
+    base[2 * j] = fmaf(s.x, scale, base[2 * j]);
+    base[2 * j + 1] = fmaf(s.y, scale, base[2 * j + 1]);
   }
-  store8<VEC>(a.table.dtype, out, e, a.dim, base);
+  store8<VEC>(dtype, out, e, dim, base);
 }
 
 template <int VECS>
@@ -599,7 +622,7 @@ __device__ __forceinline__ void join_runs(const SumArgs& a, uint32_t token, int 
     if (c.has(u)) {
       float base[8] = {};
       if (a.base.data) load8<VEC>(a.base.dtype, a.base.row(token), c.at(u), c.dim, base);
-      put_group<VEC>(a, out, c.at(u), sum[u], base);
+      put_group<VEC>(a.table.dtype, out, c.at(u), c.dim, a.scale, sum[u], base);
     }
 }
 
@@ -624,10 +647,11 @@ struct RunView {
     Loads l = {~0ull, ~0ull, ~0ull, 0};
     if (item < items) {
       const int64_t r = item / a.pieces, from = r * a.run, at = from + lane;
-      if (lane < a.run && at < a.n) l.pair = a.pairs[at];
-      if (from > 0) l.before = a.pairs[from - 1];
-      if (from + a.run < a.n) l.behind = a.pairs[from + a.run];
-      l.crossing = a.crossing.before[r];
+      const auto* pairs = reinterpret_cast<const unsigned long long*>(a.pairs);
+      if (lane < a.run && at < a.n) l.pair = __ldcg(pairs + at);
+      if (from > 0) l.before = __ldcg(pairs + from - 1);
+      if (from + a.run < a.n) l.behind = __ldcg(pairs + from + a.run);
+      l.crossing = __ldcg(a.crossing.before + r);
     }
     return l;
   }
@@ -648,7 +672,7 @@ struct RunView {
     whole = comes ? ends & (ends - 1u) : ends;
     // (a token that comes and goes is the one that came)
     if (lane < 2 ? comes : (lane < 4 && goes && !(comes && ends == 0u)))
-      cross = (lane & 1 ? a.crossing.last : a.crossing.at)[l.crossing - (lane < 2 ? 1 : 0)];
+      cross = __ldcg((lane & 1 ? a.crossing.last : a.crossing.at) + l.crossing - (lane < 2 ? 1 : 0));
   }
 };
 
@@ -719,7 +743,7 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
               else if (a.base.dtype == SS_BF16) copied<SS_BF16>(from + kRowBytes, u).unpack(base);
               else copied<SS_FP16>(from + kRowBytes, u).unpack(base);
             }
-            put_group<TVEC>(a, out, c.at(u), sum[u], base);
+            put_group<TVEC>(a.table.dtype, out, c.at(u), c.dim, a.scale, sum[u], base);
           }
       } else {
         const int which = now.comes && (now.ends & ((1u << i) - 1u)) == 0u ? 0 : 2;  // the run's first token, or its last
@@ -731,6 +755,148 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
     item += warps;
     if (item >= items) break;
     now = next;
+  }
+}
+
+// ------------------------------------------------------------------ few positions
+//
+// One launch and no sort: a block for each position looks all of them over, goes if an
+// earlier one has its token, and else lists the token's positions in order and adds
+// their rows. Other blocks fill the rows of tokens that do not occur, so nobody waits.
+// Looking takes positions squared: TODO figures
+
+constexpr int kDirectThreads = 256;
+constexpr int kDirectWarps = kDirectThreads / 32;
+constexpr int kDirectLoads = 8;                                // ids that a thread has
+constexpr int kDirectMost = kDirectThreads * kDirectLoads;     // positions
+constexpr int kDirectPiece = kSumPiece<1>;
+constexpr int kFewRows = 8;                                    // a token's rows that a warp adds alone
+constexpr int kFillRows = 4096;                                // rows whose tokens are looked for at a time
+
+struct DirectArgs {
+  const void* ids;
+  Rows d_out, base, table;
+  int64_t vocab;
+  int32_t n, dim, fill_blocks;
+  float scale;
+  bool wide;
+};
+
+// Rows of tokens that do not occur, of block `block` of a.fill_blocks.
+template <bool VEC>
+__device__ __forceinline__ void fill_others(const DirectArgs& a, int block, uint32_t (&occurs)[kFillRows / 32]) {
+  const int tid = threadIdx.x;
+  const int64_t last = a.vocab * (block + 1) / a.fill_blocks;
+  for (int64_t first = a.vocab * block / a.fill_blocks; first < last; first += kFillRows) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kFillRows), last - first));
+    __syncthreads();  // the rows before are done
+    for (int i = tid; i < kFillRows / 32; i += kDirectThreads) occurs[i] = 0u;
+    __syncthreads();
+    for (int i = tid; i < a.n; i += kDirectThreads) {
+      const int64_t r = load_id(a.ids, i, a.wide) - first;
+      if (r >= 0 && r < rows) atomicOr(&occurs[r / 32], 1u << (r % 32));
+    }
+    __syncthreads();
+    for (int r = tid >> 5; r < rows; r += kDirectWarps)
+      if (!((occurs[r / 32] >> (r % 32)) & 1u)) fill_row<VEC>(a.base, a.table, first + r, a.dim);
+  }
+}
+
+template <int DT, bool VEC, bool TVEC>
+__global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_constant__ DirectArgs a) {
+  __shared__ uint32_t occurs[kFillRows / 32];
+  __shared__ uint16_t list[kDirectMost];
+  __shared__ __align__(16) int32_t counts[kDirectLoads * kDirectWarps];
+  __shared__ __align__(16) float parts[kDirectWarps][kDirectPiece];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the two kinds of blocks by turns, as long as there are both
+  const int both = 2 * min(a.fill_blocks, a.n), b = static_cast<int>(blockIdx.x);
+  const bool fills = b < both ? b % 2 == 0 : a.fill_blocks > a.n;
+  const int me = b < both ? b / 2 : b - both / 2;
+  if (fills) return fill_others<TVEC>(a, me, occurs);
+  const int64_t token = load_id(a.ids, me, a.wide);
+  int64_t id[kDirectLoads];
+#pragma unroll
+  for (int u = 0; u < kDirectLoads; ++u) {
+    const int j = u * kDirectThreads + tid;
+    id[u] = j < a.n ? load_id(a.ids, j, a.wide) : -1;
+  }
+  if (token < 0 || token >= a.vocab) return;
+  bool earlier = false;
+  unsigned votes[kDirectLoads];
+#pragma unroll
+  for (int u = 0; u < kDirectLoads; ++u) {
+    const bool same = id[u] == token;
+    earlier = earlier || (same && u * kDirectThreads + tid < me);
+    votes[u] = __ballot_sync(0xFFFFFFFFu, same);
+    if (lane == 0) counts[u * kDirectWarps + warp] = __popc(votes[u]);
+  }
+  if (__syncthreads_or(earlier)) return;
+  // places in the list: the counts of the 32 positions' groups before, two groups a lane
+  static_assert(kDirectLoads * kDirectWarps == 64, "two groups a lane");
+  const int2 own = reinterpret_cast<const int2*>(counts)[lane];
+  int upto = own.x + own.y;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+    if (lane >= off) upto += o;
+  }
+  const int rows = __shfl_sync(0xFFFFFFFFu, upto, 31);
+#pragma unroll
+  for (int u = 0; u < kDirectLoads; ++u) {
+    const int group = u * kDirectWarps + warp;
+    const int before = __shfl_sync(0xFFFFFFFFu, upto - own.y - (group % 2 ? 0 : own.x), group / 2);
+    if ((votes[u] >> lane) & 1u) list[before + __popc(votes[u] & ((1u << lane) - 1u))] = static_cast<uint16_t>(u * kDirectThreads + tid);
+  }
+  __syncthreads();
+  const int pieces = (a.dim + kDirectPiece - 1) / kDirectPiece;
+  char* out = a.table.row(token);
+  const char* base_row = a.base.data ? a.base.row(token) : nullptr;
+  // rows first, first + step, ... of the list, kFewRows of them in flight
+  auto add_rows = [&](int first, int step, int e, Pair (&sum)[4]) {
+    for (int q = first; q < rows; q += step * kFewRows) {
+      Raw8<DT> f[kFewRows];
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r)
+        if (q + r * step < rows) f[r].template load<VEC>(a.d_out.row(list[q + r * step]), e, a.dim);
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r)
+        if (q + r * step < rows) f[r].add_to(sum);
+    }
+  };
+  if (rows <= kFewRows) {  // a piece a warp
+    for (int piece = warp; piece < pieces; piece += kDirectWarps) {
+      const int e = piece * kDirectPiece + lane * 8;
+      if (e >= a.dim) continue;
+      Pair sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = Pair::both(0.0f);
+      float base[8] = {};
+      if (base_row) load8<TVEC>(a.base.dtype, base_row, e, a.dim, base);
+      add_rows(0, 1, e, sum);
+      put_group<TVEC>(a.table.dtype, out, e, a.dim, a.scale, sum, base);
+    }
+    return;
+  }
+  for (int piece = 0; piece < pieces; ++piece) {  // a piece by all warps, every eighth row each
+    const int e = piece * kDirectPiece + lane * 8;
+    Pair sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = Pair::both(0.0f);
+    if (e < a.dim) add_rows(warp, kDirectWarps, e, sum);
+    __syncthreads();  // the piece before has been written
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<float2*>(parts[warp] + lane * 8)[j] = sum[j].split();
+    __syncthreads();
+    const int column = piece * kDirectPiece + tid;
+    if (column < a.dim) {
+      float total = parts[0][tid];
+#pragma unroll
+      for (int w = 1; w < kDirectWarps; ++w) total += parts[w][tid];
+      put1(a.table.dtype, out, column, fmaf(total, a.scale, base_row ? load1(a.base.dtype, base_row, column) : 0.0f));
+    }
   }
 }
 
@@ -831,6 +997,12 @@ ss_status lookup_impl(const ss_table* t, const void* ids, ss_idtype idtype, int6
   return launch(fn, grid_for(reinterpret_cast<const void*>(fn), n * a.pieces * 32), a, stream);
 }
 
+template <int DT>
+auto pick_direct(bool vec, bool tvec) {
+  return vec ? (tvec ? direct_kernel<DT, true, true> : direct_kernel<DT, true, false>)
+             : (tvec ? direct_kernel<DT, false, true> : direct_kernel<DT, false, false>);
+}
+
 template <int DT, int VECS>
 auto pick_sum(bool vec, bool tvec) {
   return vec ? (tvec ? sum_kernel<DT, true, true, VECS> : sum_kernel<DT, true, false, VECS>)
@@ -882,32 +1054,40 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   const Rows from = base ? Rows{base->data, base->ld, base->dtype} : Rows{nullptr, 0, SS_FP32};
   const bool groups = dim % 8 == 0;
   const bool tvec = groups && aligned_rows(table) && (!base || aligned_rows(from));
-  SortFillArgs sf = {};
-  char* w = static_cast<char*>(workspace);
-  if (n > 0) {
-    int bits = 1;  // of the keys 0 .. vocab
-    while ((t->vocab >> bits) != 0) ++bits;
-    const int passes = (bits + kDigitBits - 1) / kDigitBits;
-    sf.sort = {ids, {reinterpret_cast<uint64_t*>(w + ws.pairs[0]), reinterpret_cast<uint64_t*>(w + ws.pairs[1])},
-               {reinterpret_cast<int32_t*>(w + ws.before), reinterpret_cast<int32_t*>(w + ws.at),
-                reinterpret_cast<int32_t*>(w + ws.last)},
-               reinterpret_cast<uint32_t*>(w + ws.arrived), ws.n_arrived, t->vocab, static_cast<int32_t>(n), passes,
-               (bits + passes - 1) / passes, static_cast<int32_t>(ws.run), idtype == SS_I64};
+  const Rows rows = {const_cast<void*>(d_out), d_ld, d_dtype};
+  const bool vec = groups && n > 0 && aligned_rows(rows);
+  const int64_t row_bytes = static_cast<int64_t>(dim) * dtype_bytes(t->dtype), fill_rows = std::max<int64_t>(1, kFillBytes / row_bytes);
+  const unsigned fill_blocks = in_place ? 0u : static_cast<unsigned>((t->vocab + fill_rows - 1) / fill_rows);
+  if (n <= kDirectMost) {
+    const DirectArgs a = {ids, rows, from, table, t->vocab, static_cast<int32_t>(n), dim, static_cast<int32_t>(fill_blocks), scale,
+                          idtype == SS_I64};
+    auto* fn = d_dtype == SS_FP16 ? pick_direct<SS_FP16>(vec, tvec)
+                                  : (d_dtype == SS_FP32 ? pick_direct<SS_FP32>(vec, tvec) : pick_direct<SS_BF16>(vec, tvec));
+    return launch(fn, fill_blocks + static_cast<unsigned>(n), a, stream, kDirectThreads);
   }
-  sf.fill = {from, table, in_place ? 0 : t->vocab, dim, pieces_of(dim, kRowPiece)};
-  auto* sort_fill = tvec ? sort_fill_kernel<true> : sort_fill_kernel<false>;
-  st = allow_shared(sort_fill, sizeof(SortShared));
+  char* w = static_cast<char*>(workspace);
+  int bits = 1;  // of the keys 0 .. vocab
+  while ((t->vocab >> bits) != 0) ++bits;
+  const int passes = (bits + kDigitBits - 1) / kDigitBits;
+  const SortArgs sort = {ids, {reinterpret_cast<uint64_t*>(w + ws.pairs[0]), reinterpret_cast<uint64_t*>(w + ws.pairs[1])},
+                         {reinterpret_cast<int32_t*>(w + ws.before), reinterpret_cast<int32_t*>(w + ws.at),
+                          reinterpret_cast<int32_t*>(w + ws.last)},
+                         reinterpret_cast<uint32_t*>(w + ws.arrived), ws.n_arrived, t->vocab, static_cast<int32_t>(n),
+                         passes, (bits + passes - 1) / passes, static_cast<int32_t>(ws.run), idtype == SS_I64};
+  st = allow_shared(sort_kernel, sizeof(SortShared));
   if (st != SS_OK) return st;
-  const int cluster = n > kAloneMost ? kSortBlocks : 1;
-  const int fill_clusters = in_place ? 0 : std::max(1, 2 * sm_count() / cluster);
-  st = launch_rows(sort_fill, 1 + fill_clusters, cluster, kSortThreads, sizeof(SortShared), sf, stream);
-  if (st != SS_OK || n == 0) return st;
+  st = launch_rows(sort_kernel, 1, kSortBlocks, kSortThreads, sizeof(SortShared), sort, stream);
+  if (st != SS_OK) return st;
+  if (!in_place) {
+    const FillArgs fill = {from, table, t->vocab, dim};
+    st = launch(tvec ? fill_kernel<true> : fill_kernel<false>, fill_blocks, fill, stream, kFillThreads);
+    if (st != SS_OK) return st;
+  }
   const int stage_bytes = (vecs_of(dim) == 1 ? kSumPiece<1> : kSumPiece<2>) * static_cast<int>(dtype_bytes(d_dtype) + (base ? dtype_bytes(base->dtype) : 0));
-  const SumArgs a = {sf.sort.pairs[sf.sort.passes & 1 ? 0 : 1], sf.sort.crossing, sf.sort.arrived,
-                     reinterpret_cast<float*>(w + ws.partial), {const_cast<void*>(d_out), d_ld, d_dtype}, from, table,
+  const SumArgs a = {sort.pairs[sort.passes & 1 ? 0 : 1], sort.crossing, sort.arrived,
+                     reinterpret_cast<float*>(w + ws.partial), rows, from, table,
                      pitch_of(dim), t->vocab, static_cast<int32_t>(n), static_cast<int32_t>(ws.run),
                      static_cast<int32_t>(ws.runs), dim, sum_pieces_of(dim), stage_bytes, scale};
-  const bool vec = groups && aligned_rows(a.d_out);
   auto* fn = vecs_of(dim) == 1 ? pick_sum<1>(d_dtype, vec, tvec) : pick_sum<2>(d_dtype, vec, tvec);
   const size_t smem = static_cast<size_t>(stage_bytes) * kStages * (kSumThreads / 32);
   st = allow_shared(fn, smem);
