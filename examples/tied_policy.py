@@ -7,7 +7,7 @@ table of the start and its gradient over the logits (ss_policy_loss), and the ta
 product, the embedding's on top of it, summed over the rows of each token (ss_embedding_grad, in place). The ranks'
 gradients then go through the shard step of examples/distill_head.py.
 
-    python examples/tied_policy.py [--rounds 8] [--updates 3] [--vocab 2003] [--dim 64] [--rows 512] [--ranks 4]
+    python examples/tied_policy.py [--rounds 20] [--updates 4] [--vocab 257] [--dim 64] [--rows 512] [--ranks 4]
 """
 from __future__ import annotations
 
@@ -31,7 +31,7 @@ def hidden_of(table, tokens, scale):
 
 
 def table_gradient(table, previous, batch, scale, workspace, *, kl_coef=0.02, entropy_coef=0.001):
-    """(losses of the rows, gradient of their sum with respect to the table, flat and 16-bit) of one rank's batch."""
+    """(losses of the rows, gradient of their sum with respect to the table, flat, of the table's type) of one rank."""
     h = hidden_of(table, previous, scale)
     z = h @ table.t()
     loss = torch.empty(previous.numel(), device=table.device)
@@ -50,8 +50,8 @@ def log_probs(table, previous, tokens, scale):
     return lp
 
 
-def train(rounds=8, updates=3, vocab=2003, dim=64, rows=512, n_ranks=4, lr=5e-3, device="cuda"):
-    """Mean reward of every round's samples: 1 for a token of an odd number behind one of an even number, or the reverse."""
+def train(rounds=20, updates=4, vocab=257, dim=64, rows=512, n_ranks=4, lr=5e-3, device="cuda"):
+    """Mean reward of every round's samples: 1 for an even token behind an even one or an odd one behind an odd one."""
     g = torch.Generator(device=device)
     g.manual_seed(11)
     scale = 12.0
@@ -66,7 +66,7 @@ def train(rounds=8, updates=3, vocab=2003, dim=64, rows=512, n_ranks=4, lr=5e-3,
             previous = torch.randint(0, vocab, (rows,), generator=g, device=device)
             p = torch.softmax((hidden_of(policy.weight, previous, scale) @ policy.weight.t()).float(), dim=1)
             tokens = torch.multinomial(p, 1, generator=g)[:, 0]
-            reward = ((tokens + previous) % 2).float()
+            reward = ((tokens + previous + 1) % 2).float()
             batches.append((previous, dict(
                 tokens=tokens, advantage=reward - reward.mean(), weight=weight, reward=reward,
                 old=log_probs(policy.weight, previous, tokens, scale),
@@ -81,9 +81,9 @@ def train(rounds=8, updates=3, vocab=2003, dim=64, rows=512, n_ranks=4, lr=5e-3,
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("--rounds", type=int, default=8)
-    ap.add_argument("--updates", type=int, default=3)
-    ap.add_argument("--vocab", type=int, default=2003)
+    ap.add_argument("--rounds", type=int, default=20)
+    ap.add_argument("--updates", type=int, default=4)
+    ap.add_argument("--vocab", type=int, default=257)
     ap.add_argument("--dim", type=int, default=64)
     ap.add_argument("--rows", type=int, default=512)
     ap.add_argument("--ranks", type=int, default=4)

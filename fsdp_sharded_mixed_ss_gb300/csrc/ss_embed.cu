@@ -232,7 +232,8 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
   const int64_t last = min(first + each, static_cast<int64_t>(n));
   const uint32_t none = static_cast<uint32_t>(a.vocab);
   const int digits = 1 << a.bits;
-  for (int64_t i = static_cast<int64_t>(cl.rank) * kSortThreads + tid; i < a.n_arrived; i += warps * 32) a.arrived[i] = 0u;
+  for (int64_t i = static_cast<int64_t>(cl.rank) * kSortThreads + tid; i < a.n_arrived; i += warps * 32)
+    a.arrived[i] = 0u;
   for (int pass = 0; pass < a.passes; ++pass) {
     const uint64_t* from = a.pairs[(pass & 1) ^ 1];
     uint64_t* to = a.pairs[pass & 1];
@@ -427,10 +428,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
   sort_positions(a, cl, *reinterpret_cast<SortShared*>(sort_shared));
 }
 
-// The table's rows while the sort, which is launched before, goes on: it starts once the sort's blocks have waited for what
-// was ahead of them, so that is done (its writes are in L2, from where the base is read); its last block ends when the
-// sort has ended, and with it the grid, which is what the sums wait for. A block has a part of the rows, kFillBytes: 128256 x 4096 bf16 144 us, 7.3 TB/s;
-// rows dealt out to 304 blocks of 1024 threads that took turns 170.
+// The table's rows while the sort, which is launched before, goes on. It starts once the sort's blocks have waited for
+// what was ahead of them, so that is done (its writes are in L2, from where the base is read). Its last block ends when
+// the sort has ended, and with it the grid, which is what the sums wait for. A block has kFillBytes of the rows: 128256
+// x 4096 bf16 144 us, 7.3 TB/s; rows dealt out by turns to 304 blocks of 1024 threads 170.
 constexpr int kFillThreads = 256;
 constexpr int kFillBytes = 96 * 1024;
 
@@ -446,7 +447,9 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constan
 // ------------------------------------------------------------------ the sums
 //
 // A warp takes a run of sorted positions and up to 512 columns, adds one row after
-// another and writes the sum out where the token changes. The next kStages - 1 rows,
+// another and writes the sum out where the token changes: 65536 x 4096 bf16 in 125 us of
+// the call's 270, 0.68 of the copy; what is over is the joins (29 us) and the instructions
+// a row (an issue slot and a half in two). The next kStages - 1 rows,
 // and the base's where a token ends, are on their way to shared memory meanwhile
 // (registers for as many would halve the warps); a lane copies and reads its own
 // columns only, so nothing is waited for but its own copies. A token that reaches into
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constan
 // do so of kGroup neighbouring runs adds these up, and the last of those the groups'
 // sums: the order of the sums is that of the positions whichever warp adds them.
 
-constexpr int kGroup = 8;
+constexpr int kGroup = 8;  // 4, 8, 16, 32: 16384 x 768 68.6, 66.5, 69.8, 77.5 us; 65536 x 4096 301, 300, 311, 330
 constexpr int kStages = 4;
 constexpr int kSumThreads = 256;
 
@@ -610,7 +613,8 @@ __device__ __forceinline__ void join_runs(const SumArgs& a, uint32_t token, int 
   const int groups = last / kGroup - first / kGroup + 1;
   if (groups > 1) {
     put_partial<VECS>(a.partial + slot(lo) * a.pitch, c, sum);
-    if (!last_to_arrive(a.arrived + (2 * static_cast<int64_t>(a.runs) + slot(first)) * a.pieces + piece, groups)) return;
+    const int64_t counter = 2 * static_cast<int64_t>(a.runs) + slot(first);
+    if (!last_to_arrive(a.arrived + counter * a.pieces + piece, groups)) return;
     clear<VECS>(sum);
 #pragma unroll 2
     for (int g = first / kGroup; g <= last / kGroup; ++g)
@@ -630,7 +634,7 @@ __device__ __forceinline__ void join_runs(const SumArgs& a, uint32_t token, int 
 struct RunView {
   uint32_t token;
   int32_t row;
-  int32_t cross;   // lanes 0, 1: first position and last run of the token that comes into the run; 2, 3: that goes out of it
+  int32_t cross;   // lanes 0, 1: first position and last run of the token that comes into the run; 2, 3: that goes out
   int live;        // positions with a token
   bool comes;      // the first token begins in an earlier run
   unsigned ends;   // bit i: the token of position i ends there
@@ -695,7 +699,8 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
   auto issue = [&](const RunView& v, int i) {
     if (i < v.live) {
       const Columns<VECS> c(v.piece, a.dim);
-      copy_row<DT, VEC>(stages + put, static_cast<const char*>(a.d_out.data) + __shfl_sync(0xFFFFFFFFu, v.row, i) * d_pitch, c);
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, v.row, i);
+      copy_row<DT, VEC>(stages + put, static_cast<const char*>(a.d_out.data) + row * d_pitch, c);
       if (a.base.data && ((v.whole >> i) & 1u)) {
         const char* base = a.base.row(__shfl_sync(0xFFFFFFFFu, v.token, i));
         if (a.base.dtype == SS_FP32) copy_row<SS_FP32, TVEC>(stages + put + kRowBytes, base, c);
@@ -746,9 +751,10 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
             put_group<TVEC>(a.table.dtype, out, c.at(u), c.dim, a.scale, sum[u], base);
           }
       } else {
-        const int which = now.comes && (now.ends & ((1u << i) - 1u)) == 0u ? 0 : 2;  // the run's first token, or its last
-        join_runs<TVEC, VECS>(a, token, __shfl_sync(0xFFFFFFFFu, now.cross, which), __shfl_sync(0xFFFFFFFFu, now.cross, which + 1),
-                        now.index, now.piece, sum);
+        const int which = now.comes && (now.ends & ((1u << i) - 1u)) == 0u ? 0 : 2;  // the first token, or the last
+        const int start = __shfl_sync(0xFFFFFFFFu, now.cross, which);
+        const int last = __shfl_sync(0xFFFFFFFFu, now.cross, which + 1);
+        join_runs<TVEC, VECS>(a, token, start, last, now.index, now.piece, sum);
       }
       clear<VECS>(sum);
     }
@@ -763,15 +769,19 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
 // One launch and no sort: a block for each position looks all of them over, goes if an
 // earlier one has its token, and else lists the token's positions in order and adds
 // their rows. Other blocks fill the rows of tokens that do not occur, so nobody waits.
-// Looking takes positions squared: TODO figures
+// 1013 x 768 fp16 into 50257 rows 14.8 us, of which the fill is 12; in place 6 (21 with the
+// sort). Looking takes positions squared, so it ends at 2048 of them: 768 columns bf16 in
+// place, 2048 positions 8.9 us (11.3 with ids enough for 4096), 4096 19.6 against 25.8
+// sorted, 8192 61 against 29.5; 4096 columns, 4096 positions 50 against 40.
 
 constexpr int kDirectThreads = 256;
 constexpr int kDirectWarps = kDirectThreads / 32;
-constexpr int kDirectLoads = 8;                                // ids that a thread has
-constexpr int kDirectMost = kDirectThreads * kDirectLoads;     // positions
+constexpr int kDirectLoads = 8;                             // ids that a thread has
+constexpr int kDirectMost = kDirectThreads * kDirectLoads;  // positions
+constexpr int kGroups = kDirectMost / 32;
 constexpr int kDirectPiece = kSumPiece<1>;
-constexpr int kFewRows = 8;                                    // a token's rows that a warp adds alone
-constexpr int kFillRows = 4096;                                // rows whose tokens are looked for at a time
+constexpr int kFewRows = 8;      // a token's rows that a warp adds alone
+constexpr int kFillRows = 4096;  // rows whose tokens are looked for at a time
 
 struct DirectArgs {
   const void* ids;
@@ -793,8 +803,10 @@ __device__ __forceinline__ void fill_others(const DirectArgs& a, int block, uint
     for (int i = tid; i < kFillRows / 32; i += kDirectThreads) occurs[i] = 0u;
     __syncthreads();
     for (int i = tid; i < a.n; i += kDirectThreads) {
-      const int64_t r = load_id(a.ids, i, a.wide) - first;
-      if (r >= 0 && r < rows) atomicOr(&occurs[r / 32], 1u << (r % 32));
+      const int64_t id = load_id(a.ids, i, a.wide);
+      if (id < first || id >= first + rows) continue;
+      const int r = static_cast<int>(id - first);
+      atomicOr(&occurs[r / 32], 1u << (r % 32));
     }
     __syncthreads();
     for (int r = tid >> 5; r < rows; r += kDirectWarps)
@@ -806,7 +818,8 @@ template <int DT, bool VEC, bool TVEC>
 __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_constant__ DirectArgs a) {
   __shared__ uint32_t occurs[kFillRows / 32];
   __shared__ uint16_t list[kDirectMost];
-  __shared__ __align__(16) int32_t counts[kDirectLoads * kDirectWarps];
+  __shared__ int rows_shared;
+  __shared__ int32_t counts[kGroups];  // of the token, in every 32 positions; then in those before
   __shared__ __align__(16) float parts[kDirectWarps][kDirectPiece];
   pdl_wait();
   pdl_trigger();
@@ -816,14 +829,18 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
   const bool fills = b < both ? b % 2 == 0 : a.fill_blocks > a.n;
   const int me = b < both ? b / 2 : b - both / 2;
   if (fills) return fill_others<TVEC>(a, me, occurs);
-  const int64_t token = load_id(a.ids, me, a.wide);
-  int64_t id[kDirectLoads];
+  auto id_at = [&](int j) {
+    const int64_t id = load_id(a.ids, j, a.wide);
+    return id < 0 || id >= a.vocab ? -1 : static_cast<int32_t>(id);
+  };
+  const int32_t token = id_at(me);
+  int32_t id[kDirectLoads];
 #pragma unroll
   for (int u = 0; u < kDirectLoads; ++u) {
     const int j = u * kDirectThreads + tid;
-    id[u] = j < a.n ? load_id(a.ids, j, a.wide) : -1;
+    id[u] = j < a.n ? id_at(j) : -1;
   }
-  if (token < 0 || token >= a.vocab) return;
+  if (token < 0) return;
   bool earlier = false;
   unsigned votes[kDirectLoads];
 #pragma unroll
@@ -834,35 +851,45 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
     if (lane == 0) counts[u * kDirectWarps + warp] = __popc(votes[u]);
   }
   if (__syncthreads_or(earlier)) return;
-  // places in the list: the counts of the 32 positions' groups before, two groups a lane
-  static_assert(kDirectLoads * kDirectWarps == 64, "two groups a lane");
-  const int2 own = reinterpret_cast<const int2*>(counts)[lane];
-  int upto = own.x + own.y;
+  if (warp == 0) {
+    constexpr int G = kGroups / 32;  // a lane's
+    int own[G], upto = 0;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
-    if (lane >= off) upto += o;
-  }
-  const int rows = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    for (int q = 0; q < G; ++q) {
+      own[q] = upto;
+      upto += counts[lane * G + q];
+    }
+    const int all = upto;
 #pragma unroll
-  for (int u = 0; u < kDirectLoads; ++u) {
-    const int group = u * kDirectWarps + warp;
-    const int before = __shfl_sync(0xFFFFFFFFu, upto - own.y - (group % 2 ? 0 : own.x), group / 2);
-    if ((votes[u] >> lane) & 1u) list[before + __popc(votes[u] & ((1u << lane) - 1u))] = static_cast<uint16_t>(u * kDirectThreads + tid);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += o;
+    }
+#pragma unroll
+    for (int q = 0; q < G; ++q) counts[lane * G + q] = upto - all + own[q];
+    if (lane == 31) rows_shared = upto;
   }
+  __syncthreads();
+  const int rows = rows_shared;
+#pragma unroll
+  for (int u = 0; u < kDirectLoads; ++u)
+    if ((votes[u] >> lane) & 1u)
+      list[counts[u * kDirectWarps + warp] + __popc(votes[u] & ((1u << lane) - 1u))] =
+          static_cast<uint16_t>(u * kDirectThreads + tid);
   __syncthreads();
   const int pieces = (a.dim + kDirectPiece - 1) / kDirectPiece;
   char* out = a.table.row(token);
   const char* base_row = a.base.data ? a.base.row(token) : nullptr;
-  // rows first, first + step, ... of the list, kFewRows of them in flight
+  // rows first, first + step, ... of the list, R of them in flight
+  constexpr int R = DT == SS_FP32 ? 4 : 8;
   auto add_rows = [&](int first, int step, int e, Pair (&sum)[4]) {
-    for (int q = first; q < rows; q += step * kFewRows) {
-      Raw8<DT> f[kFewRows];
+    for (int q = first; q < rows; q += step * R) {
+      Raw8<DT> f[R];
 #pragma unroll
-      for (int r = 0; r < kFewRows; ++r)
+      for (int r = 0; r < R; ++r)
         if (q + r * step < rows) f[r].template load<VEC>(a.d_out.row(list[q + r * step]), e, a.dim);
 #pragma unroll
-      for (int r = 0; r < kFewRows; ++r)
+      for (int r = 0; r < R; ++r)
         if (q + r * step < rows) f[r].add_to(sum);
     }
   };
@@ -1056,24 +1083,28 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   const bool tvec = groups && aligned_rows(table) && (!base || aligned_rows(from));
   const Rows rows = {const_cast<void*>(d_out), d_ld, d_dtype};
   const bool vec = groups && n > 0 && aligned_rows(rows);
-  const int64_t row_bytes = static_cast<int64_t>(dim) * dtype_bytes(t->dtype), fill_rows = std::max<int64_t>(1, kFillBytes / row_bytes);
+  const int64_t fill_rows = std::max<int64_t>(1, kFillBytes / (dim * dtype_bytes(t->dtype)));
   const unsigned fill_blocks = in_place ? 0u : static_cast<unsigned>((t->vocab + fill_rows - 1) / fill_rows);
   if (n <= kDirectMost) {
-    const DirectArgs a = {ids, rows, from, table, t->vocab, static_cast<int32_t>(n), dim, static_cast<int32_t>(fill_blocks), scale,
-                          idtype == SS_I64};
-    auto* fn = d_dtype == SS_FP16 ? pick_direct<SS_FP16>(vec, tvec)
-                                  : (d_dtype == SS_FP32 ? pick_direct<SS_FP32>(vec, tvec) : pick_direct<SS_BF16>(vec, tvec));
+    const DirectArgs a = {ids, rows, from, table, t->vocab, static_cast<int32_t>(n), dim,
+                          static_cast<int32_t>(fill_blocks), scale, idtype == SS_I64};
+    auto* fn = d_dtype == SS_FP16   ? pick_direct<SS_FP16>(vec, tvec)
+               : d_dtype == SS_FP32 ? pick_direct<SS_FP32>(vec, tvec)
+                                    : pick_direct<SS_BF16>(vec, tvec);
     return launch(fn, fill_blocks + static_cast<unsigned>(n), a, stream, kDirectThreads);
   }
   char* w = static_cast<char*>(workspace);
   int bits = 1;  // of the keys 0 .. vocab
   while ((t->vocab >> bits) != 0) ++bits;
   const int passes = (bits + kDigitBits - 1) / kDigitBits;
-  const SortArgs sort = {ids, {reinterpret_cast<uint64_t*>(w + ws.pairs[0]), reinterpret_cast<uint64_t*>(w + ws.pairs[1])},
-                         {reinterpret_cast<int32_t*>(w + ws.before), reinterpret_cast<int32_t*>(w + ws.at),
-                          reinterpret_cast<int32_t*>(w + ws.last)},
-                         reinterpret_cast<uint32_t*>(w + ws.arrived), ws.n_arrived, t->vocab, static_cast<int32_t>(n),
-                         passes, (bits + passes - 1) / passes, static_cast<int32_t>(ws.run), idtype == SS_I64};
+  auto part = [&](int64_t at, auto* as) { return reinterpret_cast<decltype(as)>(w + at); };
+  constexpr uint64_t* kPairs = nullptr;  // types of the workspace's parts
+  constexpr int32_t* kIndexes = nullptr;
+  const SortArgs sort = {ids, {part(ws.pairs[0], kPairs), part(ws.pairs[1], kPairs)},
+                         {part(ws.before, kIndexes), part(ws.at, kIndexes), part(ws.last, kIndexes)},
+                         part(ws.arrived, static_cast<uint32_t*>(nullptr)), ws.n_arrived, t->vocab,
+                         static_cast<int32_t>(n), passes, (bits + passes - 1) / passes, static_cast<int32_t>(ws.run),
+                         idtype == SS_I64};
   st = allow_shared(sort_kernel, sizeof(SortShared));
   if (st != SS_OK) return st;
   st = launch_rows(sort_kernel, 1, kSortBlocks, kSortThreads, sizeof(SortShared), sort, stream);
@@ -1083,7 +1114,8 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
     st = launch(tvec ? fill_kernel<true> : fill_kernel<false>, fill_blocks, fill, stream, kFillThreads);
     if (st != SS_OK) return st;
   }
-  const int stage_bytes = (vecs_of(dim) == 1 ? kSumPiece<1> : kSumPiece<2>) * static_cast<int>(dtype_bytes(d_dtype) + (base ? dtype_bytes(base->dtype) : 0));
+  const int64_t element_bytes = dtype_bytes(d_dtype) + (base ? dtype_bytes(base->dtype) : 0);
+  const int stage_bytes = (vecs_of(dim) == 1 ? kSumPiece<1> : kSumPiece<2>) * static_cast<int>(element_bytes);
   const SumArgs a = {sort.pairs[sort.passes & 1 ? 0 : 1], sort.crossing, sort.arrived,
                      reinterpret_cast<float*>(w + ws.partial), rows, from, table,
                      pitch_of(dim), t->vocab, static_cast<int32_t>(n), static_cast<int32_t>(ws.run),
@@ -1093,7 +1125,8 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   st = allow_shared(fn, smem);
   if (st != SS_OK) return st;
   const int64_t blocks = (ws.runs * a.pieces + kSumThreads / 32 - 1) / (kSumThreads / 32);
-  const int64_t places = static_cast<int64_t>(sm_count()) * std::min<int64_t>(3, (224 * 1024) / static_cast<int64_t>(smem + 1024));
+  const int64_t resident = std::min<int64_t>(3, 224 * 1024 / static_cast<int64_t>(smem + 1024));
+  const int64_t places = sm_count() * resident;
   return launch_dependent(fn, dim3(static_cast<unsigned>(std::min(blocks, std::max<int64_t>(places, 1)))),
                           dim3(kSumThreads), smem, stream, a);
 }

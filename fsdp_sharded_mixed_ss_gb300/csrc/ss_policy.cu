@@ -103,7 +103,7 @@ struct PolicyRow {
     const float low = adv < 0.0f ? a.low : 0.0f, high = adv < 0.0f ? a.most : a.high;
     const float held = ratio < low ? low : (ratio > high ? high : ratio);  // NaN stays
     loss = -adv * held;
-    d_logprob = ratio < low || ratio > high ? 0.0f : -adv * ratio;
+    d_logprob = ratio < low || ratio > high ? 0.0f * adv : -adv * ratio;  // (NaN for an advantage that is)
     kl = 0.0f;
     if (a.ref) {
       const float g = nan ? nan_f() : log_ratio(lp, ref);

@@ -519,13 +519,14 @@ ss_status ss_embedding(const ss_table* table, const void* ids, ss_idtype idtype,
  * tokens that occur are read and written. Otherwise it must not overlap d_table.
  * d_out: row r at d_out[r * d_ld], of d_dtype. Negative ids and ids >= vocab carry
  * nothing (their rows are not read).
- * The sums are fp32, over a token's rows in ascending order, in parts that n and dim
- * alone decide: results do not depend on the launch.
+ * The sums are fp32, in an order that the sizes and the ids alone decide: results do
+ * not change from call to call.
  * workspace: device scratch of at least ss_embedding_grad_workspace(n, vocab, dim)
  *   bytes, 16-byte aligned, owned by the caller, overwritten (no initial contents
  *   needed); one for n positions does for fewer. Calls that share it have to be
  *   ordered, captured ones included.
- * n < 2^31; n == 0 is valid (d_table = base) and needs no workspace. */
+ * n < 2^31; n == 0 is valid (d_table = base) and needs no workspace. One launch up to
+ * 2048 positions, two in place and three otherwise beyond. */
 int64_t ss_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
 ss_status ss_embedding_grad(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype,
                             int64_t n, float scale, const ss_table* base, const ss_table* d_table, void* workspace,

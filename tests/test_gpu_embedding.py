@@ -179,7 +179,10 @@ def test_grad_sizes(ss, dtype, how):
             (1, 1, 1, 0, 0, 0, 0, "fp32"), (2, 3, 5, 0, 0, 0, 0, "bf16"), (31, 7, 8, 0, 0, 0, 0, "fp16"),
             (32, 40, 64, 8, 0, 8, 0, "bf16"), (33, 40, 768, 0, 0, 0, 0, "fp16"), (64, 513, 1000, 0, 0, 24, 0, "bf16"),
             (65, 511, 1001, 3, 1, 0, 3, "fp32"), (97, 512, 1032, 0, 0, 0, 0, "fp32"), (500, 1000, 130, 6, 0, 0, 5, "bf16"),
-            (1500, 50257, 40, 0, 0, 0, 0, "bf16"), (20011, 3000, 24, 0, 0, 0, 0, "fp32")]:
+            (1500, 50257, 40, 0, 0, 0, 0, "bf16"), (2048, 60, 264, 0, 0, 0, 0, "fp32"), (2049, 60, 264, 0, 0, 0, 0, "fp16"),
+            (2500, 700, 768, 8, 0, 16, 0, "bf16"), (3001, 90, 1001, 3, 1, 0, 3, "fp32"), (2100, 64, 2056, 0, 0, 0, 0, "bf16"),
+            (2200, 50, 2055, 0, 0, 1, 0, "fp32"), (9000, 300, 130, 6, 0, 0, 5, "bf16"), (20011, 3000, 24, 0, 0, 0, 0, "fp32"),
+            (33001, 70, 600, 0, 0, 0, 0, "bf16")]:
         _, d = _rows(n, dim, dtype, pad=dpad, off=doff)
         ids = _ids(n, vocab, how, seed=dim, idt=torch.int32 if n % 2 else torch.int64)
         k = ids.long()
@@ -206,14 +209,16 @@ def test_grad_table_sizes(ss, vocab):
 
 
 @pytest.mark.parametrize("bdt", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("dim,bpad,pad,off", [(768, 0, 0, 0), (100, 4, 0, 1), (33, 0, 3, 0)])
-def test_grad_on_a_base(ss, bdt, dim, bpad, pad, off):
-    _, d = _rows(700, dim, "bf16", seed=4)
+@pytest.mark.parametrize("n", [700, 5000])
+@pytest.mark.parametrize("dim,bpad,pad,off", [(768, 0, 0, 0), (100, 4, 0, 1), (33, 0, 3, 0), (2064, 8, 0, 0)])
+def test_grad_on_a_base(ss, bdt, dim, bpad, pad, off, n):
+    _, d = _rows(n, dim, "bf16" if n == 700 else "fp32", seed=4)
     _, base = _rows(300, dim, bdt, pad=bpad, seed=5)
-    ids = _ids(700, 300, "holes", seed=6)
-    _check(ss, d, ids, 300, base=base, pad=pad, off=off, scale=0.25)
-    _check(ss, d, ids, 300, base=base, pad=pad, off=off, dtype=bdt, in_place=True)
-    _check(ss, d, _ids(700, 300, "none"), 300, base=base, pad=pad, off=off)
+    for how in ("holes", "few"):
+        ids = _ids(n, 300, how, seed=6)
+        _check(ss, d, ids, 300, base=base, pad=pad, off=off, scale=0.25)
+        _check(ss, d, ids, 300, base=base, pad=pad, off=off, dtype=bdt, in_place=True)
+    _check(ss, d, _ids(n, 300, "none"), 300, base=base, pad=pad, off=off)
 
 
 def test_grad_without_positions(ss):
@@ -225,12 +230,13 @@ def test_grad_without_positions(ss):
     _check(ss, d, ids, 30, base=base, in_place=True)
 
 
-def test_grad_infinities_and_nan(ss):
+@pytest.mark.parametrize("n,vocab", [(90, 20), (4000, 900)])
+def test_grad_infinities_and_nan(ss, n, vocab):
     """They reach their own token's columns and no other."""
-    _, d = _rows(90, 40, "fp32", seed=7)
-    ids = _ids(90, 20, "any", seed=8)
+    _, d = _rows(n, 40, "fp32", seed=7)
+    ids = _ids(n, vocab, "any", seed=8)
     d[5, 3], d[6, 4], d[70, 9] = float("nan"), float("inf"), -float("inf")
-    _check(ss, d, ids, 20, dtype="bf16")
+    _check(ss, d, ids, vocab, dtype="bf16")
 
 
 def test_grad_is_that_of_the_lookup(ss):
@@ -285,6 +291,27 @@ def test_grad_streams_graphs_and_shared_workspace(ss):
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(t, want) for _, _, t, want in sets)
+
+
+def test_grad_of_extreme_ids(ss):
+    """Ids as far out as the type goes carry nothing."""
+    for n in (300, 3000):
+        _, d = _rows(n, 24, "bf16", seed=n)
+        for idt, far in ((torch.int64, 2 ** 63 - 1), (torch.int32, 2 ** 31 - 1)):
+            ids = _ids(n, 100, "any", idt=idt)
+            ids[::5], ids[1::7] = far, -far - 1
+            _check(ss, d, ids, 100)
+
+
+def test_grad_of_many_positions_past_2_31_elements(ss):
+    """The same for positions enough to be sorted."""
+    n, ld = 2100, (1 << 20) + 8
+    buf = torch.zeros((n - 1) * ld + 64, dtype=torch.bfloat16, device="cuda")
+    d = buf.as_strided((n, 64), (ld, 1))
+    _, src = _rows(n, 64, "bf16", seed=1)
+    d.copy_(src)
+    ids = _ids(n, 70, "any", seed=1)
+    assert torch.equal(_check(ss, d, ids, 70), _check(ss, src, ids, 70))
 
 
 def test_grad_past_2_31_elements(ss):
