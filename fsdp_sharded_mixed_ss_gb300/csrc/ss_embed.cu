@@ -116,7 +116,9 @@ constexpr int kRowPiece = 1024;  // elements of a row that a warp takes at a tim
 
 // ------------------------------------------------------------------ lookup
 //
-// A warp takes up to 1024 elements of a position's row.
+// A warp takes up to 1024 elements of a position's row. 16381 x 4096 bf16: 34.3 us, 5.5 TB/s
+// of the bytes that have to move, 0.81 of the measured copy (42 with a warp for each
+// piece and no row ahead). 96 x 4096 takes 6.4 us, what enqueueing it from Python takes.
 
 struct LookupArgs {
   const void* ids;
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 // digits, turns the counts into places (by digit, then by warp) and moves the pairs
 // there, 32 at a time; the places of equal digits within them come from votes on
 // their bits. Positions without a token (a negative id, or one past the vocabulary)
-// go behind the last one.
+// go behind the last one. 16384 positions 18 us, 65536 33, most of it scattered stores
+// of eight SMs and barriers; it is hidden beside the fill but in place.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;

@@ -78,6 +78,10 @@ __device__ __forceinline__ float sum8(const float (&v)[kTokens]) {
 // A block of 2 HALF threads a pair, or the blocks of a cluster: half of each has the chosen sequence, the other the
 // rejected one. Their sums, the pair's loss, and its derivative to every token. A thread's eight terms at a time are added
 // in fp32, the rest as pairs.
+// 2048 pairs of 6.3M tokens: 22 us, 4.6 TB/s of the bytes that have to move, 0.68 of the measured copy. A block's life is
+// a chain (offsets, tokens, sums, the pair's scalars, the tokens again) that the others on the SM hide in part: 64, 128,
+// 512 threads a pair 26.8, 22.1, 33.7 us; copies of all tokens to shared memory first 43. Calls on few pairs take 7.5 us,
+// what enqueueing them from Python takes.
 template <int HALF>
 __global__ void __launch_bounds__(2 * HALF) preference_kernel(const __grid_constant__ PreferenceArgs a) {
   __shared__ SeqSum red[HALF / 16];
@@ -225,7 +229,7 @@ ss_status preference_impl(const float* logprob, int64_t rows, const ss_preferenc
   const PreferenceArgs a = {logprob, p->ref_logprob, p->row_weight, p->pair_weight, p->offsets, loss,
                             reinterpret_cast<float2*>(reward), d_logprob, rows, pairs, p->beta, p->margin,
                             p->label_smoothing, p->kind, p->idtype == SS_I64, p->halves != 0, p->average != 0};
-  // threads and blocks by the tokens of a pair, on average
+  // threads and blocks by the tokens of a pair, on average: eight or more of a sequence a thread
   const int64_t each = rows / pairs;
   const int threads = each <= 512 ? 64 : (each <= 8192 ? 128 : 512);
   int cluster = 1;
