@@ -10,6 +10,10 @@ namespace {
 // fp32 87 us with 32, 95 with 64, 2048 x 70000 bf16 122 and 111. Without one rows stay whole where there are many: 4096
 // x 128256 171 us, halved 184.
 constexpr int kPartVectors = 32;
+// Up to parts of so many vectors four blocks an SM run instead of three: as many rows in flight as L2 takes. Three and
+// four, 2048 rows bf16: 102400 columns (25 vectors) 163 154 us, 106496 (26) 167 161, 110592 (27) 169 167, 114688 (28) 170
+// 172, 120000 (30) 183 188; 1021 x 50257 fp32 (25) 74 69, 4096 x 32000 bf16 (16) 102 97.
+constexpr int kFourVectors = 27;
 constexpr int kFewVectors = 8;  // with few rows: 24 x 50257 fp16 8.4 us, with parts of 16 vectors 9.3
 
 struct PolicyArgs {
@@ -371,10 +375,11 @@ ss_status policy_impl(const ss_logits* x, const ss_policy* p, const ss_policy_ou
   const int64_t places = 4 * sm_count();
   const bool few = rows * cluster * 2 <= places;
   while (cluster < kMaxCluster && rows * cluster * 2 <= places && vectors(cluster) > kFewVectors) cluster *= 2;
+  const bool more = few || vectors(cluster) <= kFourVectors;
   const bool entropy = p->entropy_coef != 0.0f || out->entropy;
   const auto with = [&](auto e) {
     return !d_logits ? pick(std::false_type(), e, four)
-                     : (few ? pick(std::true_type(), e, four) : pick(std::true_type(), e, three));
+                     : (more ? pick(std::true_type(), e, four) : pick(std::true_type(), e, three));
   };
   auto* fn = entropy ? with(std::true_type()) : with(std::false_type());
   if (rows * cluster > INT32_MAX) return SS_ERR_OVERFLOW;

@@ -64,7 +64,8 @@ def preference(lp, offsets, *, ref=None, weight=None, pair_weight=None, kind="si
                 value, slope, curve = ((h - 0.5) / beta) ** 2, 2 * (h - 0.5) / beta ** 2, 2 / beta ** 2
                 slope_size = abs(slope) + 2 / beta ** 2 * EPS32
         loss[i] = pw[i] * value
-        loss_b[i] = abs(pw[i]) * (slope_size * e + curve * e * e + 8 * EPS32 * abs(value)) + 1e-37
+        slope_e = slope_size * e if e else 0.0  # (a square's slope is infinite where h is)
+        loss_b[i] = abs(pw[i]) * (slope_e + curve * e * e + 8 * EPS32 * abs(value)) + 1e-37
         for k, (a, b) in enumerate(spans):
             g = (-1) ** k * pw[i] * slope * beta * per[k]
             d[a:b] = np.where(w[a:b] == 0, 0.0, w[a:b] * g)

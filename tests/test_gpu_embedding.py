@@ -293,6 +293,55 @@ def test_grad_streams_graphs_and_shared_workspace(ss):
         assert all(torch.equal(t, want) for _, _, t, want in sets)
 
 
+def test_grad_calls_right_behind_one_another(ss):
+    """Calls that share a workspace, without a wait in between, their inputs written right before and overwritten right
+    after, their tables read right after: sorted ones, others, in place and on a base."""
+    sets = []
+    for n, vocab, kind in ((5000, 3000, "none"), (1000, 2000, "base"), (4001, 500, "base"), (9000, 70, "place"),
+                           (300, 40, "place")):
+        _, d = _rows(n, 200, "bf16", seed=n)
+        _, base = _rows(vocab, 200, "bf16", seed=vocab)
+        ids = _ids(n, vocab, "few", seed=n)
+        want = _check(ss, d, ids, vocab, base=None if kind == "none" else base, in_place=kind == "place")
+        sets.append((n, vocab, kind, d, base, ids, want))
+    ws = torch.empty(ss.ss_embedding_grad_workspace(9000, 3000, 200), dtype=torch.uint8, device="cuda")
+    d = torch.empty((9000, 200), dtype=torch.bfloat16, device="cuda")
+    ids = torch.empty(9000, dtype=torch.int64, device="cuda")
+    b, t = (torch.empty((3000, 200), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    got = []
+    for _ in range(6):
+        for n, vocab, kind, src, base, tokens, _ in sets:
+            d[:n].copy_(src)
+            ids[:n].copy_(tokens)
+            (t if kind == "place" else b)[:vocab].copy_(base)
+            ss.ss_embedding_grad(d[:n], ids[:n], t[:vocab], ws,
+                                 base={"none": None, "base": b[:vocab], "place": t[:vocab]}[kind])
+            d.fill_(float("nan"))
+            ids.fill_(3)
+            b.fill_(float("nan"))
+            got.append(t[:vocab].clone())
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, sets[i % len(sets)][-1]), sets[i % len(sets)][:3]
+
+
+def test_grad_on_two_streams_at_once(ss):
+    """Each with a workspace of its own."""
+    sets = []
+    for n, vocab in ((6000, 20000), (7000, 900)):
+        _, d = _rows(n, 264, "bf16", seed=n)
+        ids = _ids(n, vocab, "few", seed=n)
+        sets.append((d, ids, _workspace(ss, n, vocab, 264), _check(ss, d, ids, vocab), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    tables = [[torch.empty_like(s[3]) for _ in range(8)] for s in sets]
+    for i in range(8):
+        for (d, ids, ws, _, st), t in zip(sets, tables):
+            ss.ss_embedding_grad(d, ids, t[i], ws, stream=st)
+    torch.cuda.synchronize()
+    for s, t in zip(sets, tables):
+        assert all(torch.equal(x, s[3]) for x in t)
+
+
 def test_grad_of_extreme_ids(ss):
     """Ids as far out as the type goes carry nothing."""
     for n in (300, 3000):

@@ -330,6 +330,23 @@ def test_policy_streams_and_graph_replay(ss):
         assert torch.equal(loss, want["loss"]) and torch.equal(d, wd)
 
 
+def test_policy_calls_right_behind_one_another(ss):
+    """Logits written right before a call, their gradient over them read right after, without a wait in between."""
+    x = _logits(90, 9001, "bf16")
+    r = _rows(x, 1.0)
+    kw = dict(old_logprob=r["old"], row_weight=r["weight"])
+    want, loss = torch.empty_like(x), torch.empty(90, device="cuda")
+    ss.ss_policy_loss(x, r["tokens"], r["advantage"], loss, d_logits=want, **kw)
+    z, got = torch.empty((90, 9001), dtype=x.dtype, device="cuda"), []
+    for _ in range(10):
+        z.copy_(x)
+        ss.ss_policy_loss(z, r["tokens"], r["advantage"], d_logits=z, **kw)
+        got.append(z.clone())
+        z.fill_(float("nan"))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
 def test_policy_rows_past_2_31_elements(ss):
     """Row offsets past 2^31 elements (and bytes past 2^32): a row stride of 2^30 + 1."""
     ld, vocab, rows = (1 << 30) + 1, 5001, 4
