@@ -3,6 +3,8 @@
 // (ss_embedding_grad).
 #include "ss_logits.cuh"
 
+#include <atomic>
+
 namespace ss {
 namespace {
 
@@ -186,12 +188,15 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 // digits, turns the counts into places (by digit, then by warp) and moves the pairs
 // there, 32 at a time; the places of equal digits within them come from votes on
 // their bits. Positions without a token (a negative id, or one past the vocabulary)
-// go behind the last one. 16384 positions 18 us, 65536 33, most of it scattered stores
-// of eight SMs and barriers; it is hidden beside the fill but in place.
+// go behind the last one. 16384 positions 19 us, 65536 28, most of it barriers and the
+// scattered stores of so few SMs; it is hidden beside the fill but in place. The cluster
+// is of 8 blocks, the portable size, or from 32768 positions on of 16 where the GPU has
+// room for it: 8 and 16, 4096 positions 15.8 18.4 us, 16384 19.4 19.4, 65536 36 28,
+// 262144 109 64.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortBlocks = 8;
+constexpr int kSortBlocks = 8, kManySortBlocks = 16;
 constexpr int kSortLoads = 8;  // pairs that a lane has in flight
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
@@ -229,7 +234,7 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n;
   // this warp's part
-  constexpr int64_t warps = kSortBlocks * kSortWarps;
+  const int64_t warps = static_cast<int64_t>(cl.size) * kSortWarps;
   const int64_t each = (n + warps * 32 - 1) / (warps * 32) * 32;
   const int64_t first = (static_cast<int64_t>(cl.rank) * kSortWarps + warp) * each;
   const int64_t last = min(first + each, static_cast<int64_t>(n));
@@ -271,7 +276,7 @@ __device__ void sort_positions(const SortArgs& a, const Cluster& cl, SortShared&
     // places: all smaller digits of all blocks, this digit of the blocks before, of the warps before
     if (tid < kDigits) {
       uint32_t all = 0, before = 0;
-      for (unsigned r = 0; r < kSortBlocks; ++r) {
+      for (unsigned r = 0; r < cl.size; ++r) {
         const uint32_t t = tid < digits ? cl.at(s.total, r)[tid] : 0u;
         before += r < cl.rank ? t : 0u;
         all += t;
@@ -1044,6 +1049,35 @@ auto pick_sum(int32_t dtype, bool vec, bool tvec) {
                           : (dtype == SS_FP16 ? pick_sum<SS_FP16, VECS>(vec, tvec) : pick_sum<SS_FP32, VECS>(vec, tvec));
 }
 
+// Whether the current device runs the sort as one cluster of kManySortBlocks (found out once a device).
+bool many_sort_blocks() {
+  static std::atomic<int> known[64];  // 0: not yet, 1: no, 2: yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  int state = known[dev].load(std::memory_order_relaxed);
+  if (state == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kManySortBlocks);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sizeof(SortShared);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kManySortBlocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool yes =
+        cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &cfg) == cudaSuccess && clusters > 0;
+    if (!yes) cudaGetLastError();  // not the caller's
+    state = yes ? 2 : 1;
+    known[dev].store(state, std::memory_order_relaxed);
+  }
+  return state == 2;
+}
+
 ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype, int64_t n,
                     float scale, const ss_table* base, const ss_table* t, void* workspace, int64_t workspace_bytes,
                     void* stream) {
@@ -1110,7 +1144,8 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
                          idtype == SS_I64};
   st = allow_shared(sort_kernel, sizeof(SortShared));
   if (st != SS_OK) return st;
-  st = launch_rows(sort_kernel, 1, kSortBlocks, kSortThreads, sizeof(SortShared), sort, stream);
+  const int sort_blocks = n > kMiddleMost && many_sort_blocks() ? kManySortBlocks : kSortBlocks;
+  st = launch_rows(sort_kernel, 1, sort_blocks, kSortThreads, sizeof(SortShared), sort, stream);
   if (st != SS_OK) return st;
   if (!in_place) {
     const FillArgs fill = {from, table, t->vocab, dim};
