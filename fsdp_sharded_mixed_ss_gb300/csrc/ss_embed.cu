@@ -8,22 +8,31 @@
 namespace ss {
 namespace {
 
-// ------------------------------------------------------------------ eight elements of a row
+// ------------------------------------------------------------------ a lane's eight elements of a row
+//
+// A warp takes a row in groups of 256 elements, eight a lane: neighbours, as 16-byte vectors, where every row of a call
+// begins on a 16-byte boundary and has whole vectors only (VEC); else every 32nd, one by one, so that a warp's accesses
+// are of neighbours, and those from `dim` on are left out. 16384 bf16 rows looked up: 1000 columns 8.2 us, 1001 columns
+// 16 (eight neighbours one by one 51); summed into 50257 rows 51 and 68 us.
 
-// Elements e .. e + 7 of a row as fp32: as 16-byte vectors (VEC), or one by one, those from `dim` on left 0.
+// The first of the lane's elements of the group that begins at element `group`.
+template <bool VEC>
+__device__ __forceinline__ int first_of(int group) {
+  return group + static_cast<int>(threadIdx.x & 31) * (VEC ? 8 : 1);
+}
+
+// The lane's elements from e on (e < dim) as fp32.
 template <int DT, bool VEC>
 __device__ __forceinline__ void load8(const void* row, int e, int dim, float (&f)[8]) {
   const Elem<DT>* p = static_cast<const Elem<DT>*>(row) + e;
-  if (VEC && e + 8 <= dim) {
-    if constexpr (DT == SS_FP32) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-      widen8<DT>(__ldcg(reinterpret_cast<const uint4*>(p)), f);
-    }
-  } else {
+  if constexpr (!VEC) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = e + j < dim ? to_float<DT>(__ldcg(p + j)) : 0.0f;
+    for (int j = 0; j < 8; ++j) f[j] = e + 32 * j < dim ? to_float<DT>(__ldcg(p + 32 * j)) : 0.0f;
+  } else if constexpr (DT == SS_FP32) {
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    widen8<DT>(__ldcg(reinterpret_cast<const uint4*>(p)), f);
   }
 }
 
@@ -31,17 +40,18 @@ __device__ __forceinline__ void load8(const void* row, int e, int dim, float (&f
 template <int DT, bool VEC>
 __device__ __forceinline__ void store8(void* row, int e, int dim, const float (&f)[8]) {
   Elem<DT>* p = static_cast<Elem<DT>*>(row) + e;
-  if (VEC && e + 8 <= dim) {
-    if constexpr (DT == SS_FP32) st8f(p, f);
-    else __stcs(reinterpret_cast<uint4*>(p), narrow8<DT>(f));
-  } else {
+  if constexpr (!VEC) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (e + j < dim) p[j] = from_float<DT>(f[j]);
+      if (e + 32 * j < dim) p[32 * j] = from_float<DT>(f[j]);
+  } else if constexpr (DT == SS_FP32) {
+    st8f(p, f);
+  } else {
+    __stcs(reinterpret_cast<uint4*>(p), narrow8<DT>(f));
   }
 }
 
-// Eight elements as they lie in memory.
+// The elements as they lie in memory.
 template <int DT>
 struct Raw8 {
   uint4 w[DT == SS_FP32 ? 2 : 1];
@@ -49,14 +59,14 @@ struct Raw8 {
   template <bool VEC>
   __device__ __forceinline__ void load(const void* row, int e, int dim) {
     const Elem<DT>* p = static_cast<const Elem<DT>*>(row) + e;
-    if (VEC && e + 8 <= dim) {
+    if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(w) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
     } else {
       uint32_t* q = &w[0].x;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const Elem<DT> v = e + j < dim ? p[j] : Elem<DT>(0);
+        const Elem<DT> v = e + 32 * j < dim ? p[32 * j] : Elem<DT>(0);
         if constexpr (DT == SS_FP32) q[j] = __float_as_uint(v);
         else q[j / 2] = j % 2 ? q[j / 2] | static_cast<uint32_t>(v) << 16 : v;
       }
@@ -135,7 +145,6 @@ template <int DT, int OT, bool VEC>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32), tasks = a.n * a.pieces;
   int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   // the next task's row is on its way while this one's is written, and the id of the one after
@@ -146,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
     const int from = static_cast<int>(t % a.pieces) * kRowPiece;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int e = from + (u * 32 + lane) * 8;
+      const int e = first_of<VEC>(from + u * 256);
       if (e < a.dim) raw[u].template load<VEC>(row, e, a.dim);
     }
   };
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
     const float none = id < 0 ? 0.0f : nan_f();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int e = from + (u * 32 + lane) * 8;
+      const int e = first_of<VEC>(from + u * 256);
       float v[8];
       here[u].unpack(v);
 #pragma unroll
@@ -394,35 +403,65 @@ struct FillArgs {
   int32_t dim;
 };
 
+// `bytes` bytes (64 MB at most) at `to`, by a warp: zeros, or those at `from`, which lies at the same 16-byte phase: 0 with
+// whole vectors only (VEC), or any, with elements of `es` bytes.
+template <bool VEC>
+__device__ __forceinline__ void put_bytes(char* to, const char* from, int bytes, int es) {
+  const int lane = threadIdx.x & 31;
+  int vecs = bytes / 16;
+  if constexpr (!VEC) {
+    const int head = min(-static_cast<int>(reinterpret_cast<uintptr_t>(to) & 15u) & 15, bytes);
+    vecs = (bytes - head) / 16;
+    const int tail = head + vecs * 16;
+    auto element = [&](int at) {
+      if (es == 4)
+        *reinterpret_cast<uint32_t*>(to + at) = from ? __ldcg(reinterpret_cast<const uint32_t*>(from + at)) : 0u;
+      else
+        *reinterpret_cast<uint16_t*>(to + at) =
+            from ? __ldcg(reinterpret_cast<const uint16_t*>(from + at)) : uint16_t(0);
+    };
+    if (lane * es < head) element(lane * es);
+    if (tail + lane * es < bytes) element(tail + lane * es);
+    to += head;
+    if (from) from += head;
+  }
+  uint4* out = reinterpret_cast<uint4*>(to);
+  if (!from) {
+    for (int i = lane; i < vecs; i += 32) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
+    return;
+  }
+  const uint4* in = reinterpret_cast<const uint4*>(from);
+  for (int i = lane; i < vecs; i += 128) {
+    uint4 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 32 * u < vecs) w[u] = __ldcg(in + i + 32 * u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 32 * u < vecs) __stcs(out + i + 32 * u, w[u]);
+  }
+}
+
 // A table's row as it is without its token, by a warp: zeros, or the base's.
 template <bool VEC>
 __device__ __forceinline__ void fill_row(const Rows& base, const Rows& table, int64_t r, int dim) {
-  const int lane = threadIdx.x & 31;
   char* out = table.row(r);
-  const int vecs = VEC ? dim / (table.dtype == SS_FP32 ? 4 : 8) : 0;  // whole, as VEC is
-  if (VEC && !base.data) {
-    for (int i = lane; i < vecs; i += 32) __stcs(reinterpret_cast<uint4*>(out) + i, make_uint4(0u, 0u, 0u, 0u));
-  } else if (VEC && base.dtype == table.dtype) {
-    const uint4* from = reinterpret_cast<const uint4*>(base.row(r));
-    for (int i = lane; i < vecs; i += 128) {
-      uint4 w[4];
+  const char* row = base.data ? base.row(r) : nullptr;
+  const int es = table.dtype == SS_FP32 ? 4 : 2;
+  const auto phase = [](const char* p) { return reinterpret_cast<uintptr_t>(p) & 15u; };
+  if (!row || (base.dtype == table.dtype && phase(row) == phase(out)))
+    return put_bytes<VEC>(out, row, dim * es, es);
+  for (int group = 0; group < dim; group += 1024) {
+    float f[4][8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + 32 * u < vecs) w[u] = __ldcg(from + i + 32 * u);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + 32 * u < vecs) __stcs(reinterpret_cast<uint4*>(out) + i + 32 * u, w[u]);
+    for (int u = 0; u < 4; ++u) {
+      const int e = first_of<VEC>(group + 256 * u);
+      if (e < dim) load8<VEC>(base.dtype, row, e, dim, f[u]);
     }
-  } else {
-    const char* row = base.data ? base.row(r) : nullptr;
-    for (int e = lane * 8; e < dim; e += 1024) {
-      float f[4][8] = {};
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (row && e + 256 * u < dim) load8<VEC>(base.dtype, row, e + 256 * u, dim, f[u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (e + 256 * u < dim) store8<VEC>(table.dtype, out, e + 256 * u, dim, f[u]);
+    for (int u = 0; u < 4; ++u) {
+      const int e = first_of<VEC>(group + 256 * u);
+      if (e < dim) store8<VEC>(table.dtype, out, e, dim, f[u]);
     }
   }
 }
@@ -487,12 +526,11 @@ struct SumArgs {
   float scale;
 };
 
-// A lane's columns of a piece: groups of eight, 32 * 8 apart.
-template <int VECS>
+// A lane's columns of a piece: eight of each of its groups of 256.
+template <bool VEC, int VECS>
 struct Columns {
   int from, dim;
-  __device__ __forceinline__ Columns(int piece, int dim_)
-      : from(piece * kSumPiece<VECS> + (threadIdx.x & 31) * 8), dim(dim_) {}
+  __device__ __forceinline__ Columns(int piece, int dim_) : from(first_of<VEC>(piece * kSumPiece<VECS>)), dim(dim_) {}
   __device__ __forceinline__ int at(int u) const { return from + u * 256; }
   __device__ __forceinline__ bool has(int u) const { return at(u) < dim; }
 };
@@ -516,10 +554,10 @@ __device__ __forceinline__ void wait_copies() {  // all but the latest N
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's columns of a row on their way to `shared` (the lane's own 16 bytes of every 512). VEC: the row is on a 16-byte
-// boundary and has whole groups only.
+// A lane's columns of a row on their way to `shared` (the lane's own 16 bytes of every 512); without VEC the lane loads
+// them and waits.
 template <int DT, bool VEC, int VECS>
-__device__ __forceinline__ void copy_row(char* shared, const char* row, const Columns<VECS>& c) {
+__device__ __forceinline__ void copy_row(char* shared, const char* row, const Columns<VEC, VECS>& c) {
   constexpr int W = DT == SS_FP32 ? 2 : 1;
   if constexpr (VEC) {
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(shared));
@@ -563,13 +601,18 @@ __device__ __forceinline__ void put_group(int dtype, char* out, int e, int dim, 
   store8<VEC>(dtype, out, e, dim, base);
 }
 
+// Partial sums: a lane's eight of a group lie together, whichever columns they are.
 template <int VECS>
-__device__ __forceinline__ void add_partial(const float* p, const Columns<VECS>& c, Sum<VECS>& sum) {
+__device__ __forceinline__ int partial_at(int piece, int u) {
+  return piece * kSumPiece<VECS> + u * 256 + static_cast<int>(threadIdx.x & 31) * 8;
+}
+template <int VECS>
+__device__ __forceinline__ void add_partial(const float* p, int piece, int dim, Sum<VECS>& sum) {
 #pragma unroll
   for (int u = 0; u < VECS; ++u)
-    if (c.has(u)) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + c.at(u)));
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p + c.at(u) + 4));
+    if (piece * kSumPiece<VECS> + u * 256 < dim) {
+      const float* q = p + partial_at<VECS>(piece, u);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(q)), y = __ldcg(reinterpret_cast<const float4*>(q) + 1);
       sum[u][0] = add2(sum[u][0], Pair::of(x.x, x.y));
       sum[u][1] = add2(sum[u][1], Pair::of(x.z, x.w));
       sum[u][2] = add2(sum[u][2], Pair::of(y.x, y.y));
@@ -577,11 +620,11 @@ __device__ __forceinline__ void add_partial(const float* p, const Columns<VECS>&
     }
 }
 template <int VECS>
-__device__ __forceinline__ void put_partial(float* p, const Columns<VECS>& c, const Sum<VECS>& sum) {
+__device__ __forceinline__ void put_partial(float* p, int piece, int dim, const Sum<VECS>& sum) {
 #pragma unroll
   for (int u = 0; u < VECS; ++u)
-    if (c.has(u)) {
-      float4* q = reinterpret_cast<float4*>(p + c.at(u));
+    if (piece * kSumPiece<VECS> + u * 256 < dim) {
+      float4* q = reinterpret_cast<float4*>(p + partial_at<VECS>(piece, u));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 s = sum[u][2 * i].split(), t = sum[u][2 * i + 1].split();
@@ -607,27 +650,27 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int of) {
 template <bool VEC, int VECS>
 __device__ __forceinline__ void join_runs(const SumArgs& a, uint32_t token, int start, int last, int run, int piece,
                                           Sum<VECS>& sum) {
-  const Columns<VECS> c(piece, a.dim);
   const int first = start / a.run;
   const bool inside = start % a.run != 0;  // the token begins inside its first run
   auto slot = [&](int r) { return 2 * static_cast<int64_t>(r) + (r == first && inside); };
-  put_partial<VECS>(a.partial + slot(run) * a.pitch, c, sum);
+  put_partial<VECS>(a.partial + slot(run) * a.pitch, piece, a.dim, sum);
   // this group's runs
   const int lo = max(first, run / kGroup * kGroup), hi = min(last, run / kGroup * kGroup + kGroup - 1);
   if (!last_to_arrive(a.arrived + slot(lo) * a.pieces + piece, hi - lo + 1)) return;
   clear<VECS>(sum);
 #pragma unroll 2
-  for (int r = lo; r <= hi; ++r) add_partial<VECS>(a.partial + slot(r) * a.pitch, c, sum);
+  for (int r = lo; r <= hi; ++r) add_partial<VECS>(a.partial + slot(r) * a.pitch, piece, a.dim, sum);
   const int groups = last / kGroup - first / kGroup + 1;
   if (groups > 1) {
-    put_partial<VECS>(a.partial + slot(lo) * a.pitch, c, sum);
+    put_partial<VECS>(a.partial + slot(lo) * a.pitch, piece, a.dim, sum);
     const int64_t counter = 2 * static_cast<int64_t>(a.runs) + slot(first);
     if (!last_to_arrive(a.arrived + counter * a.pieces + piece, groups)) return;
     clear<VECS>(sum);
 #pragma unroll 2
     for (int g = first / kGroup; g <= last / kGroup; ++g)
-      add_partial<VECS>(a.partial + slot(max(first, g * kGroup)) * a.pitch, c, sum);
+      add_partial<VECS>(a.partial + slot(max(first, g * kGroup)) * a.pitch, piece, a.dim, sum);
   }
+  const Columns<VEC, VECS> c(piece, a.dim);
   char* out = a.table.row(token);
 #pragma unroll
   for (int u = 0; u < VECS; ++u)
@@ -688,7 +731,7 @@ struct RunView {
   }
 };
 
-template <int DT, bool VEC, bool TVEC, int VECS>
+template <int DT, bool VEC, int VECS>
 __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_constant__ SumArgs a) {
   extern __shared__ __align__(16) char shared[];
   pdl_wait();
@@ -706,13 +749,13 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
   auto forth = [&](int at) { return at + a.stage_bytes == ring ? 0 : at + a.stage_bytes; };
   auto issue = [&](const RunView& v, int i) {
     if (i < v.live) {
-      const Columns<VECS> c(v.piece, a.dim);
+      const Columns<VEC, VECS> c(v.piece, a.dim);
       const int64_t row = __shfl_sync(0xFFFFFFFFu, v.row, i);
       copy_row<DT, VEC>(stages + put, static_cast<const char*>(a.d_out.data) + row * d_pitch, c);
       if (a.base.data && ((v.whole >> i) & 1u)) {
         const char* base = a.base.row(__shfl_sync(0xFFFFFFFFu, v.token, i));
-        if (a.base.dtype == SS_FP32) copy_row<SS_FP32, TVEC>(stages + put + kRowBytes, base, c);
-        else copy_row<SS_BF16, TVEC>(stages + put + kRowBytes, base, c);  // the bits, of either 16-bit type
+        if (a.base.dtype == SS_FP32) copy_row<SS_FP32, VEC>(stages + put + kRowBytes, base, c);
+        else copy_row<SS_BF16, VEC>(stages + put + kRowBytes, base, c);  // the bits, of either 16-bit type
       }
     }
     commit_copies();
@@ -727,7 +770,7 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
     const int steps = max(now.live, kStages - 1);
     const RunView next(a, ahead, item + warps);
     ahead = RunView::load(a, item + 2 * warps, items);
-    const Columns<VECS> c(now.piece, a.dim);
+    const Columns<VEC, VECS> c(now.piece, a.dim);
     Sum<VECS> sum;
     clear<VECS>(sum);
 #pragma unroll 1
@@ -756,13 +799,13 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
               else if (a.base.dtype == SS_BF16) copied<SS_BF16>(from + kRowBytes, u).unpack(base);
               else copied<SS_FP16>(from + kRowBytes, u).unpack(base);
             }
-            put_group<TVEC>(a.table.dtype, out, c.at(u), c.dim, a.scale, sum[u], base);
+            put_group<VEC>(a.table.dtype, out, c.at(u), c.dim, a.scale, sum[u], base);
           }
       } else {
         const int which = now.comes && (now.ends & ((1u << i) - 1u)) == 0u ? 0 : 2;  // the first token, or the last
         const int start = __shfl_sync(0xFFFFFFFFu, now.cross, which);
         const int last = __shfl_sync(0xFFFFFFFFu, now.cross, which + 1);
-        join_runs<TVEC, VECS>(a, token, start, last, now.index, now.piece, sum);
+        join_runs<VEC, VECS>(a, token, start, last, now.index, now.piece, sum);
       }
       clear<VECS>(sum);
     }
@@ -822,7 +865,7 @@ __device__ __forceinline__ void fill_others(const DirectArgs& a, int block, uint
   }
 }
 
-template <int DT, bool VEC, bool TVEC>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_constant__ DirectArgs a) {
   __shared__ uint32_t occurs[kFillRows / 32];
   __shared__ uint16_t list[kDirectMost];
@@ -836,7 +879,7 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
   const int both = 2 * min(a.fill_blocks, a.n), b = static_cast<int>(blockIdx.x);
   const bool fills = b < both ? b % 2 == 0 : a.fill_blocks > a.n;
   const int me = b < both ? b / 2 : b - both / 2;
-  if (fills) return fill_others<TVEC>(a, me, occurs);
+  if (fills) return fill_others<VEC>(a, me, occurs);
   auto id_at = [&](int j) {
     const int64_t id = load_id(a.ids, j, a.wide);
     return id < 0 || id >= a.vocab ? -1 : static_cast<int32_t>(id);
@@ -903,20 +946,20 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
   };
   if (rows <= kFewRows) {  // a piece a warp
     for (int piece = warp; piece < pieces; piece += kDirectWarps) {
-      const int e = piece * kDirectPiece + lane * 8;
+      const int e = first_of<VEC>(piece * kDirectPiece);
       if (e >= a.dim) continue;
       Pair sum[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum[j] = Pair::both(0.0f);
       float base[8] = {};
-      if (base_row) load8<TVEC>(a.base.dtype, base_row, e, a.dim, base);
+      if (base_row) load8<VEC>(a.base.dtype, base_row, e, a.dim, base);
       add_rows(0, 1, e, sum);
-      put_group<TVEC>(a.table.dtype, out, e, a.dim, a.scale, sum, base);
+      put_group<VEC>(a.table.dtype, out, e, a.dim, a.scale, sum, base);
     }
     return;
   }
   for (int piece = 0; piece < pieces; ++piece) {  // a piece by all warps, every eighth row each
-    const int e = piece * kDirectPiece + lane * 8;
+    const int e = first_of<VEC>(piece * kDirectPiece);
     Pair sum[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] = Pair::both(0.0f);
@@ -925,11 +968,11 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < 4; ++j) reinterpret_cast<float2*>(parts[warp] + lane * 8)[j] = sum[j].split();
     __syncthreads();
-    const int column = piece * kDirectPiece + tid;
+    const int column = piece * kDirectPiece + tid, at = VEC ? tid : tid % 32 * 8 + tid / 32;  // which lane has it
     if (column < a.dim) {
-      float total = parts[0][tid];
+      float total = parts[0][at];
 #pragma unroll
-      for (int w = 1; w < kDirectWarps; ++w) total += parts[w][tid];
+      for (int w = 1; w < kDirectWarps; ++w) total += parts[w][at];
       put1(a.table.dtype, out, column, fmaf(total, a.scale, base_row ? load1(a.base.dtype, base_row, column) : 0.0f));
     }
   }
@@ -937,7 +980,7 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
-int64_t pitch_of(int64_t dim) { return (dim + 7) / 8 * 8; }
+int64_t pitch_of(int64_t dim) { return (dim + 255) / 256 * 256; }
 int pieces_of(int64_t dim, int piece) { return static_cast<int>((dim + piece - 1) / piece); }
 
 int sum_pieces_of(int64_t dim) { return pieces_of(dim, vecs_of(dim) == 1 ? kSumPiece<1> : kSumPiece<2>); }
@@ -1027,26 +1070,22 @@ ss_status lookup_impl(const ss_table* t, const void* ids, ss_idtype idtype, int6
   if (ranges.overlap()) return SS_ERR_OVERLAP;
   const LookupArgs a = {ids, {t->data, t->ld, t->dtype}, {out, out_ld, out_dtype}, n, t->vocab,
                         static_cast<int32_t>(t->dim), pieces_of(t->dim, kRowPiece), scale, idtype == SS_I64};
-  auto* fn = aligned_rows(a.table) && aligned_rows(a.out) ? pick_lookup<true>(t->dtype, out_dtype)
-                                                          : pick_lookup<false>(t->dtype, out_dtype);
+  auto* fn = t->dim % 8 == 0 && aligned_rows(a.table) && aligned_rows(a.out) ? pick_lookup<true>(t->dtype, out_dtype)
+                                                                             : pick_lookup<false>(t->dtype, out_dtype);
   return launch(fn, grid_for(reinterpret_cast<const void*>(fn), n * a.pieces * 32), a, stream);
 }
 
-template <int DT>
-auto pick_direct(bool vec, bool tvec) {
-  return vec ? (tvec ? direct_kernel<DT, true, true> : direct_kernel<DT, true, false>)
-             : (tvec ? direct_kernel<DT, false, true> : direct_kernel<DT, false, false>);
+template <bool VEC>
+auto pick_direct(int32_t dtype) {
+  return dtype == SS_FP16   ? direct_kernel<SS_FP16, VEC>
+         : dtype == SS_FP32 ? direct_kernel<SS_FP32, VEC>
+                            : direct_kernel<SS_BF16, VEC>;
 }
-
-template <int DT, int VECS>
-auto pick_sum(bool vec, bool tvec) {
-  return vec ? (tvec ? sum_kernel<DT, true, true, VECS> : sum_kernel<DT, true, false, VECS>)
-             : (tvec ? sum_kernel<DT, false, true, VECS> : sum_kernel<DT, false, false, VECS>);
-}
-template <int VECS>
-auto pick_sum(int32_t dtype, bool vec, bool tvec) {
-  return dtype == SS_BF16 ? pick_sum<SS_BF16, VECS>(vec, tvec)
-                          : (dtype == SS_FP16 ? pick_sum<SS_FP16, VECS>(vec, tvec) : pick_sum<SS_FP32, VECS>(vec, tvec));
+template <bool VEC, int VECS>
+auto pick_sum(int32_t dtype) {
+  return dtype == SS_FP16   ? sum_kernel<SS_FP16, VEC, VECS>
+         : dtype == SS_FP32 ? sum_kernel<SS_FP32, VEC, VECS>
+                            : sum_kernel<SS_BF16, VEC, VECS>;
 }
 
 // Whether the current device runs the sort as one cluster of kManySortBlocks (found out once a device).
@@ -1116,18 +1155,14 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   const int32_t dim = static_cast<int32_t>(t->dim);
   const Rows table = {t->data, t->ld, t->dtype};
   const Rows from = base ? Rows{base->data, base->ld, base->dtype} : Rows{nullptr, 0, SS_FP32};
-  const bool groups = dim % 8 == 0;
-  const bool tvec = groups && aligned_rows(table) && (!base || aligned_rows(from));
   const Rows rows = {const_cast<void*>(d_out), d_ld, d_dtype};
-  const bool vec = groups && n > 0 && aligned_rows(rows);
+  const bool vec = dim % 8 == 0 && aligned_rows(table) && (!base || aligned_rows(from)) && (n == 0 || aligned_rows(rows));
   const int64_t fill_rows = std::max<int64_t>(1, kFillBytes / (dim * dtype_bytes(t->dtype)));
   const unsigned fill_blocks = in_place ? 0u : static_cast<unsigned>((t->vocab + fill_rows - 1) / fill_rows);
   if (n <= kDirectMost) {
     const DirectArgs a = {ids, rows, from, table, t->vocab, static_cast<int32_t>(n), dim,
                           static_cast<int32_t>(fill_blocks), scale, idtype == SS_I64};
-    auto* fn = d_dtype == SS_FP16   ? pick_direct<SS_FP16>(vec, tvec)
-               : d_dtype == SS_FP32 ? pick_direct<SS_FP32>(vec, tvec)
-                                    : pick_direct<SS_BF16>(vec, tvec);
+    auto* fn = vec ? pick_direct<true>(d_dtype) : pick_direct<false>(d_dtype);
     return launch(fn, fill_blocks + static_cast<unsigned>(n), a, stream, kDirectThreads);
   }
   char* w = static_cast<char*>(workspace);
@@ -1149,7 +1184,7 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   if (st != SS_OK) return st;
   if (!in_place) {
     const FillArgs fill = {from, table, t->vocab, dim};
-    st = launch(tvec ? fill_kernel<true> : fill_kernel<false>, fill_blocks, fill, stream, kFillThreads);
+    st = launch(vec ? fill_kernel<true> : fill_kernel<false>, fill_blocks, fill, stream, kFillThreads);
     if (st != SS_OK) return st;
   }
   const int64_t element_bytes = dtype_bytes(d_dtype) + (base ? dtype_bytes(base->dtype) : 0);
@@ -1158,7 +1193,8 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
                      reinterpret_cast<float*>(w + ws.partial), rows, from, table,
                      pitch_of(dim), t->vocab, static_cast<int32_t>(n), static_cast<int32_t>(ws.run),
                      static_cast<int32_t>(ws.runs), dim, sum_pieces_of(dim), stage_bytes, scale};
-  auto* fn = vecs_of(dim) == 1 ? pick_sum<1>(d_dtype, vec, tvec) : pick_sum<2>(d_dtype, vec, tvec);
+  auto* fn = vecs_of(dim) == 1 ? (vec ? pick_sum<true, 1>(d_dtype) : pick_sum<false, 1>(d_dtype))
+                               : (vec ? pick_sum<true, 2>(d_dtype) : pick_sum<false, 2>(d_dtype));
   const size_t smem = static_cast<size_t>(stage_bytes) * kStages * (kSumThreads / 32);
   st = allow_shared(fn, smem);
   if (st != SS_OK) return st;
