@@ -128,8 +128,8 @@ constexpr int kRowPiece = 1024;  // elements of a row that a warp takes at a tim
 
 // ------------------------------------------------------------------ lookup
 //
-// A warp takes up to 1024 elements of a position's row. 16381 x 4096 bf16: 34.3 us, 5.5 TB/s
-// of the bytes that have to move, 0.81 of the measured copy (42 with a warp for each
+// A warp takes up to 1024 elements of a position's row. 16381 x 4096 bf16: 35 us, 5.4 TB/s
+// of the bytes that have to move, 0.80 of the measured copy (42 with a warp for each
 // piece and no row ahead). 96 x 4096 takes 6.4 us, what enqueueing it from Python takes.
 
 struct LookupArgs {
@@ -403,8 +403,8 @@ struct FillArgs {
   int32_t dim;
 };
 
-// `bytes` bytes (64 MB at most) at `to`, by a warp: zeros, or those at `from`, which lies at the same 16-byte phase: 0 with
-// whole vectors only (VEC), or any, with elements of `es` bytes.
+// `bytes` bytes (64 MB at most) at `to`, by a warp: zeros, or those at `from`, which lies at the same 16-byte phase. VEC:
+// on the boundary, whole vectors; else elements of `es` bytes.
 template <bool VEC>
 __device__ __forceinline__ void put_bytes(char* to, const char* from, int bytes, int es) {
   const int lane = threadIdx.x & 31;
@@ -821,15 +821,17 @@ __global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const __grid_consta
 // earlier one has its token, and else lists the token's positions in order and adds
 // their rows. Other blocks fill the rows of tokens that do not occur, so nobody waits.
 // 1013 x 768 fp16 into 50257 rows 14.8 us, of which the fill is 12; in place 6 (21 with the
-// sort). Looking takes positions squared, so it ends at 2048 of them: 768 columns bf16 in
-// place, 2048 positions 8.9 us (11.3 with ids enough for 4096), 4096 19.6 against 25.8
-// sorted, 8192 61 against 29.5; 4096 columns, 4096 positions 50 against 40.
+// sort). Looking takes positions squared, so it ends at 2048 of them, or at 4096 where rows
+// are short and aligned, with twice the ids a thread: 768 columns bf16, 2049 positions 18.8
+// us, sorted 28.7, 3000 22.7 and 30.0, 4096 27.3 and 29.7, in place 19.6 and 25.8, 8192 61
+// and 29.5; 4096 columns in place, 4096 positions 50 and 40; 1001 columns 70 and 34. (2048
+// positions of 768 columns with 8 and 16 ids a thread 15.6 and 18.4.)
 
 constexpr int kDirectThreads = 256;
 constexpr int kDirectWarps = kDirectThreads / 32;
-constexpr int kDirectLoads = 8;                             // ids that a thread has
-constexpr int kDirectMost = kDirectThreads * kDirectLoads;  // positions
-constexpr int kGroups = kDirectMost / 32;
+constexpr int kFewLoads = 8, kMoreLoads = 16;  // ids that a thread has
+template <int LOADS>
+constexpr int kDirectMost = kDirectThreads * LOADS;  // positions
 constexpr int kDirectPiece = kSumPiece<1>;
 constexpr int kFewRows = 8;      // a token's rows that a warp adds alone
 constexpr int kFillRows = 4096;  // rows whose tokens are looked for at a time
@@ -865,10 +867,11 @@ __device__ __forceinline__ void fill_others(const DirectArgs& a, int block, uint
   }
 }
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, int LOADS>
 __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_constant__ DirectArgs a) {
+  constexpr int kGroups = kDirectMost<LOADS> / 32;
   __shared__ uint32_t occurs[kFillRows / 32];
-  __shared__ uint16_t list[kDirectMost];
+  __shared__ uint16_t list[kDirectMost<LOADS>];
   __shared__ int rows_shared;
   __shared__ int32_t counts[kGroups];  // of the token, in every 32 positions; then in those before
   __shared__ __align__(16) float parts[kDirectWarps][kDirectPiece];
@@ -885,17 +888,17 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
     return id < 0 || id >= a.vocab ? -1 : static_cast<int32_t>(id);
   };
   const int32_t token = id_at(me);
-  int32_t id[kDirectLoads];
+  int32_t id[LOADS];
 #pragma unroll
-  for (int u = 0; u < kDirectLoads; ++u) {
+  for (int u = 0; u < LOADS; ++u) {
     const int j = u * kDirectThreads + tid;
     id[u] = j < a.n ? id_at(j) : -1;
   }
   if (token < 0) return;
   bool earlier = false;
-  unsigned votes[kDirectLoads];
+  unsigned votes[LOADS];
 #pragma unroll
-  for (int u = 0; u < kDirectLoads; ++u) {
+  for (int u = 0; u < LOADS; ++u) {
     const bool same = id[u] == token;
     earlier = earlier || (same && u * kDirectThreads + tid < me);
     votes[u] = __ballot_sync(0xFFFFFFFFu, same);
@@ -923,7 +926,7 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(const __grid_
   __syncthreads();
   const int rows = rows_shared;
 #pragma unroll
-  for (int u = 0; u < kDirectLoads; ++u)
+  for (int u = 0; u < LOADS; ++u)
     if ((votes[u] >> lane) & 1u)
       list[counts[u * kDirectWarps + warp] + __popc(votes[u] & ((1u << lane) - 1u))] =
           static_cast<uint16_t>(u * kDirectThreads + tid);
@@ -1075,11 +1078,11 @@ ss_status lookup_impl(const ss_table* t, const void* ids, ss_idtype idtype, int6
   return launch(fn, grid_for(reinterpret_cast<const void*>(fn), n * a.pieces * 32), a, stream);
 }
 
-template <bool VEC>
+template <bool VEC, int LOADS>
 auto pick_direct(int32_t dtype) {
-  return dtype == SS_FP16   ? direct_kernel<SS_FP16, VEC>
-         : dtype == SS_FP32 ? direct_kernel<SS_FP32, VEC>
-                            : direct_kernel<SS_BF16, VEC>;
+  return dtype == SS_FP16   ? direct_kernel<SS_FP16, VEC, LOADS>
+         : dtype == SS_FP32 ? direct_kernel<SS_FP32, VEC, LOADS>
+                            : direct_kernel<SS_BF16, VEC, LOADS>;
 }
 template <bool VEC, int VECS>
 auto pick_sum(int32_t dtype) {
@@ -1156,13 +1159,17 @@ ss_status grad_impl(const void* d_out, int32_t d_dtype, int64_t d_ld, const void
   const Rows table = {t->data, t->ld, t->dtype};
   const Rows from = base ? Rows{base->data, base->ld, base->dtype} : Rows{nullptr, 0, SS_FP32};
   const Rows rows = {const_cast<void*>(d_out), d_ld, d_dtype};
-  const bool vec = dim % 8 == 0 && aligned_rows(table) && (!base || aligned_rows(from)) && (n == 0 || aligned_rows(rows));
+  const bool vec =
+      dim % 8 == 0 && aligned_rows(table) && (!base || aligned_rows(from)) && (n == 0 || aligned_rows(rows));
   const int64_t fill_rows = std::max<int64_t>(1, kFillBytes / (dim * dtype_bytes(t->dtype)));
   const unsigned fill_blocks = in_place ? 0u : static_cast<unsigned>((t->vocab + fill_rows - 1) / fill_rows);
-  if (n <= kDirectMost) {
+  const bool few = n <= kDirectMost<kFewLoads>;
+  if (few || (n <= kDirectMost<kMoreLoads> && vecs_of(dim) == 1 && vec)) {
     const DirectArgs a = {ids, rows, from, table, t->vocab, static_cast<int32_t>(n), dim,
                           static_cast<int32_t>(fill_blocks), scale, idtype == SS_I64};
-    auto* fn = vec ? pick_direct<true>(d_dtype) : pick_direct<false>(d_dtype);
+    auto* fn = !vec  ? pick_direct<false, kFewLoads>(d_dtype)
+               : few ? pick_direct<true, kFewLoads>(d_dtype)
+                     : pick_direct<true, kMoreLoads>(d_dtype);
     return launch(fn, fill_blocks + static_cast<unsigned>(n), a, stream, kDirectThreads);
   }
   char* w = static_cast<char*>(workspace);

@@ -526,7 +526,8 @@ ss_status ss_embedding(const ss_table* table, const void* ids, ss_idtype idtype,
  *   needed); one for n positions does for fewer. Calls that share it have to be
  *   ordered, captured ones included.
  * n < 2^31; n == 0 is valid (d_table = base) and needs no workspace. One launch up to
- * 2048 positions, two in place and three otherwise beyond. */
+ * 2048 positions (4096 where rows are short and aligned), beyond two in place and
+ * three otherwise. */
 int64_t ss_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
 ss_status ss_embedding_grad(const void* d_out, int32_t d_dtype, int64_t d_ld, const void* ids, ss_idtype idtype,
                             int64_t n, float scale, const ss_table* base, const ss_table* d_table, void* workspace,
